@@ -43,7 +43,7 @@
 extern "C" {
 #endif
 
-#define RET_ABI_VERSION 7
+#define RET_ABI_VERSION 8
 
 typedef enum { RET_F32 = 0, RET_BF16 = 1 } ret_dtype_t;
 
@@ -222,7 +222,7 @@ ret_status_t ret_chunkwise_bwd(const void* q, const void* k, const void* v, cons
  * "ret_chunk_wide", "ret_chunk_dma_local", "ret_chunk_dma_scan", "ret_chunk_dma" and "ret_rotate_qk" (bf16 input),
  * "ret_chunk_full", "ret_chunk_local", "ret_segment_scan" (fp32 input), "ret_parallel", "ret_recurrent_step",
  * "ret_msr_epilogue", "ret_permute_rotate" (gradients), "ret_norm_zseg", "ret_norm_rows", "ret_norm_scale",
- * "ret_norm_step" (score normalizations). A timer must not be attached to calls that are being captured into a
+ * "ret_norm_step" (score normalizations); the entry points after them name theirs. A timer must not be attached to calls that are being captured into a
  * graph. One timer may be shared by calls on several threads.
  */
 typedef struct ret_timer ret_timer_t;
@@ -387,6 +387,54 @@ ret_status_t ret_chunkwise_fwd_noalloc(const void* q, const void* k, const void*
                                        int dk, int dv, ret_dtype_t in_dt, ret_dtype_t out_dt, const float* gamma,
                                        const double* theta, int64_t pos0, int chunk, const float* state_in,
                                        float* state_out, void* stream);
+
+/*
+ * Gradients of ret_msr_epilogue, y = swish(gate) (.) n with n = w xh + b and xh the standardized head row of o:
+ *     dn = dy (.) swish(gate),  dgate = dy (.) n (.) swish'(gate),  swish'(x) = s + x s (1 - s), s = sigmoid(x)
+ *     do = rstd (a - mean(a) - xh mean(a xh)),  a = w (.) dn, the means over the d_v values of a head
+ *     dweight[h d_v + c] = sum over rows of dn xh,  dbias = sum over rows of dn
+ * dy, o, gate, dout, dgate: [rows, H, d_v], each F32 or BF16; gate, gn_weight, gn_bias as the forward call had them
+ * (NULL where it had NULL). dgate, dweight, dbias (device float[H * d_v]) may each be NULL: not wanted. rows = 0 writes
+ * zeros to dweight and dbias. dout and dgate may take the place of dy, o or gate (same start and dtype); no other
+ * overlap (RET_ERR_INVALID_ARG). workspace: ret_msr_epilogue_bwd_workspace_bytes device bytes when dweight or dbias is
+ * wanted (RET_ERR_WORKSPACE if short), of any content; calls sharing one must not overlap in time. The sums are added
+ * in a fixed order: the same call gives the same bits. Pointers 16-byte aligned; supported: d_v in {16, 32, 64, 128,
+ * 256, 512}. Kernels: "ret_msr_epilogue_bwd", "ret_column_sums". opts: the timer, or NULL.
+ */
+size_t ret_msr_epilogue_bwd_workspace_bytes(int64_t rows, int H, int dv);
+ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gate, const float* gn_weight,
+                                  const float* gn_bias, void* dout, void* dgate, float* dweight, float* dbias,
+                                  int64_t rows, int H, int dv, ret_dtype_t dy_dt, ret_dtype_t o_dt,
+                                  ret_dtype_t gate_dt, ret_dtype_t do_dt, ret_dtype_t dgate_dt, float eps,
+                                  void* workspace, size_t workspace_bytes, void* stream, const ret_options_t* opts);
+
+/*
+ * Layer norm, the pre-norm of a retention or gated-delta block, with the residual stream's addition:
+ *     s = x + residual (rounded to x_dt; s = x without one),  y = w (.) (s - mean) rstd + b,  rstd = 1/sqrt(var + eps)
+ * over the last axis of x [rows, D] (biased variance, statistics in fp32). residual, sum_out: as x, or NULL; sum_out
+ * receives s, the stream the next block adds to. weight, bias: device float[D], NULL means 1 and 0. mean, rstd: device
+ * float[rows], or NULL; the gradients want them. x_dt, y_dt: F32 or BF16 each. y and sum_out may take the place of x or
+ * residual (same start and dtype); no other overlap. Pointers 16-byte aligned; rows = 0 does nothing; 1 <= D <= 16384
+ * (rows with D a multiple of 8 move as 16-byte vectors). Kernel: "ret_layer_norm".
+ */
+ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias, void* y,
+                                void* sum_out, float* mean, float* rstd, int64_t rows, int D, ret_dtype_t x_dt,
+                                ret_dtype_t y_dt, float eps, void* stream, const ret_options_t* opts);
+
+/*
+ * Gradients of ret_layer_norm_fwd: x [rows, D] is what was normalized (s where there was a residual), mean and rstd are
+ * the forward call's.
+ *     dx = rstd (a - mean(a) - xh mean(a xh)) + dsum,  a = w (.) dy,  xh = (x - mean) rstd
+ *     dweight = sum over rows of dy xh,  dbias = sum over rows of dy     (device float[D]; NULL: not wanted)
+ * dsum ([rows, D] in dx_dt, or NULL) is the gradient that reaches s past the norm; dx is then the gradient of x and of
+ * residual alike. dx may take the place of dy, x or dsum (same start and dtype). rows = 0 writes zeros to dweight and
+ * dbias. workspace: as ret_msr_epilogue_bwd's. Kernels: "ret_layer_norm_bwd", "ret_column_sums".
+ */
+size_t ret_layer_norm_bwd_workspace_bytes(int64_t rows, int D);
+ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weight, const float* mean,
+                                const float* rstd, const void* dsum, void* dx, float* dweight, float* dbias,
+                                int64_t rows, int D, ret_dtype_t x_dt, ret_dtype_t dy_dt, ret_dtype_t dx_dt,
+                                void* workspace, size_t workspace_bytes, void* stream, const ret_options_t* opts);
 
 #ifdef __cplusplus
 }

@@ -14,19 +14,19 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "retention.h"
 
 // =====================================================================================================
 // Host side: validation, kernel selection, launches, timing records.
 // =====================================================================================================
+namespace ret {
+
 namespace {
-
-using namespace ret;
-
 thread_local std::string g_last_error;
+}  // namespace
 
-ret_status_t fail(ret_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ret_status_t fail(ret_status_t st, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -37,27 +37,6 @@ ret_status_t fail(ret_status_t st, const char* fmt, ...) {
     return st;
 }
 
-}  // namespace
-
-// ---- launch records: a caller-owned object (ret_options_t.timer); the library keeps none of its own ----
-struct ret_timer {
-    struct Rec {
-        const char* name;
-        hipEvent_t start, stop;
-    };
-    std::mutex mu;
-    std::vector<Rec> recs;
-};
-
-namespace {
-
-// The plan options with the library's defaults filled in (ret_options_t documents each field).
-struct Opts {
-    int segments = 0, target_wgs = 0, prerotate = -1, onchip = 1, variant = 0;
-    int step_cw = 0, step_wr = 0, step_pairs = 0, bwd_direct = 1, step_cache = 0;
-    long long chain_spin = 0;
-    ret_timer_t* timer = nullptr;
-};
 Opts resolve(const ret_options_t* o) {
     Opts r;
     if (!o) return r;
@@ -75,32 +54,6 @@ Opts resolve(const ret_options_t* o) {
     r.timer = o->timer;
     return r;
 }
-const Opts kDefaultOpts;
-
-// Kernel-argument form of the chain's wait limit: ticks, or -1 (every wait gives up at once).
-long long chain_spin_arg(const Opts& op) {
-    if (op.chain_spin < 0) return -1;
-    return op.chain_spin > 0 ? op.chain_spin : (1ll << 24);
-}
-
-struct LaunchTimer {
-    hipEvent_t start = nullptr, stop = nullptr;
-    hipStream_t stream;
-    const char* name;
-    ret_timer_t* t;
-    LaunchTimer(const char* n, hipStream_t s, const Opts& op) : stream(s), name(n), t(op.timer) {
-        if (t && hipEventCreate(&start) == hipSuccess && hipEventCreate(&stop) == hipSuccess)
-            (void)hipEventRecord(start, stream);
-        else
-            t = nullptr;
-    }
-    void done() {
-        if (!t) return;
-        (void)hipEventRecord(stop, stream);
-        std::lock_guard<std::mutex> lk(t->mu);
-        t->recs.push_back({name, start, stop});
-    }
-};
 
 ret_status_t launch_status(const char* what) {
     hipError_t e = hipGetLastError();
@@ -108,7 +61,19 @@ ret_status_t launch_status(const char* what) {
     return RET_OK;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+}  // namespace ret
+
+namespace {
+
+using namespace ret;
+
+const Opts kDefaultOpts;
+
+// Kernel-argument form of the chain's wait limit: ticks, or -1 (every wait gives up at once).
+long long chain_spin_arg(const Opts& op) {
+    if (op.chain_spin < 0) return -1;
+    return op.chain_spin > 0 ? op.chain_spin : (1ll << 24);
+}
 
 ret_status_t check_common(const void* q, const void* k, const void* v, void* o, int B, int N, int H, int dk, int dv,
                           ret_dtype_t in_dt, ret_dtype_t out_dt, const float* gamma, const double* theta) {
@@ -271,7 +236,7 @@ const char* ret_status_string(int status) {
     }
 }
 
-const char* ret_last_error(void) { return g_last_error.c_str(); }
+const char* ret_last_error(void) { return ret::g_last_error.c_str(); }
 
 ret_status_t ret_parallel_fwd(const void* q, const void* k, const void* v, void* o, int B, int N, int H, int dk,
                               int dv, ret_dtype_t in_dt, ret_dtype_t out_dt, const float* gamma,

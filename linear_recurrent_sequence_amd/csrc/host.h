@@ -1,0 +1,66 @@
+// Host-side helpers shared by the entry points' sources: status and detail text, plan options, launch records.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <mutex>
+#include <vector>
+
+#include "retention.h"
+
+// Launch records: a caller-owned object (ret_options_t.timer); the library keeps none of its own.
+struct ret_timer {
+    struct Rec {
+        const char* name;
+        hipEvent_t start, stop;
+    };
+    std::mutex mu;
+    std::vector<Rec> recs;
+};
+
+namespace ret {
+
+// Sets the calling thread's detail text (ret_last_error) and returns st.
+ret_status_t fail(ret_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+
+// The plan options with the library's defaults filled in (ret_options_t documents each field).
+struct Opts {
+    int segments = 0, target_wgs = 0, prerotate = -1, onchip = 1, variant = 0;
+    int step_cw = 0, step_wr = 0, step_pairs = 0, bwd_direct = 1, step_cache = 0;
+    long long chain_spin = 0;
+    ret_timer_t* timer = nullptr;
+};
+Opts resolve(const ret_options_t* o);
+
+struct LaunchTimer {
+    hipEvent_t start = nullptr, stop = nullptr;
+    hipStream_t stream;
+    const char* name;
+    ret_timer_t* t;
+    LaunchTimer(const char* n, hipStream_t s, const Opts& op) : stream(s), name(n), t(op.timer) {
+        if (t && hipEventCreate(&start) == hipSuccess && hipEventCreate(&stop) == hipSuccess)
+            (void)hipEventRecord(start, stream);
+        else
+            t = nullptr;
+    }
+    void done() {
+        if (!t) return;
+        (void)hipEventRecord(stop, stream);
+        std::lock_guard<std::mutex> lk(t->mu);
+        t->recs.push_back({name, start, stop});
+    }
+};
+
+ret_status_t launch_status(const char* what);
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte (null ranges share none).
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace ret

@@ -176,6 +176,17 @@ def load(build_if_missing: bool = True):
     lib.ret_recurrent_step_normalized.restype = i32
     lib.ret_chunkwise_fwd_noalloc.argtypes = lib.ret_chunkwise_fwd.argtypes[:17] + [vp]
     lib.ret_chunkwise_fwd_noalloc.restype = i32
+    fl = ctypes.c_float
+    lib.ret_msr_epilogue_bwd_workspace_bytes.argtypes = [i64, i32, i32]
+    lib.ret_msr_epilogue_bwd_workspace_bytes.restype = sz
+    lib.ret_msr_epilogue_bwd.argtypes = [vp] * 9 + [i64, i32, i32] + [i32] * 5 + [fl, vp, sz, vp, op]
+    lib.ret_msr_epilogue_bwd.restype = i32
+    lib.ret_layer_norm_fwd.argtypes = [vp] * 8 + [i64, i32, i32, i32, fl, vp, op]
+    lib.ret_layer_norm_fwd.restype = i32
+    lib.ret_layer_norm_bwd_workspace_bytes.argtypes = [i64, i32]
+    lib.ret_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.ret_layer_norm_bwd.argtypes = [vp] * 9 + [i64, i32, i32, i32, i32, vp, sz, vp, op]
+    lib.ret_layer_norm_bwd.restype = i32
     lib.ret_options_default.argtypes = [op]
     lib.ret_options_default.restype = None
     lib.ret_timer_create.restype = vp
@@ -558,3 +569,143 @@ def ret_chunkwise_fwd_noalloc(q, k, v, o, gamma, chunk, theta=None, pos0=0, stat
                                        _dev(state_out, "state_out"), _stream(stream))
     _check("ret_chunkwise_fwd_noalloc", st)
     return o
+
+
+# ---- the entry points below take their stream from the tensors' device ----
+def _launch(t, stream, workspace, make):
+    """(device guard, stream handle, workspace): the stream of the call, torch's current one of t's device by default,
+    and a workspace made on that stream where the caller gave none (torch reuses its memory in that stream's order)."""
+    s = stream if stream is not None else torch.cuda.current_stream(t.device)
+    if workspace is None and make is not None:
+        with torch.cuda.stream(s):
+            workspace = make()
+    return torch.cuda.device(t.device), ctypes.c_void_p(s.cuda_stream), workspace
+
+
+def _need_gpu(t, name):
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError("%s must be a GPU tensor" % name)
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _rows_workspace(nbytes, device):
+    return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
+def msr_epilogue_bwd_workspace(o):
+    """A workspace of ret_msr_epilogue_bwd_workspace_bytes for o [..., H, d_v]."""
+    H, dv = o.shape[-2], o.shape[-1]
+    rows = o.numel() // (H * dv) if H * dv else 0
+    nbytes = load().ret_msr_epilogue_bwd_workspace_bytes(rows, H, dv)
+    if nbytes == 0:
+        raise ValueError("epilogue gradients: unsupported shape")
+    return _rows_workspace(nbytes, o.device)
+
+
+def ret_msr_epilogue_bwd(dy, o, do, gate=None, dgate=None, gn_weight=None, gn_bias=None, dweight=None, dbias=None,
+                         eps=1e-5, workspace=None, stream=None, options=None):
+    """Gradients of ret_msr_epilogue(o, y, gate, gn_weight, gn_bias, eps) for dy: do, and dgate, dweight, dbias where
+    given (float32 [H * d_v] the last two). Without a workspace one is allocated for the call."""
+    lib = load()
+    if not isinstance(o, torch.Tensor) or o.dim() < 2:
+        raise ValueError("o must be a tensor [..., H, d_v]")
+    for name, t in (("dy", dy), ("do", do), ("gate", gate), ("dgate", dgate)):
+        if t is None and name in ("dy", "do"):
+            raise ValueError("%s must be a tensor" % name)
+        _shape(t, name, o.shape, _IO)
+    if o.dtype not in _IO:
+        raise ValueError("o must be float32 or bfloat16, got %s" % o.dtype)
+    if dgate is not None and gate is None:
+        raise ValueError("dgate without a gate")
+    H, dv = o.shape[-2], o.shape[-1]
+    rows = o.numel() // (H * dv) if H * dv else 0
+    for name, t in (("gn_weight", gn_weight), ("gn_bias", gn_bias), ("dweight", dweight), ("dbias", dbias)):
+        _shape(t, name, (H * dv,), (torch.float32,))
+    _same_device(dy, o, do, gate, dgate, gn_weight, gn_bias, dweight, dbias, workspace)
+    _need_gpu(o, "o")
+    make = (lambda: msr_epilogue_bwd_workspace(o)) if dweight is not None or dbias is not None else None
+    guard, sp, workspace = _launch(o, stream, workspace, make)
+    with guard:
+        st = lib.ret_msr_epilogue_bwd(_dev(dy, "dy"), _dev(o, "o"), _dev(gate, "gate"), _dev(gn_weight, "gn_weight"),
+                                      _dev(gn_bias, "gn_bias"), _dev(do, "do"), _dev(dgate, "dgate"),
+                                      _dev(dweight, "dweight"), _dev(dbias, "dbias"), rows, H, dv, _dt(dy), _dt(o),
+                                      _dt(gate) if gate is not None else RET_BF16, _dt(do),
+                                      _dt(dgate) if dgate is not None else RET_BF16, float(eps),
+                                      _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+    _check("ret_msr_epilogue_bwd", st)
+    return do
+
+
+def _norm_rows(x):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in _IO:
+        raise ValueError("x must be a float32 or bfloat16 tensor [..., D]")
+    D = x.shape[-1]
+    return (x.numel() // D if D else 0), D
+
+
+def ret_layer_norm_fwd(x, y, weight=None, bias=None, eps=1e-5, residual=None, sum_out=None, mean=None, rstd=None,
+                       stream=None, options=None):
+    """y = layer norm of s = x (+ residual) over the last axis; sum_out <- s; mean, rstd <- the rows' statistics
+    (float32, the shape of x without its last axis). weight, bias: float32 [D] or None."""
+    lib = load()
+    rows, D = _norm_rows(x)
+    if y is None:
+        raise ValueError("y must be a tensor")
+    _shape(y, "y", x.shape, _IO)
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        _shape(t, name, x.shape, (x.dtype,))
+    for name, t in (("weight", weight), ("bias", bias)):
+        _shape(t, name, (D,), (torch.float32,))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _shape(t, name, x.shape[:-1], (torch.float32,))
+    _same_device(x, y, weight, bias, residual, sum_out, mean, rstd)
+    _need_gpu(x, "x")
+    guard, sp, _ = _launch(x, stream, None, None)
+    with guard:
+        st = lib.ret_layer_norm_fwd(_dev(x, "x"), _dev(residual, "residual"), _dev(weight, "weight"),
+                                    _dev(bias, "bias"), _dev(y, "y"), _dev(sum_out, "sum_out"), _dev(mean, "mean"),
+                                    _dev(rstd, "rstd"), rows, D, _dt(x), _dt(y), float(eps), sp, _options(options))
+    _check("ret_layer_norm_fwd", st)
+    return y
+
+
+def layer_norm_bwd_workspace(x):
+    """A workspace of ret_layer_norm_bwd_workspace_bytes for x [..., D]."""
+    rows, D = _norm_rows(x)
+    nbytes = load().ret_layer_norm_bwd_workspace_bytes(rows, D)
+    if nbytes == 0:
+        raise ValueError("layer norm gradients: unsupported shape")
+    return _rows_workspace(nbytes, x.device)
+
+
+def ret_layer_norm_bwd(dy, x, mean, rstd, dx, weight=None, dsum=None, dweight=None, dbias=None, workspace=None,
+                       stream=None, options=None):
+    """Gradients of ret_layer_norm_fwd: x is what was normalized (sum_out where there was a residual), mean and rstd its
+    statistics; dx gets dsum (the gradient reaching the sum past the norm) added. dweight, dbias: float32 [D] or None.
+    Without a workspace one is allocated for the call."""
+    lib = load()
+    rows, D = _norm_rows(x)
+    for name, t in (("dy", dy), ("dx", dx), ("mean", mean), ("rstd", rstd)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+    _shape(dy, "dy", x.shape, _IO)
+    _shape(dx, "dx", x.shape, _IO)
+    _shape(dsum, "dsum", x.shape, (dx.dtype,))
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _shape(t, name, x.shape[:-1], (torch.float32,))
+    for name, t in (("weight", weight), ("dweight", dweight), ("dbias", dbias)):
+        _shape(t, name, (D,), (torch.float32,))
+    _same_device(dy, x, mean, rstd, dx, weight, dsum, dweight, dbias, workspace)
+    _need_gpu(x, "x")
+    make = (lambda: layer_norm_bwd_workspace(x)) if dweight is not None or dbias is not None else None
+    guard, sp, workspace = _launch(x, stream, workspace, make)
+    with guard:
+        st = lib.ret_layer_norm_bwd(_dev(dy, "dy"), _dev(x, "x"), _dev(weight, "weight"), _dev(mean, "mean"),
+                                    _dev(rstd, "rstd"), _dev(dsum, "dsum"), _dev(dx, "dx"), _dev(dweight, "dweight"),
+                                    _dev(dbias, "dbias"), rows, D, _dt(x), _dt(dy), _dt(dx),
+                                    _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+    _check("ret_layer_norm_bwd", st)
+    return dx
