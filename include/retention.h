@@ -436,6 +436,44 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
                                 int64_t rows, int D, ret_dtype_t x_dt, ret_dtype_t dy_dt, ret_dtype_t dx_dt,
                                 void* workspace, size_t workspace_bytes, void* stream, const ret_options_t* opts);
 
+/*
+ * The gated delta rule: the state decays per token and each token writes the difference between its value and what the
+ * state already holds for its key. Per batch b and value head h, alpha_t = exp(g_t):
+ *     S'_t = alpha_t S_{t-1},  u_t = beta_t (v_t - S'_t^T k_t),  S_t = S'_t + k_t u_t^T,  o_t = scale S_t^T q_t
+ * Layouts: q, k [B, N, Hk, d_k] with H a multiple of Hk (value head h reads key head h / (H / Hk)), v, o
+ * [B, N, H, d_v], g, beta [B, N, H], state [B, H, d_k, d_v] fp32; a step has no N axis. dtypes: q, k, v in in_dt, o in
+ * out_dt, g and beta in gate_dt; F32 input takes F32 output and gates, BF16 input either. g is the natural logarithm of
+ * the decay (g <= 0 as a rule; values below -200, -inf included, clear the state); beta usually lies in [0, 1] and k has
+ * unit length, which keeps the state bounded; neither is checked. scale = 0 means 1 / sqrt(d_k).
+ *
+ * ret_gated_delta_fwd computes a whole sequence in chunks of 64 tokens. state_in (NULL: zeros), state_out (NULL: not
+ * wanted; may equal state_in): the state before token 0 and after the last token, so that a sequence can be resumed or
+ * handed to ret_gated_delta_step. lengths (device int32[B], or NULL): sequence b has lengths[b] tokens (0 .. N, other
+ * values are taken as the nearest of these); inputs past them are not used, outputs past them are zero, and state_out is
+ * the state after lengths[b] tokens. Products accumulate in fp32; on BF16 input everything the kernels compute and
+ * multiply again (the state among it) is split in two bf16 parts, so results carry about 2^-17. A NaN or infinity of a
+ * token can reach the outputs of its own chunk's earlier tokens.
+ * workspace: ret_gated_delta_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing
+ * one must not overlap in time. Supported: d_k in {32, 64, 128, 256} (BF16) or {16, 32, 64, 128} (F32), d_v a multiple
+ * of 16, B*H <= 65535, N >= 1, H * max(d_k, d_v) < 2^22. Written buffers must not overlap other buffers. Pointers 16-byte
+ * aligned. opts: segments (> 0: segments per sequence that run in parallel, joined by their transitions) and timer.
+ * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_full".
+ *
+ * ret_gated_delta_step computes one token of every sequence, the state updated in place; d_k in {16, 32, 64, 128, 256},
+ * d_v a multiple of 16, fp32 arithmetic for either input dtype. Kernel: "ret_delta_step".
+ */
+size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                       const ret_options_t* opts);
+ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
+                                 int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt, ret_dtype_t out_dt,
+                                 ret_dtype_t gate_dt, float scale, const int32_t* lengths, const float* state_in,
+                                 float* state_out, void* workspace, size_t workspace_bytes, void* stream,
+                                 const ret_options_t* opts);
+ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
+                                  float* state, int B, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                  ret_dtype_t out_dt, ret_dtype_t gate_dt, float scale, void* stream,
+                                  const ret_options_t* opts);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,218 @@
+// The gated delta rule (gfx950). Per batch b and value head h, with state S (d_k x d_v), decay alpha_t = exp(g_t) and
+// write strength beta_t,
+//     S'_t = alpha_t S_{t-1},  u_t = beta_t (v_t - S'_t^T k_t),  S_t = S'_t + k_t u_t^T,  o_t = scale S_t^T q_t.
+// Over a chunk of C = 64 tokens with G_i = g_1 + .. + g_i, entering state S_0 and
+//     A_ij = beta_i exp(G_i - G_j) k_i.k_j (j < i),   T = (I + A)^-1,   P_ij = scale exp(G_i - G_j) q_i.k_j (j <= i)
+// the tokens' writes U solve (I + A) U = R, so that everything is products of matrices:
+//     Y = K S_0,  R = beta (V - exp(G) Y),  U = T R,
+//     O = scale exp(G) Q S_0 + P U,         S_C = exp(G_C) S_0 + (exp(G_C - G) K)^T U.
+// T and P do not depend on the state: one kernel makes them for every chunk at once (delta_prep). The rest is a chain
+// over chunks with the state in MFMA accumulators. Columns of S are independent of each other, so each wave owns some of
+// them and no product of the chain leaves its wave: an accumulator tile (column in the lane, rows 4g .. 4g+3 of lane
+// group g) is the other operand of the next product once the reduction index is taken in that order.
+//
+// Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, U, T, P) is split in
+// two bf16 parts, x = hi + lo + e with |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two products where the
+// other side is an input, which is exact): the carried state keeps fp32-like accuracy over any number of chunks, where a
+// single rounding of U and S would leave 2^-9 in it. F32 inputs run on the fp32 MFMA.
+#pragma once
+
+#include "chunk_bf16.h"
+
+namespace ret {
+
+constexpr int kDeltaC = 64;  // tokens per chunk
+
+// Per (chunk, b, h): fragments of T and P, then per-token factors.
+constexpr int kDeltaMatBytes = 16384;  // one 64 x 64 matrix as operand fragments (two bf16 parts, or fp32)
+
+struct DeltaArgs {
+    const void *q, *k, *v;       // [B, N, Hk, dk], [B, N, H, dv]
+    const void *g, *beta;        // [B, N, H]
+    const int* lengths;          // [B] or null (N)
+    const float* state_in;       // [B, H, dk, dv] or null (zeros)
+    float* state_out;            // [B, H, dk, dv] or null
+    void* o;                     // [B, N, H, dv]
+    // workspace
+    char* mats;                  // [B*H][nchunks][nmats][kDeltaMatBytes]: T, P (gradients: also their transposes)
+    float* fac;                  // [B*H][nchunks][3][64]: exp(G_i), exp(G_C - G_i), beta_i
+    float* segE;                 // [B*H][nseg][dk][dv]: end states from zero, then the states entering the segments
+    float* segM;                 // [B*H][nseg][dk][dk]: transitions
+    // gradients
+    const void* dout;            // [B, N, H, dv]
+    const float* dstate_out;     // [B, H, dk, dv] or null (zeros)
+    float* dstate_in;            // or null
+    void *dq, *dk_, *dv_, *dg, *dbeta;
+    int B, N, H, Hk, dk, dv;
+    int nchunks, nmats;
+    int nseg, seg_chunks;        // segments per sequence and chunks per segment
+    int local_segs;              // segments that the local pass runs over (nseg - 1: all but the last)
+    int out_bf16, gate_bf16;
+    float scale;
+};
+typedef void (*delta_kernel_t)(DeltaArgs);
+
+// Live tokens of sequence b.
+__device__ __forceinline__ int delta_len(const DeltaArgs& a, int b) {
+    if (!a.lengths) return a.N;
+    const int n = a.lengths[b];
+    return n < 0 ? 0 : n > a.N ? a.N : n;
+}
+__device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
+    return bf16 ? bf16_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Operands. KS: reduction length of one step; TPS: accumulator tiles (16 rows) that make one step. In a step lane group g
+// holds indices 4g..4g+3 of each tile. Fa: rows of an input matrix in LDS (exact). Fb: an operand made from accumulators.
+// Fm: a 64 x 64 matrix fragment from the workspace. mma_ab(acc, a, b) adds a.b with accumulator rows along a's rows;
+// mma_ba swaps the sides (accumulator rows along b's columns), so a lane holds 4 consecutive columns of one token.
+// ---------------------------------------------------------------------------------------------------
+template <class E>
+struct DOps;
+
+template <>
+struct DOps<BF16> {
+    typedef uint16_t st;
+    static constexpr int KS = 32, TPS = 2;
+    typedef bf16x8_t Fa;
+    struct Fb {
+        bf16x8_t hi, lo;
+    };
+    typedef Fb Fm;
+    __device__ static __forceinline__ Fb split(f32x4_t a, f32x4_t b) {
+        Fb f;
+        f.hi = acc_pair(a, b);
+        const u32x4_t u = __builtin_bit_cast(u32x4_t, f.hi);
+        const f32x4_t ha = {__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u),
+                            __uint_as_float(u[1] << 16), __uint_as_float(u[1] & 0xffff0000u)};
+        const f32x4_t hb = {__uint_as_float(u[2] << 16), __uint_as_float(u[2] & 0xffff0000u),
+                            __uint_as_float(u[3] << 16), __uint_as_float(u[3] & 0xffff0000u)};
+        f.lo = acc_pair(a - ha, b - hb);
+        return f;
+    }
+    // step s of a column of accumulator tiles
+    template <int NT>
+    __device__ static __forceinline__ Fb step(const f32x4_t (&x)[NT], int s) {
+        return split(x[2 * s], x[2 * s + 1]);
+    }
+    __device__ static __forceinline__ void mfma1(f32x4_t& acc, bf16x8_t a, bf16x8_t b) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+    }
+    __device__ static __forceinline__ void mma_ab(f32x4_t& acc, Fa a, const Fb& b) {
+        mfma1(acc, a, b.lo);
+        mfma1(acc, a, b.hi);
+    }
+    __device__ static __forceinline__ void mma_ba(f32x4_t& acc, Fa a, const Fb& b) {
+        mfma1(acc, b.lo, a);
+        mfma1(acc, b.hi, a);
+    }
+    __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) {
+        mfma1(acc, a.hi, b.lo);
+        mfma1(acc, a.lo, b.hi);
+        mfma1(acc, a.hi, b.hi);
+    }
+    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) {
+        mfma1(acc, b.lo, a.hi);
+        mfma1(acc, b.hi, a.lo);
+        mfma1(acc, b.hi, a.hi);
+    }
+    // fragment f (= row tile * steps + step) of a workspace matrix
+    __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
+        const u32x4_t* p = reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane;
+        return {__builtin_bit_cast(bf16x8_t, p[0]), __builtin_bit_cast(bf16x8_t, p[64])};
+    }
+    // writes the fragment of x: a: the step's first 4 values of this lane, b: its last 4
+    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b) {
+        const Fb x = split(a, b);
+        u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * 128 + lane;
+        p[0] = __builtin_bit_cast(u32x4_t, x.hi);
+        p[64] = __builtin_bit_cast(u32x4_t, x.lo);
+    }
+    // LDS tile [rows][W], read by rows and transposed
+    template <int W>
+    struct Tile {
+        static constexpr int LD = Swz<W>::LD;
+        __device__ static __forceinline__ int off(int r, int c) { return Swz<W>::off(r, c); }
+        __device__ static __forceinline__ Fa rows(const st* X, int r0, int k0, int lane) {
+            return frag_ps<W>(X, r0, k0, Swz<W>::lane_p(lane));
+        }
+        __device__ static __forceinline__ Fa cols(const st* X, int k0, int n0, int lane) {
+            return frag_trps<W>(X, k0, n0, Swz<W>::lane_trp(lane));
+        }
+    };
+};
+
+template <>
+struct DOps<F32> {
+    typedef float st;
+    static constexpr int KS = 16, TPS = 1;
+    typedef f32x4_t Fa;
+    typedef f32x4_t Fb;
+    typedef f32x4_t Fm;
+    template <int NT>
+    __device__ static __forceinline__ Fb step(const f32x4_t (&x)[NT], int s) {
+        return x[s];
+    }
+    __device__ static __forceinline__ void mma_ab(f32x4_t& acc, const Fa& a, const Fb& b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
+    }
+    __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
+    __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }
+    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, b, a); }
+    __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
+        return reinterpret_cast<const f32x4_t*>(m)[f * 64 + lane];
+    }
+    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a) {
+        reinterpret_cast<f32x4_t*>(m)[f * 64 + lane] = a;
+    }
+    template <int W>
+    struct Tile {
+        static constexpr int LD = W + 4;
+        __device__ static __forceinline__ int off(int r, int c) { return r * LD + c; }
+        __device__ static __forceinline__ Fa rows(const st* X, int r0, int k0, int lane) {
+            return *reinterpret_cast<const f32x4_t*>(X + (r0 + (lane & 15)) * LD + k0 + 4 * (lane >> 4));
+        }
+        __device__ static __forceinline__ Fa cols(const st* X, int k0, int n0, int lane) {
+            const st* p = X + (k0 + 4 * (lane >> 4)) * LD + n0 + (lane & 15);
+            return f32x4_t{p[0], p[LD], p[2 * LD], p[3 * LD]};
+        }
+    };
+};
+
+// 64 rows of W elements of one head moved as 16-byte segments by 256 threads: rows past the live ones read as zeros
+// (the buffer resource ends with the last live row).
+template <class E, int W>
+struct DRows {
+    typedef typename E::st st;
+    static constexpr int EPS = 16 / sizeof(st), SPR = W / EPS, RP = kThreads / SPR, NP = (kDeltaC + RP - 1) / RP;
+    typedef typename DOps<E>::template Tile<W> Tile;
+    u32x4_t x[NP];
+    // p: the head's row of the chunk's first token; stride: elements between tokens; live: rows to read (may be <= 0)
+    __device__ __forceinline__ void load(const st* p, int stride, int live, int tid) {
+        const int bytes = live > 0 ? ((live - 1) * stride + W) * (int)sizeof(st) : 0;
+        const rsrc_t r = bytes_rsrc(p, bytes);
+        const int row = tid / SPR, c = tid % SPR * EPS;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            x[i] = buf_load16(r, (row * stride + c) * (int)sizeof(st), i * RP * stride * (int)sizeof(st));
+    }
+    __device__ __forceinline__ void store(st* lds, int tid) const {
+        const int row = tid / SPR, c = tid % SPR * EPS;
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (NP * RP == kDeltaC || row + i * RP < kDeltaC)
+                *reinterpret_cast<u32x4_t*>(lds + Tile::off(row + i * RP, c)) = x[i];
+    }
+};
+
+// ---- kernel selection ----
+struct DeltaKernels {
+    delta_kernel_t prep, local, full, scan;
+    int cols;  // columns of d_v (or of a transition) per workgroup
+};
+// d_k in {32, 64, 128, 256} for bf16 and {16, 32, 64, 128} for fp32; false otherwise.
+bool delta_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);
+
+}  // namespace ret

@@ -1,0 +1,218 @@
+// Entry points of the gated delta rule: argument checks, segment plan, workspace layout, launches.
+#include "delta.h"
+#include "delta_step.h"
+#include "host.h"
+
+#include <math.h>
+#include <string.h>
+
+namespace ret {
+
+namespace {
+
+size_t esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Shape {
+    int B, N, H, Hk, dk, dv;
+};
+
+// Sizes, dtypes and head counts of any of the calls; N = 1 for a step.
+ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, ret_dtype_t gate_dt) {
+    if (s.B <= 0 || s.N <= 0 || s.H <= 0 || s.Hk <= 0 || s.dk <= 0 || s.dv <= 0)
+        return fail(RET_ERR_INVALID_ARG, "sizes must be positive (B=%d N=%d H=%d Hk=%d dk=%d dv=%d)", s.B, s.N, s.H,
+                    s.Hk, s.dk, s.dv);
+    for (ret_dtype_t t : {in_dt, out_dt, gate_dt})
+        if (t != RET_F32 && t != RET_BF16) return fail(RET_ERR_INVALID_ARG, "bad dtype %d", (int)t);
+    if (in_dt == RET_F32 && (out_dt != RET_F32 || gate_dt != RET_F32))
+        return fail(RET_ERR_INVALID_ARG, "F32 input requires F32 output and gates");
+    if (s.H % s.Hk) return fail(RET_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", s.H, s.Hk);
+    if ((long long)s.B * s.H > 65535) return fail(RET_ERR_UNSUPPORTED, "B*H=%lld exceeds 65535", (long long)s.B * s.H);
+    // a chunk of one head is addressed with 32-bit byte offsets
+    const long long w = (long long)s.H * (s.dk > s.dv ? s.dk : s.dv);
+    if (w * kDeltaC * 4 >= 1LL << 30)
+        return fail(RET_ERR_UNSUPPORTED, "H*max(d_k,d_v)=%lld too large", w);
+    return RET_OK;
+}
+
+float scale_of(float scale, int dk) { return scale == 0.f ? (float)(1.0 / sqrt((double)dk)) : scale; }
+
+struct Buf {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+
+// Every written buffer apart from every other buffer of the call, except the pairs that may be the same one.
+template <int NW, int NR>
+ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR], const void* may_a, const void* may_b) {
+    for (int i = 0; i < NW; ++i) {
+        for (int j = i + 1; j < NW; ++j)
+            if (overlaps(w[i].p, w[i].bytes, w[j].p, w[j].bytes))
+                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, w[j].name);
+        for (int j = 0; j < NR; ++j)
+            if (overlaps(w[i].p, w[i].bytes, r[j].p, r[j].bytes) &&
+                !(w[i].p == r[j].p && w[i].bytes == r[j].bytes && w[i].p == may_a && r[j].p == may_b))
+                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, r[j].name);
+    }
+    for (int i = 0; i < NW; ++i)
+        if (!aligned16(w[i].p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", w[i].name);
+    for (int j = 0; j < NR; ++j)
+        if (!aligned16(r[j].p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", r[j].name);
+    return RET_OK;
+}
+
+// Segments per sequence.
+struct Plan {
+    int nchunks, nseg, seg_chunks;
+    size_t mats, fac, segE, segM, bytes;  // byte offsets of the parts, and their end
+};
+Plan make_plan(const Shape& s, const DeltaKernels& k, int nmats, const Opts& op) {
+    Plan p;
+    p.nchunks = (s.N + kDeltaC - 1) / kDeltaC;
+    const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
+    int n = 1;
+    if (op.segments > 0) n = op.segments;
+    else if (units <= 96) n = (int)(256 / units);
+    if (op.segments <= 0 && n > p.nchunks / 4) n = p.nchunks / 4;  // at least 4 chunks a segment
+    if (n > p.nchunks) n = p.nchunks;
+    if (n < 1) n = 1;
+    p.seg_chunks = (p.nchunks + n - 1) / n;
+    p.nseg = (p.nchunks + p.seg_chunks - 1) / p.seg_chunks;
+    const size_t bh = (size_t)s.B * s.H;
+    p.mats = 0;
+    p.fac = p.mats + bh * p.nchunks * nmats * kDeltaMatBytes;
+    p.segE = p.fac + round256(bh * p.nchunks * 3 * kDeltaC * sizeof(float));
+    p.segM = p.segE + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dv * sizeof(float)) : 0);
+    p.bytes = p.segM + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dk * sizeof(float)) : 0);
+    return p;
+}
+
+void fill(DeltaArgs& A, const Shape& s, const Plan& p, int nmats, void* workspace, ret_dtype_t out_dt,
+          ret_dtype_t gate_dt, float scale) {
+    memset(&A, 0, sizeof(A));
+    A.B = s.B;
+    A.N = s.N;
+    A.H = s.H;
+    A.Hk = s.Hk;
+    A.dk = s.dk;
+    A.dv = s.dv;
+    A.nchunks = p.nchunks;
+    A.nmats = nmats;
+    A.nseg = p.nseg;
+    A.seg_chunks = p.seg_chunks;
+    A.mats = (char*)workspace + p.mats;
+    A.fac = (float*)((char*)workspace + p.fac);
+    A.segE = (float*)((char*)workspace + p.segE);
+    A.segM = (float*)((char*)workspace + p.segM);
+    A.out_bf16 = out_dt == RET_BF16;
+    A.gate_bf16 = gate_dt == RET_BF16;
+    A.scale = scale_of(scale, s.dk);
+}
+
+ret_status_t launch(const char* name, delta_kernel_t fn, dim3 grid, hipStream_t s, const Opts& op, const DeltaArgs& A) {
+    LaunchTimer tm(name, s, op);
+    hipLaunchKernelGGL(fn, grid, dim3(kThreads), 0, s, A);
+    tm.done();
+    return launch_status(name);
+}
+
+unsigned blocks(int n, int per) { return (unsigned)((n + per - 1) / per); }
+
+}  // namespace
+
+}  // namespace ret
+
+using namespace ret;
+
+extern "C" {
+
+size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                       const ret_options_t* opts) {
+    const Shape s = {B, N, H, Hk, dk, dv};
+    DeltaKernels k;
+    if (check_shape(s, in_dt, RET_F32, RET_F32) != RET_OK || !delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
+    return make_plan(s, k, 2, resolve(opts)).bytes;
+}
+
+ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
+                                 int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt, ret_dtype_t out_dt,
+                                 ret_dtype_t gate_dt, float scale, const int32_t* lengths, const float* state_in,
+                                 float* state_out, void* workspace, size_t workspace_bytes, void* stream,
+                                 const ret_options_t* opts) {
+    const Shape s = {B, N, H, Hk, dk, dv};
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    if (st != RET_OK) return st;
+    if (!q || !k || !v || !g || !beta || !o) return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/o pointer");
+    if (!isfinite(scale)) return fail(RET_ERR_INVALID_ARG, "scale is not finite");
+    DeltaKernels kn;
+    if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &kn))
+        return fail(RET_ERR_UNSUPPORTED, "gated delta rule: unsupported d_k=%d d_v=%d for %s input", dk, dv,
+                    in_dt == RET_F32 ? "F32" : "BF16");
+    const Opts op = resolve(opts);
+    const Plan p = make_plan(s, kn, 2, op);
+    const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
+    const Buf w[] = {{"o", o, T * H * dv * esize(out_dt)}, {"state_out", state_out, sb},
+                     {"the workspace", workspace, workspace_bytes}};
+    const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
+                     {"g", g, T * H * esize(gate_dt)}, {"beta", beta, T * H * esize(gate_dt)},
+                     {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}};
+    // state_out may be state_in: every kernel that reads the latter has read it before the former is written, except
+    // within a segment chain's first launches, which precede it
+    if ((st = check_apart(w, r, state_out, state_in)) != RET_OK) return st;
+    if (!workspace || workspace_bytes < p.bytes)
+        return fail(RET_ERR_WORKSPACE, "gated delta rule: workspace of %zu bytes, %zu needed",
+                    workspace ? workspace_bytes : 0, p.bytes);
+    DeltaArgs A;
+    fill(A, s, p, 2, workspace, out_dt, gate_dt, scale);
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.g = g;
+    A.beta = beta;
+    A.o = o;
+    A.lengths = lengths;
+    A.state_in = state_in;
+    A.state_out = state_out;
+    A.local_segs = p.nseg - 1;
+    hipStream_t str = (hipStream_t)stream;
+    if ((st = launch("ret_delta_prep", kn.prep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
+    const unsigned nc = blocks(dv, kn.cols);
+    if (p.nseg > 1) {
+        if ((st = launch("ret_delta_local", kn.local, dim3(B * H * (p.nseg - 1), nc + blocks(dk, kn.cols)), str, op, A)) !=
+            RET_OK)
+            return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+    }
+    return launch("ret_delta_full", kn.full, dim3(B * H * p.nseg, nc), str, op, A);
+}
+
+ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
+                                  float* state, int B, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                  ret_dtype_t out_dt, ret_dtype_t gate_dt, float scale, void* stream,
+                                  const ret_options_t* opts) {
+    const Shape s = {B, 1, H, Hk, dk, dv};
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    if (st != RET_OK) return st;
+    if (!q || !k || !v || !g || !beta || !o || !state)
+        return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/o/state pointer");
+    if (!isfinite(scale)) return fail(RET_ERR_INVALID_ARG, "scale is not finite");
+    const delta_step_kernel_t fn = delta_step_kernel_get(in_dt == RET_BF16, dk);
+    if (!fn || dv % 16)
+        return fail(RET_ERR_UNSUPPORTED, "gated delta step: d_k=%d not in {16,32,64,128,256} or d_v=%d not a multiple of 16",
+                    dk, dv);
+    const size_t ei = esize(in_dt), ng = (size_t)B * H * esize(gate_dt);
+    const Buf w[] = {{"o", o, (size_t)B * H * dv * esize(out_dt)}, {"state", state, (size_t)B * H * dk * dv * 4}};
+    const Buf r[] = {{"q", q, (size_t)B * Hk * dk * ei}, {"k", k, (size_t)B * Hk * dk * ei},
+                     {"v", v, (size_t)B * H * dv * ei}, {"g", g, ng}, {"beta", beta, ng}};
+    if ((st = check_apart(w, r, nullptr, nullptr)) != RET_OK) return st;
+    DeltaStepArgs A = {q, k, v, g, beta, state, o, B, H, Hk, dv, out_dt == RET_BF16, gate_dt == RET_BF16,
+                       scale_of(scale, dk)};
+    hipStream_t str = (hipStream_t)stream;
+    LaunchTimer tm("ret_delta_step", str, resolve(opts));
+    hipLaunchKernelGGL(fn, dim3(B * H, blocks(dv, 64)), dim3(dk >= 32 ? 2 * dk : 64), 0, str, A);
+    tm.done();
+    return launch_status("ret_delta_step");
+}
+
+}  // extern "C"

@@ -187,6 +187,12 @@ def load(build_if_missing: bool = True):
     lib.ret_layer_norm_bwd_workspace_bytes.restype = sz
     lib.ret_layer_norm_bwd.argtypes = [vp] * 9 + [i64, i32, i32, i32, i32, vp, sz, vp, op]
     lib.ret_layer_norm_bwd.restype = i32
+    lib.ret_gated_delta_workspace_bytes.argtypes = [i32] * 7 + [op]
+    lib.ret_gated_delta_workspace_bytes.restype = sz
+    lib.ret_gated_delta_fwd.argtypes = [vp] * 6 + [i32] * 9 + [fl, vp, vp, vp, vp, sz, vp, op]
+    lib.ret_gated_delta_fwd.restype = i32
+    lib.ret_gated_delta_step.argtypes = [vp] * 7 + [i32] * 8 + [fl, vp, op]
+    lib.ret_gated_delta_step.restype = i32
     lib.ret_options_default.argtypes = [op]
     lib.ret_options_default.restype = None
     lib.ret_timer_create.restype = vp
@@ -709,3 +715,96 @@ def ret_layer_norm_bwd(dy, x, mean, rstd, dx, weight=None, dsum=None, dweight=No
                                     _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
     _check("ret_layer_norm_bwd", st)
     return dx
+
+
+def _delta_qkv(q, k, v, g, beta, step=False):
+    """Shapes and dtypes of q, k [B, N, Hk, dk], v [B, N, H, dv], g, beta [B, N, H] (a step: no N axis)."""
+    nd = 3 if step else 4
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != nd:
+            raise ValueError("%s must be a %d-d tensor" % (name, nd))
+    _shape(k, "k", q.shape, (q.dtype,))
+    if tuple(v.shape[:-2]) != tuple(q.shape[:-2]) or v.dtype != q.dtype or q.dtype not in _IO:
+        raise ValueError("q, k, v must share their leading axes and one dtype (float32 or bfloat16)")
+    if q.shape[-2] == 0 or v.shape[-2] % q.shape[-2]:
+        raise ValueError("the heads of v (%d) must be a multiple of those of q and k (%d)" % (v.shape[-2], q.shape[-2]))
+    for name, t in (("g", g), ("beta", beta)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+        _shape(t, name, v.shape[:-1], _IO)
+    if g.dtype != beta.dtype:
+        raise ValueError("g and beta must share one dtype")
+
+
+def _delta_scale(scale):
+    if scale is None:
+        return 0.0
+    if float(scale) == 0.0:
+        raise ValueError("scale must not be zero")
+    return float(scale)
+
+
+def _delta_lengths(lengths, B):
+    if lengths is not None and (not isinstance(lengths, torch.Tensor) or lengths.dtype != torch.int32
+                                or tuple(lengths.shape) != (B,)):
+        raise ValueError("lengths must be an int32 tensor [B]")
+
+
+def gated_delta_workspace(q, v, options=None):
+    """A workspace of ret_gated_delta_workspace_bytes for these shapes."""
+    B, N, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    nbytes = load().ret_gated_delta_workspace_bytes(B, N, H, Hk, dk, dv, _dt(q), _options(options))
+    if nbytes == 0:
+        raise ValueError("gated delta rule: unsupported shape")
+    return torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+
+
+def ret_gated_delta_fwd(q, k, v, g, beta, o, scale=None, lengths=None, state_in=None, state_out=None, workspace=None,
+                        stream=None, options=None):
+    """o <- the gated delta rule over q, k [B,N,Hk,dk], v [B,N,H,dv] with log decays g and write strengths beta
+    [B,N,H], from state_in [B,H,dk,dv] (None: zeros); the final state to state_out. scale None: 1/sqrt(dk). lengths:
+    int32 [B] tokens of each sequence on the device, or None. Without a workspace one is allocated for the call."""
+    lib = load()
+    _delta_qkv(q, k, v, g, beta)
+    B, N, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    if o is None:
+        raise ValueError("o must be a tensor")
+    _shape(o, "o", v.shape, _IO)
+    for name, s in (("state_in", state_in), ("state_out", state_out)):
+        _shape(s, name, (B, H, dk, dv), (torch.float32,))
+    _delta_lengths(lengths, B)
+    _same_device(q, k, v, g, beta, o, lengths, state_in, state_out, workspace)
+    _need_gpu(q, "q")
+    guard, sp, workspace = _launch(q, stream, workspace, lambda: gated_delta_workspace(q, v, options))
+    with guard:
+        st = lib.ret_gated_delta_fwd(_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g"), _dev(beta, "beta"),
+                                     _dev(o, "o"), B, N, H, Hk, dk, dv, _dt(q), _dt(o), _dt(g), _delta_scale(scale),
+                                     _dev(lengths, "lengths"), _dev(state_in, "state_in"),
+                                     _dev(state_out, "state_out"), _dev(workspace, "workspace"), _nbytes(workspace),
+                                     sp, _options(options))
+    _check("ret_gated_delta_fwd", st)
+    return o
+
+
+def ret_gated_delta_step(q, k, v, g, beta, o, state, scale=None, stream=None, options=None):
+    """One token of the gated delta rule: q, k [B,Hk,dk], v, o [B,H,dv], g, beta [B,H]; state [B,H,dk,dv] (float32) is
+    updated in place."""
+    lib = load()
+    _delta_qkv(q, k, v, g, beta, step=True)
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    if o is None or state is None:
+        raise ValueError("o and state must be tensors")
+    _shape(o, "o", v.shape, _IO)
+    _shape(state, "state", (B, H, dk, dv), (torch.float32,))
+    _same_device(q, k, v, g, beta, o, state)
+    _need_gpu(q, "q")
+    guard, sp, _ = _launch(q, stream, None, None)
+    with guard:
+        st = lib.ret_gated_delta_step(_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g"), _dev(beta, "beta"),
+                                      _dev(o, "o"), _dev(state, "state"), B, H, Hk, dk, dv, _dt(q), _dt(o), _dt(g),
+                                      _delta_scale(scale), sp, _options(options))
+    _check("ret_gated_delta_step", st)
+    return o
