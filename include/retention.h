@@ -474,6 +474,26 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
                                   ret_dtype_t out_dt, ret_dtype_t gate_dt, float scale, void* stream,
                                   const ret_options_t* opts);
 
+/*
+ * Gradients of ret_gated_delta_fwd: with dout = dL/do [B, N, H, d_v] in in_dt and, optionally, dstate_out = dL/dstate_out
+ * [B, H, d_k, d_v] fp32, writes dq, dk [B, N, Hk, d_k] (summed over the value heads that share a key head), dv
+ * [B, N, H, d_v] in out_dt, dg, dbeta [B, N, H] in gate_dt and, unless NULL, dstate_in. The other arguments are the
+ * forward call's. Gradients of the padding past lengths[b] are zero. dq, dk, dbeta and dg come from states and writes
+ * stored as BF16 on BF16 input, whatever out_dt and gate_dt (a relative 2^-8); dv and dstate_in carry 2^-17 like the
+ * forward. workspace: ret_gated_delta_bwd_workspace_bytes (it holds the state entering and the state gradient leaving
+ * every chunk of 64 tokens). Same limits as the forward. Sums have one order: the same call gives the same bits.
+ * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_states", "ret_delta_local_bwd",
+ * "ret_delta_full_bwd", "ret_delta_grad".
+ */
+size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                           const ret_options_t* opts);
+ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                 const void* dout, void* dq, void* dk_out, void* dv_out, void* dg, void* dbeta, int B,
+                                 int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt, ret_dtype_t out_dt,
+                                 ret_dtype_t gate_dt, float scale, const int32_t* lengths, const float* state_in,
+                                 const float* dstate_out, float* dstate_in, void* workspace, size_t workspace_bytes,
+                                 void* stream, const ret_options_t* opts);
+
 #ifdef __cplusplus
 }
 #endif

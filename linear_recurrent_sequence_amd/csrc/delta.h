@@ -1,20 +1,20 @@
 // The gated delta rule (gfx950). Per batch b and value head h, with state S (d_k x d_v), decay alpha_t = exp(g_t) and
 // write strength beta_t,
 //     S'_t = alpha_t S_{t-1},  u_t = beta_t (v_t - S'_t^T k_t),  S_t = S'_t + k_t u_t^T,  o_t = scale S_t^T q_t.
-// Over a chunk of C = 64 tokens with G_i = g_1 + .. + g_i, entering state S_0 and
-//     A_ij = beta_i exp(G_i - G_j) k_i.k_j (j < i),   T = (I + A)^-1,   P_ij = scale exp(G_i - G_j) q_i.k_j (j <= i)
-// the tokens' writes U solve (I + A) U = R, so that everything is products of matrices:
-//     Y = K S_0,  R = beta (V - exp(G) Y),  U = T R,
-//     O = scale exp(G) Q S_0 + P U,         S_C = exp(G_C) S_0 + (exp(G_C - G) K)^T U.
+// Over a chunk of C = 64 tokens with G_i = g_1 + .. + g_i and entering state S_0, write u_i = beta_i e_i. With
+//     A_ij = exp(G_i - G_j) (k_i.k_j) beta_j (j < i),   T = (I + A)^-1,   P_ij = scale exp(G_i - G_j) (q_i.k_j) beta_j (j <= i)
+// the e solve (I + A) E = R, so that everything is products of matrices:
+//     Y = K S_0,  R = V - exp(G) Y,  E = T R,
+//     O = scale exp(G) Q S_0 + P E,         S_C = exp(G_C) S_0 + (exp(G_C - G) beta K)^T E.
 // T and P do not depend on the state: one kernel makes them for every chunk at once (delta_prep). The rest is a chain
 // over chunks with the state in MFMA accumulators. Columns of S are independent of each other, so each wave owns some of
 // them and no product of the chain leaves its wave: an accumulator tile (column in the lane, rows 4g .. 4g+3 of lane
 // group g) is the other operand of the next product once the reduction index is taken in that order.
 //
-// Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, U, T, P) is split in
+// Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, E, T, P) is split in
 // two bf16 parts, x = hi + lo + e with |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two products where the
 // other side is an input, which is exact): the carried state keeps fp32-like accuracy over any number of chunks, where a
-// single rounding of U and S would leave 2^-9 in it. F32 inputs run on the fp32 MFMA.
+// single rounding of E and S would leave 2^-9 in it. F32 inputs run on the fp32 MFMA.
 #pragma once
 
 #include "chunk_bf16.h"
@@ -24,6 +24,8 @@ namespace ret {
 constexpr int kDeltaC = 64;  // tokens per chunk
 
 // Per (chunk, b, h): fragments of T and P, then per-token factors.
+// Factors of a chunk (rows of 64): exp(G_i), exp(G_C - G_i) beta_i, exp(G_C - G_i), beta_i, then G_i log2(e) in fp64.
+constexpr int kDeltaFac = 6 * kDeltaC;
 constexpr int kDeltaMatBytes = 16384;  // one 64 x 64 matrix as operand fragments (two bf16 parts, or fp32)
 
 struct DeltaArgs {
@@ -34,11 +36,14 @@ struct DeltaArgs {
     float* state_out;            // [B, H, dk, dv] or null
     void* o;                     // [B, N, H, dv]
     // workspace
-    char* mats;                  // [B*H][nchunks][nmats][kDeltaMatBytes]: T, P (gradients: also their transposes)
-    float* fac;                  // [B*H][nchunks][3][64]: exp(G_i), exp(G_C - G_i), beta_i
+    char* mats;                  // [B*H][nchunks][nmats][kDeltaMatBytes]: T, P (gradients: T, Tr^T, Pr^T)
+    float* fac;                  // [B*H][nchunks][kDeltaFac] per-token factors
     float* segE;                 // [B*H][nseg][dk][dv]: end states from zero, then the states entering the segments
     float* segM;                 // [B*H][nseg][dk][dk]: transitions
     // gradients
+    float* segF;                 // [B*H][nseg][dk][dv]: state gradients of the segments, from their right ends
+    void *s0t, *ds1t;            // [B*H][nchunks][dv][dk] in the input type: states entering, gradients leaving the chunks
+    void *et, *dut;              // [B*H][nchunks][dv][64]: E and dU
     const void* dout;            // [B, N, H, dv]
     const float* dstate_out;     // [B, H, dk, dv] or null (zeros)
     float* dstate_in;            // or null
@@ -46,7 +51,6 @@ struct DeltaArgs {
     int B, N, H, Hk, dk, dv;
     int nchunks, nmats;
     int nseg, seg_chunks;        // segments per sequence and chunks per segment
-    int local_segs;              // segments that the local pass runs over (nseg - 1: all but the last)
     int out_bf16, gate_bf16;
     float scale;
 };
@@ -117,6 +121,18 @@ struct DOps<BF16> {
         mfma1(acc, b.hi, a.lo);
         mfma1(acc, b.hi, a.hi);
     }
+    // both sides exact
+    __device__ static __forceinline__ void mma_aa(f32x4_t& acc, Fa a, Fa b) { mfma1(acc, a, b); }
+    // a workspace matrix times an exact operand made from accumulator-ordered values
+    typedef bf16x8_t Fx;
+    template <int NT>
+    __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
+        return acc_pair(x[2 * s], x[2 * s + 1]);
+    }
+    __device__ static __forceinline__ void mma_mx(f32x4_t& acc, const Fm& a, Fx b) {
+        mfma1(acc, a.lo, b);
+        mfma1(acc, a.hi, b);
+    }
     // fragment f (= row tile * steps + step) of a workspace matrix
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         const u32x4_t* p = reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane;
@@ -161,6 +177,13 @@ struct DOps<F32> {
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, b, a); }
+    __device__ static __forceinline__ void mma_aa(f32x4_t& acc, const Fa& a, const Fa& b) { mma_ab(acc, a, b); }
+    typedef f32x4_t Fx;
+    template <int NT>
+    __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
+        return x[s];
+    }
+    __device__ static __forceinline__ void mma_mx(f32x4_t& acc, const Fm& a, const Fx& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         return reinterpret_cast<const f32x4_t*>(m)[f * 64 + lane];
     }
@@ -210,9 +233,13 @@ struct DRows {
 // ---- kernel selection ----
 struct DeltaKernels {
     delta_kernel_t prep, local, full, scan;
-    int cols;  // columns of d_v (or of a transition) per workgroup
+    delta_kernel_t bprep, states, rlocal, rscan, rfull, grad;  // gradients
+    int cols;          // columns of d_v (or of a transition) per workgroup
+    int grad_threads;
 };
 // d_k in {32, 64, 128, 256} for bf16 and {16, 32, 64, 128} for fp32; false otherwise.
 bool delta_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);
+// The gradients' own kernels (rlocal, rfull, grad, grad_threads) of a supported shape.
+void delta_bwd_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);
 
 }  // namespace ret

@@ -65,9 +65,10 @@ ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR], const void* may
 // Segments per sequence.
 struct Plan {
     int nchunks, nseg, seg_chunks;
-    size_t mats, fac, segE, segM, bytes;  // byte offsets of the parts, and their end
+    size_t mats, fac, segE, segM, segF, s0t, ds1t, et, dut, bytes;  // byte offsets of the parts, and their end
 };
-Plan make_plan(const Shape& s, const DeltaKernels& k, int nmats, const Opts& op) {
+Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bwd, const Opts& op) {
+    const int nmats = bwd ? 3 : 2;
     Plan p;
     p.nchunks = (s.N + kDeltaC - 1) / kDeltaC;
     const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
@@ -82,13 +83,23 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, int nmats, const Opts& op)
     const size_t bh = (size_t)s.B * s.H;
     p.mats = 0;
     p.fac = p.mats + bh * p.nchunks * nmats * kDeltaMatBytes;
-    p.segE = p.fac + round256(bh * p.nchunks * 3 * kDeltaC * sizeof(float));
+    p.segE = p.fac + round256(bh * p.nchunks * kDeltaFac * sizeof(float));
     p.segM = p.segE + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dv * sizeof(float)) : 0);
-    p.bytes = p.segM + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dk * sizeof(float)) : 0);
+    p.segF = p.segM + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dk * sizeof(float)) : 0);
+    p.s0t = p.ds1t = p.et = p.dut = p.bytes = p.segF;
+    if (bwd) {
+        const size_t state = round256(bh * p.nchunks * s.dk * s.dv * esize(in_dt));
+        const size_t rows = round256(bh * p.nchunks * kDeltaC * s.dv * esize(in_dt));
+        p.s0t = p.segF + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dv * sizeof(float)) : 0);
+        p.ds1t = p.s0t + state;
+        p.et = p.ds1t + state;
+        p.dut = p.et + rows;
+        p.bytes = p.dut + rows;
+    }
     return p;
 }
 
-void fill(DeltaArgs& A, const Shape& s, const Plan& p, int nmats, void* workspace, ret_dtype_t out_dt,
+void fill(DeltaArgs& A, const Shape& s, const Plan& p, bool bwd, void* workspace, ret_dtype_t out_dt,
           ret_dtype_t gate_dt, float scale) {
     memset(&A, 0, sizeof(A));
     A.B = s.B;
@@ -98,21 +109,27 @@ void fill(DeltaArgs& A, const Shape& s, const Plan& p, int nmats, void* workspac
     A.dk = s.dk;
     A.dv = s.dv;
     A.nchunks = p.nchunks;
-    A.nmats = nmats;
+    A.nmats = bwd ? 3 : 2;
     A.nseg = p.nseg;
     A.seg_chunks = p.seg_chunks;
     A.mats = (char*)workspace + p.mats;
     A.fac = (float*)((char*)workspace + p.fac);
     A.segE = (float*)((char*)workspace + p.segE);
     A.segM = (float*)((char*)workspace + p.segM);
+    A.segF = (float*)((char*)workspace + p.segF);
+    A.s0t = (char*)workspace + p.s0t;
+    A.ds1t = (char*)workspace + p.ds1t;
+    A.et = (char*)workspace + p.et;
+    A.dut = (char*)workspace + p.dut;
     A.out_bf16 = out_dt == RET_BF16;
     A.gate_bf16 = gate_dt == RET_BF16;
     A.scale = scale_of(scale, s.dk);
 }
 
-ret_status_t launch(const char* name, delta_kernel_t fn, dim3 grid, hipStream_t s, const Opts& op, const DeltaArgs& A) {
+ret_status_t launch(const char* name, delta_kernel_t fn, dim3 grid, hipStream_t s, const Opts& op, const DeltaArgs& A,
+                    int threads = kThreads) {
     LaunchTimer tm(name, s, op);
-    hipLaunchKernelGGL(fn, grid, dim3(kThreads), 0, s, A);
+    hipLaunchKernelGGL(fn, grid, dim3(threads), 0, s, A);
     tm.done();
     return launch_status(name);
 }
@@ -132,7 +149,7 @@ size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int 
     const Shape s = {B, N, H, Hk, dk, dv};
     DeltaKernels k;
     if (check_shape(s, in_dt, RET_F32, RET_F32) != RET_OK || !delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
-    return make_plan(s, k, 2, resolve(opts)).bytes;
+    return make_plan(s, k, in_dt, false, resolve(opts)).bytes;
 }
 
 ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
@@ -150,7 +167,7 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
         return fail(RET_ERR_UNSUPPORTED, "gated delta rule: unsupported d_k=%d d_v=%d for %s input", dk, dv,
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
-    const Plan p = make_plan(s, kn, 2, op);
+    const Plan p = make_plan(s, kn, in_dt, false, op);
     const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
     const Buf w[] = {{"o", o, T * H * dv * esize(out_dt)}, {"state_out", state_out, sb},
                      {"the workspace", workspace, workspace_bytes}};
@@ -164,7 +181,7 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
         return fail(RET_ERR_WORKSPACE, "gated delta rule: workspace of %zu bytes, %zu needed",
                     workspace ? workspace_bytes : 0, p.bytes);
     DeltaArgs A;
-    fill(A, s, p, 2, workspace, out_dt, gate_dt, scale);
+    fill(A, s, p, false, workspace, out_dt, gate_dt, scale);
     A.q = q;
     A.k = k;
     A.v = v;
@@ -174,17 +191,88 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     A.lengths = lengths;
     A.state_in = state_in;
     A.state_out = state_out;
-    A.local_segs = p.nseg - 1;
     hipStream_t str = (hipStream_t)stream;
     if ((st = launch("ret_delta_prep", kn.prep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
     const unsigned nc = blocks(dv, kn.cols);
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local", kn.local, dim3(B * H * (p.nseg - 1), nc + blocks(dk, kn.cols)), str, op, A)) !=
+        if ((st = launch("ret_delta_local", kn.local, dim3(B * H * p.nseg, nc + blocks(dk, kn.cols)), str, op, A)) !=
             RET_OK)
             return st;
         if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
     }
     return launch("ret_delta_full", kn.full, dim3(B * H * p.nseg, nc), str, op, A);
+}
+
+size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
+                                           const ret_options_t* opts) {
+    const Shape s = {B, N, H, Hk, dk, dv};
+    DeltaKernels k;
+    if (check_shape(s, in_dt, RET_F32, RET_F32) != RET_OK || !delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
+    return make_plan(s, k, in_dt, true, resolve(opts)).bytes;
+}
+
+ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                                 const void* dout, void* dq, void* dk_out, void* dv_out, void* dg, void* dbeta, int B,
+                                 int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt, ret_dtype_t out_dt,
+                                 ret_dtype_t gate_dt, float scale, const int32_t* lengths, const float* state_in,
+                                 const float* dstate_out, float* dstate_in, void* workspace, size_t workspace_bytes,
+                                 void* stream, const ret_options_t* opts) {
+    const Shape s = {B, N, H, Hk, dk, dv};
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    if (st != RET_OK) return st;
+    if (!q || !k || !v || !g || !beta || !dout || !dq || !dk_out || !dv_out || !dg || !dbeta)
+        return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/dout or gradient pointer");
+    if (!isfinite(scale)) return fail(RET_ERR_INVALID_ARG, "scale is not finite");
+    DeltaKernels kn;
+    if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &kn))
+        return fail(RET_ERR_UNSUPPORTED, "gated delta gradients: unsupported d_k=%d d_v=%d for %s input", dk, dv,
+                    in_dt == RET_F32 ? "F32" : "BF16");
+    const Opts op = resolve(opts);
+    const Plan p = make_plan(s, kn, in_dt, true, op);
+    const size_t T = (size_t)B * N, ei = esize(in_dt), eo = esize(out_dt), eg = esize(gate_dt);
+    const size_t sb = (size_t)B * H * dk * dv * 4;
+    const Buf w[] = {{"dq", dq, T * Hk * dk * eo}, {"dk", dk_out, T * Hk * dk * eo}, {"dv", dv_out, T * H * dv * eo},
+                     {"dg", dg, T * H * eg}, {"dbeta", dbeta, T * H * eg}, {"dstate_in", dstate_in, sb},
+                     {"the workspace", workspace, workspace_bytes}};
+    const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
+                     {"g", g, T * H * eg}, {"beta", beta, T * H * eg}, {"dout", dout, T * H * dv * ei},
+                     {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}, {"dstate_out", dstate_out, sb}};
+    if ((st = check_apart(w, r, nullptr, nullptr)) != RET_OK) return st;
+    if (!workspace || workspace_bytes < p.bytes)
+        return fail(RET_ERR_WORKSPACE, "gated delta gradients: workspace of %zu bytes, %zu needed",
+                    workspace ? workspace_bytes : 0, p.bytes);
+    DeltaArgs A;
+    fill(A, s, p, true, workspace, out_dt, gate_dt, scale);
+    A.q = q;
+    A.k = k;
+    A.v = v;
+    A.g = g;
+    A.beta = beta;
+    A.dout = dout;
+    A.lengths = lengths;
+    A.state_in = state_in;
+    A.dstate_out = dstate_out;
+    A.dstate_in = dstate_in;
+    A.dq = dq;
+    A.dk_ = dk_out;
+    A.dv_ = dv_out;
+    A.dg = dg;
+    A.dbeta = dbeta;
+    hipStream_t str = (hipStream_t)stream;
+    if ((st = launch("ret_delta_prep", kn.bprep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
+    const unsigned nc = blocks(dv, kn.cols), units = B * H * p.nseg;
+    if (p.nseg > 1) {
+        if ((st = launch("ret_delta_local", kn.local, dim3(units, nc + blocks(dk, kn.cols)), str, op, A)) != RET_OK)
+            return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+    }
+    if ((st = launch("ret_delta_states", kn.states, dim3(units, nc), str, op, A)) != RET_OK) return st;
+    if (p.nseg > 1) {
+        if ((st = launch("ret_delta_local_bwd", kn.rlocal, dim3(units, nc), str, op, A)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+    }
+    if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units, nc), str, op, A)) != RET_OK) return st;
+    return launch("ret_delta_grad", kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
 }
 
 ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,

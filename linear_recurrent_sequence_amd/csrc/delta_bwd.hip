@@ -1,0 +1,548 @@
+// Gradients of the gated delta rule. In the chunk form of delta.h, with the gradient dS_C of the state leaving a chunk,
+// Tr = (I + Ar)^-1, Ar_ij = beta_i exp(G_i - G_j) (k_i.k_j) (j < i), Pr_ij = scale exp(G_i - G_j) (q_i.k_j) (j <= i) and
+// D_ij = exp(G_i - G_j):
+//     W = Pr^T dO + exp(G_C - G) K dS_C,  dU = Tr^T W   (gradients of the writes u = beta e),  dV = beta dU,
+//     dS_0 = exp(G_C) dS_C + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
+// is a second chain, from the last chunk to the first, whose products stay within a wave like the forward's. What is left
+// is local to a chunk, given S_0, dS_C, E and dU (stored by the two chains):
+//     X_ij = scale D_ij beta_j (dO_i.E_j) (j <= i),   Z_ij = -D_ij beta_i beta_j (dU_i.E_j) (j < i),
+//     dQ = scale exp(G) dO S_0^T + X K,
+//     dK = Kr + Kw,  Kr = -exp(G) beta dU S_0^T + Z K  (k as it reads),
+//                    Kw = exp(G_C - G) beta E dS_C^T + X^T Q + Z^T K  (k as it writes),
+//     dbeta_i = dU_i.E_i,
+//     dG_i = q_i.dq_i + k_i.Kr_i - k_i.Kw_i,  dG_C gets <S_C, dS_C> more,  dg_t = sum of dG_i over i >= t in the chunk:
+// exp(G_i) stands with every q_i and reading k_i, exp(-G_i) with every writing k_i, exp(G_C) with S_C. Solving for E with
+// beta along the columns and for dU with beta along the rows leaves no division by beta, which may be zero.
+#include "delta.h"
+
+namespace ret {
+
+namespace {
+
+typedef double f64;
+
+// ---------------------------------------------------------------------------------------------------
+// The chain from the right: one segment of one head, 64 NC columns per workgroup, dS in accumulators. LOCAL: the gradient
+// of the state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise
+// dS_C of each chunk and dU, transposed, and dV; the first segment leaves dstate_in.
+// ---------------------------------------------------------------------------------------------------
+template <class E, int DK, int NC, bool LOCAL>
+__global__ __launch_bounds__(kThreads) void delta_rchain_kernel(DeltaArgs a) {
+    typedef typename E::st st;
+    typedef DOps<E> D;
+    typedef DRows<E, DK> Rows;
+    typedef typename Rows::Tile Tile;
+    constexpr int DT = DK / 16, NS = kDeltaC / D::KS;
+    __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
+    __shared__ __align__(16) st sq[kDeltaC * Tile::LD];
+    __shared__ __align__(16) float sf[256];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, b = bh / a.H, h = bh % a.H;
+    const int col0 = (int)blockIdx.y * 64 * NC + w * 16 * NC;
+    const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
+    const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
+    const bool active = col0 < a.dv;
+    if (LOCAL && seg == 0) return;  // no one is left of it
+
+    f32x4_t S[NC][DT];
+    const float* sin = nullptr;
+    if (LOCAL ? seg == a.nseg - 1 : a.nseg == 1)
+        sin = a.dstate_out ? a.dstate_out + (long long)bh * DK * a.dv : nullptr;
+    else if (!LOCAL) sin = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        const int col = col0 + 16 * n + n16;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                S[n][t][i] = sin && col0 + 16 * n < a.dv ? sin[(long long)(16 * t + g4 + i) * a.dv + col] : 0.f;
+    }
+    Rows rk, rq;
+    float ff = 0.f;
+    const st* kp = (const st*)a.k + (((long long)b * a.N) * a.Hk + hk) * DK;
+    const st* qp = (const st*)a.q + (((long long)b * a.N) * a.Hk + hk) * DK;
+    auto fetch = [&](int c) {
+        const int live = min(kDeltaC, len - c * kDeltaC);
+        const long long base = (long long)c * kDeltaC * a.Hk * DK;
+        rk.load(kp + base, a.Hk * DK, live, tid);
+        rq.load(qp + base, a.Hk * DK, live, tid);
+        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
+    };
+    // dV of padding chunks is zero
+    auto store_dv = [&](int c, int m, int n, const f32x4_t& x) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = c * kDeltaC + 16 * m + g4 + i;
+            if (t >= a.N) continue;
+            const long long e = (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + n16;
+            const float y = t < len ? x[i] : 0.f;
+            if (a.out_bf16) ((uint16_t*)a.dv_)[e] = f32_to_bf16(y);
+            else ((float*)a.dv_)[e] = y;
+        }
+    };
+    const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
+    if constexpr (!LOCAL) {
+        if (active)
+            for (int c = max(c0, cend); c < c1; ++c)
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    if (col0 + 16 * n < a.dv)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) store_dv(c, m, n, f32x4_t{0.f, 0.f, 0.f, 0.f});
+    }
+    if (c0 < cend) fetch(cend - 1);
+    for (int c = cend - 1; c >= c0; --c) {
+        __syncthreads();
+        rk.store(sk, tid);
+        rq.store(sq, tid);
+        sf[tid] = ff;
+        __syncthreads();
+        if (c > c0) fetch(c - 1);
+        if (!active) continue;
+        const int live = min(kDeltaC, len - c * kDeltaC);
+        const long long unit = (long long)bh * a.nchunks + c;
+        const char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
+        // dO in accumulator order: lane's column, tokens 16 m + 4 g + i
+        f32x4_t d[NC][4];
+        {
+            const int stride = a.H * a.dv;
+            const st* dp = (const st*)a.dout + (((long long)b * a.N + c * kDeltaC) * a.H + h) * a.dv;
+            const rsrc_t r = bytes_rsrc(dp, ((live - 1) * stride + a.dv) * (int)sizeof(st));
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int off = col0 + 16 * n < a.dv ? (g4 * stride + col0 + 16 * n + n16) * (int)sizeof(st)
+                                                             : 0x40000000;
+                        const int so = (16 * m + i) * stride * (int)sizeof(st);
+                        if constexpr (sizeof(st) == 2)
+                            d[n][m][i] = bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0));
+                        else d[n][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
+                    }
+        }
+        if constexpr (!LOCAL) {
+            st* sp = (st*)a.ds1t + unit * a.dv * DK;
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+                if (col0 + 16 * n < a.dv)
+#pragma unroll
+                    for (int t = 0; t < DT; ++t) store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
+        }
+        // W = exp(G_C - G) K dS + Pr^T dO
+        f32x4_t x[NC][4];
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) x[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < DK / D::KS; ++s) {
+            typename D::Fb fs[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const typename D::Fa fk = Tile::rows(sk, 16 * m, s * D::KS, lane);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) D::mma_ab(x[n][m], fk, fs[n]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf + 128 + 16 * m + g4);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) x[n][m] *= ta;
+        }
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            typename D::Fx fd[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) fd[n] = D::step_exact(d[n], s);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if ((s + 1) * D::KS <= 16 * m) continue;  // below the diagonal of a transpose
+                const typename D::Fm fp = D::mat_frag(mats + 2 * kDeltaMatBytes, m * NS + s, lane);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp, fd[n]);
+            }
+        }
+        // dU = Tr^T W
+        f32x4_t u[NC][4];
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) u[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            typename D::Fb fw[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) fw[n] = D::step(x[n], s);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                if ((s + 1) * D::KS <= 16 * m) continue;
+                const typename D::Fm ft = D::mat_frag(mats + kDeltaMatBytes, m * NS + s, lane);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fw[n]);
+            }
+        }
+        if constexpr (!LOCAL) {
+            st* up = (st*)a.dut + unit * a.dv * kDeltaC;
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+                if (col0 + 16 * n < a.dv)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        store4(up + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
+                        const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf + 192 + 16 * m + g4);
+                        store_dv(c, m, n, be * u[n][m]);
+                    }
+        }
+        // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
+        const float end = sf[63];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf + 16 * m + g4);
+            const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf + 192 + 16 * m + g4);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                d[n][m] *= a.scale * ga;
+                u[n][m] *= -(ga * be);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int t = 0; t < DT; ++t) S[n][t] *= end;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            typename D::Fb fu[NC], fd[NC];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                fu[n] = D::step(u[n], s);
+                fd[n] = D::step(d[n], s);
+            }
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+                const typename D::Fa fk = Tile::cols(sk, s * D::KS, 16 * t, lane);
+                const typename D::Fa fq = Tile::cols(sq, s * D::KS, 16 * t, lane);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) {
+                    D::mma_ab(S[n][t], fk, fu[n]);
+                    D::mma_ab(S[n][t], fq, fd[n]);
+                }
+            }
+        }
+    }
+    if (!active) return;
+    float* out = nullptr;
+    if (LOCAL) out = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
+    else if (seg == 0 && a.dstate_in) out = a.dstate_in + (long long)bh * DK * a.dv;
+    if (!out) return;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+        if (col0 + 16 * n >= a.dv) continue;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[(long long)(16 * t + g4 + i) * a.dv + col0 + 16 * n + n16] = S[n][t][i];
+    }
+}
+
+// R rows of W elements to an LDS tile by NT threads: rows at or past `rows` and columns at or past `cols` are zero.
+template <class E, int R, int W, int NT>
+struct GRows {
+    typedef typename E::st st;
+    static constexpr int EPS = 16 / sizeof(st), SPR = W / EPS, NP = (R * SPR + NT - 1) / NT;
+    typedef typename DOps<E>::template Tile<W> Tile;
+    u32x4_t x[NP];
+    __device__ __forceinline__ void load(const st* p, int stride, int rows, int cols, int tid) {
+        const int bytes = rows > 0 ? ((rows - 1) * stride + cols) * (int)sizeof(st) : 0;
+        const rsrc_t r = bytes_rsrc(p, bytes);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int s = tid + i * NT, row = s / SPR, c = s % SPR * EPS;
+            x[i] = buf_load16(r, row < rows && c < cols ? (row * stride + c) * (int)sizeof(st) : 0x40000000, 0);
+        }
+    }
+    __device__ __forceinline__ void store(st* lds, int tid) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int s = tid + i * NT;
+            if (R * SPR % NT == 0 || s < R * SPR)
+                *reinterpret_cast<u32x4_t*>(lds + Tile::off(s / SPR, s % SPR * EPS)) = x[i];
+        }
+    }
+};
+
+// sum of the products of two operand fragments
+__device__ __forceinline__ float frag_dot(bf16x8_t a, bf16x8_t b) {
+    const u32x4_t x = __builtin_bit_cast(u32x4_t, a), y = __builtin_bit_cast(u32x4_t, b);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s += __uint_as_float(x[i] << 16) * __uint_as_float(y[i] << 16);
+        s += __uint_as_float(x[i] & 0xffff0000u) * __uint_as_float(y[i] & 0xffff0000u);
+    }
+    return s;
+}
+__device__ __forceinline__ float frag_dot(f32x4_t a, f32x4_t b) {
+    return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+}
+__device__ __forceinline__ f32x4_t lds4(const uint16_t* p) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                   __uint_as_float(u.y & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4_t lds4(const float* p) { return *reinterpret_cast<const f32x4_t*>(p); }
+__device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
+    return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+}
+
+// ---------------------------------------------------------------------------------------------------
+// delta_grad: dq, dk, dg, dbeta of one chunk and key head (the value heads that share it one after another, their dq and
+// dk added up in registers: no atomics, one order). Wave w owns tokens 16 (w % 4) .. + 15 and the columns of d_k of its
+// half w / 4. Every product has its accumulator rows along d_k (or j) and columns along tokens: per-token factors are one
+// value per lane and a lane holds 4 consecutive values of its token's row. d_v is walked in blocks of 32.
+// ---------------------------------------------------------------------------------------------------
+template <class E, int DK, int NW>
+__global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
+    typedef typename E::st st;
+    typedef DOps<E> D;
+    constexpr int NT = 64 * NW, DH = DK / (NW / 4), DT = DH / 16, NS = kDeltaC / D::KS, VB = 32;
+    typedef typename D::template Tile<DK> TK;
+    typedef typename D::template Tile<VB> TO;
+    typedef typename D::template Tile<kDeltaC> TC;
+    constexpr int kStage = 2 * VB * TK::LD + kDeltaC * TO::LD + 2 * VB * TC::LD, kXZ = 2 * kDeltaC * TC::LD;
+    __shared__ __align__(16) st sk[kDeltaC * TK::LD];
+    __shared__ __align__(16) st sq[kDeltaC * TK::LD];
+    __shared__ __align__(16) st buf[kStage > kXZ ? kStage : kXZ];
+    __shared__ f64 sG[kDeltaC];
+    __shared__ float sF[256], sDg[2][kDeltaC], sDb[kDeltaC], sR[2][NW];
+    st *sS = buf, *sD = sS + VB * TK::LD, *sO = sD + VB * TK::LD, *sE = sO + kDeltaC * TO::LD, *sU = sE + VB * TC::LD;
+    st *sX = buf, *sZ = buf + kDeltaC * TC::LD;
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
+    const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
+    const int t0 = c * kDeltaC, len = delta_len(a, b), live = min(kDeltaC, len - t0);
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t tq[DT], tk[DT];
+#pragma unroll
+    for (int t = 0; t < DT; ++t) tq[t] = tk[t] = zero;
+    if (live > 0) {
+        GRows<E, kDeltaC, DK, NT> rk, rq;
+        const long long base = (((long long)b * a.N + t0) * a.Hk + hk) * DK;
+        rk.load((const st*)a.k + base, a.Hk * DK, live, DK, tid);
+        rq.load((const st*)a.q + base, a.Hk * DK, live, DK, tid);
+        rk.store(sk, tid);
+        rq.store(sq, tid);
+    }
+    for (int r = 0; r < rep; ++r) {
+        const int h = hk * rep + r;
+        if (live <= 0) {  // padding: zero gradients
+            if (tid < kDeltaC && t0 + tid < a.N) {
+                const long long e = ((long long)b * a.N + t0 + tid) * a.H + h;
+                if (a.gate_bf16) ((uint16_t*)a.dg)[e] = ((uint16_t*)a.dbeta)[e] = 0;
+                else ((float*)a.dg)[e] = ((float*)a.dbeta)[e] = 0.f;
+            }
+            continue;
+        }
+        const long long unit = ((long long)b * a.H + h) * a.nchunks + c;
+        f32x4_t Dq[DT], Dr[DT], Du[DT], M1[4], M2[4];
+#pragma unroll
+        for (int t = 0; t < DT; ++t) Dq[t] = Dr[t] = Du[t] = zero;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) M1[j] = M2[j] = zero;
+        float dot = 0.f;
+        GRows<E, VB, DK, NT> rs, rd;
+        GRows<E, kDeltaC, VB, NT> ro;
+        GRows<E, VB, kDeltaC, NT> re, ru;
+        const st* sp = (const st*)a.s0t + unit * a.dv * DK;
+        const st* dp = (const st*)a.ds1t + unit * a.dv * DK;
+        const st* ep = (const st*)a.et + unit * a.dv * kDeltaC;
+        const st* up = (const st*)a.dut + unit * a.dv * kDeltaC;
+        const st* op = (const st*)a.dout + (((long long)b * a.N + t0) * a.H + h) * a.dv;
+        auto fetch = [&](int v0) {
+            const int nv = min(VB, a.dv - v0);
+            rs.load(sp + (long long)v0 * DK, DK, nv, DK, tid);
+            rd.load(dp + (long long)v0 * DK, DK, nv, DK, tid);
+            ro.load(op + v0, a.H * a.dv, live, nv, tid);
+            re.load(ep + v0 * kDeltaC, kDeltaC, nv, kDeltaC, tid);
+            ru.load(up + v0 * kDeltaC, kDeltaC, nv, kDeltaC, tid);
+        };
+        fetch(0);
+        const float* f = a.fac + unit * kDeltaFac;
+        __syncthreads();  // the last head's readers are done
+        if (tid < 256) sF[tid] = f[tid];
+        if (tid < kDeltaC) sG[tid] = reinterpret_cast<const f64*>(f + 256)[tid];
+        for (int v0 = 0; v0 < a.dv; v0 += VB) {
+            __syncthreads();
+            rs.store(sS, tid);
+            rd.store(sD, tid);
+            ro.store(sO, tid);
+            re.store(sE, tid);
+            ru.store(sU, tid);
+            __syncthreads();
+            if (v0 + VB < a.dv) fetch(v0 + VB);
+#pragma unroll
+            for (int s = 0; s < VB / D::KS; ++s) {
+                const typename D::Fa fo = TO::rows(sO, 16 * tw, s * D::KS, lane);
+                const typename D::Fa fu = TC::cols(sU, s * D::KS, 16 * tw, lane);
+                const typename D::Fa fe = TC::cols(sE, s * D::KS, 16 * tw, lane);
+#pragma unroll
+                for (int t = 0; t < DT; ++t) {
+                    const typename D::Fa fs = TK::cols(sS, s * D::KS, dk0 + 16 * t, lane);
+                    const typename D::Fa fd = TK::cols(sD, s * D::KS, dk0 + 16 * t, lane);
+                    D::mma_aa(Dq[t], fs, fo);
+                    D::mma_aa(Dr[t], fs, fu);
+                    D::mma_aa(Du[t], fd, fe);
+                    if ((t & 3) == tw) dot += frag_dot(fs, fd);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j > tw) continue;
+                    const typename D::Fa fj = TC::cols(sE, s * D::KS, 16 * j, lane);
+                    if (NW == 4 || hf == 0) D::mma_aa(M1[j], fj, fo);
+                    if (NW == 4 || hf == 1) D::mma_aa(M2[j], fj, fu);
+                }
+            }
+        }
+        __syncthreads();
+        const float ga = sF[i], tb = sF[64 + i], be = sF[192 + i], end = sF[63];
+        float csum = 0.f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            Dq[t] *= a.scale * ga;
+            Dr[t] *= -(ga * be);
+            Du[t] *= tb;
+            csum += dot4(Du[t], lds4(sk + TK::off(i, dk0 + 16 * t + g4)));
+        }
+        // X and Z: this lane's row i, columns 16 j + g4 ..
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4_t x = zero, z = zero;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int jj = 16 * j + g4 + e;
+                if (jj > i) continue;
+                const float d = __builtin_amdgcn_exp2f((float)(sG[i] - sG[jj])) * sF[192 + jj];
+                x[e] = a.scale * d * M1[j][e];
+                if (jj < i) z[e] = -d * be * M2[j][e];
+                else if (NW == 4 || hf == 1) sDb[i] = M2[j][e];
+            }
+            if (NW == 4 || hf == 0) store4(sX + TC::off(i, 16 * j + g4), x);
+            if (NW == 4 || hf == 1) store4(sZ + TC::off(i, 16 * j + g4), z);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+            const bool lower = s * D::KS <= 16 * tw + 15, upper = (s + 1) * D::KS > 16 * tw;
+            const typename D::Fa fx = TC::rows(sX, 16 * tw, s * D::KS, lane), fz = TC::rows(sZ, 16 * tw, s * D::KS, lane);
+            const typename D::Fa gx = TC::cols(sX, s * D::KS, 16 * tw, lane), gz = TC::cols(sZ, s * D::KS, 16 * tw, lane);
+#pragma unroll
+            for (int t = 0; t < DT; ++t) {
+                const typename D::Fa fk = TK::cols(sk, s * D::KS, dk0 + 16 * t, lane);
+                if (lower) {
+                    D::mma_aa(Dq[t], fk, fx);
+                    D::mma_aa(Dr[t], fk, fz);
+                }
+                if (upper) {
+                    D::mma_aa(Du[t], TK::cols(sq, s * D::KS, dk0 + 16 * t, lane), gx);
+                    D::mma_aa(Du[t], fk, gz);
+                }
+            }
+        }
+        float dg = 0.f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) {
+            const f32x4_t kv = lds4(sk + TK::off(i, dk0 + 16 * t + g4)), qv = lds4(sq + TK::off(i, dk0 + 16 * t + g4));
+            dg += dot4(qv, Dq[t]) + dot4(kv, Dr[t] - Du[t]);
+            tq[t] += Dq[t];
+            tk[t] += Dr[t] + Du[t];
+        }
+        dg += __shfl_xor(dg, 16);
+        dg += __shfl_xor(dg, 32);
+        if (lane < 16) sDg[hf][i] = dg;
+        dot = lanes_sum<64>(dot);
+        csum = lanes_sum<64>(csum);
+        if (lane == 0) {
+            sR[0][w] = dot;
+            sR[1][w] = csum;
+        }
+        __syncthreads();
+        if (w == 0) {
+            f64 x = sDg[0][lane];
+            if (NW == 8) x += sDg[1][lane];
+            if (lane == 63)
+#pragma unroll
+                for (int j = 0; j < NW; ++j) x += (f64)end * sR[0][j] + sR[1][j];
+#pragma unroll
+            for (int m = 1; m < 64; m *= 2) {
+                const f64 down = __shfl_down(x, m);
+                if (lane + m < 64) x += down;
+            }
+            if (t0 + lane < a.N) {
+                const long long e = ((long long)b * a.N + t0 + lane) * a.H + h;
+                const float y = lane < live ? (float)x : 0.f, z = lane < live ? sDb[lane] : 0.f;
+                if (a.gate_bf16) {
+                    ((uint16_t*)a.dg)[e] = f32_to_bf16(y);
+                    ((uint16_t*)a.dbeta)[e] = f32_to_bf16(z);
+                } else {
+                    ((float*)a.dg)[e] = y;
+                    ((float*)a.dbeta)[e] = z;
+                }
+            }
+        }
+    }
+    const int t = t0 + i;
+    if (t >= a.N) return;
+#pragma unroll
+    for (int j = 0; j < DT; ++j) {
+        const long long e = (((long long)b * a.N + t) * a.Hk + hk) * DK + dk0 + 16 * j + g4;
+        const f32x4_t x = t < len ? tq[j] : zero, y = t < len ? tk[j] : zero;
+        if (a.out_bf16) {
+            store4((uint16_t*)a.dq + e, x);
+            store4((uint16_t*)a.dk_ + e, y);
+        } else {
+            store4((float*)a.dq + e, x);
+            store4((float*)a.dk_ + e, y);
+        }
+    }
+}
+
+template <class E, int DK>
+void pick(int dv, DeltaKernels* o) {
+    constexpr int NW = DK * sizeof(typename E::st) > 256 ? 8 : 4;  // half of d_k per wave where a row is long
+    if (dv > 64) {
+        o->rlocal = delta_rchain_kernel<E, DK, 2, true>;
+        o->rfull = delta_rchain_kernel<E, DK, 2, false>;
+    } else {
+        o->rlocal = delta_rchain_kernel<E, DK, 1, true>;
+        o->rfull = delta_rchain_kernel<E, DK, 1, false>;
+    }
+    o->grad = delta_grad_kernel<E, DK, NW>;
+    o->grad_threads = 64 * NW;
+}
+
+}  // namespace
+
+void delta_bwd_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* o) {
+    if (bf16_in) {
+        switch (dk) {
+            case 32: return pick<BF16, 32>(dv, o);
+            case 64: return pick<BF16, 64>(dv, o);
+            case 128: return pick<BF16, 128>(dv, o);
+            case 256: return pick<BF16, 256>(dv, o);
+        }
+    } else {
+        switch (dk) {
+            case 16: return pick<F32, 16>(dv, o);
+            case 32: return pick<F32, 32>(dv, o);
+            case 64: return pick<F32, 64>(dv, o);
+            case 128: return pick<F32, 128>(dv, o);
+        }
+    }
+}
+
+}  // namespace ret

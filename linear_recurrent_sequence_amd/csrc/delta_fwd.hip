@@ -51,6 +51,56 @@ __device__ __forceinline__ void write_mat(char* m, const float* X, int w, int la
     }
 }
 
+// sT <- (I + sA)^-1 for a strictly lower triangular sA, by the workgroup's four waves. Ends with a barrier.
+__device__ __forceinline__ void tri_inverse(const float* sA, float* sT, int w, int lane) {
+    const int n16 = lane & 15, g = lane >> 4;
+    // diagonal block w: column n16 of its inverse (the four lane groups hold the same)
+    {
+        float x[16];
+        const float* Ad = sA + (16 * w) * kTriLD + 16 * w;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float s = i == n16 ? 1.f : 0.f;
+#pragma unroll
+            for (int m = 0; m < i; ++m) s -= Ad[i * kTriLD + m] * x[m];
+            x[i] = s;
+        }
+        if (g == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sT[(16 * w + i) * kTriLD + 16 * w + n16] = x[i];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // the blocks above the diagonal
+            if (j > w) tri_store(sT, 16 * w, 16 * j, lane, f32x4_t{0.f, 0.f, 0.f, 0.f});
+    }
+    __syncthreads();
+    // 32 x 32 blocks: rows 16 .. 31 (wave 0) and 48 .. 63 (wave 1)
+    if (w < 2) {
+        const int r0 = 32 * w + 16, c0 = 32 * w;
+        f32x4_t m = {0.f, 0.f, 0.f, 0.f}, t = {0.f, 0.f, 0.f, 0.f};
+        DOps<F32>::mma_ab(m, tri_a(sA, r0, c0, lane), tri_b(sT, c0, c0, lane));
+        DOps<F32>::mma_ab(t, tri_a(sT, r0, r0, lane), m);
+        tri_store(sT, r0, c0, lane, -t);
+    }
+    __syncthreads();
+    // the 64 x 64 one: wave w makes the tile at rows 32 + 16 (w / 2), columns 16 (w % 2)
+    {
+        const int rt = w / 2, ct = w % 2;
+        f32x4_t m[2], t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            m[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                DOps<F32>::mma_ab(m[i], tri_a(sA, 32 + 16 * i, 16 * j, lane), tri_b(sT, 16 * j, 16 * ct, lane));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) DOps<F32>::mma_ab(t, tri_a(sT, 32 + 16 * rt, 32 + 16 * i, lane), m[i]);
+        tri_store(sT, 32 + 16 * rt, 16 * ct, lane, -t);
+    }
+    __syncthreads();
+}
+
 template <class E, int DK, bool BWD>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     typedef typename E::st st;
@@ -77,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     }
     __syncthreads();
     // K K^T and Q K^T, row tile w, column tiles 0 .. w (the ones past it stay zero)
-    f32x4_t kk[4], qk[4];
+    f32x4_t kk[4], qk[4], av[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     auto dot = [&](f32x4_t& acc, const typename D::Fa& x, const typename D::Fa& y) {
@@ -111,80 +161,51 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
             const float be = in ? gate_at(a.beta, i, a.gate_bf16) : 0.f;
             sG[lane] = G;
             sB[lane] = be;
-            float* f = a.fac + unit * 192;
-            const f64 last = __shfl(G, 63);
+            float* f = a.fac + unit * kDeltaFac;
+            const float tail = __builtin_amdgcn_exp2f((float)(__shfl(G, 63) - G));
             f[lane] = __builtin_amdgcn_exp2f((float)G);
-            f[64 + lane] = __builtin_amdgcn_exp2f((float)(last - G));
-            f[128 + lane] = be;
+            f[64 + lane] = tail * be;
+            f[128 + lane] = tail;
+            f[192 + lane] = be;
+            reinterpret_cast<f64*>(f + 256)[lane] = G;
         }
         __syncthreads();
         char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
-        // A into sA; P into sT until it is written out
+        // A into sA; P into sT until it is written out (the gradients take P without beta)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4_t av, pv;
+            f32x4_t pv;
+            const int col = 16 * j + n16;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = 16 * w + 4 * g + i, col = 16 * j + n16;
+                const int row = 16 * w + 4 * g + i;
                 const float d = col <= row ? __builtin_amdgcn_exp2f((float)(sG[row] - sG[col])) : 0.f;
-                av[i] = col < row ? sB[row] * d * kk[j][i] : 0.f;
-                pv[i] = col <= row ? a.scale * d * qk[j][i] : 0.f;
+                av[j][i] = col < row ? d * kk[j][i] : 0.f;
+                pv[i] = col <= row ? a.scale * (BWD ? 1.f : sB[col]) * d * qk[j][i] : 0.f;
             }
-            tri_store(sA, 16 * w, 16 * j, lane, av);
+            tri_store(sA, 16 * w, 16 * j, lane, av[j] * sB[col]);
             tri_store(sT, 16 * w, 16 * j, lane, pv);
         }
         __syncthreads();
-        write_mat<E, false>(mats + kDeltaMatBytes, sT, w, lane);
-        if constexpr (BWD) write_mat<E, true>(mats + 3 * kDeltaMatBytes, sT, w, lane);
-        __syncthreads();
-        // diagonal block w: column n16 of its inverse (the four lane groups hold the same)
-        {
-            float x[16];
-            const float* Ad = sA + (16 * w) * kTriLD + 16 * w;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float s = i == n16 ? 1.f : 0.f;
-#pragma unroll
-                for (int m = 0; m < i; ++m) s -= Ad[i * kTriLD + m] * x[m];
-                x[i] = s;
-            }
-            if (g == 0) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sT[(16 * w + i) * kTriLD + 16 * w + n16] = x[i];
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // the blocks above the diagonal
-                if (j > w) tri_store(sT, 16 * w, 16 * j, lane, f32x4_t{0.f, 0.f, 0.f, 0.f});
-        }
-        __syncthreads();
-        // 32 x 32 blocks: rows 16 .. 31 (wave 0) and 48 .. 63 (wave 1)
-        if (w < 2) {
-            const int r0 = 32 * w + 16, c0 = 32 * w;
-            f32x4_t m = {0.f, 0.f, 0.f, 0.f}, t = {0.f, 0.f, 0.f, 0.f};
-            DOps<F32>::mma_ab(m, tri_a(sA, r0, c0, lane), tri_b(sT, c0, c0, lane));
-            DOps<F32>::mma_ab(t, tri_a(sT, r0, r0, lane), m);
-            tri_store(sT, r0, c0, lane, -t);
-        }
-        __syncthreads();
-        // the 64 x 64 one: wave w makes the tile at rows 32 + 16 (w / 2), columns 16 (w % 2)
-        {
-            const int rt = w / 2, ct = w % 2;
-            f32x4_t m[2], t = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                m[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    DOps<F32>::mma_ab(m[i], tri_a(sA, 32 + 16 * i, 16 * j, lane), tri_b(sT, 16 * j, 16 * ct, lane));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                DOps<F32>::mma_ab(t, tri_a(sT, 32 + 16 * rt, 32 + 16 * i, lane), m[i]);
-            tri_store(sT, 32 + 16 * rt, 16 * ct, lane, -t);
-        }
-        __syncthreads();
-        write_mat<E, false>(mats, sT, w, lane);
         if constexpr (BWD) write_mat<E, true>(mats + 2 * kDeltaMatBytes, sT, w, lane);
+        else write_mat<E, false>(mats + kDeltaMatBytes, sT, w, lane);
+        __syncthreads();
+        tri_inverse(sA, sT, w, lane);
+        write_mat<E, false>(mats, sT, w, lane);
+        if constexpr (BWD) {
+            // Tr = (I + Ar)^-1 with beta along the rows: the gradients' solve
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                f32x4_t x = av[j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] *= sB[16 * w + 4 * g + i];
+                tri_store(sA, 16 * w, 16 * j, lane, x);
+            }
+            __syncthreads();
+            tri_inverse(sA, sT, w, lane);
+            write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane);
+        }
         __syncthreads();
     }
 }
@@ -194,19 +215,20 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
 // LOCAL: the segment's end state from zero (columns of V; segment 0 starts from state_in) or its transition (columns of
 // the identity, V = 0), into segE / segM. Otherwise the outputs, and after the last segment the final state.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NC, bool LOCAL>
+enum { kFull = 0, kLocal = 1, kStates = 2 };
+template <class E, int DK, int NC, int MODE>
 __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
     typedef DRows<E, DK> Rows;
     typedef typename Rows::Tile Tile;
+    constexpr bool LOCAL = MODE == kLocal, FULL = MODE == kFull;
     constexpr int DT = DK / 16, NS = kDeltaC / D::KS;
     __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
-    __shared__ __align__(16) st sq[LOCAL ? 16 : kDeltaC * Tile::LD];
-    __shared__ __align__(16) float sf[192];
+    __shared__ __align__(16) st sq[FULL ? kDeltaC * Tile::LD : 16];
+    __shared__ __align__(16) float sf[128];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int per = LOCAL ? a.local_segs : a.nseg;
-    const int bh = blockIdx.x / per, seg = blockIdx.x % per, b = bh / a.H, h = bh % a.H;
+    const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, b = bh / a.H, h = bh % a.H;
     const int nE = (a.dv + 64 * NC - 1) / (64 * NC);  // workgroups over d_v; a local pass has those of d_k behind them
     const bool trans = LOCAL && (int)blockIdx.y >= nE;
     const int width = trans ? DK : a.dv;
@@ -214,7 +236,8 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const bool active = col0 < width;
-    if (trans && seg == 0 && a.local_segs < a.nseg) return;  // segment 0's end state is known
+    // segment 0's end state is known, and no one asks for the last one's
+    if (LOCAL && (trans ? seg == 0 : seg == a.nseg - 1)) return;
 
     f32x4_t S[NC][DT];
     const float* sin = nullptr;
@@ -243,16 +266,16 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
         rk.load(kp + base, a.Hk * DK, live, tid);
-        if constexpr (!LOCAL) rq.load(qp + base, a.Hk * DK, live, tid);
-        if (tid < 192) ff = a.fac[((long long)bh * a.nchunks + c) * 192 + tid];
+        if constexpr (FULL) rq.load(qp + base, a.Hk * DK, live, tid);
+        if (tid < 128) ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
     };
     const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
     if (c0 < cend) fetch(c0);
     for (int c = c0; c < cend; ++c) {
         __syncthreads();
         rk.store(sk, tid);
-        if constexpr (!LOCAL) rq.store(sq, tid);
-        if (tid < 192) sf[tid] = ff;
+        if constexpr (FULL) rq.store(sq, tid);
+        if (tid < 128) sf[tid] = ff;
         __syncthreads();
         if (c + 1 < cend) fetch(c + 1);
         if (!active) continue;
@@ -294,24 +317,31 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
                 const typename D::Fa fk = Tile::rows(sk, 16 * m, s * D::KS, lane);
 #pragma unroll
                 for (int n = 0; n < NC; ++n) D::mma_ab(y[n][m], fk, fs[n]);
-                if constexpr (!LOCAL) {
+                if constexpr (FULL) {
                     const typename D::Fa fq = Tile::rows(sq, 16 * m, s * D::KS, lane);
 #pragma unroll
                     for (int n = 0; n < NC; ++n) D::mma_ba(o[n][m], fq, fs[n]);
                 }
             }
         }
-        // R = beta (V - exp(G) Y)
+        if constexpr (MODE == kStates) {
+            st* sp = (st*)a.s0t + ((long long)bh * a.nchunks + c) * a.dv * DK;
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+                if (col0 + 16 * n < width)
+#pragma unroll
+                    for (int t = 0; t < DT; ++t) store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
+        }
+        // R = V - exp(G) Y
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf + 16 * m + g4);
-            const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf + 128 + 16 * m + g4);
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[n][m][i] = be[i] * ((trans ? 0.f : v[n][m][i]) - ga[i] * y[n][m][i]);
+                for (int i = 0; i < 4; ++i) y[n][m][i] = (trans ? 0.f : v[n][m][i]) - ga[i] * y[n][m][i];
         }
-        // U = T R
+        // E = T R
         f32x4_t u[NC][4];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -330,8 +360,16 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
                 for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fr[n]);
             }
         }
-        if constexpr (!LOCAL) {
-            // O^T = scale exp(G) (Q S)^T + U^T P^T: a lane holds 4 columns of token 16 m + n16
+        if constexpr (MODE == kStates) {
+            st* ep = (st*)a.et + ((long long)bh * a.nchunks + c) * a.dv * kDeltaC;
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+                if (col0 + 16 * n < width)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) store4(ep + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
+        }
+        if constexpr (FULL) {
+            // O^T = scale exp(G) (Q S)^T + E^T P^T: a lane holds 4 columns of token 16 m + n16
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const float f = a.scale * sf[16 * m + n16];
@@ -367,14 +405,14 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
                 }
             }
         }
-        // S = exp(G_C) S + K^T (exp(G_C - G) U)
+        // S = exp(G_C) S + K^T (exp(G_C - G) beta E)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf + 64 + 16 * m + g4);
 #pragma unroll
             for (int n = 0; n < NC; ++n) u[n][m] *= ta;
         }
-        const float end = sf[63];
+        const float end = sf[63];  // exp(G_C)
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -394,7 +432,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
     }
     if (!active) return;
     // outputs of padding chunks are zero
-    if constexpr (!LOCAL) {
+    if constexpr (FULL) {
         for (int c = max(c0, cend); c < c1; ++c)
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
@@ -409,6 +447,7 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
                 }
             }
     }
+    if constexpr (MODE == kStates) return;
     float* out = nullptr;
     if (LOCAL) out = (trans ? a.segM : a.segE) + ((long long)bh * a.nseg + seg) * DK * width;
     else if (seg == a.nseg - 1 && a.state_out) out = a.state_out + (long long)bh * DK * a.dv;
@@ -426,10 +465,10 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
 // ---------------------------------------------------------------------------------------------------
 // delta_scan: the states entering the segments. In: segE[s] = segment s's end state from zero (segment 0: its true end
 // state), segM[s] its transition. Out: segE[s] = the state entering segment s, S_{s+1} = M_s S_s + E_s. One workgroup per
-// (b, h, 16 columns); the waves share the rows of M, S goes round through LDS. BF16
+// (b, h, 16 columns); REV: the gradients' chain, D_{s-1} = M_s^T D_s + F_s over segF from the right. The waves share the rows of M, S goes round through LDS. BF16
 // input: M and S split in two bf16 parts like the chain's operands.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK>
+template <class E, int DK, bool REV>
 __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
     typedef DOps<E> D;
     constexpr int NT = DK / 16, TW = NT >= 4 ? NT / 4 : 1, LD = 20;
@@ -438,9 +477,10 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
     const int bh = blockIdx.x, col = blockIdx.y * 16 + n16;
     const bool mine = w * TW < NT;
     const long long sz = (long long)DK * a.dv;
-    float* X = a.segE + (long long)bh * a.nseg * sz;
+    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz;
     const float* M = a.segM + (long long)bh * a.nseg * DK * DK;
-    const float* sin = a.state_in ? a.state_in + bh * sz : nullptr;
+    const float* from = REV ? a.dstate_out : a.state_in;
+    const float* sin = from ? from + bh * sz : nullptr;
     const int len = delta_len(a, bh / a.H);
     f32x4_t S[TW];
     auto tile = [&](int k) {  // 16 rows of the entering state as accumulators hold them
@@ -449,7 +489,8 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
         for (int i = 0; i < 4; ++i) x[i] = sS[(16 * k + g4 + i) * LD + n16];
         return x;
     };
-    for (int s = 0; s < a.nseg; ++s) {
+    for (int j = 0; j < a.nseg; ++j) {
+        const int s = REV ? a.nseg - 1 - j : j;
         if (mine) {
             f32x4_t e[TW];
 #pragma unroll
@@ -457,34 +498,42 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const long long at = (long long)(16 * (w * TW + t) + g4 + i) * a.dv + col;
-                    if (s < a.nseg - 1) e[t][i] = X[s * sz + at];
-                    X[s * sz + at] = s == 0 ? (sin ? sin[at] : 0.f) : S[t][i];
+                    if (j < a.nseg - 1) e[t][i] = X[s * sz + at];
+                    X[s * sz + at] = j == 0 ? (sin ? sin[at] : 0.f) : S[t][i];
                 }
-            if (s == a.nseg - 1) break;
-            if (s > 0 && s * a.seg_chunks * kDeltaC >= len) {  // no live token: the state passes as it is
+            if (j == a.nseg - 1) break;
+            if (j > 0 && s * a.seg_chunks * kDeltaC >= len) {  // no live token: the state passes as it is
 #pragma unroll
                 for (int t = 0; t < TW; ++t) e[t] = S[t];
-            } else if (s > 0) {
+            } else if (j > 0) {
                 const float* Ms = M + (long long)s * DK * DK;
 #pragma unroll
                 for (int k = 0; k < DK / D::KS; ++k) {
                     f32x4_t x[D::TPS];
 #pragma unroll
-                    for (int j = 0; j < D::TPS; ++j) x[j] = tile(D::TPS * k + j);
+                    for (int p = 0; p < D::TPS; ++p) x[p] = tile(D::TPS * k + p);
                     const typename D::Fb fs = D::step(x, 0);
 #pragma unroll
                     for (int t = 0; t < TW; ++t) {
-                        const float* m = Ms + (16 * (w * TW + t) + n16) * DK + D::KS * k + g4;
                         f32x4_t y[D::TPS];
+                        if constexpr (REV) {  // rows of the transpose
+                            const float* m = Ms + (D::KS * k + g4) * DK + 16 * (w * TW + t) + n16;
 #pragma unroll
-                        for (int j = 0; j < D::TPS; ++j) y[j] = *reinterpret_cast<const f32x4_t*>(m + 16 * j);
+                            for (int p = 0; p < D::TPS; ++p)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) y[p][i] = m[(16 * p + i) * DK];
+                        } else {
+                            const float* m = Ms + (16 * (w * TW + t) + n16) * DK + D::KS * k + g4;
+#pragma unroll
+                            for (int p = 0; p < D::TPS; ++p) y[p] = *reinterpret_cast<const f32x4_t*>(m + 16 * p);
+                        }
                         D::mma_mb(e[t], D::step(y, 0), fs);
                     }
                 }
             }
 #pragma unroll
             for (int t = 0; t < TW; ++t) S[t] = e[t];
-        } else if (s == a.nseg - 1) {
+        } else if (j == a.nseg - 1) {
             break;
         }
         __syncthreads();
@@ -497,20 +546,23 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
     }
 }
 
-template <class E, int DK>
-bool pick(int dv, DeltaKernels* o) {
+template <class E, int DK, int NC>
+void pick_cols(DeltaKernels* o) {
+    *o = {};
     o->prep = delta_prep_kernel<E, DK, false>;
-    if (dv > 64) {
-        o->local = delta_chain_kernel<E, DK, 2, true>;
-        o->full = delta_chain_kernel<E, DK, 2, false>;
-        o->cols = 128;
-    } else {
-        o->local = delta_chain_kernel<E, DK, 1, true>;
-        o->full = delta_chain_kernel<E, DK, 1, false>;
-        o->cols = 64;
-    }
-    o->scan = delta_scan_kernel<E, DK>;
-    return true;
+    o->bprep = delta_prep_kernel<E, DK, true>;
+    o->local = delta_chain_kernel<E, DK, NC, kLocal>;
+    o->full = delta_chain_kernel<E, DK, NC, kFull>;
+    o->states = delta_chain_kernel<E, DK, NC, kStates>;
+    o->scan = delta_scan_kernel<E, DK, false>;
+    o->rscan = delta_scan_kernel<E, DK, true>;
+    o->cols = 64 * NC;
+}
+// Two column tiles per wave halve the operand reads per product; one where d_v would leave waves idle.
+template <class E, int DK>
+void pick(int dv, DeltaKernels* o) {
+    if (dv > 64) pick_cols<E, DK, 2>(o);
+    else pick_cols<E, DK, 1>(o);
 }
 
 }  // namespace
@@ -519,20 +571,24 @@ bool delta_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* o) {
     if (dv <= 0 || dv % 16) return false;
     if (bf16_in) {
         switch (dk) {
-            case 32: return pick<BF16, 32>(dv, o);
-            case 64: return pick<BF16, 64>(dv, o);
-            case 128: return pick<BF16, 128>(dv, o);
-            case 256: return pick<BF16, 256>(dv, o);
+            case 32: pick<BF16, 32>(dv, o); break;
+            case 64: pick<BF16, 64>(dv, o); break;
+            case 128: pick<BF16, 128>(dv, o); break;
+            case 256: pick<BF16, 256>(dv, o); break;
             default: return false;
         }
+        delta_bwd_kernels_get(true, dk, dv, o);
+        return true;
     }
     switch (dk) {
-        case 16: return pick<F32, 16>(dv, o);
-        case 32: return pick<F32, 32>(dv, o);
-        case 64: return pick<F32, 64>(dv, o);
-        case 128: return pick<F32, 128>(dv, o);
+        case 16: pick<F32, 16>(dv, o); break;
+        case 32: pick<F32, 32>(dv, o); break;
+        case 64: pick<F32, 64>(dv, o); break;
+        case 128: pick<F32, 128>(dv, o); break;
         default: return false;
     }
+    delta_bwd_kernels_get(false, dk, dv, o);
+    return true;
 }
 
 }  // namespace ret

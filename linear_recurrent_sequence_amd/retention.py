@@ -193,6 +193,10 @@ def load(build_if_missing: bool = True):
     lib.ret_gated_delta_fwd.restype = i32
     lib.ret_gated_delta_step.argtypes = [vp] * 7 + [i32] * 8 + [fl, vp, op]
     lib.ret_gated_delta_step.restype = i32
+    lib.ret_gated_delta_bwd_workspace_bytes.argtypes = [i32] * 7 + [op]
+    lib.ret_gated_delta_bwd_workspace_bytes.restype = sz
+    lib.ret_gated_delta_bwd.argtypes = [vp] * 11 + [i32] * 9 + [fl, vp, vp, vp, vp, vp, sz, vp, op]
+    lib.ret_gated_delta_bwd.restype = i32
     lib.ret_options_default.argtypes = [op]
     lib.ret_options_default.restype = None
     lib.ret_timer_create.restype = vp
@@ -786,6 +790,51 @@ def ret_gated_delta_fwd(q, k, v, g, beta, o, scale=None, lengths=None, state_in=
                                      sp, _options(options))
     _check("ret_gated_delta_fwd", st)
     return o
+
+
+def gated_delta_bwd_workspace(q, v, options=None):
+    """A workspace of ret_gated_delta_bwd_workspace_bytes for these shapes."""
+    B, N, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    nbytes = load().ret_gated_delta_bwd_workspace_bytes(B, N, H, Hk, dk, dv, _dt(q), _options(options))
+    if nbytes == 0:
+        raise ValueError("gated delta gradients: unsupported shape")
+    return torch.empty((nbytes,), dtype=torch.uint8, device=q.device)
+
+
+def ret_gated_delta_bwd(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, scale=None, lengths=None, state_in=None,
+                        dstate_out=None, dstate_in=None, workspace=None, stream=None, options=None):
+    """dq, dk, dv, dg, dbeta (and dstate_in) <- gradients of sum(dout o) (+ sum(dstate_out state_out)) of
+    ret_gated_delta_fwd on the same inputs. dq, dk, dv share one dtype; dg, dbeta have that of g and beta. Without a
+    workspace one is allocated for the call."""
+    lib = load()
+    _delta_qkv(q, k, v, g, beta)
+    B, N, Hk, d_k = q.shape
+    H, d_v = v.shape[2], v.shape[3]
+    for name, t in (("dout", dout), ("dq", dq), ("dk", dk), ("dv", dv), ("dg", dg), ("dbeta", dbeta)):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError("%s must be a tensor" % name)
+    _shape(dout, "dout", v.shape, (q.dtype,))
+    _shape(dq, "dq", q.shape, _IO)
+    _shape(dk, "dk", q.shape, (dq.dtype,))
+    _shape(dv, "dv", v.shape, (dq.dtype,))
+    for name, t in (("dg", dg), ("dbeta", dbeta)):
+        _shape(t, name, g.shape, (g.dtype,))
+    for name, s in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
+        _shape(s, name, (B, H, d_k, d_v), (torch.float32,))
+    _delta_lengths(lengths, B)
+    _same_device(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, lengths, state_in, dstate_out, dstate_in, workspace)
+    _need_gpu(q, "q")
+    guard, sp, workspace = _launch(q, stream, workspace, lambda: gated_delta_bwd_workspace(q, v, options))
+    with guard:
+        st = lib.ret_gated_delta_bwd(_dev(q, "q"), _dev(k, "k"), _dev(v, "v"), _dev(g, "g"), _dev(beta, "beta"),
+                                     _dev(dout, "dout"), _dev(dq, "dq"), _dev(dk, "dk"), _dev(dv, "dv"), _dev(dg, "dg"),
+                                     _dev(dbeta, "dbeta"), B, N, H, Hk, d_k, d_v, _dt(q), _dt(dq), _dt(g),
+                                     _delta_scale(scale), _dev(lengths, "lengths"), _dev(state_in, "state_in"),
+                                     _dev(dstate_out, "dstate_out"), _dev(dstate_in, "dstate_in"),
+                                     _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+    _check("ret_gated_delta_bwd", st)
+    return dq, dk, dv, dg, dbeta
 
 
 def ret_gated_delta_step(q, k, v, g, beta, o, state, scale=None, stream=None, options=None):
