@@ -25,8 +25,11 @@ COMMON = [
     "-mllvm", "-amdgpu-atomic-optimizer-strategy=None",
     "-Wall", "-Wno-unused-function", "-Wno-unused-result",
 ]
-# per-source additions: the wide-head kernel keeps its MFMA accumulators in architectural registers
-EXTRA = {"chunk_wide.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# per-source additions: the wide-head kernel and the gated delta rule's keep their MFMA accumulators in architectural
+# registers (the latter's states are operands and accumulators in turn; and with accumulators in AGPRs this compiler has
+# merged two of delta_prep's LDS stores into one with a wrong offset)
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+EXTRA = {"chunk_wide.hip": VGPR_FORM, "delta_fwd.hip": VGPR_FORM, "delta_bwd.hip": VGPR_FORM}
 NOISE = "'-packed-fp32-ops' is not a recognized feature"
 
 

@@ -5,8 +5,9 @@
 //     A_ij = exp(G_i - G_j) (k_i.k_j) beta_j (j < i),   T = (I + A)^-1,   P_ij = scale exp(G_i - G_j) (q_i.k_j) beta_j (j <= i)
 // the e solve (I + A) E = R, so that everything is products of matrices:
 //     Y = K S_0,  R = V - exp(G) Y,  E = T R,
-//     O = scale exp(G) Q S_0 + P E,         S_C = exp(G_C) S_0 + (exp(G_C - G) beta K)^T E.
-// T and P do not depend on the state: one kernel makes them for every chunk at once (delta_prep). The rest is a chain
+//     O = scale exp(G) Q S_0 + P E,         S_C = exp(G_C) S_0 + K^T diag(exp(G_C - G) beta) E.
+// T and P do not depend on the state: one kernel makes them for every chunk at once (delta_prep); the forward takes
+// Ts = diag(exp(G_C - G) beta) T and P T, so that one operand, R, gives both outputs and the state's update. The rest is a chain
 // over chunks with the state in MFMA accumulators. Columns of S are independent of each other, so each wave owns some of
 // them and no product of the chain leaves its wave: an accumulator tile (column in the lane, rows 4g .. 4g+3 of lane
 // group g) is the other operand of the next product once the reduction index is taken in that order.
@@ -26,7 +27,8 @@ constexpr int kDeltaC = 64;  // tokens per chunk
 // Per (chunk, b, h): fragments of T and P, then per-token factors.
 // Factors of a chunk (rows of 64): exp(G_i), exp(G_C - G_i) beta_i, exp(G_C - G_i), beta_i, then G_i log2(e) in fp64.
 constexpr int kDeltaFac = 6 * kDeltaC;
-constexpr int kDeltaMatBytes = 16384;  // one 64 x 64 matrix as operand fragments (two bf16 parts, or fp32)
+// One triangular 64 x 64 matrix as operand fragments (two bf16 parts, or fp32), those with entries only: bytes reserved.
+constexpr int kDeltaMatBytes = 12288;
 
 struct DeltaArgs {
     const void *q, *k, *v;       // [B, N, Hk, dk], [B, N, H, dv]
@@ -36,7 +38,7 @@ struct DeltaArgs {
     float* state_out;            // [B, H, dk, dv] or null
     void* o;                     // [B, N, H, dv]
     // workspace
-    char* mats;                  // [B*H][nchunks][nmats][kDeltaMatBytes]: T, P (gradients: T, Tr^T, Pr^T)
+    char* mats;                  // [B*H][nchunks][nmats][kDeltaMatBytes]: Ts, P T (gradients: T, Tr^T, Pr^T)
     float* fac;                  // [B*H][nchunks][kDeltaFac] per-token factors
     float* segE;                 // [B*H][nseg][dk][dv]: end states from zero, then the states entering the segments
     float* segM;                 // [B*H][nseg][dk][dk]: transitions
@@ -52,10 +54,21 @@ struct DeltaArgs {
     int nchunks, nmats;
     int nseg, seg_chunks;        // segments per sequence and chunks per segment
     int out_bf16, gate_bf16;
+    int p_lo;                    // the forward's P T has its low part (outputs in fp32)
     float scale;
 };
 typedef void (*delta_kernel_t)(DeltaArgs);
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
+// Which segment and column block a workgroup has. Workgroups go round the 8 XCDs by their index; the column blocks of a
+// segment read the same q, k and matrices, so they get indices 8 apart: one XCD, one L2, one after the other.
+struct DeltaBlock {
+    int bh, seg, cb;
+};
+__device__ __forceinline__ DeltaBlock delta_block(const DeltaArgs& a, int ncb) {
+    const int i = blockIdx.x / 8, unit = i / ncb * 8 + blockIdx.x % 8;
+    return {unit / a.nseg, unit % a.nseg, i % ncb};
+}
 // Live tokens of sequence b.
 __device__ __forceinline__ int delta_len(const DeltaArgs& a, int b) {
     if (!a.lengths) return a.N;
@@ -65,6 +78,28 @@ __device__ __forceinline__ int delta_len(const DeltaArgs& a, int b) {
 __device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
     return bf16 ? bf16_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
 }
+
+// Between LDS accesses of one wave whose lanes read what other lanes wrote: the accesses before are complete, and the
+// compiler moves none across.
+__device__ __forceinline__ void wave_fence() { __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Fragments of a lower triangular 64 x 64 matrix by (row tile m, step s of KS columns), row after row, and those of the
+// transpose of one.
+template <int KS>
+struct TriFrags {
+    static constexpr int NS = kDeltaC / KS, COUNT = NS == 2 ? 6 : 10;
+    __host__ __device__ static constexpr bool lower(int m, int s) { return s * KS <= 16 * m + 15; }
+    __host__ __device__ static constexpr bool upper(int m, int s) { return (s + 1) * KS > 16 * m; }
+    __host__ __device__ static constexpr int at(int m, int s, bool up) {
+        int n = 0;
+        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < NS; ++j) {
+                if (i == m && j == s) return n;
+                if (up ? upper(i, j) : lower(i, j)) ++n;
+            }
+        return n;
+    }
+};
 
 // ---------------------------------------------------------------------------------------------------
 // Operands. KS: reduction length of one step; TPS: accumulator tiles (16 rows) that make one step. In a step lane group g
@@ -116,11 +151,6 @@ struct DOps<BF16> {
         mfma1(acc, a.lo, b.hi);
         mfma1(acc, a.hi, b.hi);
     }
-    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) {
-        mfma1(acc, b.lo, a.hi);
-        mfma1(acc, b.hi, a.lo);
-        mfma1(acc, b.hi, a.hi);
-    }
     // both sides exact
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, Fa a, Fa b) { mfma1(acc, a, b); }
     // a workspace matrix times an exact operand made from accumulator-ordered values
@@ -133,17 +163,23 @@ struct DOps<BF16> {
         mfma1(acc, a.lo, b);
         mfma1(acc, a.hi, b);
     }
-    // fragment f (= row tile * steps + step) of a workspace matrix
+    // what the low part of a workspace matrix adds to b.a^T
+    __device__ static __forceinline__ void mma_lo(f32x4_t& acc, const Fm& a, const Fb& b) { mfma1(acc, b.hi, a.lo); }
+    // fragment f of a workspace matrix
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         const u32x4_t* p = reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane;
         return {__builtin_bit_cast(bf16x8_t, p[0]), __builtin_bit_cast(bf16x8_t, p[64])};
     }
+    // the high part alone
+    __device__ static __forceinline__ Fa mat_frag_hi(const char* m, int f, int lane) {
+        return __builtin_bit_cast(bf16x8_t, (reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane)[0]);
+    }
     // writes the fragment of x: a: the step's first 4 values of this lane, b: its last 4
-    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b) {
+    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b, bool lo) {
         const Fb x = split(a, b);
         u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * 128 + lane;
         p[0] = __builtin_bit_cast(u32x4_t, x.hi);
-        p[64] = __builtin_bit_cast(u32x4_t, x.lo);
+        if (lo) p[64] = __builtin_bit_cast(u32x4_t, x.lo);
     }
     // LDS tile [rows][W], read by rows and transposed
     template <int W>
@@ -155,6 +191,14 @@ struct DOps<BF16> {
         }
         __device__ static __forceinline__ Fa cols(const st* X, int k0, int n0, int lane) {
             return frag_trps<W>(X, k0, n0, Swz<W>::lane_trp(lane));
+        }
+        // rows 16m .. 16m+15, columns n0 .. n0+15 in accumulator order
+        __device__ static __forceinline__ f32x4_t acc(const st* X, int m, int n0, int lane) {
+            typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4_t;
+            st* p = const_cast<st*>(X) + 16 * m * LD + n0 + Swz<W>::lane_trp(lane);
+            const uint2 u = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)p));
+            return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xffff0000u)};
         }
     };
 };
@@ -176,8 +220,8 @@ struct DOps<F32> {
     }
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }
-    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, b, a); }
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, const Fa& a, const Fa& b) { mma_ab(acc, a, b); }
+    __device__ static __forceinline__ void mma_lo(f32x4_t&, const Fm&, const Fb&) {}
     typedef f32x4_t Fx;
     template <int NT>
     __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
@@ -187,6 +231,7 @@ struct DOps<F32> {
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         return reinterpret_cast<const f32x4_t*>(m)[f * 64 + lane];
     }
+    __device__ static __forceinline__ Fa mat_frag_hi(const char* m, int f, int lane) { return mat_frag(m, f, lane); }
     __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a) {
         reinterpret_cast<f32x4_t*>(m)[f * 64 + lane] = a;
     }
@@ -201,28 +246,31 @@ struct DOps<F32> {
             const st* p = X + (k0 + 4 * (lane >> 4)) * LD + n0 + (lane & 15);
             return f32x4_t{p[0], p[LD], p[2 * LD], p[3 * LD]};
         }
+        __device__ static __forceinline__ f32x4_t acc(const st* X, int m, int n0, int lane) {
+            return cols(X, 16 * m, n0, lane);
+        }
     };
 };
 
-// 64 rows of W elements of one head moved as 16-byte segments by 256 threads: rows past the live ones read as zeros
-// (the buffer resource ends with the last live row).
-template <class E, int W>
+// 64 rows of W elements of one head moved as 16-byte segments by NT threads: rows past the live ones read as zeros (the
+// buffer resource ends with the last live row), and so do columns past `cols`. Tile column `at` receives column 0.
+template <class E, int W, int NT, class T = typename DOps<E>::template Tile<W>>
 struct DRows {
     typedef typename E::st st;
-    static constexpr int EPS = 16 / sizeof(st), SPR = W / EPS, RP = kThreads / SPR, NP = (kDeltaC + RP - 1) / RP;
-    typedef typename DOps<E>::template Tile<W> Tile;
+    static constexpr int EPS = 16 / sizeof(st), SPR = W / EPS, RP = NT / SPR, NP = (kDeltaC + RP - 1) / RP;
+    typedef T Tile;
     u32x4_t x[NP];
     // p: the head's row of the chunk's first token; stride: elements between tokens; live: rows to read (may be <= 0)
-    __device__ __forceinline__ void load(const st* p, int stride, int live, int tid) {
-        const int bytes = live > 0 ? ((live - 1) * stride + W) * (int)sizeof(st) : 0;
+    __device__ __forceinline__ void load(const st* p, int stride, int live, int cols, int tid) {
+        const int bytes = live > 0 ? ((live - 1) * stride + cols) * (int)sizeof(st) : 0;
         const rsrc_t r = bytes_rsrc(p, bytes);
         const int row = tid / SPR, c = tid % SPR * EPS;
+        const int off = c < cols ? (row * stride + c) * (int)sizeof(st) : 0x40000000;
 #pragma unroll
-        for (int i = 0; i < NP; ++i)
-            x[i] = buf_load16(r, (row * stride + c) * (int)sizeof(st), i * RP * stride * (int)sizeof(st));
+        for (int i = 0; i < NP; ++i) x[i] = buf_load16(r, off, i * RP * stride * (int)sizeof(st));
     }
-    __device__ __forceinline__ void store(st* lds, int tid) const {
-        const int row = tid / SPR, c = tid % SPR * EPS;
+    __device__ __forceinline__ void store(st* lds, int tid, int at = 0) const {
+        const int row = tid / SPR, c = at + tid % SPR * EPS;
 #pragma unroll
         for (int i = 0; i < NP; ++i)
             if (NP * RP == kDeltaC || row + i * RP < kDeltaC)
@@ -230,11 +278,31 @@ struct DRows {
     }
 };
 
+// A chunk's outputs, 4 consecutive columns of one token per lane (tile m: token 16 m + lane % 16), through a buffer
+// resource that ends with the sequence's last row: rows past it are dropped.
+struct DOut {
+    rsrc_t r;
+    int off, stride;  // bytes: this lane's place, and one token
+    __device__ __forceinline__ void init(void* base, long long row0, int rows, int H, int dv, int esz, int col, int lane) {
+        stride = H * dv * esz;
+        r = bytes_rsrc((char*)base + row0 * dv * esz, (rows - 1) * stride + dv * esz);
+        off = (lane & 15) * stride + col * esz;
+    }
+    __device__ __forceinline__ void put(uint16_t*, int m, int n, f32x4_t x) const {
+        __builtin_amdgcn_raw_buffer_store_b64(
+            __builtin_bit_cast(u32x2_t, make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]))), r, off + 32 * n,
+            16 * m * stride, 0);
+    }
+    __device__ __forceinline__ void put(float*, int m, int n, f32x4_t x) const {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), r, off + 64 * n, 16 * m * stride, 0);
+    }
+};
+
 // ---- kernel selection ----
 struct DeltaKernels {
-    delta_kernel_t prep, local, full, scan;
-    delta_kernel_t bprep, states, rlocal, rscan, rfull, grad;  // gradients
-    int cols;          // columns of d_v (or of a transition) per workgroup
+    delta_kernel_t prep, local, full, full_f32, scan;  // full_f32: F32 output
+    delta_kernel_t bprep, blocal, states, rlocal, rscan, rfull, grad;  // gradients
+    int cols, threads; // columns of d_v (or of a transition) and threads per workgroup of the chains
     int grad_threads;
 };
 // d_k in {32, 64, 128, 256} for bf16 and {16, 32, 64, 128} for fp32; false otherwise.

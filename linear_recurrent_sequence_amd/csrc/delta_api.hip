@@ -74,7 +74,7 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
     int n = 1;
     if (op.segments > 0) n = op.segments;
-    else if (units <= 96) n = (int)(256 / units);
+    else if (units <= 192) n = (int)(512 / units);
     if (op.segments <= 0 && n > p.nchunks / 4) n = p.nchunks / 4;  // at least 4 chunks a segment
     if (n > p.nchunks) n = p.nchunks;
     if (n < 1) n = 1;
@@ -123,6 +123,7 @@ void fill(DeltaArgs& A, const Shape& s, const Plan& p, bool bwd, void* workspace
     A.dut = (char*)workspace + p.dut;
     A.out_bf16 = out_dt == RET_BF16;
     A.gate_bf16 = gate_dt == RET_BF16;
+    A.p_lo = out_dt == RET_F32;
     A.scale = scale_of(scale, s.dk);
 }
 
@@ -193,14 +194,14 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     A.state_out = state_out;
     hipStream_t str = (hipStream_t)stream;
     if ((st = launch("ret_delta_prep", kn.prep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
-    const unsigned nc = blocks(dv, kn.cols);
+    const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local", kn.local, dim3(B * H * p.nseg, nc + blocks(dk, kn.cols)), str, op, A)) !=
+        if ((st = launch("ret_delta_local", kn.local, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
             RET_OK)
             return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A, 4 * dk)) != RET_OK) return st;
     }
-    return launch("ret_delta_full", kn.full, dim3(B * H * p.nseg, nc), str, op, A);
+    return launch("ret_delta_full", out_dt == RET_BF16 ? kn.full : kn.full_f32, dim3(units * nc), str, op, A, kn.threads);
 }
 
 size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
@@ -260,18 +261,19 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
     A.dbeta = dbeta;
     hipStream_t str = (hipStream_t)stream;
     if ((st = launch("ret_delta_prep", kn.bprep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
-    const unsigned nc = blocks(dv, kn.cols), units = B * H * p.nseg;
+    const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local", kn.local, dim3(units, nc + blocks(dk, kn.cols)), str, op, A)) != RET_OK)
+        if ((st = launch("ret_delta_local", kn.blocal, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
+            RET_OK)
             return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, dv / 16), str, op, A, 4 * dk)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_states", kn.states, dim3(units, nc), str, op, A)) != RET_OK) return st;
+    if ((st = launch("ret_delta_states", kn.states, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local_bwd", kn.rlocal, dim3(units, nc), str, op, A)) != RET_OK) return st;
-        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, dv / 16), str, op, A)) != RET_OK) return st;
+        if ((st = launch("ret_delta_local_bwd", kn.rlocal, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, dv / 16), str, op, A, 4 * dk)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units, nc), str, op, A)) != RET_OK) return st;
+    if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
     return launch("ret_delta_grad", kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
 }
 

@@ -26,23 +26,39 @@ typedef double f64;
 // of the state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise
 // dS_C of each chunk and dU, transposed, and dV; the first segment leaves dstate_in.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NC, bool LOCAL>
-__global__ __launch_bounds__(kThreads) void delta_rchain_kernel(DeltaArgs a) {
+template <class E, int DK, int NC, int NW>
+constexpr int rchain_waves() {  // as the forward chain's
+    typedef DOps<E> D;
+    const int rows = kDeltaC * (int)sizeof(typename E::st);
+    const int lds = rows * (3 * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 2048;
+    return NW == 8 || (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
+}
+template <class E, int DK, int NC, int NW, bool LOCAL>
+__global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delta_rchain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    typedef DRows<E, DK> Rows;
+    constexpr int NT = 64 * NW, COLS = 16 * NC * NW;
+    typedef DRows<E, DK, NT> Rows;
+    typedef DRows<E, 16 * NC, 64, typename D::template Tile<COLS>> ORows;  // a wave's own columns of dO
     typedef typename Rows::Tile Tile;
-    constexpr int DT = DK / 16, NS = kDeltaC / D::KS;
-    __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
+    typedef typename ORows::Tile OTile;
+    typedef TriFrags<D::KS> F;
+    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS;
+    constexpr int MB = NC == 2 ? 2 : 4, MG = 4 / MB, TB = DT < MB ? DT : MB;
+    __shared__ __align__(16) st sk[2][kDeltaC * Tile::LD];
     __shared__ __align__(16) st sq[kDeltaC * Tile::LD];
-    __shared__ __align__(16) float sf[256];
+    __shared__ __align__(16) st so[kDeltaC * OTile::LD];
+    __shared__ __align__(16) float sf[2][256];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, b = bh / a.H, h = bh % a.H;
-    const int col0 = (int)blockIdx.y * 64 * NC + w * 16 * NC;
+    const DeltaBlock blk = delta_block(a, (a.dv + COLS - 1) / COLS);
+    if (blk.bh >= a.B * a.H) return;
+    const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
+    const int mine = 16 * NC * w, col0 = blk.cb * COLS + mine;  // the wave's columns: in the tile, of d_v
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const bool active = col0 < a.dv;
     if (LOCAL && seg == 0) return;  // no one is left of it
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
     f32x4_t S[NC][DT];
     const float* sin = nullptr;
@@ -51,188 +67,252 @@ __global__ __launch_bounds__(kThreads) void delta_rchain_kernel(DeltaArgs a) {
     else if (!LOCAL) sin = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-        const int col = col0 + 16 * n + n16;
+        const bool in = sin && col0 + 16 * n < a.dv;
+        const float* p = in ? sin + (long long)g4 * a.dv + col0 + 16 * n + n16 : nullptr;
 #pragma unroll
-        for (int t = 0; t < DT; ++t)
+        for (int t = 0; t < DT; ++t) S[n][t] = zero;
+        if (in)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[n][t][i] = sin && col0 + 16 * n < a.dv ? sin[(long long)(16 * t + g4 + i) * a.dv + col] : 0.f;
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[n][t][i] = p[(long long)(16 * t + i) * a.dv];
     }
     Rows rk, rq;
+    ORows ro;
     float ff = 0.f;
     const st* kp = (const st*)a.k + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* qp = (const st*)a.q + (((long long)b * a.N) * a.Hk + hk) * DK;
+    const st* op = (const st*)a.dout + (((long long)b * a.N) * a.H + h) * a.dv + col0;
     auto fetch = [&](int c) {
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
-        rk.load(kp + base, a.Hk * DK, live, tid);
-        rq.load(qp + base, a.Hk * DK, live, tid);
-        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
+        rk.load(kp + base, a.Hk * DK, live, DK, tid);
+        if (tid < 256) ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
+        rq.load(qp + base, a.Hk * DK, live, DK, tid);
+        if (active) ro.load(op + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, live, a.dv - col0, lane);
     };
-    // dV of padding chunks is zero
-    auto store_dv = [&](int c, int m, int n, const f32x4_t& x) {
+    // Rows of dV of chunk c, 16 bytes a lane, from the wave's own columns of the tile that held dO (zero: zeros); rows past
+    // the live ones are zero. 32-bit outputs go from the registers.
+    constexpr int SPV = 2 * NC;  // 16-byte segments per row of the wave's columns
+    auto store_rows = [&](int c, bool blank) {
+#pragma unroll
+        for (int i = 0; i < SPV; ++i) {
+            const int row = (lane + 64 * i) / SPV, cc = (lane + 64 * i) % SPV * 8, t = c * kDeltaC + row;
+            if (t >= a.N || col0 + cc >= a.dv) continue;
+            u32x4_t x = {0, 0, 0, 0};
+            if (!blank && t < len) x = *reinterpret_cast<const u32x4_t*>(so + OTile::off(row, mine + cc));
+            *reinterpret_cast<u32x4_t*>((uint16_t*)a.dv_ + (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + cc) = x;
+        }
+    };
+    auto store_f32 = [&](int c, int m, int n, const f32x4_t& x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = c * kDeltaC + 16 * m + g4 + i;
-            if (t >= a.N) continue;
-            const long long e = (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + n16;
-            const float y = t < len ? x[i] : 0.f;
-            if (a.out_bf16) ((uint16_t*)a.dv_)[e] = f32_to_bf16(y);
-            else ((float*)a.dv_)[e] = y;
+            if (t >= a.N || col0 + 16 * n >= a.dv) continue;
+            ((float*)a.dv_)[(((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + n16] = t < len ? x[i] : 0.f;
         }
     };
     const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
     if constexpr (!LOCAL) {
         if (active)
-            for (int c = max(c0, cend); c < c1; ++c)
+            for (int c = max(c0, cend); c < c1; ++c) {  // dV of padding chunks is zero
+                if (a.out_bf16) store_rows(c, true);
+                else
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    if (col0 + 16 * n < a.dv)
+                    for (int n = 0; n < NC; ++n)
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) store_dv(c, m, n, f32x4_t{0.f, 0.f, 0.f, 0.f});
+                        for (int m = 0; m < 4; ++m) store_f32(c, m, n, zero);
+            }
     }
-    if (c0 < cend) fetch(cend - 1);
-    for (int c = cend - 1; c >= c0; --c) {
-        __syncthreads();
-        rk.store(sk, tid);
+    if (c0 < cend) {
+        fetch(cend - 1);
+        rk.store(sk[0], tid);
         rq.store(sq, tid);
-        sf[tid] = ff;
+        if (active) ro.store(so, lane, mine);
+        if (tid < 256) sf[0][tid] = ff;
+    }
+    for (int c = cend - 1, p = 0; c >= c0; --c, p ^= 1) {
         __syncthreads();
-        if (c > c0) fetch(c - 1);
-        if (!active) continue;
-        const int live = min(kDeltaC, len - c * kDeltaC);
+        const bool more = c > c0;
+        if (more) fetch(c - 1);
         const long long unit = (long long)bh * a.nchunks + c;
         const char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
-        // dO in accumulator order: lane's column, tokens 16 m + 4 g + i
-        f32x4_t d[NC][4];
-        {
-            const int stride = a.H * a.dv;
-            const st* dp = (const st*)a.dout + (((long long)b * a.N + c * kDeltaC) * a.H + h) * a.dv;
-            const rsrc_t r = bytes_rsrc(dp, ((live - 1) * stride + a.dv) * (int)sizeof(st));
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int off = col0 + 16 * n < a.dv ? (g4 * stride + col0 + 16 * n + n16) * (int)sizeof(st)
-                                                             : 0x40000000;
-                        const int so = (16 * m + i) * stride * (int)sizeof(st);
-                        if constexpr (sizeof(st) == 2)
-                            d[n][m][i] = bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0));
-                        else d[n][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
-                    }
-        }
-        if constexpr (!LOCAL) {
-            st* sp = (st*)a.ds1t + unit * a.dv * DK;
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-                if (col0 + 16 * n < a.dv)
-#pragma unroll
-                    for (int t = 0; t < DT; ++t) store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
-        }
-        // W = exp(G_C - G) K dS + Pr^T dO
+        const st* K = sk[p];
         f32x4_t x[NC][4];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) x[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int m = 0; m < 4; ++m) x[n][m] = zero;
+        if (active) {
+            if constexpr (!LOCAL) {
+                st* sp = (st*)a.ds1t + unit * a.dv * DK;
 #pragma unroll
-        for (int s = 0; s < DK / D::KS; ++s) {
+                for (int n = 0; n < NC; ++n)
+                    if (col0 + 16 * n < a.dv)
+#pragma unroll
+                        for (int t = 0; t < DT; ++t)
+                            store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
+            }
+            // W = exp(G_C - G) K dS + Pr^T dO
+            typename D::Fa fk[2][MB];
             typename D::Fb fs[NC];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
+            for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+#pragma unroll
+            for (int i = 0; i < KN * MG; ++i) {
+                const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
+                if (i + 1 < KN * MG)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
+                if (m0 == 0)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) D::mma_ab(x[n][m0 + m], fk[i & 1][m], fs[n]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const typename D::Fa fk = Tile::rows(sk, 16 * m, s * D::KS, lane);
+                const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf[p] + 128 + 16 * m + g4);
 #pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_ab(x[n][m], fk, fs[n]);
+                for (int n = 0; n < NC; ++n) x[n][m] *= ta;
+            }
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                typename D::Fa fd[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) fd[n] = OTile::cols(so, s * D::KS, mine + 16 * n, lane);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (F::upper(m, s)) {
+                        const typename D::Fm fp = D::mat_frag(mats + 2 * kDeltaMatBytes, F::at(m, s, true), lane);
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp, fd[n]);
+                    }
             }
         }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf + 128 + 16 * m + g4);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) x[n][m] *= ta;
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+            rk.store(sk[p ^ 1], tid);
+            if (tid < 256) sf[p ^ 1][tid] = ff;
         }
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            typename D::Fx fd[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) fd[n] = D::step_exact(d[n], s);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if ((s + 1) * D::KS <= 16 * m) continue;  // below the diagonal of a transpose
-                const typename D::Fm fp = D::mat_frag(mats + 2 * kDeltaMatBytes, m * NS + s, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp, fd[n]);
-            }
-        }
-        // dU = Tr^T W
+        __builtin_amdgcn_sched_barrier(0);
         f32x4_t u[NC][4];
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) u[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            typename D::Fb fw[NC];
-#pragma unroll
-            for (int n = 0; n < NC; ++n) fw[n] = D::step(x[n], s);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if ((s + 1) * D::KS <= 16 * m) continue;
-                const typename D::Fm ft = D::mat_frag(mats + kDeltaMatBytes, m * NS + s, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fw[n]);
-            }
-        }
-        if constexpr (!LOCAL) {
-            st* up = (st*)a.dut + unit * a.dv * kDeltaC;
+        const float end = sf[p][63];
+        if (active) {
+            // dU = Tr^T W
 #pragma unroll
             for (int n = 0; n < NC; ++n)
-                if (col0 + 16 * n < a.dv)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) u[n][m] = zero;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                typename D::Fb fw[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) fw[n] = D::step(x[n], s);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (F::upper(m, s)) {
+                        const typename D::Fm ft = D::mat_frag(mats + kDeltaMatBytes, F::at(m, s, true), lane);
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fw[n]);
+                    }
+            }
+            // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const f32x4_t ga = a.scale * *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) x[n][m] = ga * OTile::acc(so, m, mine + 16 * n, lane);
+            }
+            typename D::Fb fd[NC][NS];
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int s = 0; s < NS; ++s) fd[n][s] = D::step(x[n], s);
+            typename D::Fa fc[2][TB];
+#pragma unroll
+            for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(sq, 0, 16 * t, lane);
+#pragma unroll
+            for (int i = 0; i < NS * DT / TB; ++i) {
+                const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
+                if (i + 1 < NS * DT / TB)
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(sq, s1 * D::KS, 16 * (t1 + t), lane);
+                if (s == 0)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n)
+#pragma unroll
+                        for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fd[n][s]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (!LOCAL) {
+                wave_fence();  // the last reads of dO come before
+                st* up = (st*)a.dut + unit * a.dv * kDeltaC;
+                const bool rows = sizeof(st) == 2 && a.out_bf16;
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) {
-                        store4(up + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
-                        const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf + 192 + 16 * m + g4);
-                        store_dv(c, m, n, be * u[n][m]);
+                        if (col0 + 16 * n < a.dv) store4(up + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
+                        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4) * u[n][m];
+                        if constexpr (sizeof(st) == 2) {
+                            if (rows) {  // over dO, in the wave's own columns
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const int col = mine + 16 * n + n16;
+                                    so[OTile::off(16 * m + g4 + i, col & ~3) + (col & 3)] = f32_to_bf16(y[i]);
+                                }
+                            }
+                        }
+                        if (!rows) store_f32(c, m, n, y);
                     }
-        }
-        // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
-        const float end = sf[63];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf + 16 * m + g4);
-            const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf + 192 + 16 * m + g4);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                d[n][m] *= a.scale * ga;
-                u[n][m] *= -(ga * be);
+                if (rows) {
+                    wave_fence();  // the rows are read in another order
+                    store_rows(c, false);
+                    wave_fence();
+                }
             }
         }
+        if (more) {
+            __syncthreads();  // everyone is done with Q
+            rq.store(sq, tid);
+            if (active) ro.store(so, lane, mine);
+        }
+        if (!active) continue;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
+            const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) u[n][m] *= -(ga * be);
+        }
+        typename D::Fb fu[NC][NS];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int t = 0; t < DT; ++t) S[n][t] *= end;
+            for (int s = 0; s < NS; ++s) fu[n][s] = D::step(u[n], s);
+        typename D::Fa fc[2][TB];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            typename D::Fb fu[NC], fd[NC];
+        for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, 16 * t, lane);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                fu[n] = D::step(u[n], s);
-                fd[n] = D::step(d[n], s);
-            }
+        for (int i = 0; i < NS * DT / TB; ++i) {
+            const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
+            if (i + 1 < NS * DT / TB)
 #pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                const typename D::Fa fk = Tile::cols(sk, s * D::KS, 16 * t, lane);
-                const typename D::Fa fq = Tile::cols(sq, s * D::KS, 16 * t, lane);
+                for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
 #pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    D::mma_ab(S[n][t], fk, fu[n]);
-                    D::mma_ab(S[n][t], fq, fd[n]);
-                }
-            }
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!active) return;
@@ -243,10 +323,11 @@ __global__ __launch_bounds__(kThreads) void delta_rchain_kernel(DeltaArgs a) {
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         if (col0 + 16 * n >= a.dv) continue;
+        float* p = out + (long long)g4 * a.dv + col0 + 16 * n + n16;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[(long long)(16 * t + g4 + i) * a.dv + col0 + 16 * n + n16] = S[n][t][i];
+            for (int i = 0; i < 4; ++i) p[(long long)(16 * t + i) * a.dv] = S[n][t][i];
     }
 }
 
@@ -514,12 +595,13 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
     constexpr int NW = DK * sizeof(typename E::st) > 256 ? 8 : 4;  // half of d_k per wave where a row is long
-    if (dv > 64) {
-        o->rlocal = delta_rchain_kernel<E, DK, 2, true>;
-        o->rfull = delta_rchain_kernel<E, DK, 2, false>;
+    constexpr bool WIDE = DK * sizeof(typename E::st) >= 256;
+    if (o->cols == 64) {
+        o->rlocal = delta_rchain_kernel<E, DK, 1, 4, true>;
+        o->rfull = delta_rchain_kernel<E, DK, 1, 4, false>;
     } else {
-        o->rlocal = delta_rchain_kernel<E, DK, 1, true>;
-        o->rfull = delta_rchain_kernel<E, DK, 1, false>;
+        o->rlocal = delta_rchain_kernel<E, DK, WIDE ? 1 : 2, WIDE ? 8 : 4, true>;
+        o->rfull = delta_rchain_kernel<E, DK, WIDE ? 1 : 2, WIDE ? 8 : 4, false>;
     }
     o->grad = delta_grad_kernel<E, DK, NW>;
     o->grad_threads = 64 * NW;

@@ -1,6 +1,8 @@
 // The gated delta rule over a sequence: the per-chunk matrices, the chain over chunks, and the chain over segments.
 #include "delta.h"
 
+#include <type_traits>
+
 namespace ret {
 
 namespace {
@@ -34,20 +36,23 @@ __device__ __forceinline__ void tri_store(float* X, int r0, int c0, int lane, f3
     for (int i = 0; i < 4; ++i) p[i * kTriLD] = v[i];
 }
 
-// Writes a 64 x 64 fp32 LDS matrix (or its transpose) as operand fragments, two row tiles' worth of work per wave pair.
+// Writes a lower triangular 64 x 64 fp32 LDS matrix (or its transpose) as operand fragments, a row tile per wave, this
+// lane's row (16 w + lane % 16) times `scale`.
 template <class E, bool TR>
-__device__ __forceinline__ void write_mat(char* m, const float* X, int w, int lane) {
+__device__ __forceinline__ void write_mat(char* m, const float* X, int w, int lane, bool lo, float scale = 1.f) {
     typedef DOps<E> D;
-    constexpr int NS = kDeltaC / D::KS;
+    typedef TriFrags<D::KS> F;
     const int r = 16 * w + (lane & 15), g4 = 4 * (lane >> 4);
     auto take = [&](int c) {
         if constexpr (!TR) return *reinterpret_cast<const f32x4_t*>(X + r * kTriLD + c);
         else return f32x4_t{X[c * kTriLD + r], X[(c + 1) * kTriLD + r], X[(c + 2) * kTriLD + r], X[(c + 3) * kTriLD + r]};
     };
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        if constexpr (D::TPS == 2) D::mat_store(m, w * NS + s, lane, take(32 * s + g4), take(32 * s + 16 + g4));
-        else D::mat_store(m, w * NS + s, lane, take(16 * s + g4));
+    for (int s = 0; s < F::NS; ++s) {
+        if (TR ? !F::upper(w, s) : !F::lower(w, s)) continue;
+        const int f = F::at(w, s, TR);
+        if constexpr (D::TPS == 2) D::mat_store(m, f, lane, scale * take(32 * s + g4), scale * take(32 * s + 16 + g4), lo);
+        else D::mat_store(m, f, lane, scale * take(16 * s + g4));
     }
 }
 
@@ -104,7 +109,7 @@ __device__ __forceinline__ void tri_inverse(const float* sA, float* sT, int w, i
 template <class E, int DK, bool BWD>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     typedef typename E::st st;
-    typedef DRows<E, DK> Rows;
+    typedef DRows<E, DK, kThreads> Rows;
     typedef typename Rows::Tile Tile;
     typedef DOps<E> D;
     __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
@@ -112,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     __shared__ __align__(16) float sA[kDeltaC * kTriLD];
     __shared__ __align__(16) float sT[kDeltaC * kTriLD];
     __shared__ f64 sG[kDeltaC];
-    __shared__ float sB[kDeltaC];
+    __shared__ float sB[kDeltaC], sF[kDeltaC];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g = lane >> 4;
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
     const int t0 = c * kDeltaC, live = min(kDeltaC, delta_len(a, b) - t0);
@@ -120,8 +125,8 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     {
         Rows rk, rq;
         const long long base = (((long long)b * a.N + t0) * a.Hk + hk) * DK;
-        rk.load((const st*)a.k + base, a.Hk * DK, live, tid);
-        rq.load((const st*)a.q + base, a.Hk * DK, live, tid);
+        rk.load((const st*)a.k + base, a.Hk * DK, live, DK, tid);
+        rq.load((const st*)a.q + base, a.Hk * DK, live, DK, tid);
         rk.store(sk, tid);
         rq.store(sq, tid);
     }
@@ -164,35 +169,35 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
             float* f = a.fac + unit * kDeltaFac;
             const float tail = __builtin_amdgcn_exp2f((float)(__shfl(G, 63) - G));
             f[lane] = __builtin_amdgcn_exp2f((float)G);
-            f[64 + lane] = tail * be;
+            f[64 + lane] = sF[lane] = tail * be;
             f[128 + lane] = tail;
             f[192 + lane] = be;
             reinterpret_cast<f64*>(f + 256)[lane] = G;
         }
         __syncthreads();
         char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
-        // A into sA; P into sT until it is written out (the gradients take P without beta)
+        f32x4_t pv[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4_t pv;
             const int col = 16 * j + n16;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int row = 16 * w + 4 * g + i;
                 const float d = col <= row ? __builtin_amdgcn_exp2f((float)(sG[row] - sG[col])) : 0.f;
                 av[j][i] = col < row ? d * kk[j][i] : 0.f;
-                pv[i] = col <= row ? a.scale * (BWD ? 1.f : sB[col]) * d * qk[j][i] : 0.f;
+                pv[j][i] = col <= row ? a.scale * d * qk[j][i] : 0.f;
             }
             tri_store(sA, 16 * w, 16 * j, lane, av[j] * sB[col]);
-            tri_store(sT, 16 * w, 16 * j, lane, pv);
+            if constexpr (BWD) tri_store(sT, 16 * w, 16 * j, lane, pv[j]);  // until it is written out
         }
         __syncthreads();
-        if constexpr (BWD) write_mat<E, true>(mats + 2 * kDeltaMatBytes, sT, w, lane);
-        else write_mat<E, false>(mats + kDeltaMatBytes, sT, w, lane);
-        __syncthreads();
-        tri_inverse(sA, sT, w, lane);
-        write_mat<E, false>(mats, sT, w, lane);
         if constexpr (BWD) {
+            write_mat<E, true>(mats + 2 * kDeltaMatBytes, sT, w, lane, true);
+            __syncthreads();
+        }
+        tri_inverse(sA, sT, w, lane);
+        if constexpr (BWD) {
+            write_mat<E, false>(mats, sT, w, lane, true);
             // Tr = (I + Ar)^-1 with beta along the rows: the gradients' solve
             __syncthreads();
 #pragma unroll
@@ -204,7 +209,26 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
             }
             __syncthreads();
             tri_inverse(sA, sT, w, lane);
-            write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane);
+            write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane, true);
+        } else {
+            // P T: row tile w through sA (its own rows only), and T with its rows scaled
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pv[j] * sB[16 * j + n16]);
+            __syncthreads();
+            f32x4_t pt[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                pt[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = j; i < 4; ++i)
+                    if (i <= w) DOps<F32>::mma_ab(pt[j], tri_a(sA, 16 * w, 16 * i, lane), tri_b(sT, 16 * i, 16 * j, lane));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pt[j]);
+            __syncthreads();
+            write_mat<E, false>(mats + kDeltaMatBytes, sA, w, lane, a.p_lo);
+            write_mat<E, false>(mats, sT, w, lane, true, sF[16 * w + n16]);
         }
         __syncthreads();
     }
@@ -215,29 +239,56 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
 // LOCAL: the segment's end state from zero (columns of V; segment 0 starts from state_in) or its transition (columns of
 // the identity, V = 0), into segE / segM. Otherwise the outputs, and after the last segment the final state.
 // ---------------------------------------------------------------------------------------------------
-enum { kFull = 0, kLocal = 1, kStates = 2 };
-template <class E, int DK, int NC, int MODE>
-__global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
+// A step's order keeps registers few and every latency behind work: the next chunk's rows are requested first; Y and R;
+// then K and V of the next chunk go to LDS (K has two buffers; a wave stages the columns of V it owns, so no one else
+// reads them); Q S; a barrier frees Q's buffer; O; E; the state. Fragments of one reduction
+// step are read while the products of the step before run.
+// kFull: outputs (bf16 from bf16 input, else fp32); kFullF32: BF16 input, F32 output; kLocal / kLocalRaw: end state or
+// transition, with Ts / with T; kStates: with T, the states entering the chunks and E, for the gradients.
+enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
+// Waves per SIMD that the LDS leaves room for (at most 2: the state and the fragments in flight take half the registers).
+template <class E, int DK, int NC, int NW, int MODE>
+constexpr int chain_waves() {
+    typedef DOps<E> D;
+    const int rows = kDeltaC * (int)sizeof(typename E::st);
+    const int lds = rows * ((MODE <= kFullF32 ? 3 : 2) * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 1024;
+    return NW == 8 || (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
+}
+template <class E, int DK, int NC, int NW, int MODE>
+__global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void delta_chain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    typedef DRows<E, DK> Rows;
+    constexpr int NT = 64 * NW, COLS = 16 * NC * NW;
+    typedef DRows<E, DK, NT> Rows;
+    typedef DRows<E, 16 * NC, 64, typename D::template Tile<COLS>> VRows;  // a wave's own columns
     typedef typename Rows::Tile Tile;
-    constexpr bool LOCAL = MODE == kLocal, FULL = MODE == kFull;
-    constexpr int DT = DK / 16, NS = kDeltaC / D::KS;
-    __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
+    typedef typename VRows::Tile VTile;
+    typedef TriFrags<D::KS> F;
+    constexpr bool LOCAL = MODE == kLocal || MODE == kLocalRaw, FULL = MODE == kFull || MODE == kFullF32;
+    constexpr bool RAW = MODE == kLocalRaw || MODE == kStates;
+    constexpr bool HI = MODE == kFull && sizeof(st) == 2;  // outputs in bf16: the high parts of S and P T suffice, whose
+                                                           // rounding is like the output's own
+    typedef typename std::conditional<HI, uint16_t, float>::type out_t;
+    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS;
+    constexpr int MB = NC == 2 ? 2 : 4, MG = 4 / MB;  // token tiles whose fragments are read together: 8 products' worth
+    __shared__ __align__(16) st sk[2][kDeltaC * Tile::LD];
     __shared__ __align__(16) st sq[FULL ? kDeltaC * Tile::LD : 16];
-    __shared__ __align__(16) float sf[128];
+    __shared__ __align__(16) st sv[kDeltaC * VTile::LD];
+    __shared__ __align__(16) float sf[2][128];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int bh = blockIdx.x / a.nseg, seg = blockIdx.x % a.nseg, b = bh / a.H, h = bh % a.H;
-    const int nE = (a.dv + 64 * NC - 1) / (64 * NC);  // workgroups over d_v; a local pass has those of d_k behind them
-    const bool trans = LOCAL && (int)blockIdx.y >= nE;
+    const int nE = (a.dv + COLS - 1) / COLS;  // workgroups over d_v; a local pass has those of d_k behind them
+    const DeltaBlock blk = delta_block(a, nE + (LOCAL ? (DK + COLS - 1) / COLS : 0));
+    if (blk.bh >= a.B * a.H) return;
+    const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
+    const bool trans = LOCAL && blk.cb >= nE;
     const int width = trans ? DK : a.dv;
-    const int col0 = ((int)blockIdx.y - (trans ? nE : 0)) * 64 * NC + w * 16 * NC;
+    const int col0 = (blk.cb - (trans ? nE : 0)) * COLS + w * 16 * NC;
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const bool active = col0 < width;
     // segment 0's end state is known, and no one asks for the last one's
     if (LOCAL && (trans ? seg == 0 : seg == a.nseg - 1)) return;
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
     f32x4_t S[NC][DT];
     const float* sin = nullptr;
@@ -247,119 +298,200 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         const int col = col0 + 16 * n + n16;
+        const bool in = sin && col0 + 16 * n < width;
+        const float* p = in ? sin + (long long)g4 * a.dv + col : nullptr;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 16 * t + g4 + i;
-                float x = trans && row == col ? 1.f : 0.f;
-                if (sin && col0 + 16 * n < width) x = sin[(long long)row * a.dv + col];
-                S[n][t][i] = x;
-            }
+            for (int i = 0; i < 4; ++i) S[n][t][i] = trans && 16 * t + g4 + i == col ? 1.f : 0.f;
+        if (in)
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[n][t][i] = p[(long long)(16 * t + i) * a.dv];
     }
 
     Rows rk, rq;
+    VRows rv;
     float ff = 0.f;
     const st* kp = (const st*)a.k + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* qp = (const st*)a.q + (((long long)b * a.N) * a.Hk + hk) * DK;
+    const st* vp = (const st*)a.v + (((long long)b * a.N) * a.H + h) * a.dv + col0;
     auto fetch = [&](int c) {
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
-        rk.load(kp + base, a.Hk * DK, live, tid);
-        if constexpr (FULL) rq.load(qp + base, a.Hk * DK, live, tid);
+        rk.load(kp + base, a.Hk * DK, live, DK, tid);
+        if (!trans && active) rv.load(vp + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, live, a.dv - col0, lane);
+        if constexpr (FULL) rq.load(qp + base, a.Hk * DK, live, DK, tid);
         if (tid < 128) ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
     };
+    auto stage = [&](int p) {
+        rk.store(sk[p], tid);
+        if (!trans && active) rv.store(sv, lane, 16 * NC * w);
+        if (tid < 128) sf[p][tid] = ff;
+    };
     const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
-    if (c0 < cend) fetch(c0);
-    for (int c = c0; c < cend; ++c) {
-        __syncthreads();
-        rk.store(sk, tid);
+    if (c0 < cend) {
+        fetch(c0);
+        stage(0);
         if constexpr (FULL) rq.store(sq, tid);
-        if (tid < 128) sf[tid] = ff;
+    }
+    for (int c = c0, p = 0; c < cend; ++c, p ^= 1) {
         __syncthreads();
-        if (c + 1 < cend) fetch(c + 1);
-        if (!active) continue;
-        const int live = min(kDeltaC, len - c * kDeltaC);
+        const bool more = c + 1 < cend;
+        if (more) fetch(c + 1);
         const char* mats = a.mats + ((long long)bh * a.nchunks + c) * a.nmats * kDeltaMatBytes;
-        // V in accumulator order: lane's column, tokens 16 m + 4 g + i
-        float v[NC][4][4];
-        if (!trans) {
-            const int stride = a.H * a.dv;
-            const st* vp = (const st*)a.v + (((long long)b * a.N + c * kDeltaC) * a.H + h) * a.dv;
-            const rsrc_t r = bytes_rsrc(vp, ((live - 1) * stride + a.dv) * (int)sizeof(st));
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int off = col0 + 16 * n < width ? (g4 * stride + col0 + 16 * n + n16) * (int)sizeof(st)
-                                                              : 0x40000000;
-                        const int so = (16 * m + i) * stride * (int)sizeof(st);
-                        if constexpr (sizeof(st) == 2)
-                            v[n][m][i] = bf16_to_f32((uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, so, 0));
-                        else v[n][m][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, so, 0));
-                    }
-        }
-        // Y = K S, and (Q S)^T beside it
-        f32x4_t y[NC][4], o[NC][4];
+        const st* K = sk[p];
+        f32x4_t y[NC][4];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) y[n][m] = o[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int m = 0; m < 4; ++m) y[n][m] = zero;
+        if (active) {
+            if constexpr (MODE == kStates) {
+                st* sp = (st*)a.s0t + ((long long)bh * a.nchunks + c) * a.dv * DK;
 #pragma unroll
-        for (int s = 0; s < DK / D::KS; ++s) {
+                for (int n = 0; n < NC; ++n)
+                    if (col0 + 16 * n < width)
+#pragma unroll
+                        for (int t = 0; t < DT; ++t)
+                            store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
+            }
+            // Y = K S
+            typename D::Fa fk[2][MB];
             typename D::Fb fs[NC];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
+            for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+#pragma unroll
+            for (int i = 0; i < KN * MG; ++i) {
+                const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
+                if (i + 1 < KN * MG)
+#pragma unroll
+                    for (int m = 0; m < MB; ++m)
+                        fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
+                if (m0 == 0)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
+#pragma unroll
+                for (int m = 0; m < MB; ++m)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) D::mma_ab(y[n][m0 + m], fk[i & 1][m], fs[n]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // R = V - exp(G) Y
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const typename D::Fa fk = Tile::rows(sk, 16 * m, s * D::KS, lane);
+                const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
 #pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_ab(y[n][m], fk, fs[n]);
-                if constexpr (FULL) {
-                    const typename D::Fa fq = Tile::rows(sq, 16 * m, s * D::KS, lane);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_ba(o[n][m], fq, fs[n]);
+                for (int n = 0; n < NC; ++n) {
+                    const f32x4_t v = trans ? zero : VTile::acc(sv, m, 16 * NC * w + 16 * n, lane);
+                    y[n][m] = v - ga * y[n][m];
                 }
             }
         }
-        if constexpr (MODE == kStates) {
-            st* sp = (st*)a.s0t + ((long long)bh * a.nchunks + c) * a.dv * DK;
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) stage(p ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        typename D::Fb fr[NC][NS];
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-                if (col0 + 16 * n < width)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-                    for (int t = 0; t < DT; ++t) store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
+            for (int s = 0; s < NS; ++s) fr[n][s] = D::step(y[n], s);
+        if constexpr (FULL) {
+            // O^T = scale exp(G) (Q S)^T + R^T (P T)^T: a lane holds 4 columns of token 16 m + n16
+            f32x4_t o[NC][4];
+            if (active) {
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) o[n][m] = zero;
+                typename D::Fa fq[2][MB];
+                typename D::Fb fs[NC];
+                typename D::Fx fx[NC];
+#pragma unroll
+                for (int m = 0; m < MB; ++m) fq[0][m] = Tile::rows(sq, 16 * m, 0, lane);
+#pragma unroll
+                for (int i = 0; i < KN * MG; ++i) {
+                    const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
+                    if (i + 1 < KN * MG)
+#pragma unroll
+                        for (int m = 0; m < MB; ++m)
+                            fq[(i + 1) & 1][m] = Tile::rows(sq, 16 * (m1 + m), s1 * D::KS, lane);
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) {
+                        if (m0 == 0) {
+                            if constexpr (HI) fx[n] = D::step_exact(S[n], s);
+                            else fs[n] = D::step(S[n], s);
+                        }
+#pragma unroll
+                        for (int m = 0; m < MB; ++m) {
+                            if constexpr (HI) D::mma_aa(o[n][m0 + m], fx[n], fq[i & 1][m]);
+                            else D::mma_ba(o[n][m0 + m], fq[i & 1][m], fs[n]);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            typename D::Fa fp[F::COUNT];
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag_hi(mats + kDeltaMatBytes, f, lane);
+            if (more) {
+                __syncthreads();
+                rq.store(sq, tid);
+            }
+            if (active) {
+                const int live = min(kDeltaC, len - c * kDeltaC);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float f = a.scale * sf[p][16 * m + n16];
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) o[n][m] *= f;
+                }
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        if (F::lower(m, s)) {
+#pragma unroll
+                            for (int n = 0; n < NC; ++n) D::mma_ba(o[n][m], fp[F::at(m, s, false)], fr[n][s]);
+                            if constexpr (MODE == kFullF32) {
+                                const typename D::Fm fl = D::mat_frag(mats + kDeltaMatBytes, F::at(m, s, false), lane);
+#pragma unroll
+                                for (int n = 0; n < NC; ++n) D::mma_lo(o[n][m], fl, fr[n][s]);
+                            }
+                        }
+                if (live < kDeltaC)  // padding
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int n = 0; n < NC; ++n)
+                            if (16 * m + n16 >= live) o[n][m] = zero;
+                DOut out;
+                out.init(a.o, ((long long)b * a.N + c * kDeltaC) * a.H + h, min(kDeltaC, a.N - c * kDeltaC), a.H, a.dv,
+                         sizeof(out_t), col0 + g4, lane);
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    if (col0 + 16 * n < width)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, o[n][m]);
+            }
         }
-        // R = V - exp(G) Y
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf + 16 * m + g4);
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[n][m][i] = (trans ? 0.f : v[n][m][i]) - ga[i] * y[n][m][i];
-        }
-        // E = T R
+        if (!active) continue;
+        // E' = exp(G_C - G) beta T R
         f32x4_t u[NC][4];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) u[n][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int m = 0; m < 4; ++m) u[n][m] = zero;
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            typename D::Fb fr[NC];
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-            for (int n = 0; n < NC; ++n) fr[n] = D::step(y[n], s);
+            for (int m = 0; m < 4; ++m)
+                if (F::lower(m, s)) {
+                    const typename D::Fm ft = D::mat_frag(mats, F::at(m, s, false), lane);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                if (s * D::KS > 16 * m + 15) continue;  // above the diagonal
-                const typename D::Fm ft = D::mat_frag(mats, m * NS + s, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fr[n]);
-            }
-        }
+                    for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fr[n][s]);
+                }
         if constexpr (MODE == kStates) {
             st* ep = (st*)a.et + ((long long)bh * a.nchunks + c) * a.dv * kDeltaC;
 #pragma unroll
@@ -368,84 +500,55 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m) store4(ep + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
         }
-        if constexpr (FULL) {
-            // O^T = scale exp(G) (Q S)^T + E^T P^T: a lane holds 4 columns of token 16 m + n16
+        if constexpr (RAW)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-                const float f = a.scale * sf[16 * m + n16];
+                const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf[p] + 64 + 16 * m + g4);
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[n][m][i] *= f;
+                for (int n = 0; n < NC; ++n) u[n][m] *= ta;
             }
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                typename D::Fb fu[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) fu[n] = D::step(u[n], s);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    if (s * D::KS > 16 * m + 15) continue;
-                    const typename D::Fm fp = D::mat_frag(mats + kDeltaMatBytes, m * NS + s, lane);
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_bm(o[n][m], fp, fu[n]);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                if (col0 + 16 * n >= width) continue;
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int t = c * kDeltaC + 16 * m + n16;
-                    if (t >= a.N) continue;
-                    const f32x4_t x = t < len ? o[n][m] : f32x4_t{0.f, 0.f, 0.f, 0.f};
-                    const long long e = (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + g4;
-                    if (a.out_bf16) store4((uint16_t*)a.o + e, x);
-                    else store4((float*)a.o + e, x);
-                }
-            }
-        }
-        // S = exp(G_C) S + K^T (exp(G_C - G) beta E)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf + 64 + 16 * m + g4);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) u[n][m] *= ta;
-        }
-        const float end = sf[63];  // exp(G_C)
+        // S = exp(G_C) S + K^T E'
+        const float end = sf[p][63];
+        typename D::Fb fu[NC][NS];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int t = 0; t < DT; ++t) S[n][t] *= end;
+            for (int s = 0; s < NS; ++s) fu[n][s] = D::step(u[n], s);
+        constexpr int TB = DT < MB ? DT : MB;  // tiles whose fragments are read together
+        typename D::Fa fc[2][TB];
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-            typename D::Fb fu[NC];
+        for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, 16 * t, lane);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) fu[n] = D::step(u[n], s);
+        for (int i = 0; i < NS * DT / TB; ++i) {
+            const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
+            if (i + 1 < NS * DT / TB)
 #pragma unroll
-            for (int t = 0; t < DT; ++t) {
-                const typename D::Fa fk = Tile::cols(sk, s * D::KS, 16 * t, lane);
+                for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
+            if (s == 0)
 #pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t], fk, fu[n]);
-            }
+                for (int n = 0; n < NC; ++n)
+#pragma unroll
+                    for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+#pragma unroll
+                for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if (!active) return;
     // outputs of padding chunks are zero
     if constexpr (FULL) {
-        for (int c = max(c0, cend); c < c1; ++c)
+        for (int c = max(c0, cend); c < c1; ++c) {
+            DOut out;
+            out.init(a.o, ((long long)b * a.N + c * kDeltaC) * a.H + h, min(kDeltaC, a.N - c * kDeltaC), a.H, a.dv,
+                     sizeof(out_t), col0 + g4, lane);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-                if (col0 + 16 * n >= width) continue;
+            for (int n = 0; n < NC; ++n)
+                if (col0 + 16 * n < width)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int t = c * kDeltaC + 16 * m + n16;
-                    if (t >= a.N) continue;
-                    const long long e = (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + g4;
-                    if (a.out_bf16) store4((uint16_t*)a.o + e, f32x4_t{0.f, 0.f, 0.f, 0.f});
-                    else store4((float*)a.o + e, f32x4_t{0.f, 0.f, 0.f, 0.f});
-                }
-            }
+                    for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, zero);
+        }
     }
     if constexpr (MODE == kStates) return;
     float* out = nullptr;
@@ -455,10 +558,11 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         if (col0 + 16 * n >= width) continue;
+        float* p = out + (long long)g4 * width + col0 + 16 * n + n16;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) out[(long long)(16 * t + g4 + i) * width + col0 + 16 * n + n16] = S[n][t][i];
+            for (int i = 0; i < 4; ++i) p[(long long)(16 * t + i) * width] = S[n][t][i];
     }
 }
 
@@ -469,100 +573,98 @@ __global__ __launch_bounds__(kThreads) void delta_chain_kernel(DeltaArgs a) {
 // input: M and S split in two bf16 parts like the chain's operands.
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, bool REV>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
     typedef DOps<E> D;
-    constexpr int NT = DK / 16, TW = NT >= 4 ? NT / 4 : 1, LD = 20;
-    __shared__ __align__(16) float sS[DK * LD];
+    constexpr int NS = DK / D::KS, LD = 20, TPS = D::TPS;
+    __shared__ __align__(16) float sS[2][DK * LD];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
     const int bh = blockIdx.x, col = blockIdx.y * 16 + n16;
-    const bool mine = w * TW < NT;
     const long long sz = (long long)DK * a.dv;
-    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz;
-    const float* M = a.segM + (long long)bh * a.nseg * DK * DK;
+    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz + (long long)(16 * w + g4) * a.dv + col;
+    // this lane's part of the rows of M (REV: of its transpose) that wave w multiplies
+    const float* M = a.segM + (long long)bh * a.nseg * DK * DK + (REV ? g4 * DK + 16 * w + n16 : (16 * w + n16) * DK + g4);
     const float* from = REV ? a.dstate_out : a.state_in;
-    const float* sin = from ? from + bh * sz : nullptr;
+    const float* sin = from ? from + bh * sz + (long long)(16 * w + g4) * a.dv + col : nullptr;
     const int len = delta_len(a, bh / a.H);
-    f32x4_t S[TW];
-    auto tile = [&](int k) {  // 16 rows of the entering state as accumulators hold them
-        f32x4_t x;
+    f32x4_t S, e, m[NS][TPS];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = sS[(16 * k + g4 + i) * LD + n16];
-        return x;
-    };
-    for (int j = 0; j < a.nseg; ++j) {
+    for (int i = 0; i < 4; ++i) S[i] = sin ? sin[(long long)i * a.dv] : 0.f;
+    auto fetch = [&](int j) {  // the j-th segment on the way: its end state from zero and its transition
         const int s = REV ? a.nseg - 1 - j : j;
-        if (mine) {
-            f32x4_t e[TW];
 #pragma unroll
-            for (int t = 0; t < TW; ++t)
+        for (int i = 0; i < 4; ++i) e[i] = X[s * sz + (long long)i * a.dv];
+        if (j == 0) return;
+        const float* p = M + (long long)s * DK * DK;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long at = (long long)(16 * (w * TW + t) + g4 + i) * a.dv + col;
-                    if (j < a.nseg - 1) e[t][i] = X[s * sz + at];
-                    X[s * sz + at] = j == 0 ? (sin ? sin[at] : 0.f) : S[t][i];
-                }
-            if (j == a.nseg - 1) break;
-            if (j > 0 && s * a.seg_chunks * kDeltaC >= len) {  // no live token: the state passes as it is
+        for (int k = 0; k < NS; ++k)
 #pragma unroll
-                for (int t = 0; t < TW; ++t) e[t] = S[t];
-            } else if (j > 0) {
-                const float* Ms = M + (long long)s * DK * DK;
+            for (int t = 0; t < TPS; ++t) {
+                if constexpr (REV) {
 #pragma unroll
-                for (int k = 0; k < DK / D::KS; ++k) {
-                    f32x4_t x[D::TPS];
-#pragma unroll
-                    for (int p = 0; p < D::TPS; ++p) x[p] = tile(D::TPS * k + p);
-                    const typename D::Fb fs = D::step(x, 0);
-#pragma unroll
-                    for (int t = 0; t < TW; ++t) {
-                        f32x4_t y[D::TPS];
-                        if constexpr (REV) {  // rows of the transpose
-                            const float* m = Ms + (D::KS * k + g4) * DK + 16 * (w * TW + t) + n16;
-#pragma unroll
-                            for (int p = 0; p < D::TPS; ++p)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) y[p][i] = m[(16 * p + i) * DK];
-                        } else {
-                            const float* m = Ms + (16 * (w * TW + t) + n16) * DK + D::KS * k + g4;
-#pragma unroll
-                            for (int p = 0; p < D::TPS; ++p) y[p] = *reinterpret_cast<const f32x4_t*>(m + 16 * p);
-                        }
-                        D::mma_mb(e[t], D::step(y, 0), fs);
-                    }
+                    for (int i = 0; i < 4; ++i) m[k][t][i] = p[(D::KS * k + 16 * t + i) * DK];
+                } else {
+                    m[k][t] = *reinterpret_cast<const f32x4_t*>(p + D::KS * k + 16 * t);
                 }
             }
+    };
+    fetch(0);
+    for (int j = 0;; ++j) {
+        const int s = REV ? a.nseg - 1 - j : j;
+        float* x = sS[j & 1];
 #pragma unroll
-            for (int t = 0; t < TW; ++t) S[t] = e[t];
-        } else if (j == a.nseg - 1) {
-            break;
+        for (int i = 0; i < 4; ++i) {
+            x[(16 * w + g4 + i) * LD + n16] = S[i];
+            X[s * sz + (long long)i * a.dv] = S[i];
         }
-        __syncthreads();
-        if (mine)
+        if (j == a.nseg - 1) return;
+        const f32x4_t e0 = e;
+        typename D::Fb fm[NS];
+        if (j > 0)
 #pragma unroll
-            for (int t = 0; t < TW; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sS[(16 * (w * TW + t) + g4 + i) * LD + n16] = S[t][i];
+            for (int k = 0; k < NS; ++k) fm[k] = D::step(m[k], 0);
+        if (j + 1 < a.nseg - 1) fetch(j + 1);
         __syncthreads();
+        if (j == 0) {
+            S = e0;  // from the state entering the first segment
+        } else if (s * a.seg_chunks * kDeltaC < len) {  // else no live token: the state passes as it is
+            S = e0;
+#pragma unroll
+            for (int k = 0; k < NS; ++k) {
+                f32x4_t y[TPS];
+#pragma unroll
+                for (int t = 0; t < TPS; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[t][i] = x[(D::KS * k + 16 * t + g4 + i) * LD + n16];
+                D::mma_mb(S, fm[k], D::step(y, 0));
+            }
+        }
     }
 }
 
-template <class E, int DK, int NC>
+template <class E, int DK, int NC, int NW>
 void pick_cols(DeltaKernels* o) {
     *o = {};
     o->prep = delta_prep_kernel<E, DK, false>;
     o->bprep = delta_prep_kernel<E, DK, true>;
-    o->local = delta_chain_kernel<E, DK, NC, kLocal>;
-    o->full = delta_chain_kernel<E, DK, NC, kFull>;
-    o->states = delta_chain_kernel<E, DK, NC, kStates>;
+    o->local = delta_chain_kernel<E, DK, NC, NW, kLocal>;
+    o->blocal = delta_chain_kernel<E, DK, NC, NW, kLocalRaw>;
+    o->full = delta_chain_kernel<E, DK, NC, NW, kFull>;
+    o->full_f32 = delta_chain_kernel<E, DK, NC, NW, sizeof(typename E::st) == 2 ? kFullF32 : kFull>;
+    o->states = delta_chain_kernel<E, DK, NC, NW, kStates>;
     o->scan = delta_scan_kernel<E, DK, false>;
     o->rscan = delta_scan_kernel<E, DK, true>;
-    o->cols = 64 * NC;
+    o->cols = 16 * NC * NW;
+    o->threads = 64 * NW;
 }
-// Two column tiles per wave halve the operand reads per product; one where d_v would leave waves idle.
+// Two column tiles per wave halve the operand reads per product; one where d_v would leave waves idle, and where a row of
+// K takes 512 bytes: the state of two tiles would take the registers of a second wave on the SIMD, so eight waves share
+// the rows instead.
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
-    if (dv > 64) pick_cols<E, DK, 2>(o);
-    else pick_cols<E, DK, 1>(o);
+    constexpr bool WIDE = DK * sizeof(typename E::st) >= 256;
+    if (dv <= 64) pick_cols<E, DK, 1, 4>(o);
+    else if constexpr (WIDE) pick_cols<E, DK, 1, 8>(o);
+    else pick_cols<E, DK, 2, 4>(o);
 }
 
 }  // namespace

@@ -190,7 +190,7 @@ ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gat
     if (!cols) return RET_OK;
     ColSumArgs R = {(const float*)workspace, dweight, dbias, strips, C};
     LaunchTimer tm("ret_column_sums", s, op);
-    hipLaunchKernelGGL(colsum_kernel_get(), dim3((unsigned)((2LL * C + kColSumCols - 1) / kColSumCols)), dim3(256), 0, s, R);
+    hipLaunchKernelGGL(colsum_kernel_get(), dim3((unsigned)((2LL * C + kColSumCols - 1) / kColSumCols)), dim3(kColSumThreads), 0, s, R);
     tm.done();
     return launch_status("ret_column_sums");
 }

@@ -196,17 +196,29 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LnBwdArgs
     }
 }
 
-// Sums of `parts` partial rows: 64 columns per workgroup, the rows dealt to its four waves.
-__global__ __launch_bounds__(256) void colsum_kernel(ColSumArgs a) {
-    __shared__ float part[256];
+// Sums of `parts` partial rows: 64 columns per workgroup, the rows dealt to its 16 waves, 8 loads of a wave in flight.
+__global__ __launch_bounds__(kColSumThreads) void colsum_kernel(ColSumArgs a) {
+    constexpr int NW = kColSumThreads / 64, U = 8;
+    __shared__ float part[kColSumThreads];
     const int c = blockIdx.x * kColSumCols + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    const bool in = c < 2 * a.cols;
+    const float* p = a.partial + (in ? c : 0);
     float s = 0.f;
-    if (c < 2 * a.cols)
-        for (int p = w; p < a.parts; p += 4) s += a.partial[(long long)p * 2 * a.cols + c];
+    for (int r = w; r < a.parts; r += NW * U) {
+        float x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int q = r + i * NW;
+            x[i] = p[(long long)(q < a.parts ? q : r) * 2 * a.cols];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) s += r + i * NW < a.parts ? x[i] : 0.f;
+    }
     part[threadIdx.x] = s;
     __syncthreads();
-    if (w != 0 || c >= 2 * a.cols) return;
-    s = (part[threadIdx.x] + part[threadIdx.x + 64]) + (part[threadIdx.x + 128] + part[threadIdx.x + 192]);
+    if (w != 0 || !in) return;
+#pragma unroll
+    for (int i = 1; i < NW; ++i) s += part[threadIdx.x + 64 * i];
     if (c < a.cols) {
         if (a.out0) a.out0[c] = s;
     } else if (a.out1) {
@@ -359,7 +371,7 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
     if (!cols) return RET_OK;
     ColSumArgs C = {(const float*)workspace, dweight, dbias, grid, D};
     LaunchTimer tm("ret_column_sums", s, op);
-    hipLaunchKernelGGL(colsum_kernel, dim3((2 * D + kColSumCols - 1) / kColSumCols), dim3(256), 0, s, C);
+    hipLaunchKernelGGL(colsum_kernel, dim3((2 * D + kColSumCols - 1) / kColSumCols), dim3(kColSumThreads), 0, s, C);
     tm.done();
     return launch_status("ret_column_sums");
 }

@@ -61,7 +61,7 @@ struct ColSumArgs {
 };
 typedef void (*colsum_kernel_t)(ColSumArgs);
 colsum_kernel_t colsum_kernel_get();
-constexpr int kColSumCols = 64;  // columns (of the 2 * cols) per 256-thread workgroup
+constexpr int kColSumCols = 64, kColSumThreads = 1024;  // columns (of the 2 * cols) and threads per workgroup
 
 // Layer norm of rows of D values, with an optional residual added first, and its gradients.
 struct LnArgs {

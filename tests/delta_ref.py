@@ -22,6 +22,31 @@ def forward(q, k, v, g, beta, scale, state=None, lengths=None):
     return o, S, before
 
 
+def term_sums(q, k, v, g, beta, scale, before):
+    """Sums of magnitudes behind each output when it is computed from the state entering its chunk of 64 tokens and the
+    chunk's residuals R = V - exp(G) K S0: scale exp(G_i) sum_d |q_id S0_dc| + sum_j |(P T)_ij R_jc|."""
+    B, N, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    rep = H // Hk
+    out = np.zeros((B, N, H, dv))
+    for c in range(0, N, 64):
+        e = min(c + 64, N)
+        S0 = before[c]
+        qc, kc = (np.repeat(x[:, c:e].astype(np.float64), rep, axis=2).transpose(0, 2, 1, 3) for x in (q, k))
+        vc = v[:, c:e].astype(np.float64).transpose(0, 2, 1, 3)
+        G = np.cumsum(g[:, c:e].astype(np.float64), 1).transpose(0, 2, 1)
+        be = beta[:, c:e].astype(np.float64).transpose(0, 2, 1)
+        low = np.tril(np.ones((e - c, e - c)))
+        D = np.exp((G[..., :, None] - G[..., None, :]) * low) * low * be[..., None, :]
+        A = np.einsum("bhid,bhjd->bhij", kc, kc) * D * np.tril(np.ones_like(low), -1)
+        T = np.linalg.inv(np.eye(e - c) + A)
+        PT = np.matmul(scale * np.einsum("bhid,bhjd->bhij", qc, kc) * D, T)
+        R = vc - np.exp(G)[..., None] * np.matmul(kc, S0)
+        m = scale * np.exp(G)[..., None] * np.matmul(np.abs(qc), np.abs(S0)) + np.matmul(np.abs(PT), np.abs(R))
+        out[:, c:e] = m.transpose(0, 2, 1, 3)
+    return out
+
+
 def gradients(q, k, v, g, beta, scale, dout, state=None, dstate_out=None, lengths=None):
     """Gradients of sum(dout o) + sum(dstate_out state): dq, dk, dv, dg, dbeta, dstate_in."""
     B, N, Hk, dk = q.shape
