@@ -22,7 +22,8 @@
 
 namespace ret {
 
-constexpr int kDeltaC = 64;  // tokens per chunk
+constexpr int kDeltaC = 64;    // tokens per chunk
+constexpr int kScanCols = 32;  // columns of the state per workgroup of the segment scan
 
 // Per (chunk, b, h): fragments of T and P, then per-token factors.
 // Factors of a chunk (rows of 64): exp(G_i), exp(G_C - G_i) beta_i, exp(G_C - G_i), beta_i, then G_i log2(e) in fp64.
@@ -303,7 +304,7 @@ struct DeltaKernels {
     delta_kernel_t prep, local, full, full_f32, scan;  // full_f32: F32 output
     delta_kernel_t bprep, blocal, states, rlocal, rscan, rfull, grad;  // gradients
     int cols, threads; // columns of d_v (or of a transition) and threads per workgroup of the chains
-    int grad_threads;
+    int grad_threads, scan_threads;
 };
 // d_k in {32, 64, 128, 256} for bf16 and {16, 32, 64, 128} for fp32; false otherwise.
 bool delta_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);

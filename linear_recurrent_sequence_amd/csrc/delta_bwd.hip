@@ -14,6 +14,9 @@
 // exp(G_i) stands with every q_i and reading k_i, exp(-G_i) with every writing k_i, exp(G_C) with S_C. Solving for E with
 // beta along the columns and for dU with beta along the rows leaves no division by beta, which may be zero.
 #include "delta.h"
+#ifndef SB
+#define SB
+#endif
 
 namespace ret {
 
@@ -31,7 +34,8 @@ constexpr int rchain_waves() {  // as the forward chain's
     typedef DOps<E> D;
     const int rows = kDeltaC * (int)sizeof(typename E::st);
     const int lds = rows * (3 * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 2048;
-    return NW == 8 || (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
+    if (NW == 8) return 2 * lds <= 160 * 1024 ? 4 : 2;
+    return (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
 }
 template <class E, int DK, int NC, int NW, bool LOCAL>
 __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delta_rchain_kernel(DeltaArgs a) {
@@ -49,7 +53,7 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
     __shared__ __align__(16) st sq[kDeltaC * Tile::LD];
     __shared__ __align__(16) st so[kDeltaC * OTile::LD];
     __shared__ __align__(16) float sf[2][256];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
     const DeltaBlock blk = delta_block(a, (a.dv + COLS - 1) / COLS);
     if (blk.bh >= a.B * a.H) return;
     const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
@@ -138,6 +142,9 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
         const long long unit = (long long)bh * a.nchunks + c;
         const char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
         const st* K = sk[p];
+        typename D::Fm fp[F::COUNT], ft[F::COUNT];
+#pragma unroll
+        for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag(mats + 2 * kDeltaMatBytes, f, lane);
         f32x4_t x[NC][4];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -172,8 +179,10 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                 for (int m = 0; m < MB; ++m)
 #pragma unroll
                     for (int n = 0; n < NC; ++n) D::mma_ab(x[n][m0 + m], fk[i & 1][m], fs[n]);
-                __builtin_amdgcn_sched_barrier(0);
+                SB;
             }
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats + kDeltaMatBytes, f, lane);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf[p] + 128 + 16 * m + g4);
@@ -188,9 +197,8 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     if (F::upper(m, s)) {
-                        const typename D::Fm fp = D::mat_frag(mats + 2 * kDeltaMatBytes, F::at(m, s, true), lane);
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp, fd[n]);
+                        for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp[F::at(m, s, true)], fd[n]);
                     }
             }
         }
@@ -216,11 +224,11 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     if (F::upper(m, s)) {
-                        const typename D::Fm ft = D::mat_frag(mats + kDeltaMatBytes, F::at(m, s, true), lane);
 #pragma unroll
-                        for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fw[n]);
+                        for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, true)], fw[n]);
                     }
             }
+            __builtin_amdgcn_sched_barrier(0);
             // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -251,7 +259,7 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                 for (int t = 0; t < TB; ++t)
 #pragma unroll
                     for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fd[n][s]);
-                __builtin_amdgcn_sched_barrier(0);
+                SB;
             }
             if constexpr (!LOCAL) {
                 wave_fence();  // the last reads of dO come before
@@ -312,7 +320,7 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
             for (int t = 0; t < TB; ++t)
 #pragma unroll
                 for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
-            __builtin_amdgcn_sched_barrier(0);
+            SB;
         }
     }
     if (!active) return;
@@ -403,7 +411,7 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
     __shared__ float sF[256], sDg[2][kDeltaC], sDb[kDeltaC], sR[2][NW];
     st *sS = buf, *sD = sS + VB * TK::LD, *sO = sD + VB * TK::LD, *sE = sO + kDeltaC * TO::LD, *sU = sE + VB * TC::LD;
     st *sX = buf, *sZ = buf + kDeltaC * TC::LD;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
     const int tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
     const int t0 = c * kDeltaC, len = delta_len(a, b), live = min(kDeltaC, len - t0);

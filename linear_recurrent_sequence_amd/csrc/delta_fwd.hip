@@ -1,5 +1,8 @@
 // The gated delta rule over a sequence: the per-chunk matrices, the chain over chunks, and the chain over segments.
 #include "delta.h"
+#ifndef SB
+#define SB
+#endif
 
 #include <type_traits>
 
@@ -118,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     __shared__ __align__(16) float sT[kDeltaC * kTriLD];
     __shared__ f64 sG[kDeltaC];
     __shared__ float sB[kDeltaC], sF[kDeltaC];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g = lane >> 4;
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
     const int t0 = c * kDeltaC, live = min(kDeltaC, delta_len(a, b) - t0);
     if (live <= 0) return;  // no one reads this chunk
@@ -252,7 +255,8 @@ constexpr int chain_waves() {
     typedef DOps<E> D;
     const int rows = kDeltaC * (int)sizeof(typename E::st);
     const int lds = rows * ((MODE <= kFullF32 ? 3 : 2) * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 1024;
-    return NW == 8 || (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
+    if (NW == 8) return 2 * lds <= 160 * 1024 ? 4 : 2;
+    return (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
 }
 template <class E, int DK, int NC, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void delta_chain_kernel(DeltaArgs a) {
@@ -275,7 +279,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
     __shared__ __align__(16) st sq[FULL ? kDeltaC * Tile::LD : 16];
     __shared__ __align__(16) st sv[kDeltaC * VTile::LD];
     __shared__ __align__(16) float sf[2][128];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
     const int nE = (a.dv + COLS - 1) / COLS;  // workgroups over d_v; a local pass has those of d_k behind them
     const DeltaBlock blk = delta_block(a, nE + (LOCAL ? (DK + COLS - 1) / COLS : 0));
     if (blk.bh >= a.B * a.H) return;
@@ -376,7 +380,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                 for (int m = 0; m < MB; ++m)
 #pragma unroll
                     for (int n = 0; n < NC; ++n) D::mma_ab(y[n][m0 + m], fk[i & 1][m], fs[n]);
-                __builtin_amdgcn_sched_barrier(0);
+                SB;
             }
             // R = V - exp(G) Y
 #pragma unroll
@@ -392,6 +396,10 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
         __builtin_amdgcn_sched_barrier(0);
         if (more) stage(p ^ 1);
         __builtin_amdgcn_sched_barrier(0);
+        typename D::Fm ft[F::COUNT];
+        if constexpr (!FULL)
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats, f, lane);
         typename D::Fb fr[NC][NS];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -429,12 +437,15 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                             else D::mma_ba(o[n][m0 + m], fq[i & 1][m], fs[n]);
                         }
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    SB;
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
             typename D::Fa fp[F::COUNT];
 #pragma unroll
             for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag_hi(mats + kDeltaMatBytes, f, lane);
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats, f, lane);
             if (more) {
                 __syncthreads();
                 rq.store(sq, tid);
@@ -476,6 +487,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                         for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, o[n][m]);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (!active) continue;
         // E' = exp(G_C - G) beta T R
         f32x4_t u[NC][4];
@@ -488,10 +500,10 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
 #pragma unroll
             for (int m = 0; m < 4; ++m)
                 if (F::lower(m, s)) {
-                    const typename D::Fm ft = D::mat_frag(mats, F::at(m, s, false), lane);
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft, fr[n][s]);
+                    for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, false)], fr[n][s]);
                 }
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (MODE == kStates) {
             st* ep = (st*)a.et + ((long long)bh * a.nchunks + c) * a.dv * kDeltaC;
 #pragma unroll
@@ -533,7 +545,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
             for (int t = 0; t < TB; ++t)
 #pragma unroll
                 for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
-            __builtin_amdgcn_sched_barrier(0);
+            SB;
         }
     }
     if (!active) return;
@@ -572,72 +584,101 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
 // (b, h, 16 columns); REV: the gradients' chain, D_{s-1} = M_s^T D_s + F_s over segF from the right. The waves share the rows of M, S goes round through LDS. BF16
 // input: M and S split in two bf16 parts like the chain's operands.
 // ---------------------------------------------------------------------------------------------------
+// waves of a scan workgroup: 16 rows of the state each, 32 at d_k = 256 (the rows of M in flight take the registers)
+template <int DK>
+constexpr int scan_waves() { return DK / 16 <= 8 ? DK / 16 : 8; }
 template <class E, int DK, bool REV>
-__global__ __launch_bounds__(4 * DK) void delta_scan_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * scan_waves<DK>()) void delta_scan_kernel(DeltaArgs a) {
     typedef DOps<E> D;
-    constexpr int NS = DK / D::KS, LD = 20, TPS = D::TPS;
+    constexpr int NS = DK / D::KS, TPS = D::TPS, RT = DK / 16 / scan_waves<DK>(), CT = kScanCols / 16, LD = kScanCols + 4;
     __shared__ __align__(16) float sS[2][DK * LD];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int bh = blockIdx.x, col = blockIdx.y * 16 + n16;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
+    const int g4 = 4 * (lane >> 4), bh = blockIdx.x, c0 = blockIdx.y * kScanCols;
     const long long sz = (long long)DK * a.dv;
-    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz + (long long)(16 * w + g4) * a.dv + col;
+    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz + (long long)(16 * RT * w + g4) * a.dv + c0 + n16;
     // this lane's part of the rows of M (REV: of its transpose) that wave w multiplies
-    const float* M = a.segM + (long long)bh * a.nseg * DK * DK + (REV ? g4 * DK + 16 * w + n16 : (16 * w + n16) * DK + g4);
+    const float* M = a.segM + (long long)bh * a.nseg * DK * DK +
+                     (REV ? g4 * DK + 16 * RT * w + n16 : (16 * RT * w + n16) * DK + g4);
     const float* from = REV ? a.dstate_out : a.state_in;
-    const float* sin = from ? from + bh * sz + (long long)(16 * w + g4) * a.dv + col : nullptr;
+    const float* sin = from ? from + bh * sz + (long long)(16 * RT * w + g4) * a.dv + c0 + n16 : nullptr;
     const int len = delta_len(a, bh / a.H);
-    f32x4_t S, e, m[NS][TPS];
+    f32x4_t S[RT][CT], e[RT][CT], m[RT][NS][TPS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[i] = sin ? sin[(long long)i * a.dv] : 0.f;
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                S[r][t][i] = sin && c0 + 16 * t < a.dv ? sin[(long long)(16 * r + i) * a.dv + 16 * t] : 0.f;
     auto fetch = [&](int j) {  // the j-th segment on the way: its end state from zero and its transition
         const int s = REV ? a.nseg - 1 - j : j;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = X[s * sz + (long long)i * a.dv];
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (c0 + 16 * t < a.dv)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) e[r][t][i] = X[s * sz + (long long)(16 * r + i) * a.dv + 16 * t];
         if (j == 0) return;
         const float* p = M + (long long)s * DK * DK;
 #pragma unroll
-        for (int k = 0; k < NS; ++k)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int t = 0; t < TPS; ++t) {
-                if constexpr (REV) {
+            for (int k = 0; k < NS; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) m[k][t][i] = p[(D::KS * k + 16 * t + i) * DK];
-                } else {
-                    m[k][t] = *reinterpret_cast<const f32x4_t*>(p + D::KS * k + 16 * t);
+                for (int t = 0; t < TPS; ++t) {
+                    if constexpr (REV) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) m[r][k][t][i] = p[(D::KS * k + 16 * t + i) * DK + 16 * r];
+                    } else {
+                        m[r][k][t] = *reinterpret_cast<const f32x4_t*>(p + 16 * r * DK + D::KS * k + 16 * t);
+                    }
                 }
-            }
     };
     fetch(0);
     for (int j = 0;; ++j) {
         const int s = REV ? a.nseg - 1 - j : j;
         float* x = sS[j & 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[(16 * w + g4 + i) * LD + n16] = S[i];
-            X[s * sz + (long long)i * a.dv] = S[i];
-        }
-        if (j == a.nseg - 1) return;
-        const f32x4_t e0 = e;
-        typename D::Fb fm[NS];
-        if (j > 0)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < NS; ++k) fm[k] = D::step(m[k], 0);
-        if (j + 1 < a.nseg - 1) fetch(j + 1);
+            for (int t = 0; t < CT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[(16 * (RT * w + r) + g4 + i) * LD + 16 * t + n16] = S[r][t][i];
+                    if (c0 + 16 * t < a.dv) X[s * sz + (long long)(16 * r + i) * a.dv + 16 * t] = S[r][t][i];
+                }
+        if (j == a.nseg - 1) return;
         __syncthreads();
-        if (j == 0) {
-            S = e0;  // from the state entering the first segment
+        if (j == 0) {  // from the state entering the first segment
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < CT; ++t) S[r][t] = e[r][t];
         } else if (s * a.seg_chunks * kDeltaC < len) {  // else no live token: the state passes as it is
-            S = e0;
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < CT; ++t) S[r][t] = e[r][t];
 #pragma unroll
             for (int k = 0; k < NS; ++k) {
-                f32x4_t y[TPS];
+                typename D::Fb fm[RT];
 #pragma unroll
-                for (int t = 0; t < TPS; ++t)
+                for (int r = 0; r < RT; ++r) fm[r] = D::step(m[r][k], 0);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) y[t][i] = x[(D::KS * k + 16 * t + g4 + i) * LD + n16];
-                D::mma_mb(S, fm[k], D::step(y, 0));
+                for (int t = 0; t < CT; ++t) {
+                    f32x4_t y[TPS];
+#pragma unroll
+                    for (int p = 0; p < TPS; ++p)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) y[p][i] = x[(D::KS * k + 16 * p + g4 + i) * LD + 16 * t + n16];
+                    const typename D::Fb fy = D::step(y, 0);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) D::mma_mb(S[r][t], fm[r], fy);
+                }
             }
         }
+        if (j + 1 < a.nseg - 1) fetch(j + 1);
     }
 }
 
@@ -653,6 +694,7 @@ void pick_cols(DeltaKernels* o) {
     o->states = delta_chain_kernel<E, DK, NC, NW, kStates>;
     o->scan = delta_scan_kernel<E, DK, false>;
     o->rscan = delta_scan_kernel<E, DK, true>;
+    o->scan_threads = 64 * scan_waves<DK>();
     o->cols = 16 * NC * NW;
     o->threads = 64 * NW;
 }
@@ -662,7 +704,7 @@ void pick_cols(DeltaKernels* o) {
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
     constexpr bool WIDE = DK * sizeof(typename E::st) >= 256;
-    if (dv <= 64) pick_cols<E, DK, 1, 4>(o);
+    if (dv <= 64 || DK <= 128) pick_cols<E, DK, 1, 4>(o);
     else if constexpr (WIDE) pick_cols<E, DK, 1, 8>(o);
     else pick_cols<E, DK, 2, 4>(o);
 }

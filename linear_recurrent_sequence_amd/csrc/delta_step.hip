@@ -17,7 +17,7 @@ __global__ __launch_bounds__(DK >= 32 ? DK * 2 : 64) void delta_step_kernel(Delt
     typedef typename E::st st;
     constexpr int NW = DK >= 32 ? DK / 32 : 1, RPT = DK / (4 * NW);
     __shared__ float part[NW][16][9];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, cg = lane & 15, rg = lane >> 4;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), cg = lane & 15, rg = lane >> 4;
     const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H;
     const int c0 = blockIdx.y * 64 + 4 * cg, r0 = RPT * (4 * w + rg);
     const bool in = c0 < a.dv;

@@ -20,7 +20,7 @@ template <int DV>
 __global__ __launch_bounds__(64 * kEpiBwdWaves) void epilogue_bwd_kernel(EpiBwdArgs a) {
     constexpr int LPG = DV / 8;
     __shared__ float cols[kEpiBwdWaves * kEpiBwdCols];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int C = a.H * DV, c = blockIdx.x * kEpiBwdCols + lane * 8;
     const bool in = c < C;  // whole heads: C and the first column of a workgroup are multiples of a head's run
     const int cc = in ? c : 0;

@@ -30,7 +30,7 @@ struct RowSum {
         } else {
             constexpr int NW = THREADS / 64, GW = L / 64;
             v = lanes_sum<64>(v);
-            const int w = threadIdx.x >> 6;
+            const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
             float* r = red + slot * NW;
             slot ^= 1;
             if ((threadIdx.x & 63) == 0) r[w] = v;
@@ -200,7 +200,7 @@ __global__ __launch_bounds__(kLnBwdThreads) void layer_norm_bwd_kernel(LnBwdArgs
 __global__ __launch_bounds__(kColSumThreads) void colsum_kernel(ColSumArgs a) {
     constexpr int NW = kColSumThreads / 64, U = 8;
     __shared__ float part[kColSumThreads];
-    const int c = blockIdx.x * kColSumCols + (threadIdx.x & 63), w = threadIdx.x >> 6;
+    const int c = blockIdx.x * kColSumCols + (threadIdx.x & 63), w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool in = c < 2 * a.cols;
     const float* p = a.partial + (in ? c : 0);
     float s = 0.f;
