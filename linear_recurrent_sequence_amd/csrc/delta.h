@@ -84,6 +84,9 @@ __device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
 // compiler moves none across.
 __device__ __forceinline__ void wave_fence() { __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// The scheduler moves nothing across: keeps the reads of the next step's fragments ahead of this step's products.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // Fragments of a lower triangular 64 x 64 matrix by (row tile m, step s of KS columns), row after row, and those of the
 // transpose of one.
 template <int KS>
@@ -142,6 +145,30 @@ struct DOps<BF16> {
     __device__ static __forceinline__ void mma_ab(f32x4_t& acc, Fa a, const Fb& b) {
         mfma1(acc, a, b.lo);
         mfma1(acc, a, b.hi);
+    }
+    // x[n][m0 + m] += a[m] b[n] over MB x NC tiles, the low parts first: no product right behind one of the same tile
+    template <int MB, int NC, int NT>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB], const Fb (&b)[NC]) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n].lo);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n].hi);
+    }
+    template <int MB, int NC, int NT, int NS>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB],
+                                                    const Fb (&b)[NC][NS], int s) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n][s].lo);
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n][s].hi);
     }
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, Fa a, const Fb& b) {
         mfma1(acc, b.lo, a);
@@ -218,6 +245,27 @@ struct DOps<F32> {
     __device__ static __forceinline__ void mma_ab(f32x4_t& acc, const Fa& a, const Fb& b) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
+    }
+    template <int MB, int NC, int NT>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB], const Fb (&b)[NC]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    x[n][m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[n][i], x[n][m0 + m], 0, 0, 0);
+    }
+    template <int MB, int NC, int NT, int NS>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB],
+                                                    const Fb (&b)[NC][NS], int s) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int n = 0; n < NC; ++n)
+                    x[n][m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[n][s][i], x[n][m0 + m], 0, 0, 0);
     }
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }

@@ -14,9 +14,6 @@
 // exp(G_i) stands with every q_i and reading k_i, exp(-G_i) with every writing k_i, exp(G_C) with S_C. Solving for E with
 // beta along the columns and for dU with beta along the rows leaves no division by beta, which may be zero.
 #include "delta.h"
-#ifndef SB
-#define SB
-#endif
 
 namespace ret {
 
@@ -91,9 +88,9 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
         rk.load(kp + base, a.Hk * DK, live, DK, tid);
-        if (tid < 256) ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
+        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 255)];
         rq.load(qp + base, a.Hk * DK, live, DK, tid);
-        if (active) ro.load(op + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, live, a.dv - col0, lane);
+        ro.load(op + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, active ? live : 0, a.dv - col0, lane);
     };
     // Rows of dV of chunk c, 16 bytes a lane, from the wave's own columns of the tile that held dO (zero: zeros); rows past
     // the live ones are zero. 32-bit outputs go from the registers.
@@ -138,7 +135,7 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
     for (int c = cend - 1, p = 0; c >= c0; --c, p ^= 1) {
         __syncthreads();
         const bool more = c > c0;
-        if (more) fetch(c - 1);
+        fetch(more ? c - 1 : c);  // unconditional: see the forward chain
         const long long unit = (long long)bh * a.nchunks + c;
         const char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
         const st* K = sk[p];
@@ -162,9 +159,11 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
             }
             // W = exp(G_C - G) K dS + Pr^T dO
             typename D::Fa fk[2][MB];
-            typename D::Fb fs[NC];
+            typename D::Fb fs[2][NC];
 #pragma unroll
             for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) fs[0][n] = D::step(S[n], 0);
 #pragma unroll
             for (int i = 0; i < KN * MG; ++i) {
                 const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
@@ -172,14 +171,12 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
                         fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
-                if (m0 == 0)
+                keep_order();
+                D::template products<MB, NC>(x, m0, fk[i & 1], fs[s & 1]);
+                if (m1 == 0 && s1 < KN)
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_ab(x[n][m0 + m], fk[i & 1][m], fs[n]);
-                SB;
+                    for (int n = 0; n < NC; ++n) fs[s1 & 1][n] = D::step(S[n], s1);
+                keep_order();
             }
 #pragma unroll
             for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats + kDeltaMatBytes, f, lane);
@@ -202,12 +199,12 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                     }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         if (more) {
             rk.store(sk[p ^ 1], tid);
             if (tid < 256) sf[p ^ 1][tid] = ff;
         }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         f32x4_t u[NC][4];
         const float end = sf[p][63];
         if (active) {
@@ -228,7 +225,7 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                         for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, true)], fw[n]);
                     }
             }
-            __builtin_amdgcn_sched_barrier(0);
+            keep_order();
             // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -250,16 +247,14 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                 if (i + 1 < NS * DT / TB)
 #pragma unroll
                     for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(sq, s1 * D::KS, 16 * (t1 + t), lane);
+                keep_order();
                 if (s == 0)
 #pragma unroll
                     for (int n = 0; n < NC; ++n)
 #pragma unroll
                         for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
-#pragma unroll
-                for (int t = 0; t < TB; ++t)
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fd[n][s]);
-                SB;
+                D::template products<TB, NC>(S, t0, fc[i & 1], fd, s);
+                keep_order();
             }
             if constexpr (!LOCAL) {
                 wave_fence();  // the last reads of dO come before
@@ -316,11 +311,9 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
             if (i + 1 < NS * DT / TB)
 #pragma unroll
                 for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
-#pragma unroll
-            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
-            SB;
+            keep_order();
+            D::template products<TB, NC>(S, t0, fc[i & 1], fu, s);
+            keep_order();
         }
     }
     if (!active) return;
@@ -473,7 +466,7 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
             re.store(sE, tid);
             ru.store(sU, tid);
             __syncthreads();
-            if (v0 + VB < a.dv) fetch(v0 + VB);
+            fetch(min(v0 + VB, (a.dv - 1) / VB * VB));  // unconditional: see the forward chain
 #pragma unroll
             for (int s = 0; s < VB / D::KS; ++s) {
                 const typename D::Fa fo = TO::rows(sO, 16 * tw, s * D::KS, lane);

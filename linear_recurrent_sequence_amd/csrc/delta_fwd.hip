@@ -1,8 +1,5 @@
 // The gated delta rule over a sequence: the per-chunk matrices, the chain over chunks, and the chain over segments.
 #include "delta.h"
-#ifndef SB
-#define SB
-#endif
 
 #include <type_traits>
 
@@ -325,9 +322,9 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
         rk.load(kp + base, a.Hk * DK, live, DK, tid);
-        if (!trans && active) rv.load(vp + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, live, a.dv - col0, lane);
+        rv.load(vp + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, !trans && active ? live : 0, a.dv - col0, lane);
         if constexpr (FULL) rq.load(qp + base, a.Hk * DK, live, DK, tid);
-        if (tid < 128) ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + tid];
+        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 127)];
     };
     auto stage = [&](int p) {
         rk.store(sk[p], tid);
@@ -343,7 +340,8 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
     for (int c = c0, p = 0; c < cend; ++c, p ^= 1) {
         __syncthreads();
         const bool more = c + 1 < cend;
-        if (more) fetch(c + 1);
+        // (the last chunk again at the end: a conditional request would make its registers wait where the branches join)
+        fetch(more ? c + 1 : c);
         const char* mats = a.mats + ((long long)bh * a.nchunks + c) * a.nmats * kDeltaMatBytes;
         const st* K = sk[p];
         f32x4_t y[NC][4];
@@ -363,9 +361,11 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
             }
             // Y = K S
             typename D::Fa fk[2][MB];
-            typename D::Fb fs[NC];
+            typename D::Fb fs[2][NC];
 #pragma unroll
             for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) fs[0][n] = D::step(S[n], 0);
 #pragma unroll
             for (int i = 0; i < KN * MG; ++i) {
                 const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
@@ -373,14 +373,12 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
 #pragma unroll
                     for (int m = 0; m < MB; ++m)
                         fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
-                if (m0 == 0)
+                keep_order();
+                D::template products<MB, NC>(y, m0, fk[i & 1], fs[s & 1]);
+                if (m1 == 0 && s1 < KN)
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) fs[n] = D::step(S[n], s);
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_ab(y[n][m0 + m], fk[i & 1][m], fs[n]);
-                SB;
+                    for (int n = 0; n < NC; ++n) fs[s1 & 1][n] = D::step(S[n], s1);
+                keep_order();
             }
             // R = V - exp(G) Y
 #pragma unroll
@@ -393,9 +391,9 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         if (more) stage(p ^ 1);
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         typename D::Fm ft[F::COUNT];
         if constexpr (!FULL)
 #pragma unroll
@@ -415,9 +413,12 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                     for (int m = 0; m < 4; ++m) o[n][m] = zero;
                 typename D::Fa fq[2][MB];
                 typename D::Fb fs[NC];
-                typename D::Fx fx[NC];
+                typename D::Fx fx[2][NC];
 #pragma unroll
                 for (int m = 0; m < MB; ++m) fq[0][m] = Tile::rows(sq, 16 * m, 0, lane);
+                if constexpr (HI)
+#pragma unroll
+                    for (int n = 0; n < NC; ++n) fx[0][n] = D::step_exact(S[n], 0);
 #pragma unroll
                 for (int i = 0; i < KN * MG; ++i) {
                     const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
@@ -425,22 +426,23 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
 #pragma unroll
                         for (int m = 0; m < MB; ++m)
                             fq[(i + 1) & 1][m] = Tile::rows(sq, 16 * (m1 + m), s1 * D::KS, lane);
+                    keep_order();
 #pragma unroll
                     for (int n = 0; n < NC; ++n) {
-                        if (m0 == 0) {
-                            if constexpr (HI) fx[n] = D::step_exact(S[n], s);
-                            else fs[n] = D::step(S[n], s);
-                        }
+                        if constexpr (!HI)
+                            if (m0 == 0) fs[n] = D::step(S[n], s);
 #pragma unroll
                         for (int m = 0; m < MB; ++m) {
-                            if constexpr (HI) D::mma_aa(o[n][m0 + m], fx[n], fq[i & 1][m]);
+                            if constexpr (HI) D::mma_aa(o[n][m0 + m], fx[s & 1][n], fq[i & 1][m]);
                             else D::mma_ba(o[n][m0 + m], fq[i & 1][m], fs[n]);
                         }
+                        if constexpr (HI)
+                            if (m1 == 0 && s1 < KN) fx[s1 & 1][n] = D::step_exact(S[n], s1);
                     }
-                    SB;
+                    keep_order();
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);
+            keep_order();
             typename D::Fa fp[F::COUNT];
 #pragma unroll
             for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag_hi(mats + kDeltaMatBytes, f, lane);
@@ -487,7 +489,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
                         for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, o[n][m]);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         if (!active) continue;
         // E' = exp(G_C - G) beta T R
         f32x4_t u[NC][4];
@@ -503,7 +505,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
 #pragma unroll
                     for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, false)], fr[n][s]);
                 }
-        __builtin_amdgcn_sched_barrier(0);
+        keep_order();
         if constexpr (MODE == kStates) {
             st* ep = (st*)a.et + ((long long)bh * a.nchunks + c) * a.dv * kDeltaC;
 #pragma unroll
@@ -536,16 +538,14 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
             if (i + 1 < NS * DT / TB)
 #pragma unroll
                 for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
+            keep_order();
             if (s == 0)
 #pragma unroll
                 for (int n = 0; n < NC; ++n)
 #pragma unroll
                     for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
-#pragma unroll
-            for (int t = 0; t < TB; ++t)
-#pragma unroll
-                for (int n = 0; n < NC; ++n) D::mma_ab(S[n][t0 + t], fc[i & 1][t], fu[n][s]);
-            SB;
+            D::template products<TB, NC>(S, t0, fc[i & 1], fu, s);
+            keep_order();
         }
     }
     if (!active) return;
