@@ -25,7 +25,6 @@ namespace ret {
 constexpr int kDeltaC = 64;    // tokens per chunk
 constexpr int kScanCols = 32;  // columns of the state per workgroup of the segment scan
 
-// Per (chunk, b, h): fragments of T and P, then per-token factors.
 // Factors of a chunk (rows of 64): exp(G_i), exp(G_C - G_i) beta_i, exp(G_C - G_i), beta_i, then G_i log2(e) in fp64.
 constexpr int kDeltaFac = 6 * kDeltaC;
 // One triangular 64 x 64 matrix as operand fragments (two bf16 parts, or fp32), those with entries only: bytes reserved.
@@ -45,8 +44,9 @@ struct DeltaArgs {
     float* segM;                 // [B*H][nseg][dk][dk]: transitions
     // gradients
     float* segF;                 // [B*H][nseg][dk][dv]: state gradients of the segments, from their right ends
-    void *s0t, *ds1t;            // [B*H][nchunks][dv][dk] in the input type: states entering, gradients leaving the chunks
-    void *et, *dut;              // [B*H][nchunks][dv][64]: E and dU
+    // in the input type, as blocks of 16 columns (of d_v) x 16 TPS rows: [B*H][nchunks][dv/16][rows/(16 TPS)][1 KB]
+    void *s0t, *ds1t;            // states entering and their gradients leaving the chunks (rows: d_k)
+    void *et, *dut;              // E and dU (rows: the chunk's tokens)
     const void* dout;            // [B, N, H, dv]
     const float* dstate_out;     // [B, H, dk, dv] or null (zeros)
     float* dstate_in;            // or null
@@ -55,7 +55,7 @@ struct DeltaArgs {
     int nchunks, nmats;
     int nseg, seg_chunks;        // segments per sequence and chunks per segment
     int out_bf16, gate_bf16;
-    int p_lo;                    // the forward's P T has its low part (outputs in fp32)
+    int p_lo;                    // the forward's P T has its low parts too (outputs in fp32)
     float scale;
 };
 typedef void (*delta_kernel_t)(DeltaArgs);
@@ -92,6 +92,7 @@ __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0)
 template <int KS>
 struct TriFrags {
     static constexpr int NS = kDeltaC / KS, COUNT = NS == 2 ? 6 : 10;
+    static constexpr int BYTES = COUNT * (NS == 2 ? 2048 : 1024), HI_BYTES = COUNT * 1024;  // with both parts; high only
     __host__ __device__ static constexpr bool lower(int m, int s) { return s * KS <= 16 * m + 15; }
     __host__ __device__ static constexpr bool upper(int m, int s) { return (s + 1) * KS > 16 * m; }
     __host__ __device__ static constexpr int at(int m, int s, bool up) {
@@ -146,29 +147,13 @@ struct DOps<BF16> {
         mfma1(acc, a, b.lo);
         mfma1(acc, a, b.hi);
     }
-    // x[n][m0 + m] += a[m] b[n] over MB x NC tiles, the low parts first: no product right behind one of the same tile
-    template <int MB, int NC, int NT>
-    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB], const Fb (&b)[NC]) {
+    // x[m0 + m] += a[m] b, the low parts first: no product right behind one of the same tile
+    template <int MB, int NT>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NT], int m0, const Fa (&a)[MB], const Fb& b) {
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m) mfma1(x[m0 + m], a[m], b.lo);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n].lo);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n].hi);
-    }
-    template <int MB, int NC, int NT, int NS>
-    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB],
-                                                    const Fb (&b)[NC][NS], int s) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n][s].lo);
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int n = 0; n < NC; ++n) mfma1(x[n][m0 + m], a[m], b[n][s].hi);
+        for (int m = 0; m < MB; ++m) mfma1(x[m0 + m], a[m], b.hi);
     }
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, Fa a, const Fb& b) {
         mfma1(acc, b.lo, a);
@@ -178,6 +163,11 @@ struct DOps<BF16> {
         mfma1(acc, a.hi, b.lo);
         mfma1(acc, a.lo, b.hi);
         mfma1(acc, a.hi, b.hi);
+    }
+    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) {
+        mfma1(acc, b.lo, a.hi);
+        mfma1(acc, b.hi, a.lo);
+        mfma1(acc, b.hi, a.hi);
     }
     // both sides exact
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, Fa a, Fa b) { mfma1(acc, a, b); }
@@ -191,23 +181,31 @@ struct DOps<BF16> {
         mfma1(acc, a.lo, b);
         mfma1(acc, a.hi, b);
     }
-    // what the low part of a workspace matrix adds to b.a^T
-    __device__ static __forceinline__ void mma_lo(f32x4_t& acc, const Fm& a, const Fb& b) { mfma1(acc, b.hi, a.lo); }
     // fragment f of a workspace matrix
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         const u32x4_t* p = reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane;
         return {__builtin_bit_cast(bf16x8_t, p[0]), __builtin_bit_cast(bf16x8_t, p[64])};
     }
-    // the high part alone
+    // of a matrix of high parts only
     __device__ static __forceinline__ Fa mat_frag_hi(const char* m, int f, int lane) {
-        return __builtin_bit_cast(bf16x8_t, (reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane)[0]);
+        return __builtin_bit_cast(bf16x8_t, reinterpret_cast<const u32x4_t*>(m)[f * 64 + lane]);
     }
     // writes the fragment of x: a: the step's first 4 values of this lane, b: its last 4
     __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b, bool lo) {
         const Fb x = split(a, b);
-        u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * 128 + lane;
+        u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * (lo ? 128 : 64) + lane;
         p[0] = __builtin_bit_cast(u32x4_t, x.hi);
         if (lo) p[64] = __builtin_bit_cast(u32x4_t, x.lo);
+    }
+    // A block of 16 TPS rows x 16 columns in accumulators, 16 bytes a lane and 1 KB together (block i of p), and the way
+    // of a lane's part to row n16 of an LDS tile (the block transposed: its rows become columns c0 ..)
+    __device__ static __forceinline__ void blk_store(st* p, int i, int lane, const f32x4_t* x) {
+        *reinterpret_cast<bf16x8_t*>(p + (i * 64 + lane) * 8) = acc_pair(x[0], x[1]);
+    }
+    template <class Tile>
+    __device__ static __forceinline__ void blk_lds(st* lds, int row, int c0, int g4, u32x4_t x) {
+        *reinterpret_cast<uint2*>(lds + Tile::off(row, c0 + g4)) = make_uint2(x[0], x[1]);
+        *reinterpret_cast<uint2*>(lds + Tile::off(row, c0 + 16 + g4)) = make_uint2(x[2], x[3]);
     }
     // LDS tile [rows][W], read by rows and transposed
     template <int W>
@@ -246,31 +244,25 @@ struct DOps<F32> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], acc, 0, 0, 0);
     }
-    template <int MB, int NC, int NT>
-    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB], const Fb (&b)[NC]) {
+    template <int MB, int NT>
+    __device__ static __forceinline__ void products(f32x4_t (&x)[NT], int m0, const Fa (&a)[MB], const Fb& b) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    x[n][m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[n][i], x[n][m0 + m], 0, 0, 0);
-    }
-    template <int MB, int NC, int NT, int NS>
-    __device__ static __forceinline__ void products(f32x4_t (&x)[NC][NT], int m0, const Fa (&a)[MB],
-                                                    const Fb (&b)[NC][NS], int s) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int m = 0; m < MB; ++m)
-#pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    x[n][m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[n][s][i], x[n][m0 + m], 0, 0, 0);
+                x[m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[i], x[m0 + m], 0, 0, 0);
     }
     __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, const Fa& a, const Fa& b) { mma_ab(acc, a, b); }
-    __device__ static __forceinline__ void mma_lo(f32x4_t&, const Fm&, const Fb&) {}
+    __device__ static __forceinline__ void blk_store(st* p, int i, int lane, const f32x4_t* x) {
+        *reinterpret_cast<f32x4_t*>(p + (i * 64 + lane) * 4) = x[0];
+    }
+    template <class Tile>
+    __device__ static __forceinline__ void blk_lds(st* lds, int row, int c0, int g4, u32x4_t x) {
+        *reinterpret_cast<u32x4_t*>(lds + Tile::off(row, c0 + g4)) = x;
+    }
+    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, b, a); }
     typedef f32x4_t Fx;
     template <int NT>
     __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
@@ -302,21 +294,28 @@ struct DOps<F32> {
 };
 
 // 64 rows of W elements of one head moved as 16-byte segments by NT threads: rows past the live ones read as zeros (the
-// buffer resource ends with the last live row), and so do columns past `cols`. Tile column `at` receives column 0.
+// buffer resource ends with the last live row), and so do columns past `cols`. Tile column `at` receives column 0. The
+// requests (get) go out one by one, so that a kernel can spread them over its products.
 template <class E, int W, int NT, class T = typename DOps<E>::template Tile<W>>
 struct DRows {
     typedef typename E::st st;
     static constexpr int EPS = 16 / sizeof(st), SPR = W / EPS, RP = NT / SPR, NP = (kDeltaC + RP - 1) / RP;
     typedef T Tile;
     u32x4_t x[NP];
+    rsrc_t r;
+    int off, step;
     // p: the head's row of the chunk's first token; stride: elements between tokens; live: rows to read (may be <= 0)
-    __device__ __forceinline__ void load(const st* p, int stride, int live, int cols, int tid) {
-        const int bytes = live > 0 ? ((live - 1) * stride + cols) * (int)sizeof(st) : 0;
-        const rsrc_t r = bytes_rsrc(p, bytes);
+    __device__ __forceinline__ void from(const st* p, int stride, int live, int cols, int tid) {
+        r = bytes_rsrc(p, live > 0 ? ((live - 1) * stride + cols) * (int)sizeof(st) : 0);
         const int row = tid / SPR, c = tid % SPR * EPS;
-        const int off = c < cols ? (row * stride + c) * (int)sizeof(st) : 0x40000000;
+        off = c < cols ? (row * stride + c) * (int)sizeof(st) : 0x40000000;
+        step = RP * stride * (int)sizeof(st);
+    }
+    __device__ __forceinline__ void get(int i) { x[i] = buf_load16(r, off, i * step); }
+    __device__ __forceinline__ void load(const st* p, int stride, int live, int cols, int tid) {
+        from(p, stride, live, cols, tid);
 #pragma unroll
-        for (int i = 0; i < NP; ++i) x[i] = buf_load16(r, off, i * RP * stride * (int)sizeof(st));
+        for (int i = 0; i < NP; ++i) get(i);
     }
     __device__ __forceinline__ void store(st* lds, int tid, int at = 0) const {
         const int row = tid / SPR, c = at + tid % SPR * EPS;
@@ -324,6 +323,25 @@ struct DRows {
         for (int i = 0; i < NP; ++i)
             if (NP * RP == kDeltaC || row + i * RP < kDeltaC)
                 *reinterpret_cast<u32x4_t*>(lds + Tile::off(row + i * RP, c)) = x[i];
+    }
+};
+
+// `BYTES` bytes of a workspace matrix (a multiple of 16) moved to LDS by NT threads, as they are.
+template <int BYTES, int NT>
+struct DMat {
+    static constexpr int N = BYTES / 16, NP = (N + NT - 1) / NT;
+    u32x4_t x[NP];
+    const u32x4_t* p;
+    int tid;
+    __device__ __forceinline__ void from(const char* m, int t) {
+        p = reinterpret_cast<const u32x4_t*>(m);
+        tid = t;
+    }
+    __device__ __forceinline__ void get(int i) { x[i] = p[tid + i * NT < N ? tid + i * NT : N - 1]; }
+    __device__ __forceinline__ void store(char* lds) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i)
+            if (N % NT == 0 || tid + i * NT < N) reinterpret_cast<u32x4_t*>(lds)[tid + i * NT] = x[i];
     }
 };
 
@@ -337,13 +355,13 @@ struct DOut {
         r = bytes_rsrc((char*)base + row0 * dv * esz, (rows - 1) * stride + dv * esz);
         off = (lane & 15) * stride + col * esz;
     }
-    __device__ __forceinline__ void put(uint16_t*, int m, int n, f32x4_t x) const {
+    __device__ __forceinline__ void put(uint16_t*, int m, f32x4_t x) const {
         __builtin_amdgcn_raw_buffer_store_b64(
-            __builtin_bit_cast(u32x2_t, make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]))), r, off + 32 * n,
+            __builtin_bit_cast(u32x2_t, make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]))), r, off,
             16 * m * stride, 0);
     }
-    __device__ __forceinline__ void put(float*, int m, int n, f32x4_t x) const {
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), r, off + 64 * n, 16 * m * stride, 0);
+    __device__ __forceinline__ void put(float*, int m, f32x4_t x) const {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), r, off, 16 * m * stride, 0);
     }
 };
 

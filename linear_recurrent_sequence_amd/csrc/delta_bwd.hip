@@ -22,95 +22,105 @@ namespace {
 typedef double f64;
 
 // ---------------------------------------------------------------------------------------------------
-// The chain from the right: one segment of one head, 64 NC columns per workgroup, dS in accumulators. LOCAL: the gradient
-// of the state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise
-// dS_C of each chunk and dU, transposed, and dV; the first segment leaves dstate_in.
+// The chain from the right: one segment of one head, 16 columns per wave, dS in accumulators. LOCAL: the gradient of the
+// state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise dS_C of
+// each chunk and dU, as blocks, and dV; the first segment leaves dstate_in. Built as the forward's chain: requests a chunk
+// ahead between the products of K dS, K in two buffers, Q's product before the second barrier.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NC, int NW>
-constexpr int rchain_waves() {  // as the forward chain's
-    typedef DOps<E> D;
-    const int rows = kDeltaC * (int)sizeof(typename E::st);
-    const int lds = rows * (3 * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 2048;
-    if (NW == 8) return 2 * lds <= 160 * 1024 ? 4 : 2;
-    return (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
-}
-template <class E, int DK, int NC, int NW, bool LOCAL>
-__global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delta_rchain_kernel(DeltaArgs a) {
+template <class E, int DK, int NW, bool LOCAL>
+__global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    constexpr int NT = 64 * NW, COLS = 16 * NC * NW;
+    constexpr int NT = 64 * NW, COLS = 16 * NW;
     typedef DRows<E, DK, NT> Rows;
-    typedef DRows<E, 16 * NC, 64, typename D::template Tile<COLS>> ORows;  // a wave's own columns of dO
+    typedef DRows<E, 16, 64, typename D::template Tile<COLS>> ORows;  // a wave's own columns of dO
     typedef typename Rows::Tile Tile;
     typedef typename ORows::Tile OTile;
     typedef TriFrags<D::KS> F;
-    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS;
-    constexpr int MB = NC == 2 ? 2 : 4, MG = 4 / MB, TB = DT < MB ? DT : MB;
+    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS, TB = DT < 4 ? DT : 4;
     __shared__ __align__(16) st sk[2][kDeltaC * Tile::LD];
     __shared__ __align__(16) st sq[kDeltaC * Tile::LD];
     __shared__ __align__(16) st so[kDeltaC * OTile::LD];
+    __shared__ __align__(16) char sm[F::BYTES], sp[F::BYTES];  // Tr^T, Pr^T
     __shared__ __align__(16) float sf[2][256];
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
+    const int g4 = 4 * (lane >> 4);
     const DeltaBlock blk = delta_block(a, (a.dv + COLS - 1) / COLS);
     if (blk.bh >= a.B * a.H) return;
     const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
-    const int mine = 16 * NC * w, col0 = blk.cb * COLS + mine;  // the wave's columns: in the tile, of d_v
+    const int mine = 16 * w, col0 = blk.cb * COLS + mine;  // the wave's columns: in the tile, of d_v
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
-    const bool active = col0 < a.dv;
+    const bool active = col0 < a.dv;  // (a wave without columns computes on zeros)
     if (LOCAL && seg == 0) return;  // no one is left of it
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
-    f32x4_t S[NC][DT];
+    f32x4_t S[DT];
     const float* sin = nullptr;
     if (LOCAL ? seg == a.nseg - 1 : a.nseg == 1)
         sin = a.dstate_out ? a.dstate_out + (long long)bh * DK * a.dv : nullptr;
     else if (!LOCAL) sin = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const bool in = sin && col0 + 16 * n < a.dv;
-        const float* p = in ? sin + (long long)g4 * a.dv + col0 + 16 * n + n16 : nullptr;
+    for (int t = 0; t < DT; ++t) S[t] = zero;
+    if (sin && active) {
+        const float* p = sin + (long long)g4 * a.dv + col0 + n16;
 #pragma unroll
-        for (int t = 0; t < DT; ++t) S[n][t] = zero;
-        if (in)
+        for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][t][i] = p[(long long)(16 * t + i) * a.dv];
+            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(16 * t + i) * a.dv];
     }
     Rows rk, rq;
     ORows ro;
+    DMat<F::BYTES, NT> rm, rp;
     float ff = 0.f;
+    const float* fp;
     const st* kp = (const st*)a.k + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* qp = (const st*)a.q + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* op = (const st*)a.dout + (((long long)b * a.N) * a.H + h) * a.dv + col0;
-    auto fetch = [&](int c) {
+    auto from = [&](int c) {  // the places of chunk c's operands
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
-        rk.load(kp + base, a.Hk * DK, live, DK, tid);
-        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 255)];
-        rq.load(qp + base, a.Hk * DK, live, DK, tid);
-        ro.load(op + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, active ? live : 0, a.dv - col0, lane);
+        const char* mats = a.mats + ((long long)bh * a.nchunks + c) * a.nmats * kDeltaMatBytes;
+        rk.from(kp + base, a.Hk * DK, live, DK, tid);
+        rq.from(qp + base, a.Hk * DK, live, DK, tid);
+        ro.from(op + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, active ? live : 0, a.dv - col0, lane);
+        rm.from(mats + kDeltaMatBytes, tid);
+        rp.from(mats + 2 * kDeltaMatBytes, tid);
+        fp = a.fac + ((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 255);
+    };
+    constexpr int NK = Rows::NP, NO = ORows::NP, NM = DMat<F::BYTES, NT>::NP, NL = 2 * NK + NO + 2 * NM + 1;
+    auto request = [&](int i) {
+        if (i < NK) rk.get(i);
+        else if (i < NK + NM) rp.get(i - NK);
+        else if (i < NK + 2 * NM) rm.get(i - NK - NM);
+        else if (i < NK + 2 * NM + 1) ff = *fp;
+        else if (i < NL - NK) ro.get(i - NK - 2 * NM - 1);
+        else rq.get(i - (NL - NK));
+    };
+    auto stage = [&](int p) {
+        rk.store(sk[p], tid);
+        rq.store(sq, tid);
+        ro.store(so, lane, mine);
+        if (tid < 256) sf[p][tid] = ff;
     };
     // Rows of dV of chunk c, 16 bytes a lane, from the wave's own columns of the tile that held dO (zero: zeros); rows past
     // the live ones are zero. 32-bit outputs go from the registers.
-    constexpr int SPV = 2 * NC;  // 16-byte segments per row of the wave's columns
     auto store_rows = [&](int c, bool blank) {
 #pragma unroll
-        for (int i = 0; i < SPV; ++i) {
-            const int row = (lane + 64 * i) / SPV, cc = (lane + 64 * i) % SPV * 8, t = c * kDeltaC + row;
-            if (t >= a.N || col0 + cc >= a.dv) continue;
+        for (int i = 0; i < 2; ++i) {
+            const int row = (lane + 64 * i) / 2, cc = lane % 2 * 8, t = c * kDeltaC + row;
+            if (t >= a.N) continue;
             u32x4_t x = {0, 0, 0, 0};
             if (!blank && t < len) x = *reinterpret_cast<const u32x4_t*>(so + OTile::off(row, mine + cc));
             *reinterpret_cast<u32x4_t*>((uint16_t*)a.dv_ + (((long long)b * a.N + t) * a.H + h) * a.dv + col0 + cc) = x;
         }
     };
-    auto store_f32 = [&](int c, int m, int n, const f32x4_t& x) {
+    auto store_f32 = [&](int c, int m, const f32x4_t& x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = c * kDeltaC + 16 * m + g4 + i;
-            if (t >= a.N || col0 + 16 * n >= a.dv) continue;
-            ((float*)a.dv_)[(((long long)b * a.N + t) * a.H + h) * a.dv + col0 + 16 * n + n16] = t < len ? x[i] : 0.f;
+            if (t >= a.N) continue;
+            ((float*)a.dv_)[(((long long)b * a.N + t) * a.H + h) * a.dv + col0 + n16] = t < len ? x[i] : 0.f;
         }
     };
     const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
@@ -120,163 +130,135 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                 if (a.out_bf16) store_rows(c, true);
                 else
 #pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) store_f32(c, m, n, zero);
+                    for (int m = 0; m < 4; ++m) store_f32(c, m, zero);
             }
     }
     if (c0 < cend) {
-        fetch(cend - 1);
-        rk.store(sk[0], tid);
-        rq.store(sq, tid);
-        if (active) ro.store(so, lane, mine);
-        if (tid < 256) sf[0][tid] = ff;
+        from(cend - 1);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) request(i);
+        stage(0);
     }
     for (int c = cend - 1, p = 0; c >= c0; --c, p ^= 1) {
         __syncthreads();
-        const bool more = c > c0;
-        fetch(more ? c - 1 : c);  // unconditional: see the forward chain
+        rm.store(sm);  // everyone is past the last chunk's products with them
+        rp.store(sp);
+        from(max(c - 1, c0));
         const long long unit = (long long)bh * a.nchunks + c;
-        const char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
         const st* K = sk[p];
-        typename D::Fm fp[F::COUNT], ft[F::COUNT];
+        if constexpr (!LOCAL) {
+            st* out = (st*)a.ds1t + (unit * a.dv + col0) * DK;
+            if (active)
 #pragma unroll
-        for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag(mats + 2 * kDeltaMatBytes, f, lane);
-        f32x4_t x[NC][4];
+                for (int t = 0; t < DT / D::TPS; ++t) D::blk_store(out, t, lane, &S[D::TPS * t]);
+        }
+        // W = exp(G_C - G) K dS + Pr^T dO
+        f32x4_t x[4];
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+        for (int m = 0; m < 4; ++m) x[m] = zero;
+        {
+            typename D::Fa fk[2][4];
+            typename D::Fb fs[2];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) x[n][m] = zero;
-        if (active) {
-            if constexpr (!LOCAL) {
-                st* sp = (st*)a.ds1t + unit * a.dv * DK;
+            for (int m = 0; m < 4; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+            fs[0] = D::step(S, 0);
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    if (col0 + 16 * n < a.dv)
+            for (int s = 0; s < KN; ++s) {
+                if (s + 1 < KN)
 #pragma unroll
-                        for (int t = 0; t < DT; ++t)
-                            store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
-            }
-            // W = exp(G_C - G) K dS + Pr^T dO
-            typename D::Fa fk[2][MB];
-            typename D::Fb fs[2][NC];
+                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, (s + 1) * D::KS, lane);
 #pragma unroll
-            for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
-#pragma unroll
-            for (int n = 0; n < NC; ++n) fs[0][n] = D::step(S[n], 0);
-#pragma unroll
-            for (int i = 0; i < KN * MG; ++i) {
-                const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
-                if (i + 1 < KN * MG)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m)
-                        fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
+                for (int i = NL * s / KN; i < NL * (s + 1) / KN; ++i) request(i);
                 keep_order();
-                D::template products<MB, NC>(x, m0, fk[i & 1], fs[s & 1]);
-                if (m1 == 0 && s1 < KN)
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) fs[s1 & 1][n] = D::step(S[n], s1);
+                D::template products<4>(x, 0, fk[s & 1], fs[s & 1]);
+                if (s + 1 < KN) fs[(s + 1) & 1] = D::step(S, s + 1);
                 keep_order();
             }
-#pragma unroll
-            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats + kDeltaMatBytes, f, lane);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf[p] + 128 + 16 * m + g4);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) x[n][m] *= ta;
-            }
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                typename D::Fa fd[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) fd[n] = OTile::cols(so, s * D::KS, mine + 16 * n, lane);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (F::upper(m, s)) {
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) D::mma_mx(x[n][m], fp[F::at(m, s, true)], fd[n]);
-                    }
-            }
         }
-        keep_order();
-        if (more) {
-            rk.store(sk[p ^ 1], tid);
-            if (tid < 256) sf[p ^ 1][tid] = ff;
-        }
-        keep_order();
-        f32x4_t u[NC][4];
-        const float end = sf[p][63];
-        if (active) {
-            // dU = Tr^T W
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) u[n][m] = zero;
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                typename D::Fb fw[NC];
-#pragma unroll
-                for (int n = 0; n < NC; ++n) fw[n] = D::step(x[n], s);
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (F::upper(m, s)) {
-#pragma unroll
-                        for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, true)], fw[n]);
-                    }
-            }
-            keep_order();
-            // dS = exp(G_C) dS + Q^T (scale exp(G) dO) - K^T (exp(G) beta dU)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4_t ga = a.scale * *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) x[n][m] = ga * OTile::acc(so, m, mine + 16 * n, lane);
-            }
-            typename D::Fb fd[NC][NS];
-#pragma unroll
-            for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int s = 0; s < NS; ++s) fd[n][s] = D::step(x[n], s);
+        for (int m = 0; m < 4; ++m) x[m] *= *reinterpret_cast<const f32x4_t*>(sf[p] + 128 + 16 * m + g4);
+        // S += X^T F, tile by tile, the first time scaled
+        auto update = [&](const st* X, const typename D::Fb (&f)[NS], bool scaled, float end) {
             typename D::Fa fc[2][TB];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(sq, 0, 16 * t, lane);
+            for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(X, 0, 16 * t, lane);
 #pragma unroll
             for (int i = 0; i < NS * DT / TB; ++i) {
                 const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
                 if (i + 1 < NS * DT / TB)
 #pragma unroll
-                    for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(sq, s1 * D::KS, 16 * (t1 + t), lane);
+                    for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(X, s1 * D::KS, 16 * (t1 + t), lane);
                 keep_order();
-                if (s == 0)
+                if (scaled && s == 0)
 #pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
-                D::template products<TB, NC>(S, t0, fc[i & 1], fd, s);
+                    for (int t = 0; t < TB; ++t) S[t0 + t] *= end;
+                D::template products<TB>(S, t0, fc[i & 1], f[s]);
                 keep_order();
             }
-            if constexpr (!LOCAL) {
-                wave_fence();  // the last reads of dO come before
-                st* up = (st*)a.dut + unit * a.dv * kDeltaC;
+        };
+        typename D::Fx fd[NS];  // dO as it came
+        {                       // dS = exp(G_C) dS + Q^T (scale exp(G) dO) ..
+            f32x4_t y[4];
+            typename D::Fb f[NS];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) y[m] = OTile::acc(so, m, mine, lane);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) fd[s] = D::step_exact(y, s);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) y[m] *= a.scale * *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
+#pragma unroll
+            for (int s = 0; s < NS; ++s) f[s] = D::step(y, s);
+            update(sq, f, true, sf[p][63]);
+        }
+        __syncthreads();  // the matrices are there, and everyone is done with Q
+        {
+            typename D::Fm fm[F::COUNT];
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) fm[f] = D::mat_frag(sp, f, lane);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (F::upper(m, s)) D::mma_mx(x[m], fm[F::at(m, s, true)], fd[s]);
+        }
+        // dU = Tr^T W
+        f32x4_t u[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) u[m] = zero;
+        {
+            typename D::Fm fm[F::COUNT];
+#pragma unroll
+            for (int f = 0; f < F::COUNT; ++f) fm[f] = D::mat_frag(sm, f, lane);
+            typename D::Fb fw[NS];
+#pragma unroll
+            for (int s = 0; s < NS; ++s) fw[s] = D::step(x, s);
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (F::upper(m, s)) D::mma_mb(u[m], fm[F::at(m, s, true)], fw[s]);
+        }
+        if constexpr (!LOCAL) {
+            if (active) {
+                st* out = (st*)a.dut + (unit * a.dv + col0) * kDeltaC;
+#pragma unroll
+                for (int s = 0; s < NS; ++s) D::blk_store(out, s, lane, &u[D::TPS * s]);
                 const bool rows = sizeof(st) == 2 && a.out_bf16;
+                wave_fence();  // the last reads of dO come before
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
+                for (int m = 0; m < 4; ++m) {
+                    const f32x4_t y = *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4) * u[m];
+                    if constexpr (sizeof(st) == 2) {
+                        if (rows) {  // over dO, in the wave's own columns
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        if (col0 + 16 * n < a.dv) store4(up + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
-                        const f32x4_t y = *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4) * u[n][m];
-                        if constexpr (sizeof(st) == 2) {
-                            if (rows) {  // over dO, in the wave's own columns
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const int col = mine + 16 * n + n16;
-                                    so[OTile::off(16 * m + g4 + i, col & ~3) + (col & 3)] = f32_to_bf16(y[i]);
-                                }
+                            for (int i = 0; i < 4; ++i) {
+                                const int col = mine + n16;
+                                so[OTile::off(16 * m + g4 + i, col & ~3) + (col & 3)] = f32_to_bf16(y[i]);
                             }
                         }
-                        if (!rows) store_f32(c, m, n, y);
                     }
+                    if (!rows) store_f32(c, m, y);
+                }
                 if (rows) {
                     wave_fence();  // the rows are read in another order
                     store_rows(c, false);
@@ -284,52 +266,27 @@ __global__ __launch_bounds__(64 * NW, (rchain_waves<E, DK, NC, NW>())) void delt
                 }
             }
         }
-        if (more) {
-            __syncthreads();  // everyone is done with Q
-            rq.store(sq, tid);
-            if (active) ro.store(so, lane, mine);
-        }
-        if (!active) continue;
+        // .. - K^T (exp(G) beta dU)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-            const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
-            const f32x4_t be = *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4);
+        for (int m = 0; m < 4; ++m)
+            u[m] *= -(*reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4) *
+                      *reinterpret_cast<const f32x4_t*>(sf[p] + 192 + 16 * m + g4));
+        typename D::Fb fu[NS];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) u[n][m] *= -(ga * be);
-        }
-        typename D::Fb fu[NC][NS];
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int s = 0; s < NS; ++s) fu[n][s] = D::step(u[n], s);
-        typename D::Fa fc[2][TB];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, 16 * t, lane);
-#pragma unroll
-        for (int i = 0; i < NS * DT / TB; ++i) {
-            const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
-            if (i + 1 < NS * DT / TB)
-#pragma unroll
-                for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
-            keep_order();
-            D::template products<TB, NC>(S, t0, fc[i & 1], fu, s);
-            keep_order();
-        }
+        for (int s = 0; s < NS; ++s) fu[s] = D::step(u, s);
+        update(K, fu, false, 0.f);
+        stage(p ^ 1);
     }
     if (!active) return;
     float* out = nullptr;
     if (LOCAL) out = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
     else if (seg == 0 && a.dstate_in) out = a.dstate_in + (long long)bh * DK * a.dv;
     if (!out) return;
+    out += (long long)g4 * a.dv + col0 + n16;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        if (col0 + 16 * n >= a.dv) continue;
-        float* p = out + (long long)g4 * a.dv + col0 + 16 * n + n16;
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[(long long)(16 * t + i) * a.dv] = S[n][t][i];
-    }
+        for (int i = 0; i < 4; ++i) out[(long long)(16 * t + i) * a.dv] = S[t][i];
 }
 
 // R rows of W elements to an LDS tile by NT threads: rows at or past `rows` and columns at or past `cols` are zero.
@@ -354,6 +311,30 @@ struct GRows {
             const int s = tid + i * NT;
             if (R * SPR % NT == 0 || s < R * SPR)
                 *reinterpret_cast<u32x4_t*>(lds + Tile::off(s / SPR, s % SPR * EPS)) = x[i];
+        }
+    }
+};
+
+// Blocks of 16 columns x R rows of an array stored by blk_store, VB columns of them, to an LDS tile [VB][R] by NT threads;
+// columns at or past `cols` are zero.
+template <class E, int R, int VB, int NT>
+struct GBlocks {
+    typedef typename E::st st;
+    typedef DOps<E> D;
+    static constexpr int PER = R / (16 * D::TPS), N = VB / 16 * PER * 64, NP = (N + NT - 1) / NT;
+    typedef typename D::template Tile<R> Tile;
+    u32x4_t x[NP];
+    __device__ __forceinline__ void load(const st* p, int cols, int tid) {
+        const rsrc_t r = bytes_rsrc(p, cols * R * (int)sizeof(st));
+#pragma unroll
+        for (int i = 0; i < NP; ++i) x[i] = buf_load16(r, 16 * (tid + i * NT), 0);
+    }
+    __device__ __forceinline__ void store(st* lds, int tid) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int s = tid + i * NT, blk = s / 64, lane = s % 64;
+            if (N % NT == 0 || s < N)
+                D::template blk_lds<Tile>(lds, blk / PER * 16 + (lane & 15), blk % PER * 16 * D::TPS, 4 * (lane >> 4), x[i]);
         }
     }
 };
@@ -437,9 +418,9 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) M1[j] = M2[j] = zero;
         float dot = 0.f;
-        GRows<E, VB, DK, NT> rs, rd;
+        GBlocks<E, DK, VB, NT> rs, rd;
         GRows<E, kDeltaC, VB, NT> ro;
-        GRows<E, VB, kDeltaC, NT> re, ru;
+        GBlocks<E, kDeltaC, VB, NT> re, ru;
         const st* sp = (const st*)a.s0t + unit * a.dv * DK;
         const st* dp = (const st*)a.ds1t + unit * a.dv * DK;
         const st* ep = (const st*)a.et + unit * a.dv * kDeltaC;
@@ -447,11 +428,11 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
         const st* op = (const st*)a.dout + (((long long)b * a.N + t0) * a.H + h) * a.dv;
         auto fetch = [&](int v0) {
             const int nv = min(VB, a.dv - v0);
-            rs.load(sp + (long long)v0 * DK, DK, nv, DK, tid);
-            rd.load(dp + (long long)v0 * DK, DK, nv, DK, tid);
+            rs.load(sp + (long long)v0 * DK, nv, tid);
+            rd.load(dp + (long long)v0 * DK, nv, tid);
             ro.load(op + v0, a.H * a.dv, live, nv, tid);
-            re.load(ep + v0 * kDeltaC, kDeltaC, nv, kDeltaC, tid);
-            ru.load(up + v0 * kDeltaC, kDeltaC, nv, kDeltaC, tid);
+            re.load(ep + v0 * kDeltaC, nv, tid);
+            ru.load(up + v0 * kDeltaC, nv, tid);
         };
         fetch(0);
         const float* f = a.fac + unit * kDeltaFac;
@@ -596,13 +577,12 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
     constexpr int NW = DK * sizeof(typename E::st) > 256 ? 8 : 4;  // half of d_k per wave where a row is long
-    constexpr bool WIDE = DK * sizeof(typename E::st) >= 256;
-    if (o->cols == 64) {
-        o->rlocal = delta_rchain_kernel<E, DK, 1, 4, true>;
-        o->rfull = delta_rchain_kernel<E, DK, 1, 4, false>;
+    if (dv <= 64) {  // as the forward's
+        o->rlocal = delta_rchain_kernel<E, DK, 4, true>;
+        o->rfull = delta_rchain_kernel<E, DK, 4, false>;
     } else {
-        o->rlocal = delta_rchain_kernel<E, DK, WIDE ? 1 : 2, WIDE ? 8 : 4, true>;
-        o->rfull = delta_rchain_kernel<E, DK, WIDE ? 1 : 2, WIDE ? 8 : 4, false>;
+        o->rlocal = delta_rchain_kernel<E, DK, 8, true>;
+        o->rfull = delta_rchain_kernel<E, DK, 8, false>;
     }
     o->grad = delta_grad_kernel<E, DK, NW>;
     o->grad_threads = 64 * NW;

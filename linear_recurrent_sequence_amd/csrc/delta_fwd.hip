@@ -235,33 +235,26 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
 }
 
 // ---------------------------------------------------------------------------------------------------
-// delta_chain: one segment of one head, 64 NC columns per workgroup (16 NC per wave), the state in accumulators.
-// LOCAL: the segment's end state from zero (columns of V; segment 0 starts from state_in) or its transition (columns of
-// the identity, V = 0), into segE / segM. Otherwise the outputs, and after the last segment the final state.
+// delta_chain: one segment of one head, 16 columns per wave, the state in accumulators. Columns are independent: what the
+// waves of a workgroup share are the rows of K and Q and the matrices, which go through LDS once for all of them.
+//   kFull: outputs (bf16 from bf16 input, else fp32); kFullF32: BF16 input, F32 output. After the last segment the state.
+//   kLocal / kLocalRaw (with Ts / with T): the segment's end state from zero (columns of V; segment 0 starts from state_in)
+//     into segE, or its transition (columns of the identity, V = 0) into segM.
+//   kStates (with T): the states entering the chunks and E, for the gradients.
+// A step: Y = K S, between its products the requests for everything the next chunk needs, into registers; R; O from
+// Q S and P T; E; the state; then the registers go to LDS. K has two buffers, so that nothing but the first barrier of a
+// chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave stages the
+// columns of V it owns. Requests are never conditional: where two branches join, their registers would be waited for.
+// Fragments of the next reduction step are read ahead of a step's products.
 // ---------------------------------------------------------------------------------------------------
-// A step's order keeps registers few and every latency behind work: the next chunk's rows are requested first; Y and R;
-// then K and V of the next chunk go to LDS (K has two buffers; a wave stages the columns of V it owns, so no one else
-// reads them); Q S; a barrier frees Q's buffer; O; E; the state. Fragments of one reduction
-// step are read while the products of the step before run.
-// kFull: outputs (bf16 from bf16 input, else fp32); kFullF32: BF16 input, F32 output; kLocal / kLocalRaw: end state or
-// transition, with Ts / with T; kStates: with T, the states entering the chunks and E, for the gradients.
 enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
-// Waves per SIMD that the LDS leaves room for (at most 2: the state and the fragments in flight take half the registers).
-template <class E, int DK, int NC, int NW, int MODE>
-constexpr int chain_waves() {
-    typedef DOps<E> D;
-    const int rows = kDeltaC * (int)sizeof(typename E::st);
-    const int lds = rows * ((MODE <= kFullF32 ? 3 : 2) * D::template Tile<DK>::LD + D::template Tile<16 * NC * NW>::LD) + 1024;
-    if (NW == 8) return 2 * lds <= 160 * 1024 ? 4 : 2;
-    return (2 * lds <= 160 * 1024 && (sizeof(typename E::st) == 2 || DK * NC <= 64)) ? 2 : 1;
-}
-template <class E, int DK, int NC, int NW, int MODE>
-__global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void delta_chain_kernel(DeltaArgs a) {
+template <class E, int DK, int NW, int MODE>
+__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    constexpr int NT = 64 * NW, COLS = 16 * NC * NW;
+    constexpr int NT = 64 * NW, COLS = 16 * NW;
     typedef DRows<E, DK, NT> Rows;
-    typedef DRows<E, 16 * NC, 64, typename D::template Tile<COLS>> VRows;  // a wave's own columns
+    typedef DRows<E, 16, 64, typename D::template Tile<COLS>> VRows;  // a wave's own columns
     typedef typename Rows::Tile Tile;
     typedef typename VRows::Tile VTile;
     typedef TriFrags<D::KS> F;
@@ -270,268 +263,224 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
     constexpr bool HI = MODE == kFull && sizeof(st) == 2;  // outputs in bf16: the high parts of S and P T suffice, whose
                                                            // rounding is like the output's own
     typedef typename std::conditional<HI, uint16_t, float>::type out_t;
-    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS;
-    constexpr int MB = NC == 2 ? 2 : 4, MG = 4 / MB;  // token tiles whose fragments are read together: 8 products' worth
+    constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS, TB = DT < 4 ? DT : 4;
+    constexpr int PB = FULL ? (HI ? F::HI_BYTES : F::BYTES) : 16;
     __shared__ __align__(16) st sk[2][kDeltaC * Tile::LD];
     __shared__ __align__(16) st sq[FULL ? kDeltaC * Tile::LD : 16];
     __shared__ __align__(16) st sv[kDeltaC * VTile::LD];
+    __shared__ __align__(16) char sm[F::BYTES];  // Ts (or T)
+    __shared__ __align__(16) char sp[PB];        // P T
     __shared__ __align__(16) float sf[2][128];
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
+    const int g4 = 4 * (lane >> 4);
     const int nE = (a.dv + COLS - 1) / COLS;  // workgroups over d_v; a local pass has those of d_k behind them
     const DeltaBlock blk = delta_block(a, nE + (LOCAL ? (DK + COLS - 1) / COLS : 0));
     if (blk.bh >= a.B * a.H) return;
     const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
     const bool trans = LOCAL && blk.cb >= nE;
     const int width = trans ? DK : a.dv;
-    const int col0 = (blk.cb - (trans ? nE : 0)) * COLS + w * 16 * NC;
+    const int col0 = (blk.cb - (trans ? nE : 0)) * COLS + 16 * w;
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
-    const bool active = col0 < width;
+    const bool active = col0 < width;  // (a wave without columns computes on zeros)
     // segment 0's end state is known, and no one asks for the last one's
     if (LOCAL && (trans ? seg == 0 : seg == a.nseg - 1)) return;
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
-    f32x4_t S[NC][DT];
+    f32x4_t S[DT];
     const float* sin = nullptr;
     if (!LOCAL) sin = a.nseg > 1 ? a.segE + ((long long)bh * a.nseg + seg) * DK * a.dv : nullptr;
     if (!LOCAL && a.nseg == 1) sin = a.state_in ? a.state_in + (long long)bh * DK * a.dv : nullptr;
     if (LOCAL && seg == 0 && !trans && a.state_in) sin = a.state_in + (long long)bh * DK * a.dv;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int col = col0 + 16 * n + n16;
-        const bool in = sin && col0 + 16 * n < width;
-        const float* p = in ? sin + (long long)g4 * a.dv + col : nullptr;
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S[t][i] = trans && 16 * t + g4 + i == col0 + n16 ? 1.f : 0.f;
+    if (sin && active) {
+        const float* p = sin + (long long)g4 * a.dv + col0 + n16;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[n][t][i] = trans && 16 * t + g4 + i == col ? 1.f : 0.f;
-        if (in)
-#pragma unroll
-            for (int t = 0; t < DT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[n][t][i] = p[(long long)(16 * t + i) * a.dv];
+            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(16 * t + i) * a.dv];
     }
 
     Rows rk, rq;
     VRows rv;
+    DMat<F::BYTES, NT> rm;
+    DMat<PB, NT> rp;
     float ff = 0.f;
+    const float* fp;
     const st* kp = (const st*)a.k + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* qp = (const st*)a.q + (((long long)b * a.N) * a.Hk + hk) * DK;
     const st* vp = (const st*)a.v + (((long long)b * a.N) * a.H + h) * a.dv + col0;
-    auto fetch = [&](int c) {
+    auto from = [&](int c) {  // the places of chunk c's operands
         const int live = min(kDeltaC, len - c * kDeltaC);
         const long long base = (long long)c * kDeltaC * a.Hk * DK;
-        rk.load(kp + base, a.Hk * DK, live, DK, tid);
-        rv.load(vp + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, !trans && active ? live : 0, a.dv - col0, lane);
-        if constexpr (FULL) rq.load(qp + base, a.Hk * DK, live, DK, tid);
-        ff = a.fac[((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 127)];
+        const char* mats = a.mats + ((long long)bh * a.nchunks + c) * a.nmats * kDeltaMatBytes;
+        rk.from(kp + base, a.Hk * DK, live, DK, tid);
+        rv.from(vp + (long long)c * kDeltaC * a.H * a.dv, a.H * a.dv, !trans && active ? live : 0, a.dv - col0, lane);
+        if constexpr (FULL) rq.from(qp + base, a.Hk * DK, live, DK, tid);
+        rm.from(mats, tid);
+        if constexpr (FULL) rp.from(mats + kDeltaMatBytes, tid);
+        fp = a.fac + ((long long)bh * a.nchunks + c) * kDeltaFac + (tid & 127);
+    };
+    constexpr int NK = Rows::NP, NV = VRows::NP, NM = DMat<F::BYTES, NT>::NP, NP = FULL ? DMat<PB, NT>::NP : 0;
+    constexpr int NQ = FULL ? Rows::NP : 0, NL = NK + NV + NM + NP + NQ + 1;
+    auto request = [&](int i) {
+        if (i < NK) rk.get(i);
+        else if (i < NK + NV) rv.get(i - NK);
+        else if (i < NK + NV + NM) rm.get(i - NK - NV);
+        else if (i < NK + NV + NM + 1) ff = *fp;
+        else if (i < NK + NV + NM + 1 + NP) rp.get(i - NK - NV - NM - 1);
+        else rq.get(i - NK - NV - NM - 1 - NP);
     };
     auto stage = [&](int p) {
         rk.store(sk[p], tid);
-        if (!trans && active) rv.store(sv, lane, 16 * NC * w);
+        rv.store(sv, lane, 16 * w);
         if (tid < 128) sf[p][tid] = ff;
+        if constexpr (FULL) rq.store(sq, tid);
     };
     const int cend = min(c1, (len + kDeltaC - 1) / kDeltaC);  // chunks with live tokens
     if (c0 < cend) {
-        fetch(c0);
+        from(c0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) request(i);
         stage(0);
-        if constexpr (FULL) rq.store(sq, tid);
     }
     for (int c = c0, p = 0; c < cend; ++c, p ^= 1) {
         __syncthreads();
-        const bool more = c + 1 < cend;
-        // (the last chunk again at the end: a conditional request would make its registers wait where the branches join)
-        fetch(more ? c + 1 : c);
-        const char* mats = a.mats + ((long long)bh * a.nchunks + c) * a.nmats * kDeltaMatBytes;
+        rm.store(sm);  // everyone is past the last chunk's products with them
+        if constexpr (FULL) rp.store(sp);
+        from(min(c + 1, cend - 1));
         const st* K = sk[p];
-        f32x4_t y[NC][4];
+        if constexpr (MODE == kStates) {
+            st* out = (st*)a.s0t + (((long long)bh * a.nchunks + c) * a.dv + col0) * DK;
+            if (active)
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+                for (int t = 0; t < DT / D::TPS; ++t) D::blk_store(out, t, lane, &S[D::TPS * t]);
+        }
+        f32x4_t y[4];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) y[n][m] = zero;
-        if (active) {
-            if constexpr (MODE == kStates) {
-                st* sp = (st*)a.s0t + ((long long)bh * a.nchunks + c) * a.dv * DK;
+        for (int m = 0; m < 4; ++m) y[m] = zero;
+        {  // Y = K S
+            typename D::Fa fk[2][4];
+            typename D::Fb fs[2];
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    if (col0 + 16 * n < width)
+            for (int m = 0; m < 4; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+            fs[0] = D::step(S, 0);
 #pragma unroll
-                        for (int t = 0; t < DT; ++t)
-                            store4(sp + (long long)(col0 + 16 * n + n16) * DK + 16 * t + g4, S[n][t]);
-            }
-            // Y = K S
-            typename D::Fa fk[2][MB];
-            typename D::Fb fs[2][NC];
+            for (int s = 0; s < KN; ++s) {
+                if (s + 1 < KN)
 #pragma unroll
-            for (int m = 0; m < MB; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
+                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, (s + 1) * D::KS, lane);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) fs[0][n] = D::step(S[n], 0);
-#pragma unroll
-            for (int i = 0; i < KN * MG; ++i) {
-                const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
-                if (i + 1 < KN * MG)
-#pragma unroll
-                    for (int m = 0; m < MB; ++m)
-                        fk[(i + 1) & 1][m] = Tile::rows(K, 16 * (m1 + m), s1 * D::KS, lane);
+                for (int i = NL * s / KN; i < NL * (s + 1) / KN; ++i) request(i);
                 keep_order();
-                D::template products<MB, NC>(y, m0, fk[i & 1], fs[s & 1]);
-                if (m1 == 0 && s1 < KN)
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) fs[s1 & 1][n] = D::step(S[n], s1);
+                D::template products<4>(y, 0, fk[s & 1], fs[s & 1]);
+                if (s + 1 < KN) fs[(s + 1) & 1] = D::step(S, s + 1);
                 keep_order();
-            }
-            // R = V - exp(G) Y
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4_t ga = *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) {
-                    const f32x4_t v = trans ? zero : VTile::acc(sv, m, 16 * NC * w + 16 * n, lane);
-                    y[n][m] = v - ga * y[n][m];
-                }
             }
         }
-        keep_order();
-        if (more) stage(p ^ 1);
-        keep_order();
-        typename D::Fm ft[F::COUNT];
-        if constexpr (!FULL)
+        // R = V - exp(G) Y
 #pragma unroll
-            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats, f, lane);
-        typename D::Fb fr[NC][NS];
+        for (int m = 0; m < 4; ++m)
+            y[m] = VTile::acc(sv, m, 16 * w, lane) - *reinterpret_cast<const f32x4_t*>(sf[p] + 16 * m + g4) * y[m];
+        typename D::Fb fr[NS];
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int s = 0; s < NS; ++s) fr[n][s] = D::step(y[n], s);
+        for (int s = 0; s < NS; ++s) fr[s] = D::step(y, s);
+        f32x4_t o[4];
         if constexpr (FULL) {
             // O^T = scale exp(G) (Q S)^T + R^T (P T)^T: a lane holds 4 columns of token 16 m + n16
-            f32x4_t o[NC][4];
-            if (active) {
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
+            for (int m = 0; m < 4; ++m) o[m] = zero;
+            typename D::Fa fq[2][4];
+            typename D::Fx fx[2];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) o[n][m] = zero;
-                typename D::Fa fq[2][MB];
-                typename D::Fb fs[NC];
-                typename D::Fx fx[2][NC];
+            for (int m = 0; m < 4; ++m) fq[0][m] = Tile::rows(sq, 16 * m, 0, lane);
+            if constexpr (HI) fx[0] = D::step_exact(S, 0);
 #pragma unroll
-                for (int m = 0; m < MB; ++m) fq[0][m] = Tile::rows(sq, 16 * m, 0, lane);
-                if constexpr (HI)
+            for (int s = 0; s < KN; ++s) {
+                if (s + 1 < KN)
 #pragma unroll
-                    for (int n = 0; n < NC; ++n) fx[0][n] = D::step_exact(S[n], 0);
+                    for (int m = 0; m < 4; ++m) fq[(s + 1) & 1][m] = Tile::rows(sq, 16 * m, (s + 1) * D::KS, lane);
+                keep_order();
+                if constexpr (HI) {
 #pragma unroll
-                for (int i = 0; i < KN * MG; ++i) {
-                    const int s = i / MG, m0 = i % MG * MB, s1 = (i + 1) / MG, m1 = (i + 1) % MG * MB;
-                    if (i + 1 < KN * MG)
+                    for (int m = 0; m < 4; ++m) D::mma_aa(o[m], fx[s & 1], fq[s & 1][m]);
+                    if (s + 1 < KN) fx[(s + 1) & 1] = D::step_exact(S, s + 1);
+                } else {
+                    const typename D::Fb fs = D::step(S, s);
 #pragma unroll
-                        for (int m = 0; m < MB; ++m)
-                            fq[(i + 1) & 1][m] = Tile::rows(sq, 16 * (m1 + m), s1 * D::KS, lane);
-                    keep_order();
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) {
-                        if constexpr (!HI)
-                            if (m0 == 0) fs[n] = D::step(S[n], s);
-#pragma unroll
-                        for (int m = 0; m < MB; ++m) {
-                            if constexpr (HI) D::mma_aa(o[n][m0 + m], fx[s & 1][n], fq[i & 1][m]);
-                            else D::mma_ba(o[n][m0 + m], fq[i & 1][m], fs[n]);
-                        }
-                        if constexpr (HI)
-                            if (m1 == 0 && s1 < KN) fx[s1 & 1][n] = D::step_exact(S[n], s1);
-                    }
-                    keep_order();
+                    for (int m = 0; m < 4; ++m) D::mma_ba(o[m], fq[s & 1][m], fs);
                 }
-            }
-            keep_order();
-            typename D::Fa fp[F::COUNT];
-#pragma unroll
-            for (int f = 0; f < F::COUNT; ++f) fp[f] = D::mat_frag_hi(mats + kDeltaMatBytes, f, lane);
-#pragma unroll
-            for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(mats, f, lane);
-            if (more) {
-                __syncthreads();
-                rq.store(sq, tid);
-            }
-            if (active) {
-                const int live = min(kDeltaC, len - c * kDeltaC);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float f = a.scale * sf[p][16 * m + n16];
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) o[n][m] *= f;
-                }
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        if (F::lower(m, s)) {
-#pragma unroll
-                            for (int n = 0; n < NC; ++n) D::mma_ba(o[n][m], fp[F::at(m, s, false)], fr[n][s]);
-                            if constexpr (MODE == kFullF32) {
-                                const typename D::Fm fl = D::mat_frag(mats + kDeltaMatBytes, F::at(m, s, false), lane);
-#pragma unroll
-                                for (int n = 0; n < NC; ++n) D::mma_lo(o[n][m], fl, fr[n][s]);
-                            }
-                        }
-                if (live < kDeltaC)  // padding
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-#pragma unroll
-                        for (int n = 0; n < NC; ++n)
-                            if (16 * m + n16 >= live) o[n][m] = zero;
-                DOut out;
-                out.init(a.o, ((long long)b * a.N + c * kDeltaC) * a.H + h, min(kDeltaC, a.N - c * kDeltaC), a.H, a.dv,
-                         sizeof(out_t), col0 + g4, lane);
-#pragma unroll
-                for (int n = 0; n < NC; ++n)
-                    if (col0 + 16 * n < width)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, o[n][m]);
+                keep_order();
             }
         }
-        keep_order();
-        if (!active) continue;
+        __syncthreads();  // the matrices are there, and everyone is done with Q
+        if constexpr (FULL) {
+            typename D::Fa fpt[HI ? F::COUNT : 1];
+            if constexpr (HI)
+#pragma unroll
+                for (int f = 0; f < F::COUNT; ++f) fpt[f] = D::mat_frag_hi(sp, f, lane);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) o[m] *= a.scale * sf[p][16 * m + n16];
+            keep_order();
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (F::lower(m, s)) {
+                        if constexpr (HI) {
+                            D::mma_ba(o[m], fpt[F::at(m, s, false)], fr[s]);
+                        } else {
+                            const typename D::Fm f = D::mat_frag(sp, F::at(m, s, false), lane);
+                            D::mma_bm(o[m], f, fr[s]);
+                        }
+                    }
+        }
         // E' = exp(G_C - G) beta T R
-        f32x4_t u[NC][4];
+        f32x4_t u[4];
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+        for (int m = 0; m < 4; ++m) u[m] = zero;
+        typename D::Fm ft[F::COUNT];
 #pragma unroll
-            for (int m = 0; m < 4; ++m) u[n][m] = zero;
+        for (int f = 0; f < F::COUNT; ++f) ft[f] = D::mat_frag(sm, f, lane);
+        if constexpr (FULL) {
+            const int live = min(kDeltaC, len - c * kDeltaC);
+            if (live < kDeltaC)  // padding
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (16 * m + n16 >= live) o[m] = zero;
+            DOut out;
+            out.init(a.o, ((long long)b * a.N + c * kDeltaC) * a.H + h, min(kDeltaC, a.N - c * kDeltaC), a.H, a.dv,
+                     sizeof(out_t), col0 + g4, lane);
+            if (active)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, o[m]);
+        }
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
             for (int m = 0; m < 4; ++m)
-                if (F::lower(m, s)) {
-#pragma unroll
-                    for (int n = 0; n < NC; ++n) D::mma_mb(u[n][m], ft[F::at(m, s, false)], fr[n][s]);
-                }
+                if (F::lower(m, s)) D::mma_mb(u[m], ft[F::at(m, s, false)], fr[s]);
         keep_order();
         if constexpr (MODE == kStates) {
-            st* ep = (st*)a.et + ((long long)bh * a.nchunks + c) * a.dv * kDeltaC;
+            st* out = (st*)a.et + (((long long)bh * a.nchunks + c) * a.dv + col0) * kDeltaC;
+            if (active)
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-                if (col0 + 16 * n < width)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) store4(ep + (col0 + 16 * n + n16) * kDeltaC + 16 * m + g4, u[n][m]);
+                for (int s = 0; s < NS; ++s) D::blk_store(out, s, lane, &u[D::TPS * s]);
         }
         if constexpr (RAW)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const f32x4_t ta = *reinterpret_cast<const f32x4_t*>(sf[p] + 64 + 16 * m + g4);
-#pragma unroll
-                for (int n = 0; n < NC; ++n) u[n][m] *= ta;
-            }
+            for (int m = 0; m < 4; ++m) u[m] *= *reinterpret_cast<const f32x4_t*>(sf[p] + 64 + 16 * m + g4);
         // S = exp(G_C) S + K^T E'
         const float end = sf[p][63];
-        typename D::Fb fu[NC][NS];
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int s = 0; s < NS; ++s) fu[n][s] = D::step(u[n], s);
-        constexpr int TB = DT < MB ? DT : MB;  // tiles whose fragments are read together
+        typename D::Fb fu[NS];
         typename D::Fa fc[2][TB];
 #pragma unroll
         for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, 16 * t, lane);
+#pragma unroll
+        for (int s = 0; s < NS; ++s) fu[s] = D::step(u, s);
 #pragma unroll
         for (int i = 0; i < NS * DT / TB; ++i) {
             const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
@@ -541,12 +490,11 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
             keep_order();
             if (s == 0)
 #pragma unroll
-                for (int n = 0; n < NC; ++n)
-#pragma unroll
-                    for (int t = 0; t < TB; ++t) S[n][t0 + t] *= end;
-            D::template products<TB, NC>(S, t0, fc[i & 1], fu, s);
+                for (int t = 0; t < TB; ++t) S[t0 + t] *= end;
+            D::template products<TB>(S, t0, fc[i & 1], fu[s]);
             keep_order();
         }
+        stage(p ^ 1);
     }
     if (!active) return;
     // outputs of padding chunks are zero
@@ -556,10 +504,7 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
             out.init(a.o, ((long long)b * a.N + c * kDeltaC) * a.H + h, min(kDeltaC, a.N - c * kDeltaC), a.H, a.dv,
                      sizeof(out_t), col0 + g4, lane);
 #pragma unroll
-            for (int n = 0; n < NC; ++n)
-                if (col0 + 16 * n < width)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, n, zero);
+            for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, zero);
         }
     }
     if constexpr (MODE == kStates) return;
@@ -567,15 +512,11 @@ __global__ __launch_bounds__(64 * NW, (chain_waves<E, DK, NC, NW, MODE>())) void
     if (LOCAL) out = (trans ? a.segM : a.segE) + ((long long)bh * a.nseg + seg) * DK * width;
     else if (seg == a.nseg - 1 && a.state_out) out = a.state_out + (long long)bh * DK * a.dv;
     if (!out) return;
+    out += (long long)g4 * width + col0 + n16;
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        if (col0 + 16 * n >= width) continue;
-        float* p = out + (long long)g4 * width + col0 + 16 * n + n16;
+    for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[(long long)(16 * t + i) * width] = S[n][t][i];
-    }
+        for (int i = 0; i < 4; ++i) out[(long long)(16 * t + i) * width] = S[t][i];
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -682,31 +623,27 @@ __global__ __launch_bounds__(64 * scan_waves<DK>()) void delta_scan_kernel(Delta
     }
 }
 
-template <class E, int DK, int NC, int NW>
-void pick_cols(DeltaKernels* o) {
+template <class E, int DK, int NW>
+void pick_waves(DeltaKernels* o) {
     *o = {};
     o->prep = delta_prep_kernel<E, DK, false>;
     o->bprep = delta_prep_kernel<E, DK, true>;
-    o->local = delta_chain_kernel<E, DK, NC, NW, kLocal>;
-    o->blocal = delta_chain_kernel<E, DK, NC, NW, kLocalRaw>;
-    o->full = delta_chain_kernel<E, DK, NC, NW, kFull>;
-    o->full_f32 = delta_chain_kernel<E, DK, NC, NW, sizeof(typename E::st) == 2 ? kFullF32 : kFull>;
-    o->states = delta_chain_kernel<E, DK, NC, NW, kStates>;
+    o->local = delta_chain_kernel<E, DK, NW, kLocal>;
+    o->blocal = delta_chain_kernel<E, DK, NW, kLocalRaw>;
+    o->full = delta_chain_kernel<E, DK, NW, kFull>;
+    o->full_f32 = delta_chain_kernel<E, DK, NW, sizeof(typename E::st) == 2 ? kFullF32 : kFull>;
+    o->states = delta_chain_kernel<E, DK, NW, kStates>;
     o->scan = delta_scan_kernel<E, DK, false>;
     o->rscan = delta_scan_kernel<E, DK, true>;
     o->scan_threads = 64 * scan_waves<DK>();
-    o->cols = 16 * NC * NW;
+    o->cols = 16 * NW;
     o->threads = 64 * NW;
 }
-// Two column tiles per wave halve the operand reads per product; one where d_v would leave waves idle, and where a row of
-// K takes 512 bytes: the state of two tiles would take the registers of a second wave on the SIMD, so eight waves share
-// the rows instead.
+// Eight waves share the rows of K and Q; four where d_v would leave the others without columns.
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
-    constexpr bool WIDE = DK * sizeof(typename E::st) >= 256;
-    if (dv <= 64 || DK <= 128) pick_cols<E, DK, 1, 4>(o);
-    else if constexpr (WIDE) pick_cols<E, DK, 1, 8>(o);
-    else pick_cols<E, DK, 2, 4>(o);
+    if (dv <= 64) pick_waves<E, DK, 4>(o);
+    else pick_waves<E, DK, 8>(o);
 }
 
 }  // namespace
