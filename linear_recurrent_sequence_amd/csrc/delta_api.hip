@@ -74,7 +74,7 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
     int n = 1;
     if (op.segments > 0) n = op.segments;
-    else if (units <= 192) n = (int)(512 / units);
+    else n = (int)((s.dk * esize(in_dt) >= 256 ? 256 : 512) / units);  // one or two workgroups per CU
     if (op.segments <= 0 && n > p.nchunks / 4) n = p.nchunks / 4;  // at least 4 chunks a segment
     if (n > p.nchunks) n = p.nchunks;
     if (n < 1) n = 1;
