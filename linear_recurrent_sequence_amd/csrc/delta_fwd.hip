@@ -522,8 +522,10 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
 // ---------------------------------------------------------------------------------------------------
 // delta_scan: the states entering the segments. In: segE[s] = segment s's end state from zero (segment 0: its true end
 // state), segM[s] its transition. Out: segE[s] = the state entering segment s, S_{s+1} = M_s S_s + E_s. One workgroup per
-// (b, h, 16 columns); REV: the gradients' chain, D_{s-1} = M_s^T D_s + F_s over segF from the right. The waves share the rows of M, S goes round through LDS. BF16
-// input: M and S split in two bf16 parts like the chain's operands.
+// (b, h, 32 columns); REV: the gradients' chain, D_{s-1} = M_s^T D_s + F_s over segF from the right. The waves share the
+// rows of M; S goes round through LDS, transposed, so that it is written and read 16 bytes at a time. A step is bound by the latency of
+// its rows of M: each part is requested for the next segment as soon as its products have it (measured below, without:
+// 64 KB transitions 2.8 us a segment). BF16 input: M and S split in two bf16 parts like the chain's operands.
 // ---------------------------------------------------------------------------------------------------
 // waves of a scan workgroup: 16 rows of the state each, 32 at d_k = 256 (the rows of M in flight take the registers)
 template <int DK>
@@ -531,12 +533,17 @@ constexpr int scan_waves() { return DK / 16 <= 8 ? DK / 16 : 8; }
 template <class E, int DK, bool REV>
 __global__ __launch_bounds__(64 * scan_waves<DK>()) void delta_scan_kernel(DeltaArgs a) {
     typedef DOps<E> D;
-    constexpr int NS = DK / D::KS, TPS = D::TPS, RT = DK / 16 / scan_waves<DK>(), CT = kScanCols / 16, LD = kScanCols + 4;
-    __shared__ __align__(16) float sS[2][DK * LD];
+    constexpr int NS = DK / D::KS, TPS = D::TPS, RT = DK / 16 / scan_waves<DK>(), CT = kScanCols / 16, LD = DK + 4;
+    __shared__ __align__(16) float sS[2][kScanCols * LD];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
     const int g4 = 4 * (lane >> 4), bh = blockIdx.x, c0 = blockIdx.y * kScanCols;
     const long long sz = (long long)DK * a.dv;
-    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz + (long long)(16 * RT * w + g4) * a.dv + c0 + n16;
+    float* X = (REV ? a.segF : a.segE) + (long long)bh * a.nseg * sz;
+    // this lane's places in a segment's state, by column tile: through a buffer resource, which drops the columns past d_v
+    int at[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+        at[t] = c0 + 16 * t < a.dv ? ((16 * RT * w + g4) * a.dv + c0 + 16 * t + n16) * 4 : 0x40000000;
     // this lane's part of the rows of M (REV: of its transpose) that wave w multiplies
     const float* M = a.segM + (long long)bh * a.nseg * DK * DK +
                      (REV ? g4 * DK + 16 * RT * w + n16 : (16 * RT * w + n16) * DK + g4);
@@ -551,58 +558,60 @@ __global__ __launch_bounds__(64 * scan_waves<DK>()) void delta_scan_kernel(Delta
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 S[r][t][i] = sin && c0 + 16 * t < a.dv ? sin[(long long)(16 * r + i) * a.dv + 16 * t] : 0.f;
-    auto fetch = [&](int j) {  // the j-th segment on the way: its end state from zero and its transition
-        const int s = REV ? a.nseg - 1 - j : j;
+    auto seg = [&](int j) { return REV ? a.nseg - 1 - j : j; };  // the j-th segment on the way
+    auto fetch_e = [&](int s) {                                  // its end state from zero
+        const rsrc_t x = bytes_rsrc(X + s * sz, (int)sz * 4);
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int t = 0; t < CT; ++t)
-                if (c0 + 16 * t < a.dv)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) e[r][t][i] = X[s * sz + (long long)(16 * r + i) * a.dv + 16 * t];
-        if (j == 0) return;
+                for (int i = 0; i < 4; ++i)
+                    e[r][t][i] = __uint_as_float(
+                        __builtin_amdgcn_raw_buffer_load_b32(x, at[t], (16 * r + i) * a.dv * 4, 0));
+    };
+    auto fetch_m = [&](int s, int k) {  // part k of its transition
         const float* p = M + (long long)s * DK * DK;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int k = 0; k < NS; ++k)
+            for (int t = 0; t < TPS; ++t) {
+                if constexpr (REV) {
 #pragma unroll
-                for (int t = 0; t < TPS; ++t) {
-                    if constexpr (REV) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m[r][k][t][i] = p[(D::KS * k + 16 * t + i) * DK + 16 * r];
-                    } else {
-                        m[r][k][t] = *reinterpret_cast<const f32x4_t*>(p + 16 * r * DK + D::KS * k + 16 * t);
-                    }
+                    for (int i = 0; i < 4; ++i) m[r][k][t][i] = p[(D::KS * k + 16 * t + i) * DK + 16 * r];
+                } else {
+                    m[r][k][t] = *reinterpret_cast<const f32x4_t*>(p + 16 * r * DK + D::KS * k + 16 * t);
                 }
+            }
     };
-    fetch(0);
+    fetch_e(seg(0));
     for (int j = 0;; ++j) {
-        const int s = REV ? a.nseg - 1 - j : j;
+        const int s = seg(j), next = seg(min(j + 1, a.nseg - 2));  // (the last one's are not needed)
         float* x = sS[j & 1];
+        const rsrc_t out = bytes_rsrc(X + s * sz, (int)sz * 4);
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < CT; ++t) {
+                *reinterpret_cast<f32x4_t*>(x + (16 * t + n16) * LD + 16 * (RT * w + r) + g4) = S[r][t];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[r][t][i]), out, at[t],
+                                                          (16 * r + i) * a.dv * 4, 0);
+            }
+        if (j == a.nseg - 1) return;
+        __syncthreads();
+        // from the state entering the first segment on; one without live tokens passes the state as it is
+        const bool live = j == 0 || s * a.seg_chunks * kDeltaC < len;
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int t = 0; t < CT; ++t)
+                if (live) S[r][t] = e[r][t];
+        fetch_e(next);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[(16 * (RT * w + r) + g4 + i) * LD + 16 * t + n16] = S[r][t][i];
-                    if (c0 + 16 * t < a.dv) X[s * sz + (long long)(16 * r + i) * a.dv + 16 * t] = S[r][t][i];
-                }
-        if (j == a.nseg - 1) return;
-        __syncthreads();
-        if (j == 0) {  // from the state entering the first segment
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int t = 0; t < CT; ++t) S[r][t] = e[r][t];
-        } else if (s * a.seg_chunks * kDeltaC < len) {  // else no live token: the state passes as it is
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int t = 0; t < CT; ++t) S[r][t] = e[r][t];
-#pragma unroll
-            for (int k = 0; k < NS; ++k) {
+        for (int k = 0; k < NS; ++k) {
+            if (j > 0 && live) {
                 typename D::Fb fm[RT];
 #pragma unroll
                 for (int r = 0; r < RT; ++r) fm[r] = D::step(m[r][k], 0);
@@ -611,15 +620,14 @@ __global__ __launch_bounds__(64 * scan_waves<DK>()) void delta_scan_kernel(Delta
                     f32x4_t y[TPS];
 #pragma unroll
                     for (int p = 0; p < TPS; ++p)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) y[p][i] = x[(D::KS * k + 16 * p + g4 + i) * LD + 16 * t + n16];
+                        y[p] = *reinterpret_cast<const f32x4_t*>(x + (16 * t + n16) * LD + D::KS * k + 16 * p + g4);
                     const typename D::Fb fy = D::step(y, 0);
 #pragma unroll
                     for (int r = 0; r < RT; ++r) D::mma_mb(S[r][t], fm[r], fy);
                 }
             }
+            fetch_m(next, k);
         }
-        if (j + 1 < a.nseg - 1) fetch(j + 1);
     }
 }
 
