@@ -143,10 +143,6 @@ struct DOps<BF16> {
     __device__ static __forceinline__ void mfma1(f32x4_t& acc, bf16x8_t a, bf16x8_t b) {
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
     }
-    __device__ static __forceinline__ void mma_ab(f32x4_t& acc, Fa a, const Fb& b) {
-        mfma1(acc, a, b.lo);
-        mfma1(acc, a, b.hi);
-    }
     // x[m0 + m] += a[m] b, the low parts first: no product right behind one of the same tile
     template <int MB, int NT>
     __device__ static __forceinline__ void products(f32x4_t (&x)[NT], int m0, const Fa (&a)[MB], const Fb& b) {
@@ -155,31 +151,35 @@ struct DOps<BF16> {
 #pragma unroll
         for (int m = 0; m < MB; ++m) mfma1(x[m0 + m], a[m], b.hi);
     }
-    __device__ static __forceinline__ void mma_ba(f32x4_t& acc, Fa a, const Fb& b) {
-        mfma1(acc, b.lo, a);
-        mfma1(acc, b.hi, a);
+    // The products of an operand pair, one by one (see tri): an input's rows (Fa), or a matrix (Fm), times b; _t: the
+    // sides swapped, accumulator rows along b's columns
+    __device__ static __forceinline__ void part(f32x4_t& acc, const Fa& a, const Fb& b, int p) {
+        if (p < 2) mfma1(acc, a, p == 0 ? b.lo : b.hi);
+    }
+    __device__ static __forceinline__ void part_t(f32x4_t& acc, const Fa& a, const Fb& b, int p) {
+        if (p < 2) mfma1(acc, p == 0 ? b.lo : b.hi, a);
+    }
+    __device__ static __forceinline__ void part(f32x4_t& acc, const Fm& a, const Fb& b, int p) {
+        if (p < 3) mfma1(acc, p == 1 ? a.lo : a.hi, p == 0 ? b.lo : b.hi);
+    }
+    __device__ static __forceinline__ void part_t(f32x4_t& acc, const Fm& a, const Fb& b, int p) {
+        if (p < 3) mfma1(acc, p == 0 ? b.lo : b.hi, p == 1 ? a.lo : a.hi);
+    }
+    // a matrix times an exact operand
+    __device__ static __forceinline__ void part(f32x4_t& acc, const Fm& a, const bf16x8_t& b, int p) {
+        if (p < 2) mfma1(acc, p == 0 ? a.lo : a.hi, b);
     }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) {
-        mfma1(acc, a.hi, b.lo);
-        mfma1(acc, a.lo, b.hi);
-        mfma1(acc, a.hi, b.hi);
-    }
-    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) {
-        mfma1(acc, b.lo, a.hi);
-        mfma1(acc, b.hi, a.lo);
-        mfma1(acc, b.hi, a.hi);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) part(acc, a, b, p);
     }
     // both sides exact
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, Fa a, Fa b) { mfma1(acc, a, b); }
-    // a workspace matrix times an exact operand made from accumulator-ordered values
+    // accumulator-ordered values that are exact in bf16
     typedef bf16x8_t Fx;
     template <int NT>
     __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
         return acc_pair(x[2 * s], x[2 * s + 1]);
-    }
-    __device__ static __forceinline__ void mma_mx(f32x4_t& acc, const Fm& a, Fx b) {
-        mfma1(acc, a.lo, b);
-        mfma1(acc, a.hi, b);
     }
     // fragment f of a workspace matrix
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
@@ -252,7 +252,10 @@ struct DOps<F32> {
             for (int m = 0; m < MB; ++m)
                 x[m0 + m] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m][i], b[i], x[m0 + m], 0, 0, 0);
     }
-    __device__ static __forceinline__ void mma_ba(f32x4_t& acc, const Fa& a, const Fb& b) { mma_ab(acc, b, a); }
+    __device__ static __forceinline__ void part(f32x4_t& acc, const Fa& a, const Fb& b, int p) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[p], b[p], acc, 0, 0, 0);
+    }
+    __device__ static __forceinline__ void part_t(f32x4_t& acc, const Fa& a, const Fb& b, int p) { part(acc, b, a, p); }
     __device__ static __forceinline__ void mma_mb(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ void mma_aa(f32x4_t& acc, const Fa& a, const Fa& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ void blk_store(st* p, int i, int lane, const f32x4_t* x) {
@@ -262,17 +265,14 @@ struct DOps<F32> {
     __device__ static __forceinline__ void blk_lds(st* lds, int row, int c0, int g4, u32x4_t x) {
         *reinterpret_cast<u32x4_t*>(lds + Tile::off(row, c0 + g4)) = x;
     }
-    __device__ static __forceinline__ void mma_bm(f32x4_t& acc, const Fm& a, const Fb& b) { mma_ab(acc, b, a); }
     typedef f32x4_t Fx;
     template <int NT>
     __device__ static __forceinline__ Fx step_exact(const f32x4_t (&x)[NT], int s) {
         return x[s];
     }
-    __device__ static __forceinline__ void mma_mx(f32x4_t& acc, const Fm& a, const Fx& b) { mma_ab(acc, a, b); }
     __device__ static __forceinline__ Fm mat_frag(const char* m, int f, int lane) {
         return reinterpret_cast<const f32x4_t*>(m)[f * 64 + lane];
     }
-    __device__ static __forceinline__ Fa mat_frag_hi(const char* m, int f, int lane) { return mat_frag(m, f, lane); }
     __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a) {
         reinterpret_cast<f32x4_t*>(m)[f * 64 + lane] = a;
     }
@@ -292,6 +292,23 @@ struct DOps<F32> {
         }
     };
 };
+
+// Products of the four row tiles with step s of b; tri: of a triangular matrix (f: its fragments; UP: a transpose's), the
+// tiles with entries in that step. SWAP: accumulator rows along b's columns. The parts of a pair go round the tiles, so
+// that no product stands right behind one into the same accumulators.
+template <class E, bool UP, bool SWAP, class A, class B, int N>
+__device__ __forceinline__ void tri(f32x4_t (&x)[4], const A (&f)[N], const B& b, int s) {
+    typedef DOps<E> D;
+    typedef TriFrags<D::KS> F;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            if (UP ? F::upper(m, s) : F::lower(m, s)) {
+                if constexpr (SWAP) D::part_t(x[m], f[F::at(m, s, UP)], b, p);
+                else D::part(x[m], f[F::at(m, s, UP)], b, p);
+            }
+}
 
 // 64 rows of W elements of one head moved as 16-byte segments by NT threads: rows past the live ones read as zeros (the
 // buffer resource ends with the last live row), and so do columns past `cols`. Tile column `at` receives column 0. The
@@ -368,7 +385,7 @@ struct DOut {
 // ---- kernel selection ----
 struct DeltaKernels {
     delta_kernel_t prep, local, full, full_f32, scan;  // full_f32: F32 output
-    delta_kernel_t bprep, blocal, states, rlocal, rscan, rfull, grad;  // gradients
+    delta_kernel_t bprep, blocal, states, rlocal, rscan, rfull, grad, grad_group;  // gradients (grad_group: H > Hk)
     int cols, threads; // columns of d_v (or of a transition) and threads per workgroup of the chains
     int grad_threads, scan_threads;
 };

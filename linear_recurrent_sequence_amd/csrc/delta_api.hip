@@ -274,7 +274,7 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
         if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
     if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
-    return launch("ret_delta_grad", kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
+    return launch("ret_delta_grad", H > Hk ? kn.grad_group : kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
 }
 
 ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,

@@ -216,10 +216,7 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
 #pragma unroll
             for (int f = 0; f < F::COUNT; ++f) fm[f] = D::mat_frag(sp, f, lane);
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (F::upper(m, s)) D::mma_mx(x[m], fm[F::at(m, s, true)], fd[s]);
+            for (int s = 0; s < NS; ++s) tri<E, true, false>(x, fm, fd[s], s);
         }
         // dU = Tr^T W
         f32x4_t u[4];
@@ -233,10 +230,7 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
 #pragma unroll
             for (int s = 0; s < NS; ++s) fw[s] = D::step(x, s);
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (F::upper(m, s)) D::mma_mb(u[m], fm[F::at(m, s, true)], fw[s]);
+            for (int s = 0; s < NS; ++s) tri<E, true, false>(u, fm, fw[s], s);
         }
         if constexpr (!LOCAL) {
             if (active) {
@@ -364,16 +358,16 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 }
 
 // ---------------------------------------------------------------------------------------------------
-// delta_grad: dq, dk, dg, dbeta of one chunk and key head (the value heads that share it one after another, their dq and
-// dk added up in registers: no atomics, one order). Wave w owns tokens 16 (w % 4) .. + 15 and the columns of d_k of its
-// half w / 4. Every product has its accumulator rows along d_k (or j) and columns along tokens: per-token factors are one
-// value per lane and a lane holds 4 consecutive values of its token's row. d_v is walked in blocks of 32.
+// delta_grad: dq, dk, dg, dbeta of one chunk and key head (GROUP: the value heads that share it one after another, their
+// dq and dk added up in registers: no atomics, one order). Wave w owns tokens 16 (w % 4) .. + 15 and 64 columns of d_k
+// (all of a shorter one). Every product has its accumulator rows along d_k (or j) and columns along tokens: per-token
+// factors are one value per lane and a lane holds 4 consecutive values of its token's row. d_v is walked in blocks of 32.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
+template <class E, int DK, int NW, bool GROUP>
+__global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <= 128 ? 2 : 1)) void delta_grad_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    constexpr int NT = 64 * NW, DH = DK / (NW / 4), DT = DH / 16, NS = kDeltaC / D::KS, VB = 32;
+    constexpr int NT = 64 * NW, HF = NW / 4, DH = DK / HF, DT = DH / 16, NS = kDeltaC / D::KS, VB = 32;
     typedef typename D::template Tile<DK> TK;
     typedef typename D::template Tile<VB> TO;
     typedef typename D::template Tile<kDeltaC> TC;
@@ -382,17 +376,20 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
     __shared__ __align__(16) st sq[kDeltaC * TK::LD];
     __shared__ __align__(16) st buf[kStage > kXZ ? kStage : kXZ];
     __shared__ f64 sG[kDeltaC];
-    __shared__ float sF[256], sDg[2][kDeltaC], sDb[kDeltaC], sR[2][NW];
+    __shared__ float sF[256], sDg[HF][kDeltaC], sDb[kDeltaC], sR[2][NW];
     st *sS = buf, *sD = sS + VB * TK::LD, *sO = sD + VB * TK::LD, *sE = sO + kDeltaC * TO::LD, *sU = sE + VB * TC::LD;
     st *sX = buf, *sZ = buf + kDeltaC * TC::LD;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
     const int tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
-    const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
+    const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk;
+    const int rep = GROUP ? a.H / a.Hk : 1;
     const int t0 = c * kDeltaC, len = delta_len(a, b), live = min(kDeltaC, len - t0);
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4_t tq[DT], tk[DT];
+    constexpr int kM2 = HF == 1 ? 1 : 0;  // M: E^T dO in the waves of the first columns, E^T dU in those of the last
+    f32x4_t tq[GROUP ? DT : 1], tk[GROUP ? DT : 1], Dq[DT], Dr[DT], Du[DT], M[1 + kM2][4];
+    if (GROUP)
 #pragma unroll
-    for (int t = 0; t < DT; ++t) tq[t] = tk[t] = zero;
+        for (int t = 0; t < DT; ++t) tq[t] = tk[t] = zero;
     if (live > 0) {
         GRows<E, kDeltaC, DK, NT> rk, rq;
         const long long base = (((long long)b * a.N + t0) * a.Hk + hk) * DK;
@@ -412,11 +409,10 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
             continue;
         }
         const long long unit = ((long long)b * a.H + h) * a.nchunks + c;
-        f32x4_t Dq[DT], Dr[DT], Du[DT], M1[4], M2[4];
 #pragma unroll
         for (int t = 0; t < DT; ++t) Dq[t] = Dr[t] = Du[t] = zero;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) M1[j] = M2[j] = zero;
+        for (int j = 0; j < 4; ++j) M[0][j] = M[kM2][j] = zero;
         float dot = 0.f;
         GBlocks<E, DK, VB, NT> rs, rd;
         GRows<E, kDeltaC, VB, NT> ro;
@@ -466,8 +462,8 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
                 for (int j = 0; j < 4; ++j) {
                     if (j > tw) continue;
                     const typename D::Fa fj = TC::cols(sE, s * D::KS, 16 * j, lane);
-                    if (NW == 4 || hf == 0) D::mma_aa(M1[j], fj, fo);
-                    if (NW == 4 || hf == 1) D::mma_aa(M2[j], fj, fu);
+                    if (hf == 0) D::mma_aa(M[0][j], fj, fo);
+                    if (hf == HF - 1) D::mma_aa(M[kM2][j], fj, fu);
                 }
             }
         }
@@ -490,12 +486,12 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
                 const int jj = 16 * j + g4 + e;
                 if (jj > i) continue;
                 const float d = __builtin_amdgcn_exp2f((float)(sG[i] - sG[jj])) * sF[192 + jj];
-                x[e] = a.scale * d * M1[j][e];
-                if (jj < i) z[e] = -d * be * M2[j][e];
-                else if (NW == 4 || hf == 1) sDb[i] = M2[j][e];
+                x[e] = a.scale * d * M[0][j][e];
+                if (jj < i) z[e] = -d * be * M[kM2][j][e];
+                else if (hf == HF - 1) sDb[i] = M[kM2][j][e];
             }
-            if (NW == 4 || hf == 0) store4(sX + TC::off(i, 16 * j + g4), x);
-            if (NW == 4 || hf == 1) store4(sZ + TC::off(i, 16 * j + g4), z);
+            if (hf == 0) store4(sX + TC::off(i, 16 * j + g4), x);
+            if (hf == HF - 1) store4(sZ + TC::off(i, 16 * j + g4), z);
         }
         __syncthreads();
 #pragma unroll
@@ -521,8 +517,11 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
         for (int t = 0; t < DT; ++t) {
             const f32x4_t kv = lds4(sk + TK::off(i, dk0 + 16 * t + g4)), qv = lds4(sq + TK::off(i, dk0 + 16 * t + g4));
             dg += dot4(qv, Dq[t]) + dot4(kv, Dr[t] - Du[t]);
-            tq[t] += Dq[t];
-            tk[t] += Dr[t] + Du[t];
+            Dr[t] += Du[t];
+            if constexpr (GROUP) {
+                tq[t] += Dq[t];
+                tk[t] += Dr[t];
+            }
         }
         dg += __shfl_xor(dg, 16);
         dg += __shfl_xor(dg, 32);
@@ -535,8 +534,9 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
         }
         __syncthreads();
         if (w == 0) {
-            f64 x = sDg[0][lane];
-            if (NW == 8) x += sDg[1][lane];
+            f64 x = 0.0;
+#pragma unroll
+            for (int j = 0; j < HF; ++j) x += sDg[j][lane];
             if (lane == 63)
 #pragma unroll
                 for (int j = 0; j < NW; ++j) x += (f64)end * sR[0][j] + sR[1][j];
@@ -563,7 +563,8 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
     for (int j = 0; j < DT; ++j) {
         const long long e = (((long long)b * a.N + t) * a.Hk + hk) * DK + dk0 + 16 * j + g4;
-        const f32x4_t x = t < len ? tq[j] : zero, y = t < len ? tk[j] : zero;
+        f32x4_t x = GROUP ? tq[GROUP ? j : 0] : Dq[j], y = GROUP ? tk[GROUP ? j : 0] : Dr[j];
+        if (t >= len) x = y = zero;
         if (a.out_bf16) {
             store4((uint16_t*)a.dq + e, x);
             store4((uint16_t*)a.dk_ + e, y);
@@ -576,7 +577,7 @@ __global__ __launch_bounds__(64 * NW) void delta_grad_kernel(DeltaArgs a) {
 
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
-    constexpr int NW = DK * sizeof(typename E::st) > 256 ? 8 : 4;  // half of d_k per wave where a row is long
+    constexpr int NW = DK > 64 ? DK / 16 : 4;
     if (dv <= 64) {  // as the forward's
         o->rlocal = delta_rchain_kernel<E, DK, 4, true>;
         o->rfull = delta_rchain_kernel<E, DK, 4, false>;
@@ -584,7 +585,8 @@ void pick(int dv, DeltaKernels* o) {
         o->rlocal = delta_rchain_kernel<E, DK, 8, true>;
         o->rfull = delta_rchain_kernel<E, DK, 8, false>;
     }
-    o->grad = delta_grad_kernel<E, DK, NW>;
+    o->grad = delta_grad_kernel<E, DK, NW, false>;
+    o->grad_group = delta_grad_kernel<E, DK, NW, true>;
     o->grad_threads = 64 * NW;
 }
 

@@ -106,22 +106,43 @@ __device__ __forceinline__ void tri_inverse(const float* sA, float* sT, int w, i
     __syncthreads();
 }
 
+// acc = row tile w of X Y for lower triangular fp32 LDS matrices
+__device__ __forceinline__ void tri_product(f32x4_t (&acc)[4], const float* X, const float* Y, int w, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i > w) continue;
+        const f32x4_t x = tri_a(X, 16 * w, 16 * i, lane);
+#pragma unroll
+        for (int j = 0; j <= i; ++j) DOps<F32>::mma_ab(acc[j], x, tri_b(Y, 16 * i, 16 * j, lane));
+    }
+}
+
 template <class E, int DK, bool BWD>
 __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DRows<E, DK, kThreads> Rows;
     typedef typename Rows::Tile Tile;
     typedef DOps<E> D;
-    __shared__ __align__(16) st sk[kDeltaC * Tile::LD];
-    __shared__ __align__(16) st sq[kDeltaC * Tile::LD];
-    __shared__ __align__(16) float sA[kDeltaC * kTriLD];
-    __shared__ __align__(16) float sT[kDeltaC * kTriLD];
+    // the rows, then (their products are in registers) the matrices
+    constexpr int kRows = 2 * kDeltaC * Tile::LD * (int)sizeof(st), kTri = 2 * kDeltaC * kTriLD * 4;
+    __shared__ __align__(16) char pool[kRows > kTri ? kRows : kTri];
+    st *sk = reinterpret_cast<st*>(pool), *sq = sk + kDeltaC * Tile::LD;
+    float *sA = reinterpret_cast<float*>(pool), *sT = sA + kDeltaC * kTriLD;
     __shared__ f64 sG[kDeltaC];
     __shared__ float sB[kDeltaC], sF[kDeltaC];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g = lane >> 4;
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk, rep = a.H / a.Hk;
     const int t0 = c * kDeltaC, live = min(kDeltaC, delta_len(a, b) - t0);
     if (live <= 0) return;  // no one reads this chunk
+    float gv, bv;  // gates of the next head, asked for a head ahead
+    auto gates = [&](int h) {
+        const long long i = ((long long)b * a.N + t0 + min(lane, live - 1)) * a.H + h;
+        gv = gate_at(a.g, i, a.gate_bf16);
+        bv = gate_at(a.beta, i, a.gate_bf16);
+    };
+    gates(hk * rep);
     {
         Rows rk, rq;
         const long long base = (((long long)b * a.N + t0) * a.Hk + hk) * DK;
@@ -155,15 +176,13 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
         const long long unit = ((long long)b * a.H + h) * a.nchunks + c;
         if (w == 0) {
             const bool in = lane < live;
-            const long long i = ((long long)b * a.N + t0 + (in ? lane : 0)) * a.H + h;
-            const float gv = gate_at(a.g, i, a.gate_bf16);
             f64 G = in ? (f64)(gv < -200.f ? -200.f : gv) * 1.4426950408889634 : 0.0;
 #pragma unroll
             for (int m = 1; m < 64; m *= 2) {
                 const f64 up = __shfl_up(G, m);
                 if (lane >= m) G += up;
             }
-            const float be = in ? gate_at(a.beta, i, a.gate_bf16) : 0.f;
+            const float be = in ? bv : 0.f;
             sG[lane] = G;
             sB[lane] = be;
             float* f = a.fac + unit * kDeltaFac;
@@ -174,6 +193,7 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
             f[192 + lane] = be;
             reinterpret_cast<f64*>(f + 256)[lane] = G;
         }
+        gates(min(h + 1, hk * rep + rep - 1));
         __syncthreads();
         char* mats = a.mats + unit * a.nmats * kDeltaMatBytes;
         f32x4_t pv[4];
@@ -198,34 +218,34 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(DeltaArgs a) {
         tri_inverse(sA, sT, w, lane);
         if constexpr (BWD) {
             write_mat<E, false>(mats, sT, w, lane, true);
-            // Tr = (I + Ar)^-1 with beta along the rows: the gradients' solve
+            // Tr = (I + Ar)^-1 with beta along the rows, the gradients' solve: with A = L diag(beta) and Ar = diag(beta) L,
+            // Tr = I - diag(beta) T L
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, av[j]);
+            __syncthreads();
+            tri_product(av, sT, sA, w, lane);
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                f32x4_t x = av[j];
+                f32x4_t x;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] *= sB[16 * w + 4 * g + i];
-                tri_store(sA, 16 * w, 16 * j, lane, x);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 16 * w + 4 * g + i;
+                    x[i] = (row == 16 * j + n16 ? 1.f : 0.f) - sB[row] * av[j][i];
+                }
+                tri_store(sT, 16 * w, 16 * j, lane, x);
             }
             __syncthreads();
-            tri_inverse(sA, sT, w, lane);
             write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane, true);
         } else {
             // P T: row tile w through sA (its own rows only), and T with its rows scaled
 #pragma unroll
             for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pv[j] * sB[16 * j + n16]);
             __syncthreads();
-            f32x4_t pt[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                pt[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = j; i < 4; ++i)
-                    if (i <= w) DOps<F32>::mma_ab(pt[j], tri_a(sA, 16 * w, 16 * i, lane), tri_b(sT, 16 * i, 16 * j, lane));
-            }
+            tri_product(pv, sA, sT, w, lane);
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pt[j]);
+            for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pv[j]);
             __syncthreads();
             write_mat<E, false>(mats + kDeltaMatBytes, sA, w, lane, a.p_lo);
             write_mat<E, false>(mats, sT, w, lane, true, sF[16 * w + n16]);
@@ -411,32 +431,26 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
                 } else {
                     const typename D::Fb fs = D::step(S, s);
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) D::mma_ba(o[m], fq[s & 1][m], fs);
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) D::part_t(o[m], fq[s & 1][m], fs, p);
                 }
                 keep_order();
             }
         }
         __syncthreads();  // the matrices are there, and everyone is done with Q
         if constexpr (FULL) {
-            typename D::Fa fpt[HI ? F::COUNT : 1];
-            if constexpr (HI)
+            typename std::conditional<HI, typename D::Fa, typename D::Fm>::type fpt[F::COUNT];
 #pragma unroll
-                for (int f = 0; f < F::COUNT; ++f) fpt[f] = D::mat_frag_hi(sp, f, lane);
+            for (int f = 0; f < F::COUNT; ++f) {
+                if constexpr (HI) fpt[f] = D::mat_frag_hi(sp, f, lane);
+                else fpt[f] = D::mat_frag(sp, f, lane);
+            }
 #pragma unroll
             for (int m = 0; m < 4; ++m) o[m] *= a.scale * sf[p][16 * m + n16];
             keep_order();
 #pragma unroll
-            for (int s = 0; s < NS; ++s)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                    if (F::lower(m, s)) {
-                        if constexpr (HI) {
-                            D::mma_ba(o[m], fpt[F::at(m, s, false)], fr[s]);
-                        } else {
-                            const typename D::Fm f = D::mat_frag(sp, F::at(m, s, false), lane);
-                            D::mma_bm(o[m], f, fr[s]);
-                        }
-                    }
+            for (int s = 0; s < NS; ++s) tri<E, false, true>(o, fpt, fr[s], s);
         }
         // E' = exp(G_C - G) beta T R
         f32x4_t u[4];
@@ -459,10 +473,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
                 for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, o[m]);
         }
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int m = 0; m < 4; ++m)
-                if (F::lower(m, s)) D::mma_mb(u[m], ft[F::at(m, s, false)], fr[s]);
+        for (int s = 0; s < NS; ++s) tri<E, false, false>(u, ft, fr[s], s);
         keep_order();
         if constexpr (MODE == kStates) {
             st* out = (st*)a.et + (((long long)bh * a.nchunks + c) * a.dv + col0) * kDeltaC;
