@@ -9,6 +9,7 @@ in-tree before it is loaded (or refused, with build_if_missing=False).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -231,7 +232,7 @@ def _dt(t: torch.Tensor) -> int:
 def _dev(t, name):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -244,7 +245,7 @@ def _shape(t, name, shape, dtypes=None):
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a tensor" % name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if dtypes is not None and t.dtype not in dtypes:
         raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
@@ -582,18 +583,30 @@ def ret_chunkwise_fwd_noalloc(q, k, v, o, gamma, chunk, theta=None, pos0=0, stat
 
 
 # ---- the entry points below take their stream from the tensors' device ----
+_SAME = contextlib.nullcontext()
+
+
 def _launch(t, stream, workspace, make):
     """(device guard, stream handle, workspace): the stream of the call, torch's current one of t's device by default,
     and a workspace made on that stream where the caller gave none (torch reuses its memory in that stream's order)."""
-    s = stream if stream is not None else torch.cuda.current_stream(t.device)
-    if workspace is None and make is not None:
-        with torch.cuda.stream(s):
-            workspace = make()
-    return torch.cuda.device(t.device), ctypes.c_void_p(s.cuda_stream), workspace
+    dev = t.device.index
+    guard = _SAME if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream is None:
+        # the handle alone: a Stream object and a guard cost as much as a small kernel takes (3 of 16 us a call)
+        sp = torch._C._cuda_getCurrentRawStream(dev)
+        if workspace is None and make is not None:
+            with guard:
+                workspace = make()
+    else:
+        sp = stream.cuda_stream
+        if workspace is None and make is not None:
+            with torch.cuda.stream(stream):
+                workspace = make()
+    return guard, ctypes.c_void_p(sp), workspace
 
 
 def _need_gpu(t, name):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
 
 
@@ -728,7 +741,7 @@ def _delta_qkv(q, k, v, g, beta, step=False):
         if not isinstance(t, torch.Tensor) or t.dim() != nd:
             raise ValueError("%s must be a %d-d tensor" % (name, nd))
     _shape(k, "k", q.shape, (q.dtype,))
-    if tuple(v.shape[:-2]) != tuple(q.shape[:-2]) or v.dtype != q.dtype or q.dtype not in _IO:
+    if v.shape[:-2] != q.shape[:-2] or v.dtype != q.dtype or q.dtype not in _IO:
         raise ValueError("q, k, v must share their leading axes and one dtype (float32 or bfloat16)")
     if q.shape[-2] == 0 or v.shape[-2] % q.shape[-2]:
         raise ValueError("the heads of v (%d) must be a multiple of those of q and k (%d)" % (v.shape[-2], q.shape[-2]))
