@@ -55,7 +55,6 @@ struct DeltaArgs {
     int nchunks, nmats;
     int nseg, seg_chunks;        // segments per sequence and chunks per segment
     int out_bf16, gate_bf16;
-    int p_lo;                    // the forward's P T has its low parts too (outputs in fp32)
     float scale;
 };
 typedef void (*delta_kernel_t)(DeltaArgs);
@@ -92,7 +91,7 @@ __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0)
 template <int KS>
 struct TriFrags {
     static constexpr int NS = kDeltaC / KS, COUNT = NS == 2 ? 6 : 10;
-    static constexpr int BYTES = COUNT * (NS == 2 ? 2048 : 1024), HI_BYTES = COUNT * 1024;  // with both parts; high only
+    static constexpr int BYTES = COUNT * (NS == 2 ? 2048 : 1024);  // bf16: two parts
     __host__ __device__ static constexpr bool lower(int m, int s) { return s * KS <= 16 * m + 15; }
     __host__ __device__ static constexpr bool upper(int m, int s) { return (s + 1) * KS > 16 * m; }
     __host__ __device__ static constexpr int at(int m, int s, bool up) {
@@ -186,16 +185,12 @@ struct DOps<BF16> {
         const u32x4_t* p = reinterpret_cast<const u32x4_t*>(m) + f * 128 + lane;
         return {__builtin_bit_cast(bf16x8_t, p[0]), __builtin_bit_cast(bf16x8_t, p[64])};
     }
-    // of a matrix of high parts only
-    __device__ static __forceinline__ Fa mat_frag_hi(const char* m, int f, int lane) {
-        return __builtin_bit_cast(bf16x8_t, reinterpret_cast<const u32x4_t*>(m)[f * 64 + lane]);
-    }
     // writes the fragment of x: a: the step's first 4 values of this lane, b: its last 4
-    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b, bool lo) {
+    __device__ static __forceinline__ void mat_store(char* m, int f, int lane, f32x4_t a, f32x4_t b) {
         const Fb x = split(a, b);
-        u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * (lo ? 128 : 64) + lane;
+        u32x4_t* p = reinterpret_cast<u32x4_t*>(m) + f * 128 + lane;
         p[0] = __builtin_bit_cast(u32x4_t, x.hi);
-        if (lo) p[64] = __builtin_bit_cast(u32x4_t, x.lo);
+        p[64] = __builtin_bit_cast(u32x4_t, x.lo);
     }
     // A block of 16 TPS rows x 16 columns in accumulators, 16 bytes a lane and 1 KB together (block i of p), and the way
     // of a lane's part to row n16 of an LDS tile (the block transposed: its rows become columns c0 ..)

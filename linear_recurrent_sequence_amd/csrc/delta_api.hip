@@ -123,7 +123,6 @@ void fill(DeltaArgs& A, const Shape& s, const Plan& p, bool bwd, void* workspace
     A.dut = (char*)workspace + p.dut;
     A.out_bf16 = out_dt == RET_BF16;
     A.gate_bf16 = gate_dt == RET_BF16;
-    A.p_lo = out_dt == RET_F32;
     A.scale = scale_of(scale, s.dk);
 }
 

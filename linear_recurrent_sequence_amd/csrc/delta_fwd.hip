@@ -39,7 +39,7 @@ __device__ __forceinline__ void tri_store(float* X, int r0, int c0, int lane, f3
 // Writes a lower triangular 64 x 64 fp32 LDS matrix (or its transpose) as operand fragments, a row tile per wave, this
 // lane's row (16 w + lane % 16) times `scale`.
 template <class E, bool TR>
-__device__ __forceinline__ void write_mat(char* m, const float* X, int w, int lane, bool lo, float scale = 1.f) {
+__device__ __forceinline__ void write_mat(char* m, const float* X, int w, int lane, float scale = 1.f) {
     typedef DOps<E> D;
     typedef TriFrags<D::KS> F;
     const int r = 16 * w + (lane & 15), g4 = 4 * (lane >> 4);
@@ -51,7 +51,7 @@ __device__ __forceinline__ void write_mat(char* m, const float* X, int w, int la
     for (int s = 0; s < F::NS; ++s) {
         if (TR ? !F::upper(w, s) : !F::lower(w, s)) continue;
         const int f = F::at(w, s, TR);
-        if constexpr (D::TPS == 2) D::mat_store(m, f, lane, scale * take(32 * s + g4), scale * take(32 * s + 16 + g4), lo);
+        if constexpr (D::TPS == 2) D::mat_store(m, f, lane, scale * take(32 * s + g4), scale * take(32 * s + 16 + g4));
         else D::mat_store(m, f, lane, scale * take(16 * s + g4));
     }
 }
@@ -213,12 +213,12 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
         }
         __syncthreads();
         if constexpr (BWD) {
-            write_mat<E, true>(mats + 2 * kDeltaMatBytes, sT, w, lane, true);
+            write_mat<E, true>(mats + 2 * kDeltaMatBytes, sT, w, lane);
             __syncthreads();
         }
         tri_inverse(sA, sT, w, lane);
         if constexpr (BWD) {
-            write_mat<E, false>(mats, sT, w, lane, true);
+            write_mat<E, false>(mats, sT, w, lane);
             // Tr = (I + Ar)^-1 with beta along the rows, the gradients' solve: with A = L diag(beta) and Ar = diag(beta) L,
             // Tr = I - diag(beta) T L
 #pragma unroll
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
                 tri_store(sT, 16 * w, 16 * j, lane, x);
             }
             __syncthreads();
-            write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane, true);
+            write_mat<E, true>(mats + kDeltaMatBytes, sT, w, lane);
         } else {
             // P T: row tile w through sA (its own rows only), and T with its rows scaled
 #pragma unroll
@@ -248,8 +248,8 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
 #pragma unroll
             for (int j = 0; j < 4; ++j) tri_store(sA, 16 * w, 16 * j, lane, pv[j]);
             __syncthreads();
-            write_mat<E, false>(mats + kDeltaMatBytes, sA, w, lane, a.p_lo);
-            write_mat<E, false>(mats, sT, w, lane, true, sF[16 * w + n16]);
+            write_mat<E, false>(mats + kDeltaMatBytes, sA, w, lane);
+            write_mat<E, false>(mats, sT, w, lane, sF[16 * w + n16]);
         }
         __syncthreads();
     }
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
 // ---------------------------------------------------------------------------------------------------
 // delta_chain: one segment of one head, 16 columns per wave, the state in accumulators. Columns are independent: what the
 // waves of a workgroup share are the rows of K and Q and the matrices, which go through LDS once for all of them.
-//   kFull: outputs (bf16 from bf16 input, else fp32); kFullF32: BF16 input, F32 output. After the last segment the state.
+//   kFull: outputs of the input's type; kFullF32: BF16 input, F32 output. After the last segment the state.
 //   kLocal / kLocalRaw (with Ts / with T): the segment's end state from zero (columns of V; segment 0 starts from state_in)
 //     into segE, or its transition (columns of the identity, V = 0) into segM.
 //   kStates (with T): the states entering the chunks and E, for the gradients.
@@ -281,11 +281,14 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     typedef TriFrags<D::KS> F;
     constexpr bool LOCAL = MODE == kLocal || MODE == kLocalRaw, FULL = MODE == kFull || MODE == kFullF32;
     constexpr bool RAW = MODE == kLocalRaw || MODE == kStates;
-    constexpr bool HI = MODE == kFull && sizeof(st) == 2;  // outputs in bf16: the high parts of S and P T suffice, whose
-                                                           // rounding is like the output's own
-    typedef typename std::conditional<HI, uint16_t, float>::type out_t;
+    constexpr bool OUT16 = MODE == kFull && sizeof(st) == 2;
+    // Q S takes S rounded once where its two parts would not fit the registers and the output is rounded like that anyway
+    // (error of bf16 outputs 0.0018 to 0.0020, their rounding alone 0.0017; 2741 tokens at d_k = 256, d_v = 512: 339 us, with both 389);
+    // at d_k <= 128 both parts cost 2 in 100
+    constexpr bool HI = OUT16 && DK > 128;
+    typedef typename std::conditional<OUT16, uint16_t, float>::type out_t;
     constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS, TB = DT < 4 ? DT : 4;
-    constexpr int PB = FULL ? (HI ? F::HI_BYTES : F::BYTES) : 16;
+    constexpr int PB = FULL ? F::BYTES : 16;
     __shared__ __align__(16) st sk[2][kDeltaC * Tile::LD];
     __shared__ __align__(16) st sq[FULL ? kDeltaC * Tile::LD : 16];
     __shared__ __align__(16) st sv[kDeltaC * VTile::LD];
@@ -441,11 +444,11 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
         }
         __syncthreads();  // the matrices are there, and everyone is done with Q
         if constexpr (FULL) {
-            typename std::conditional<HI, typename D::Fa, typename D::Fm>::type fpt[F::COUNT];
+            typename D::Fm fpt[F::COUNT];
 #pragma unroll
             for (int f = 0; f < F::COUNT; ++f) {
-                if constexpr (HI) fpt[f] = D::mat_frag_hi(sp, f, lane);
-                else fpt[f] = D::mat_frag(sp, f, lane);
+                
+                fpt[f] = D::mat_frag(sp, f, lane);
             }
 #pragma unroll
             for (int m = 0; m < 4; ++m) o[m] *= a.scale * sf[p][16 * m + n16];
