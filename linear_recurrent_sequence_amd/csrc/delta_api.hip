@@ -32,6 +32,8 @@ ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, 
     const long long w = (long long)s.H * (s.dk > s.dv ? s.dk : s.dv);
     if (w * kDeltaC * 4 >= 1LL << 30)
         return fail(RET_ERR_UNSUPPORTED, "H*max(d_k,d_v)=%lld too large", w);
+    if ((long long)s.dk * s.dv * 4 >= 1LL << 30)  // and so is a head's state
+        return fail(RET_ERR_UNSUPPORTED, "d_k*d_v=%lld too large", (long long)s.dk * s.dv);
     return RET_OK;
 }
 
