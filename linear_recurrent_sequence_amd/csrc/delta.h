@@ -61,13 +61,14 @@ typedef void (*delta_kernel_t)(DeltaArgs);
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // Which segment and column block a workgroup has. Workgroups go round the 8 XCDs by their index; the column blocks of a
-// segment read the same q, k and matrices, so they get indices 8 apart: one XCD, one L2, one after the other.
+// segment read the same q, k and matrices, so they get indices 8 apart: one XCD, one L2, one after the other. Heads go
+// before segments: an XCD gets its share of every segment, of which the first and the last are short in a local pass.
 struct DeltaBlock {
     int bh, seg, cb;
 };
 __device__ __forceinline__ DeltaBlock delta_block(const DeltaArgs& a, int ncb) {
     const int i = blockIdx.x / 8, unit = i / ncb * 8 + blockIdx.x % 8;
-    return {unit / a.nseg, unit % a.nseg, i % ncb};
+    return {unit % (a.B * a.H), unit / (a.B * a.H), i % ncb};
 }
 // Live tokens of sequence b.
 __device__ __forceinline__ int delta_len(const DeltaArgs& a, int b) {

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
     const int g4 = 4 * (lane >> 4);
     const DeltaBlock blk = delta_block(a, (a.dv + COLS - 1) / COLS);
-    if (blk.bh >= a.B * a.H) return;
+    if (blk.seg >= a.nseg) return;
     const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
     const int mine = 16 * w, col0 = blk.cb * COLS + mine;  // the wave's columns: in the tile, of d_v
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);

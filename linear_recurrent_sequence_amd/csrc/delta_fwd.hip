@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     const int g4 = 4 * (lane >> 4);
     const int nE = (a.dv + COLS - 1) / COLS;  // workgroups over d_v; a local pass has those of d_k behind them
     const DeltaBlock blk = delta_block(a, nE + (LOCAL ? (DK + COLS - 1) / COLS : 0));
-    if (blk.bh >= a.B * a.H) return;
+    if (blk.seg >= a.nseg) return;
     const int bh = blk.bh, seg = blk.seg, b = bh / a.H, h = bh % a.H;
     const bool trans = LOCAL && blk.cb >= nE;
     const int width = trans ? DK : a.dv;
@@ -307,8 +307,8 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     const int hk = h / (a.H / a.Hk), len = delta_len(a, b);
     const int c0 = seg * a.seg_chunks, c1 = min(c0 + a.seg_chunks, a.nchunks);
     const bool active = col0 < width;  // (a wave without columns computes on zeros)
-    // segment 0's end state is known, and no one asks for the last one's
-    if (LOCAL && (trans ? seg == 0 : seg == a.nseg - 1)) return;
+    // no one asks for the last segment's end state, nor (segment 0's being the true one) for either end's transition
+    if (LOCAL && (seg == a.nseg - 1 || (trans && seg == 0))) return;
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
     f32x4_t S[DT];
