@@ -100,6 +100,10 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     }
     return p;
 }
+// delta_prep: the value heads of a key head share a workgroup unless the card takes one for each at once.
+dim3 prep_grid(const Plan& p, const Shape& s) {
+    return dim3(p.nchunks, s.B * s.Hk, (long long)p.nchunks * s.B * s.H <= 512 ? s.H / s.Hk : 1);
+}
 
 void fill(DeltaArgs& A, const Shape& s, const Plan& p, bool bwd, void* workspace, ret_dtype_t out_dt,
           ret_dtype_t gate_dt, float scale) {
@@ -194,7 +198,7 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     A.state_in = state_in;
     A.state_out = state_out;
     hipStream_t str = (hipStream_t)stream;
-    if ((st = launch("ret_delta_prep", kn.prep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
+    if ((st = launch("ret_delta_prep", kn.prep, prep_grid(p, s), str, op, A)) != RET_OK) return st;
     const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
         if ((st = launch("ret_delta_local", kn.local, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
@@ -261,7 +265,7 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
     A.dg = dg;
     A.dbeta = dbeta;
     hipStream_t str = (hipStream_t)stream;
-    if ((st = launch("ret_delta_prep", kn.bprep, dim3(p.nchunks, B * Hk), str, op, A)) != RET_OK) return st;
+    if ((st = launch("ret_delta_prep", kn.bprep, prep_grid(p, s), str, op, A)) != RET_OK) return st;
     const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
         if ((st = launch("ret_delta_local", kn.blocal, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
