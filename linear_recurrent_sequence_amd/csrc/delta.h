@@ -7,15 +7,23 @@
 //     Y = K S_0,  R = V - exp(G) Y,  E = T R,
 //     O = scale exp(G) Q S_0 + P E,         S_C = exp(G_C) S_0 + K^T diag(exp(G_C - G) beta) E.
 // T and P do not depend on the state: one kernel makes them for every chunk at once (delta_prep); the forward takes
-// Ts = diag(exp(G_C - G) beta) T and P T, so that one operand, R, gives both outputs and the state's update. The rest is a chain
-// over chunks with the state in MFMA accumulators. Columns of S are independent of each other, so each wave owns some of
-// them and no product of the chain leaves its wave: an accumulator tile (column in the lane, rows 4g .. 4g+3 of lane
-// group g) is the other operand of the next product once the reduction index is taken in that order.
+// Ts = diag(exp(G_C - G) beta) T and P T, so that one operand, R, gives both outputs and the state's update. The rest is a
+// chain over chunks with the state in MFMA accumulators. Columns of S are independent of each other, so each wave owns 16
+// and no product of the chain leaves its wave: an accumulator tile (column in the lane, rows 4g .. 4g+3 of lane group g)
+// is the other operand of the next product once the reduction index is taken in that order.
+//
+// Where B H d_v / 128 chains leave CUs idle, a sequence is cut into segments: a local pass gives each segment's end state
+// from zero and its transition (the chain run on the columns of the identity), a scan over the segments the states that
+// enter them, and the full pass starts all of them at once. The gradients do the same from the right with the transposed
+// transitions. A chain step costs 4 to 10 us whatever the number of workgroups, one per CU fits, so the cut aims at one
+// workgroup per CU (two where rows are short and two fit).
 //
 // Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, E, T, P) is split in
 // two bf16 parts, x = hi + lo + e with |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two products where the
 // other side is an input, which is exact): the carried state keeps fp32-like accuracy over any number of chunks, where a
-// single rounding of E and S would leave 2^-9 in it. F32 inputs run on the fp32 MFMA.
+// single rounding of E and S would leave 2^-9 in it. What leaves a chain for the gradients' per-chunk kernel (S_0, dS_C,
+// E, dU) is stored in the input's type: at d_k = 256, d_v = 512 these are 512 KB of a chunk's 830 in bf16. F32 inputs run
+// on the fp32 MFMA.
 #pragma once
 
 #include "chunk_bf16.h"
@@ -109,8 +117,9 @@ struct TriFrags {
 // ---------------------------------------------------------------------------------------------------
 // Operands. KS: reduction length of one step; TPS: accumulator tiles (16 rows) that make one step. In a step lane group g
 // holds indices 4g..4g+3 of each tile. Fa: rows of an input matrix in LDS (exact). Fb: an operand made from accumulators.
-// Fm: a 64 x 64 matrix fragment from the workspace. mma_ab(acc, a, b) adds a.b with accumulator rows along a's rows;
-// mma_ba swaps the sides (accumulator rows along b's columns), so a lane holds 4 consecutive columns of one token.
+// Fm: a 64 x 64 matrix fragment from the workspace. part(acc, a, b, p) adds the p-th product of a.b with accumulator rows
+// along a's rows; part_t swaps the sides (accumulator rows along b's columns), so a lane holds 4 consecutive columns of
+// one token.
 // ---------------------------------------------------------------------------------------------------
 template <class E>
 struct DOps;

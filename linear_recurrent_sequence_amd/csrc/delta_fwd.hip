@@ -20,6 +20,10 @@ typedef double f64;
 //
 // The unit triangular inverse goes by 16 x 16 blocks: the four diagonal ones by forward substitution, a column per lane,
 // then twice the block rule [[X, 0], [A, Y]]^-1 = [[X', 0], [-Y' A X', Y']] with fp32 MFMA.
+//
+// A workgroup's steps wait for each other (gates, inverse, products: eight barriers), so what counts is how many share a
+// CU: the fp32 matrices lie where the rows were. 8192 chunks at d_k = 128: 109 us, 32 KB read and 26 KB written each,
+// 4.4 TB/s; the copy rate would give 93.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kTriLD = 68;  // row pitch of the fp32 matrices in LDS
 
@@ -269,6 +273,11 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
 // chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave stages the
 // columns of V it owns. Requests are never conditional: where two branches join, their registers would be waited for.
 // Fragments of the next reduction step are read ahead of a step's products.
+//
+// At d_k = 256 with 8 waves a step of the full pass takes 7 us: 2.5 us of MFMA issue, 0.75 MB of fragments out of LDS (2.7
+// us), and the rest the dependence Y -> R -> E -> S at two waves per SIMD. Eight waves rather than four halve the staging
+// per column; more workgroups per CU (128 registers) cost more in spills than they hid (local pass 200 -> 222 us). Full
+// pass, 256 workgroups: 75 us for 16 chunks at d_k = 128, 310 us for 43 at 256; local pass 173 us for 32 at 256.
 // ---------------------------------------------------------------------------------------------------
 enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
 template <class E, int DK, int NW, int MODE>
@@ -540,9 +549,10 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
 // delta_scan: the states entering the segments. In: segE[s] = segment s's end state from zero (segment 0: its true end
 // state), segM[s] its transition. Out: segE[s] = the state entering segment s, S_{s+1} = M_s S_s + E_s. One workgroup per
 // (b, h, 32 columns); REV: the gradients' chain, D_{s-1} = M_s^T D_s + F_s over segF from the right. The waves share the
-// rows of M; S goes round through LDS, transposed, so that it is written and read 16 bytes at a time. A step is bound by the latency of
-// its rows of M: each part is requested for the next segment as soon as its products have it (measured below, without:
-// 64 KB transitions 2.8 us a segment). BF16 input: M and S split in two bf16 parts like the chain's operands.
+// rows of M; S goes round through LDS, transposed, so that it is written and read 16 bytes at a time. Each part of M is
+// requested for the next segment as soon as its products have it (64 KB transitions 2.8 -> 2.3 us a segment). What is left
+// is what a CU draws, 80 KB a segment at d_k = d_v = 128: two segments in flight, or S split once in LDS, change nothing.
+// BF16 input: M and S split in two bf16 parts like the chain's operands.
 // ---------------------------------------------------------------------------------------------------
 // waves of a scan workgroup: 16 rows of the state each, 32 at d_k = 256 (the rows of M in flight take the registers)
 template <int DK>
