@@ -451,9 +451,8 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
  * handed to ret_gated_delta_step. lengths (device int32[B], or NULL): sequence b has lengths[b] tokens (0 .. N, other
  * values are taken as the nearest of these); inputs past them are not used, outputs past them are zero, and state_out is
  * the state after lengths[b] tokens. Products accumulate in fp32; on BF16 input everything the kernels compute and
- * multiply again (the state among it) is split in two bf16 parts, so results carry about 2^-17; at d_k = 256 a BF16
- * output reads the state rounded to bf16 once (a relative 2^-9 of its terms, as its own rounding). A NaN or infinity of
- * a token can reach the outputs of its own chunk's earlier tokens.
+ * multiply again (the state among it) is split in two bf16 parts, so results carry about 2^-17. A NaN or infinity of a
+ * token can reach the outputs of its own chunk's earlier tokens.
  * workspace: ret_gated_delta_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing
  * one must not overlap in time. Supported: d_k in {32, 64, 128, 256} (BF16) or {16, 32, 64, 128} (F32), d_v a multiple
  * of 16, B*H <= 65535, N >= 1, H * max(d_k, d_v) < 2^22, d_k * d_v < 2^28. Written buffers must not overlap other

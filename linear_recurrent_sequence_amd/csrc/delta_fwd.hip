@@ -268,16 +268,17 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
 //   kLocal / kLocalRaw (with Ts / with T): the segment's end state from zero (columns of V; segment 0 starts from state_in)
 //     into segE, or its transition (columns of the identity, V = 0) into segM.
 //   kStates (with T): the states entering the chunks and E, for the gradients.
-// A step: Y = K S, between its products the requests for everything the next chunk needs, into registers; R; O from
-// Q S and P T; E; the state; then the registers go to LDS. K has two buffers, so that nothing but the first barrier of a
-// chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave stages the
+// A step: Y = K S and Q S, between their products the requests for everything the next chunk needs, into registers; R; O
+// from Q S and P T; E; the state; then the registers go to LDS. K has two buffers, so that nothing but the first barrier
+// of a chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave stages the
 // columns of V it owns. Requests are never conditional: where two branches join, their registers would be waited for.
 // Fragments of the next reduction step are read ahead of a step's products.
 //
-// At d_k = 256 with 8 waves a step of the full pass takes 7 us: 2.5 us of MFMA issue, 0.75 MB of fragments out of LDS (2.7
-// us), and the rest the dependence Y -> R -> E -> S at two waves per SIMD. Eight waves rather than four halve the staging
-// per column; more workgroups per CU (128 registers) cost more in spills than they hid (local pass 200 -> 222 us). Full
-// pass, 256 workgroups: 75 us for 16 chunks at d_k = 128, 310 us for 43 at 256; local pass 173 us for 32 at 256.
+// At d_k = 256 with 8 waves a step of the full pass takes 7 us, 16600 cycles: K S and Q S 7200 (one after the other they
+// take as long), R and P T R 2600, T R and the store 1300, the state 2600, barriers and staging 2900. MFMA issue is 6000,
+// 1 MB of fragments out of LDS 8000. Eight waves rather than four halve the staging per column; more workgroups per CU (128
+// registers) cost more in spills than they hid (local pass 200 -> 222 us). Full pass, 256 workgroups: 75 us for 16 chunks
+// at d_k = 128, 310 us for 43 at 256; local pass 173 us for 32 at 256.
 // ---------------------------------------------------------------------------------------------------
 enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
 template <class E, int DK, int NW, int MODE>
@@ -293,10 +294,6 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     constexpr bool LOCAL = MODE == kLocal || MODE == kLocalRaw, FULL = MODE == kFull || MODE == kFullF32;
     constexpr bool RAW = MODE == kLocalRaw || MODE == kStates;
     constexpr bool OUT16 = MODE == kFull && sizeof(st) == 2;
-    // Q S takes S rounded once where its two parts would not fit the registers and the output is rounded like that anyway
-    // (error of bf16 outputs 0.0018 to 0.0020, their rounding alone 0.0017; 2741 tokens at d_k = 256, d_v = 512: 339 us, with both 389);
-    // at d_k <= 128 both parts cost 2 in 100
-    constexpr bool HI = OUT16 && DK > 128;
     typedef typename std::conditional<OUT16, uint16_t, float>::type out_t;
     constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS, TB = DT < 4 ? DT : 4;
     constexpr int PB = FULL ? F::BYTES : 16;
@@ -394,17 +391,21 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
                 for (int t = 0; t < DT / D::TPS; ++t) D::blk_store(out, t, lane, &S[D::TPS * t]);
         }
-        f32x4_t y[4];
+        // Y = K S and O^T = (Q S)^T: there a lane holds 4 columns of token 16 m + n16
+        f32x4_t y[4], o[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) y[m] = zero;
-        {  // Y = K S
-            typename D::Fa fk[2][4];
+        for (int m = 0; m < 4; ++m) y[m] = o[m] = zero;
+        {
+            typename D::Fa fk[2][4], fq[4];
             typename D::Fb fs[2];
 #pragma unroll
             for (int m = 0; m < 4; ++m) fk[0][m] = Tile::rows(K, 16 * m, 0, lane);
             fs[0] = D::step(S, 0);
 #pragma unroll
             for (int s = 0; s < KN; ++s) {
+                if constexpr (FULL)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) fq[m] = Tile::rows(sq, 16 * m, s * D::KS, lane);
                 if (s + 1 < KN)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, (s + 1) * D::KS, lane);
@@ -412,6 +413,13 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
                 for (int i = NL * s / KN; i < NL * (s + 1) / KN; ++i) request(i);
                 keep_order();
                 D::template products<4>(y, 0, fk[s & 1], fs[s & 1]);
+                if constexpr (FULL) {
+                    keep_order();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) D::part_t(o[m], fq[m], fs[s & 1], p);
+                }
                 if (s + 1 < KN) fs[(s + 1) & 1] = D::step(S, s + 1);
                 keep_order();
             }
@@ -423,36 +431,6 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
         typename D::Fb fr[NS];
 #pragma unroll
         for (int s = 0; s < NS; ++s) fr[s] = D::step(y, s);
-        f32x4_t o[4];
-        if constexpr (FULL) {
-            // O^T = scale exp(G) (Q S)^T + R^T (P T)^T: a lane holds 4 columns of token 16 m + n16
-#pragma unroll
-            for (int m = 0; m < 4; ++m) o[m] = zero;
-            typename D::Fa fq[2][4];
-            typename D::Fx fx[2];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) fq[0][m] = Tile::rows(sq, 16 * m, 0, lane);
-            if constexpr (HI) fx[0] = D::step_exact(S, 0);
-#pragma unroll
-            for (int s = 0; s < KN; ++s) {
-                if (s + 1 < KN)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) fq[(s + 1) & 1][m] = Tile::rows(sq, 16 * m, (s + 1) * D::KS, lane);
-                keep_order();
-                if constexpr (HI) {
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) D::mma_aa(o[m], fx[s & 1], fq[s & 1][m]);
-                    if (s + 1 < KN) fx[(s + 1) & 1] = D::step_exact(S, s + 1);
-                } else {
-                    const typename D::Fb fs = D::step(S, s);
-#pragma unroll
-                    for (int p = 0; p < 4; ++p)
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) D::part_t(o[m], fq[s & 1][m], fs, p);
-                }
-                keep_order();
-            }
-        }
         __syncthreads();  // the matrices are there, and everyone is done with Q
         if constexpr (FULL) {
             typename D::Fm fpt[F::COUNT];
