@@ -212,6 +212,33 @@ struct DOps<BF16> {
         *reinterpret_cast<uint2*>(lds + Tile::off(row, c0 + g4)) = make_uint2(x[0], x[1]);
         *reinterpret_cast<uint2*>(lds + Tile::off(row, c0 + 16 + g4)) = make_uint2(x[2], x[3]);
     }
+    // The rows of the state that lane group g holds of tile t: a step's two tiles together are 8 consecutive ones, so that
+    // rows of K and Q are read 16 bytes at a time (reads of 8 run at half the LDS's rate)
+    __device__ static __forceinline__ int srow(int t, int g4) { return 32 * (t / 2) + 4 * (t % 2) + 2 * g4; }
+    template <class T>
+    __device__ static __forceinline__ void blk_lds_s(st* lds, int row, int c0, int g4, u32x4_t x) {
+        *reinterpret_cast<u32x4_t*>(lds + T::off(row, c0 + 2 * g4)) = x;
+    }
+    // LDS tile [tokens][W] for the chains: rows(s): step s in the state's order; cols(t): the columns of the state's tile t.
+    // Rows 16 banks apart, their 16-byte pieces swapped by row / 4: 8 rows' pieces, and the 4 rows x 4 pieces of a
+    // transposing read, lie in different banks.
+    template <int W>
+    struct STile {
+        static constexpr int LD = W + 32;
+        __device__ static __forceinline__ int off(int r, int c) { return r * LD + (c ^ (((r >> 2) & 3) << 3)); }
+        __device__ static __forceinline__ Fa rows(const st* X, int r0, int s, int lane) {
+            return __builtin_bit_cast(bf16x8_t, *reinterpret_cast<const u32x4_t*>(
+                                                    X + r0 * LD + 32 * s + off(lane & 15, 8 * (lane >> 4))));
+        }
+        __device__ static __forceinline__ Fa cols(const st* X, int k0, int t, int lane) {
+            typedef __attribute__((address_space(3))) bf16x4_t lds_bf16x4_t;
+            st* p = const_cast<st*>(X) + k0 * LD + 32 * (t / 2) + 4 * (t % 2) +
+                    off(4 * (lane >> 4) + ((lane >> 2) & 3), 8 * (lane & 3));
+            const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)p));
+            const uint2 hi = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t*)(p + 16 * LD)));
+            return __builtin_bit_cast(bf16x8_t, make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
+    };
     // LDS tile [rows][W], read by rows and transposed
     template <int W>
     struct Tile {
@@ -295,6 +322,19 @@ struct DOps<F32> {
         __device__ static __forceinline__ f32x4_t acc(const st* X, int m, int n0, int lane) {
             return cols(X, 16 * m, n0, lane);
         }
+    };
+    __device__ static __forceinline__ int srow(int t, int g4) { return 16 * t + g4; }
+    template <class T>
+    __device__ static __forceinline__ void blk_lds_s(st* lds, int row, int c0, int g4, u32x4_t x) {
+        blk_lds<T>(lds, row, c0, g4, x);
+    }
+    template <int W>
+    struct STile {
+        typedef Tile<W> T;
+        static constexpr int LD = T::LD;
+        __device__ static __forceinline__ int off(int r, int c) { return T::off(r, c); }
+        __device__ static __forceinline__ Fa rows(const st* X, int r0, int s, int lane) { return T::rows(X, r0, 16 * s, lane); }
+        __device__ static __forceinline__ Fa cols(const st* X, int k0, int t, int lane) { return T::cols(X, k0, 16 * t, lane); }
     };
 };
 

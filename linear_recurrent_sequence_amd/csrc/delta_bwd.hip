@@ -33,7 +33,7 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
     constexpr int NT = 64 * NW, COLS = 16 * NW;
-    typedef DRows<E, DK, NT> Rows;
+    typedef DRows<E, DK, NT, typename D::template STile<DK>> Rows;
     typedef DRows<E, 16, 64, typename D::template Tile<COLS>> ORows;  // a wave's own columns of dO
     typedef typename Rows::Tile Tile;
     typedef typename ORows::Tile OTile;
@@ -64,11 +64,11 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < DT; ++t) S[t] = zero;
     if (sin && active) {
-        const float* p = sin + (long long)g4 * a.dv + col0 + n16;
+        const float* p = sin + col0 + n16;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(16 * t + i) * a.dv];
+            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(D::srow(t, g4) + i) * a.dv];
     }
     Rows rk, rq;
     ORows ro;
@@ -167,7 +167,7 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
             for (int s = 0; s < KN; ++s) {
                 if (s + 1 < KN)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, (s + 1) * D::KS, lane);
+                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, s + 1, lane);
 #pragma unroll
                 for (int i = NL * s / KN; i < NL * (s + 1) / KN; ++i) request(i);
                 keep_order();
@@ -182,13 +182,13 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
         auto update = [&](const st* X, const typename D::Fb (&f)[NS], bool scaled, float end) {
             typename D::Fa fc[2][TB];
 #pragma unroll
-            for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(X, 0, 16 * t, lane);
+            for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(X, 0, t, lane);
 #pragma unroll
             for (int i = 0; i < NS * DT / TB; ++i) {
                 const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
                 if (i + 1 < NS * DT / TB)
 #pragma unroll
-                    for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(X, s1 * D::KS, 16 * (t1 + t), lane);
+                    for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(X, s1 * D::KS, t1 + t, lane);
                 keep_order();
                 if (scaled && s == 0)
 #pragma unroll
@@ -277,11 +277,11 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
     if (LOCAL) out = a.segF + ((long long)bh * a.nseg + seg) * DK * a.dv;
     else if (seg == 0 && a.dstate_in) out = a.dstate_in + (long long)bh * DK * a.dv;
     if (!out) return;
-    out += (long long)g4 * a.dv + col0 + n16;
+    out += col0 + n16;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[(long long)(16 * t + i) * a.dv] = S[t][i];
+        for (int i = 0; i < 4; ++i) out[(long long)(D::srow(t, g4) + i) * a.dv] = S[t][i];
 }
 
 // R rows of W elements to an LDS tile by NT threads: rows at or past `rows` and columns at or past `cols` are zero.
@@ -312,7 +312,8 @@ struct GRows {
 
 // Blocks of 16 columns x R rows of an array stored by blk_store, VB columns of them, to an LDS tile [VB][R] by NT threads;
 // columns at or past `cols` are zero.
-template <class E, int R, int VB, int NT>
+// STATE: rows in the state's order.
+template <class E, int R, int VB, int NT, bool STATE>
 struct GBlocks {
     typedef typename E::st st;
     typedef DOps<E> D;
@@ -328,8 +329,10 @@ struct GBlocks {
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int s = tid + i * NT, blk = s / 64, lane = s % 64;
-            if (N % NT == 0 || s < N)
-                D::template blk_lds<Tile>(lds, blk / PER * 16 + (lane & 15), blk % PER * 16 * D::TPS, 4 * (lane >> 4), x[i]);
+            const int row = blk / PER * 16 + (lane & 15), c0 = blk % PER * 16 * D::TPS;
+            if (N % NT != 0 && s >= N) continue;
+            if constexpr (STATE) D::template blk_lds_s<Tile>(lds, row, c0, 4 * (lane >> 4), x[i]);
+            else D::template blk_lds<Tile>(lds, row, c0, 4 * (lane >> 4), x[i]);
         }
     }
 };
@@ -418,9 +421,9 @@ __global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <=
 #pragma unroll
         for (int j = 0; j < 4; ++j) M[0][j] = M[kM2][j] = zero;
         float dot = 0.f;
-        GBlocks<E, DK, VB, NT> rs, rd;
+        GBlocks<E, DK, VB, NT, true> rs, rd;
         GRows<E, kDeltaC, VB, NT> ro;
-        GBlocks<E, kDeltaC, VB, NT> re, ru;
+        GBlocks<E, kDeltaC, VB, NT, false> re, ru;
         const st* sp = (const st*)a.s0t + unit * a.dv * DK;
         const st* dp = (const st*)a.ds1t + unit * a.dv * DK;
         const st* ep = (const st*)a.et + unit * a.dv * kDeltaC;

@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
     constexpr int NT = 64 * NW, COLS = 16 * NW;
-    typedef DRows<E, DK, NT> Rows;
+    typedef DRows<E, DK, NT, typename D::template STile<DK>> Rows;
     typedef DRows<E, 16, 64, typename D::template Tile<COLS>> VRows;  // a wave's own columns
     typedef typename Rows::Tile Tile;
     typedef typename VRows::Tile VTile;
@@ -327,13 +327,13 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) S[t][i] = trans && 16 * t + g4 + i == col0 + n16 ? 1.f : 0.f;
+        for (int i = 0; i < 4; ++i) S[t][i] = trans && D::srow(t, g4) + i == col0 + n16 ? 1.f : 0.f;
     if (sin && active) {
-        const float* p = sin + (long long)g4 * a.dv + col0 + n16;
+        const float* p = sin + col0 + n16;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(16 * t + i) * a.dv];
+            for (int i = 0; i < 4; ++i) S[t][i] = p[(long long)(D::srow(t, g4) + i) * a.dv];
     }
 
     Rows rk, rq;
@@ -405,10 +405,10 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
             for (int s = 0; s < KN; ++s) {
                 if constexpr (FULL)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) fq[m] = Tile::rows(sq, 16 * m, s * D::KS, lane);
+                    for (int m = 0; m < 4; ++m) fq[m] = Tile::rows(sq, 16 * m, s, lane);
                 if (s + 1 < KN)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, (s + 1) * D::KS, lane);
+                    for (int m = 0; m < 4; ++m) fk[(s + 1) & 1][m] = Tile::rows(K, 16 * m, s + 1, lane);
 #pragma unroll
                 for (int i = NL * s / KN; i < NL * (s + 1) / KN; ++i) request(i);
                 keep_order();
@@ -482,7 +482,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
         typename D::Fb fu[NS];
         typename D::Fa fc[2][TB];
 #pragma unroll
-        for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, 16 * t, lane);
+        for (int t = 0; t < TB; ++t) fc[0][t] = Tile::cols(K, 0, t, lane);
 #pragma unroll
         for (int s = 0; s < NS; ++s) fu[s] = D::step(u, s);
 #pragma unroll
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
             const int s = i % NS, t0 = i / NS * TB, s1 = (i + 1) % NS, t1 = (i + 1) / NS * TB;
             if (i + 1 < NS * DT / TB)
 #pragma unroll
-                for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, 16 * (t1 + t), lane);
+                for (int t = 0; t < TB; ++t) fc[(i + 1) & 1][t] = Tile::cols(K, s1 * D::KS, t1 + t, lane);
             keep_order();
             if (s == 0)
 #pragma unroll
@@ -516,11 +516,11 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     if (LOCAL) out = (trans ? a.segM : a.segE) + ((long long)bh * a.nseg + seg) * DK * width;
     else if (seg == a.nseg - 1 && a.state_out) out = a.state_out + (long long)bh * DK * a.dv;
     if (!out) return;
-    out += (long long)g4 * width + col0 + n16;
+    out += col0 + n16;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[(long long)(16 * t + i) * width] = S[t][i];
+        for (int i = 0; i < 4; ++i) out[(long long)(D::srow(t, g4) + i) * width] = S[t][i];
 }
 
 // ---------------------------------------------------------------------------------------------------
