@@ -15,8 +15,9 @@
 // Where B H d_v / 128 chains leave CUs idle, a sequence is cut into segments: a local pass gives each segment's end state
 // from zero and its transition (the chain run on the columns of the identity), a scan over the segments the states that
 // enter them, and the full pass starts all of them at once. The gradients do the same from the right with the transposed
-// transitions. A chain step costs 4 to 10 us whatever the number of workgroups, one per CU fits, so the cut aims at one
-// workgroup per CU (two where rows are short and two fit).
+// transitions. A chain step costs 3 to 10 us whatever the number of workgroups, and one or two of
+// them fit a CU: the cut aims at one per CU, two where rows are short (two rounds of workgroups instead: 65536 tokens of 8
+// heads 708 us, one 577 then).
 //
 // Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, E, T, P) is split in
 // two bf16 parts, x = hi + lo + e with |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two products where the

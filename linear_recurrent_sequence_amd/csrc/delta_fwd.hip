@@ -274,11 +274,12 @@ __global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : 
 // columns of V it owns. Requests are never conditional: where two branches join, their registers would be waited for.
 // Fragments of the next reduction step are read ahead of a step's products.
 //
-// At d_k = 256 with 8 waves a step of the full pass takes 7 us, 16600 cycles: K S and Q S 7200 (one after the other they
-// take as long), R and P T R 2600, T R and the store 1300, the state 2600, barriers and staging 2900. MFMA issue is 6000,
-// 1 MB of fragments out of LDS 8000. Eight waves rather than four halve the staging per column; more workgroups per CU (128
-// registers) cost more in spills than they hid (local pass 200 -> 222 us). Full pass, 256 workgroups: 75 us for 16 chunks
-// at d_k = 128, 310 us for 43 at 256; local pass 173 us for 32 at 256.
+// At d_k = 256 with 8 waves a step of the full pass takes 6.4 us, 14300 cycles: K S and Q S 5050, R and P T R 1800, T R and
+// the store 1300, the state 2700, barriers and staging 3500. MFMA issue is 6000, 1 MB of fragments out of LDS 8000. Rows
+// read 8 bytes at a time cost 2300 more. Eight waves rather than four halve the staging per column; more workgroups per CU
+// (128 registers) cost more in spills than they hid (local pass at d_k = 128 200 -> 222 us). Full pass, one workgroup per
+// CU: 77 us for 16 chunks at d_k = 128, 277 us for 43 at 256; local pass 159 us for 32 at 256; states 214 for 32 at 256,
+// of which 670 MB of states and E at the copy rate are 131.
 // ---------------------------------------------------------------------------------------------------
 enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
 template <class E, int DK, int NW, int MODE>
