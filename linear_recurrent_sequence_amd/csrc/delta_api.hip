@@ -204,7 +204,9 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
         if ((st = launch("ret_delta_local", kn.local, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
             RET_OK)
             return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
+            RET_OK)
+            return st;
     }
     return launch("ret_delta_full", out_dt == RET_BF16 ? kn.full : kn.full_f32, dim3(units * nc), str, op, A, kn.threads);
 }
@@ -271,12 +273,16 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
         if ((st = launch("ret_delta_local", kn.blocal, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
             RET_OK)
             return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
+            RET_OK)
+            return st;
     }
     if ((st = launch("ret_delta_states", kn.states, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
     if (p.nseg > 1) {
         if ((st = launch("ret_delta_local_bwd", kn.rlocal, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
-        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
+            RET_OK)
+            return st;
     }
     if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
     return launch("ret_delta_grad", H > Hk ? kn.grad_group : kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);

@@ -371,7 +371,8 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 // 128 (at the copy rate 141).
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, int NW, bool GROUP>
-__global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <= 128 ? 2 : 1)) void delta_grad_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <= 128 ? 2 : 1))
+void delta_grad_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
     constexpr int NT = 64 * NW, HF = NW / 4, DH = DK / HF, DT = DH / 16, NS = kDeltaC / D::KS, VB = 32;
@@ -386,8 +387,8 @@ __global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <=
     __shared__ float sF[256], sDg[HF][kDeltaC], sDb[kDeltaC], sR[2][NW];
     st *sS = buf, *sD = sS + VB * TK::LD, *sO = sD + VB * TK::LD, *sE = sO + kDeltaC * TO::LD, *sU = sE + VB * TC::LD;
     st *sX = buf, *sZ = buf + kDeltaC * TC::LD;
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15, g4 = 4 * (lane >> 4);
-    const int tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
+    const int g4 = 4 * (lane >> 4), tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk;
     const int rep = GROUP ? a.H / a.Hk : 1;
     const int t0 = c * kDeltaC, len = delta_len(a, b), live = min(kDeltaC, len - t0);

@@ -126,7 +126,8 @@ __device__ __forceinline__ void tri_product(f32x4_t (&acc)[4], const float* X, c
 
 // As many workgroups on a CU as the LDS takes (their steps wait for each other): 2, 3 or 4.
 template <class E, int DK, bool BWD>
-__global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : BWD ? 3 : 4)) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, (DK * sizeof(typename E::st) > 256 ? 2 : BWD ? 3 : 4))
+void delta_prep_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DRows<E, DK, kThreads> Rows;
     typedef typename Rows::Tile Tile;

@@ -170,3 +170,74 @@ def test_block(R, dtype):
         off = float((got.double().cpu() - want).norm() / want.norm())
         print("   %-6s %.2e" % (name, off))
         assert off <= lim, (name, off)
+
+
+def test_two_graphs_share_a_workspace(R):
+    """A captured forward of one shape and captured gradients of another in one workspace, replayed in turn with eager
+    calls in the same workspace between: every replay has the eager call's bits. The gradients on another stream, their
+    workspace made by the call, too."""
+    import torch
+    def operands(seed, B, N, H, Hk, dk, dv):
+        return {n: t.cuda() for n, t in inputs(seed, B, N, H, Hk, dk, dv, "bf16").items()}
+    a, b = operands(1, 1, 400, 2, 2, 64, 96), operands(2, 2, 150, 4, 2, 128, 64)
+    names = ("q", "k", "v", "g", "beta")
+    opt = {"segments": 3}
+    ws = torch.empty(max(R.gated_delta_workspace(a["q"], a["v"], opt).numel(),
+                         R.gated_delta_bwd_workspace(b["q"], b["v"]).numel()), dtype=torch.uint8, device="cuda")
+    o, dout = torch.empty_like(a["v"]), torch.randn(b["v"].shape, device="cuda").bfloat16()
+    grads = [torch.empty_like(b[n]) for n in names]
+
+    def first():
+        R.ret_gated_delta_fwd(*[a[n] for n in names], o, workspace=ws, options=opt)
+
+    def second():
+        R.ret_gated_delta_bwd(*[b[n] for n in names], dout, *grads, workspace=ws)
+
+    first()
+    second()
+    torch.cuda.synchronize()
+    want_o, want_g = o.clone(), [t.clone() for t in grads]
+    graphs, s = [], torch.cuda.Stream()
+    for fn in (first, second):
+        g = torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+            fn()
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for i in range(3):
+        for t in [o] + grads:
+            t.fill_(3.0)
+        for g in graphs if i % 2 else graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want_o) and all(torch.equal(p, q) for p, q in zip(grads, want_g)), i
+        first()
+        second()
+        torch.cuda.synchronize()
+    other = [torch.empty_like(t) for t in grads]
+    s.wait_stream(torch.cuda.current_stream())
+    R.ret_gated_delta_bwd(*[b[n] for n in names], dout, *other, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(other, want_g))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("f32", 16, 32), ("bf16", 32, 80), ("bf16", 256, 128)])
+def test_more_segments_than_chunks_and_one_tensor_for_q_and_k(R, dtype, dk, dv):
+    """Every chunk a segment (the option asks for more than there are), some of them past a sequence's end; q is k."""
+    import torch
+    B, N, H = 2, 330, 2
+    print_case("gated_delta_single_chunk_segments", dtype, dk, dv)
+    x = inputs(9, B, N, H, H, dk, dv, dtype)
+    x["q"] = x["k"]
+    lengths = [70, 330]
+    gen = torch.Generator().manual_seed(4)
+    state, dstate = torch.randn(B, H, dk, dv, generator=gen), torch.randn(B, H, dk, dv, generator=gen)
+    dout = torch.randn(B, N, H, dv, generator=gen).to(x["q"].dtype)
+    a = [np64(x[n]) for n in ("q", "k", "v", "g", "beta")]
+    o, s = fwd.run(R, x, H, dv, state, lengths, "same", {"segments": 50})
+    ro, rs, before = forward(*a, dk ** -0.5, np64(state), np.array(lengths))
+    fwd.check("o", o, ro, dtype, term_sums(*a, dk ** -0.5, before))
+    fwd.check("state", s, rs, dtype)
+    got = bwd.run(R, x, dout, state, dstate, lengths, None, {"segments": 50})
+    bwd.check(got, gradients(*a, dk ** -0.5, np64(dout), np64(state), np64(dstate), np.array(lengths)), dtype)
