@@ -4,9 +4,9 @@ Tolerances. On BF16 input everything computed is split in two bf16 parts: each v
 itself, 2^-18/sqrt(3) on the average, and the product of the two low parts that is left out another 2^-18 at most. About
 six such errors stand between the inputs and an output (S, R, U, T or P, twice over), which are independent: below 1e-5
 in the 2-norm. On F32 input the sums of d_k + 64 products in fp32 leave less than 3e-6. Single values are held to 20 times the 2-norm's bound relative to the tensor's rms.
-A bf16 output of a whole sequence takes the state and P T rounded to bf16 once: each term of its sums is off by 2^-8 of
-itself at most, and the output's own rounding by 2^-8 of the value: 2^-8 (|o| + the sum of the terms' magnitudes). A
-single token's output is fp32 arithmetic and its rounding.
+A bf16 output adds its own rounding, 2^-8 of the value; a whole sequence's is also allowed 2^-16 of the sum of its terms'
+magnitudes (2^-17 for each of a term's two split operands), which can be far above the value. A single token's output is
+fp32 arithmetic and its rounding.
 """
 import numpy as np
 import pytest
@@ -36,7 +36,7 @@ def check(name, got, ref, dtype, terms=0.0):
     assert got.shape == ref.shape and np.isfinite(got).all(), name
     rms = np.sqrt((ref ** 2).mean()) if ref.size else 0.0
     d = np.abs(got - ref)
-    assert (d <= half * (np.abs(ref) + terms) + 20 * NORM[dtype] * rms).all(), (name, float(d.max()), float(rms))
+    assert (d <= half * np.abs(ref) + 2.0 ** -16 * terms + 20 * NORM[dtype] * rms).all(), (name, float(d.max()), float(rms))
     if half < 1e-6 and rms > 0:
         assert np.sqrt((d ** 2).mean()) <= NORM[dtype] * rms, (name, float(np.sqrt((d ** 2).mean()) / rms))
 
