@@ -271,8 +271,9 @@ void delta_prep_kernel(DeltaArgs a) {
 //   kStates (with T): the states entering the chunks and E, for the gradients.
 // A step: Y = K S and Q S, between their products the requests for everything the next chunk needs, into registers; R; O
 // from Q S and P T; E; the state; then the registers go to LDS. K has two buffers, so that nothing but the first barrier
-// of a chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave stages the
-// columns of V it owns. Requests are never conditional: where two branches join, their registers would be waited for.
+// of a chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave
+// stages the columns of V it owns. Requests are never conditional: where two branches join, their registers would be
+// waited for.
 // Fragments of the next reduction step are read ahead of a step's products.
 //
 // At d_k = 256 with 8 waves a step of the full pass takes 6.4 us, 14300 cycles: K S and Q S 5050, R and P T R 1800, T R and
