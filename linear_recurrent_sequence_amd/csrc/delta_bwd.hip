@@ -368,7 +368,7 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 // factors are one value per lane and a lane holds 4 consecutive values of its token's row. d_v is walked in blocks of 32.
 // Bound by HBM: 830 KB a chunk at d_k = 256, d_v = 512, 1.7 GB in 445 us, 3.8 TB/s (one workgroup of 16 waves per CU;
 // with 8 waves 545 us, their sums spilled); 190 us for 4 x 4096 tokens of 16 heads at d_k = d_v = 128 (at the copy rate
-// 141). E^T dO, E^T dU, X and Z go on in the input's type, as what the chains stored does: dq, dk, dbeta and dg of bf16 input
+// 141). X and Z go on in the input's type, like what the chains stored: dq, dk, dbeta and dg of bf16 input
 // carry two to four roundings of 2^-9, 0.003 of the 2-norm with the output's own 0.0017.
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, int NW, bool GROUP>
