@@ -427,8 +427,8 @@ ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float
  *     dx = rstd (a - mean(a) - xh mean(a xh)) + dsum,  a = w (.) dy,  xh = (x - mean) rstd
  *     dweight = sum over rows of dy xh,  dbias = sum over rows of dy     (device float[D]; NULL: not wanted)
  * dsum ([rows, D] in dx_dt, or NULL) is the gradient that reaches s past the norm; dx is then the gradient of x and of
- * residual alike. dx may take the place of dy, x or dsum (same start and dtype). rows = 0 writes zeros to dweight and
- * dbias. workspace: as ret_msr_epilogue_bwd's. Kernels: "ret_layer_norm_bwd", "ret_column_sums".
+ * residual alike. dx may take the place of dy, x or dsum (same start and dtype); no other overlap. rows = 0 writes zeros
+ * to dweight and dbias. workspace: as ret_msr_epilogue_bwd's. Kernels: "ret_layer_norm_bwd", "ret_column_sums".
  */
 size_t ret_layer_norm_bwd_workspace_bytes(int64_t rows, int D);
 ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weight, const float* mean,

@@ -39,31 +39,6 @@ ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, 
 
 float scale_of(float scale, int dk) { return scale == 0.f ? (float)(1.0 / sqrt((double)dk)) : scale; }
 
-struct Buf {
-    const char* name;
-    const void* p;
-    size_t bytes;
-};
-
-// Every written buffer apart from every other buffer of the call, except the pairs that may be the same one.
-template <int NW, int NR>
-ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR], const void* may_a, const void* may_b) {
-    for (int i = 0; i < NW; ++i) {
-        for (int j = i + 1; j < NW; ++j)
-            if (overlaps(w[i].p, w[i].bytes, w[j].p, w[j].bytes))
-                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, w[j].name);
-        for (int j = 0; j < NR; ++j)
-            if (overlaps(w[i].p, w[i].bytes, r[j].p, r[j].bytes) &&
-                !(w[i].p == r[j].p && w[i].bytes == r[j].bytes && w[i].p == may_a && r[j].p == may_b))
-                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, r[j].name);
-    }
-    for (int i = 0; i < NW; ++i)
-        if (!aligned16(w[i].p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", w[i].name);
-    for (int j = 0; j < NR; ++j)
-        if (!aligned16(r[j].p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", r[j].name);
-    return RET_OK;
-}
-
 // Segments per sequence.
 struct Plan {
     int nchunks, nseg, seg_chunks;
@@ -175,14 +150,14 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     const Opts op = resolve(opts);
     const Plan p = make_plan(s, kn, in_dt, false, op);
     const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
-    const Buf w[] = {{"o", o, T * H * dv * esize(out_dt)}, {"state_out", state_out, sb},
+    // state_out may be state_in (r[6]): every kernel that reads the latter has read it before the former is written,
+    // except within a segment chain's first launches, which precede it
+    const Buf w[] = {{"o", o, T * H * dv * esize(out_dt)}, {"state_out", state_out, sb, 1u << 6},
                      {"the workspace", workspace, workspace_bytes}};
     const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
                      {"g", g, T * H * esize(gate_dt)}, {"beta", beta, T * H * esize(gate_dt)},
                      {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}};
-    // state_out may be state_in: every kernel that reads the latter has read it before the former is written, except
-    // within a segment chain's first launches, which precede it
-    if ((st = check_apart(w, r, state_out, state_in)) != RET_OK) return st;
+    if ((st = check_apart(w, r)) != RET_OK) return st;
     if (!workspace || workspace_bytes < p.bytes)
         return fail(RET_ERR_WORKSPACE, "gated delta rule: workspace of %zu bytes, %zu needed",
                     workspace ? workspace_bytes : 0, p.bytes);
@@ -245,7 +220,7 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
     const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
                      {"g", g, T * H * eg}, {"beta", beta, T * H * eg}, {"dout", dout, T * H * dv * ei},
                      {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}, {"dstate_out", dstate_out, sb}};
-    if ((st = check_apart(w, r, nullptr, nullptr)) != RET_OK) return st;
+    if ((st = check_apart(w, r)) != RET_OK) return st;
     if (!workspace || workspace_bytes < p.bytes)
         return fail(RET_ERR_WORKSPACE, "gated delta gradients: workspace of %zu bytes, %zu needed",
                     workspace ? workspace_bytes : 0, p.bytes);
@@ -306,7 +281,7 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
     const Buf w[] = {{"o", o, (size_t)B * H * dv * esize(out_dt)}, {"state", state, (size_t)B * H * dk * dv * 4}};
     const Buf r[] = {{"q", q, (size_t)B * Hk * dk * ei}, {"k", k, (size_t)B * Hk * dk * ei},
                      {"v", v, (size_t)B * H * dv * ei}, {"g", g, ng}, {"beta", beta, ng}};
-    if ((st = check_apart(w, r, nullptr, nullptr)) != RET_OK) return st;
+    if ((st = check_apart(w, r)) != RET_OK) return st;
     DeltaStepArgs A = {q, k, v, g, beta, state, o, B, H, Hk, dv, out_dt == RET_BF16, gate_dt == RET_BF16,
                        scale_of(scale, dk)};
     hipStream_t str = (hipStream_t)stream;

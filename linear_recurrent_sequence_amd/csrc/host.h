@@ -63,4 +63,32 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// One buffer of a call. over (written ones): bit j set where it may take the place of the j-th read buffer, that is have
+// its start and size.
+struct Buf {
+    const char* name;
+    const void* p;
+    size_t bytes;
+    unsigned over = 0;
+};
+
+// Every written buffer apart from every other buffer of the call, but for the places it may take; all 16-byte aligned.
+template <int NW, int NR>
+ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR]) {
+    for (int i = 0; i < NW; ++i) {
+        for (int j = i + 1; j < NW; ++j)
+            if (overlaps(w[i].p, w[i].bytes, w[j].p, w[j].bytes))
+                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, w[j].name);
+        for (int j = 0; j < NR; ++j)
+            if (overlaps(w[i].p, w[i].bytes, r[j].p, r[j].bytes) &&
+                !((w[i].over >> j & 1) && w[i].p == r[j].p && w[i].bytes == r[j].bytes))
+                return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, r[j].name);
+    }
+    for (const Buf& b : w)
+        if (!aligned16(b.p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", b.name);
+    for (const Buf& b : r)
+        if (!aligned16(b.p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", b.name);
+    return RET_OK;
+}
+
 }  // namespace ret

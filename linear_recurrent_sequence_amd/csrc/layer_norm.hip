@@ -334,9 +334,6 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
     if (rows < 0 || D <= 0) return fail(RET_ERR_INVALID_ARG, "bad sizes (rows=%lld D=%d)", (long long)rows, D);
     if (!good_dt(x_dt) || !good_dt(dy_dt) || !good_dt(dx_dt))
         return fail(RET_ERR_INVALID_ARG, "bad dtype %d/%d/%d", (int)x_dt, (int)dy_dt, (int)dx_dt);
-    for (const void* p : {dy, x, (const void*)weight, (const void*)mean, (const void*)rstd, dsum, (const void*)dx,
-                          (const void*)dweight, (const void*)dbias, (const void*)workspace})
-        if (!aligned16(p)) return fail(RET_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
     LnKernels k;
     if (!ln_kernels_get(D, &k)) return fail(RET_ERR_UNSUPPORTED, "layer norm: D=%d exceeds %d", D, kLnMaxD);
     if (rows > (int64_t)1 << 40) return fail(RET_ERR_UNSUPPORTED, "layer norm: %lld rows", (long long)rows);
@@ -344,21 +341,14 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
     if (cols && (!workspace || workspace_bytes < ret_layer_norm_bwd_workspace_bytes(rows, D)))
         return fail(RET_ERR_WORKSPACE, "layer norm gradients: workspace of %zu bytes, %zu needed",
                     workspace ? workspace_bytes : 0, ret_layer_norm_bwd_workspace_bytes(rows, D));
-    const size_t n = (size_t)rows * D, ng = n * esize(dx_dt);
-    if ((overlaps(dx, ng, dy, n * esize(dy_dt)) && !(dx == dy && dx_dt == dy_dt)) ||
-        (overlaps(dx, ng, x, n * esize(x_dt)) && !(dx == x && dx_dt == x_dt)) ||
-        (overlaps(dx, ng, dsum, ng) && dx != dsum) || overlaps(dx, ng, mean, 4 * rows) ||
-        overlaps(dx, ng, rstd, 4 * rows) || overlaps(dx, ng, weight, 4 * (size_t)D))
-        return fail(RET_ERR_INVALID_ARG, "dx overlaps an input");
-    const size_t nd = 4 * (size_t)D, nw = cols ? workspace_bytes : 0;
-    const float* dcols[2] = {dweight, dbias};
-    for (const float* d : dcols)
-        if (overlaps(d, nd, dx, ng) || overlaps(d, nd, workspace, nw))
-            return fail(RET_ERR_INVALID_ARG, "dweight or dbias overlaps another buffer");
-    if (overlaps(dweight, nd, dbias, nd)) return fail(RET_ERR_INVALID_ARG, "dweight overlaps dbias");
-    if (overlaps(workspace, nw, dx, ng) || overlaps(workspace, nw, dy, n * esize(dy_dt)) ||
-        overlaps(workspace, nw, x, n * esize(x_dt)) || overlaps(workspace, nw, dsum, ng))
-        return fail(RET_ERR_INVALID_ARG, "the workspace overlaps another buffer");
+    // workgroups write their partial sums and rows of dx while others still read
+    const size_t n = (size_t)rows * D, nr = (size_t)rows * 4, nd = (size_t)D * 4;
+    const Buf w[] = {{"dx", dx, n * esize(dx_dt), 1u << 0 | 1u << 1 | 1u << 2}, {"dweight", dweight, nd},
+                     {"dbias", dbias, nd}, {"the workspace", workspace, cols ? workspace_bytes : 0}};
+    const Buf r[] = {{"dy", dy, n * esize(dy_dt)}, {"x", x, n * esize(x_dt)}, {"dsum", dsum, n * esize(dx_dt)},
+                     {"weight", weight, nd}, {"mean", mean, nr}, {"rstd", rstd, nr}};
+    const ret_status_t apart = check_apart(w, r);
+    if (apart != RET_OK) return apart;
     hipStream_t s = (hipStream_t)stream;
     const Opts op = resolve(opts);
     const int grid = ln_bwd_grid(rows, k);

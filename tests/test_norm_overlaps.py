@@ -1,0 +1,29 @@
+"""Buffers that the norms' entry points must not be given: an output or a workspace over something that other
+workgroups of the same launch still read (no GPU, nothing is launched)."""
+import pytest
+
+M = 1 << 20
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from linear_recurrent_sequence_amd import retention
+    return retention.load()
+
+
+def _lnb(lib, **kw):
+    a = dict(dy=1 * M, x=2 * M, w=3 * M, mean=4 * M, rstd=5 * M, ds=6 * M, dx=7 * M, dw=8 * M, db=9 * M, rows=4, D=64,
+             xt=1, dyt=1, dxt=1, ws=10 * M, wsb=M)
+    a.update(kw)
+    return lib.ret_layer_norm_bwd(*list(a.values()), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ws=3 * M), dict(ws=4 * M), dict(ws=5 * M),          # the workspace over weight, mean, rstd
+    dict(w=10 * M + 512), dict(mean=11 * M - 16), dict(rstd=10 * M),
+    dict(dw=3 * M), dict(db=3 * M + 16), dict(dw=4 * M), dict(db=5 * M), dict(dw=M), dict(db=2 * M), dict(dw=6 * M),
+    dict(dx=3 * M), dict(dx=4 * M), dict(dx=6 * M + 16),
+], ids=str)
+def test_layer_norm_gradients(lib, kw):
+    assert _lnb(lib, **kw) == -1
+    assert b"overlaps" in lib.ret_last_error()
