@@ -138,9 +138,6 @@ ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gat
     for (ret_dtype_t t : {dy_dt, o_dt, gate_dt, do_dt, dgate_dt})
         if (t != RET_F32 && t != RET_BF16) return fail(RET_ERR_INVALID_ARG, "bad dtype %d", (int)t);
     if (!(eps >= 0.f) || eps > 3e38f) return fail(RET_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);
-    for (const void* p : {dy, o, gate, (const void*)gn_weight, (const void*)gn_bias, (const void*)dout,
-                          (const void*)dgate, (const void*)dweight, (const void*)dbias, (const void*)workspace})
-        if (!aligned16(p)) return fail(RET_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
     const epi_bwd_kernel_t fn = epi_bwd_kernel_get(dv);
     if (!fn) return fail(RET_ERR_UNSUPPORTED, "epilogue gradients: d_v=%d not in {16,32,64,128,256,512}", dv);
     if ((int64_t)H * dv > 0x3fffffff || rows > (int64_t)1 << 40)
@@ -151,31 +148,14 @@ ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gat
         return fail(RET_ERR_WORKSPACE, "epilogue gradients: workspace of %zu bytes, %zu needed",
                     workspace ? workspace_bytes : 0, need);
     const int C = H * dv;
-    const size_t n = (size_t)rows * C, nd = 4 * (size_t)C, nw = cols ? workspace_bytes : 0;
-    struct Buf {
-        const void* p;
-        size_t bytes;
-        ret_dtype_t dt;
-    };
-    // each output may take the place of one tensor input (same start and dtype); other overlaps are refused
-    const Buf in[3] = {{dy, n * esize(dy_dt), dy_dt}, {o, n * esize(o_dt), o_dt}, {gate, n * esize(gate_dt), gate_dt}};
-    const Buf out[2] = {{dout, n * esize(do_dt), do_dt}, {dgate, n * esize(dgate_dt), dgate_dt}};
-    for (const Buf& b : out) {
-        for (const Buf& q : in)
-            if (overlaps(b.p, b.bytes, q.p, q.bytes) && !(b.p == q.p && b.dt == q.dt))
-                return fail(RET_ERR_INVALID_ARG, "do or dgate overlaps an input");
-        if (overlaps(b.p, b.bytes, gn_weight, nd) || overlaps(b.p, b.bytes, gn_bias, nd) ||
-            overlaps(b.p, b.bytes, dweight, nd) || overlaps(b.p, b.bytes, dbias, nd) ||
-            overlaps(b.p, b.bytes, workspace, nw))
-            return fail(RET_ERR_INVALID_ARG, "do or dgate overlaps another buffer");
-    }
-    if (overlaps(out[0].p, out[0].bytes, out[1].p, out[1].bytes))
-        return fail(RET_ERR_INVALID_ARG, "do overlaps dgate");
-    if (overlaps(dweight, nd, dbias, nd) || overlaps(dweight, nd, workspace, nw) || overlaps(dbias, nd, workspace, nw))
-        return fail(RET_ERR_INVALID_ARG, "dweight, dbias and the workspace must not overlap");
-    for (const Buf& q : in)
-        if (overlaps(workspace, nw, q.p, q.bytes) || overlaps(dweight, nd, q.p, q.bytes) || overlaps(dbias, nd, q.p, q.bytes))
-            return fail(RET_ERR_INVALID_ARG, "an input overlaps dweight, dbias or the workspace");
+    const size_t n = (size_t)rows * C, nd = 4 * (size_t)C;
+    // each output may take the place of one tensor input; workgroups write while others still read
+    const Buf w[] = {{"do", dout, n * esize(do_dt), 7u}, {"dgate", dgate, n * esize(dgate_dt), 7u}, {"dweight", dweight, nd},
+                     {"dbias", dbias, nd}, {"the workspace", workspace, cols ? workspace_bytes : 0}};
+    const Buf r[] = {{"dy", dy, n * esize(dy_dt)}, {"o", o, n * esize(o_dt)}, {"gate", gate, n * esize(gate_dt)},
+                     {"gn_weight", gn_weight, nd}, {"gn_bias", gn_bias, nd}};
+    const ret_status_t apart = check_apart(w, r);
+    if (apart != RET_OK) return apart;
     hipStream_t s = (hipStream_t)stream;
     const Opts op = resolve(opts);
     const int strips = epi_bwd_strips(rows, C);

@@ -27,3 +27,20 @@ def _lnb(lib, **kw):
 def test_layer_norm_gradients(lib, kw):
     assert _lnb(lib, **kw) == -1
     assert b"overlaps" in lib.ret_last_error()
+
+
+def _epb(lib, **kw):
+    a = dict(dy=1 * M, o=2 * M, gate=3 * M, w=4 * M, b=5 * M, do=6 * M, dg=7 * M, dw=8 * M, db=9 * M, rows=4, H=2, dv=64,
+             t1=1, t2=1, t3=1, t4=1, t5=1, eps=1e-5, ws=10 * M, wsb=M)
+    a.update(kw)
+    return lib.ret_msr_epilogue_bwd(*list(a.values()), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ws=4 * M), dict(ws=5 * M), dict(w=10 * M + 512), dict(b=11 * M - 16),  # the workspace over weight, bias
+    dict(dw=4 * M), dict(db=5 * M), dict(dw=5 * M + 16), dict(dw=M), dict(db=3 * M), dict(do=4 * M), dict(dg=5 * M),
+    dict(do=M + 16), dict(dg=2 * M, t5=0), dict(do=7 * M),
+], ids=str)
+def test_epilogue_gradients(lib, kw):
+    assert _epb(lib, **kw) == -1
+    assert b"overlaps" in lib.ret_last_error()
