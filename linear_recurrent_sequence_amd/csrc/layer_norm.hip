@@ -285,28 +285,17 @@ ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float
     if (rows < 0 || D <= 0) return fail(RET_ERR_INVALID_ARG, "bad sizes (rows=%lld D=%d)", (long long)rows, D);
     if (!good_dt(x_dt) || !good_dt(y_dt)) return fail(RET_ERR_INVALID_ARG, "bad dtype %d/%d", (int)x_dt, (int)y_dt);
     if (!(eps >= 0.f) || eps > 3e38f) return fail(RET_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);
-    for (const void* p : {x, residual, (const void*)weight, (const void*)bias, (const void*)y, (const void*)sum_out,
-                          (const void*)mean, (const void*)rstd})
-        if (!aligned16(p)) return fail(RET_ERR_INVALID_ARG, "buffers must be 16-byte aligned");
     LnKernels k;
     if (!ln_kernels_get(D, &k)) return fail(RET_ERR_UNSUPPORTED, "layer norm: D=%d exceeds %d", D, kLnMaxD);
     if (rows > (int64_t)1 << 40) return fail(RET_ERR_UNSUPPORTED, "layer norm: %lld rows", (long long)rows);
     if (rows == 0) return RET_OK;
-    // outputs may take an input's place (same start and dtype); any other overlap is refused
-    const size_t nx = (size_t)rows * D * esize(x_dt), ny = (size_t)rows * D * esize(y_dt);
-    for (const void* in : {x, residual}) {
-        if (overlaps(in, nx, y, ny) && !(in == y && x_dt == y_dt))
-            return fail(RET_ERR_INVALID_ARG, "y overlaps x or residual");
-        if (overlaps(in, nx, sum_out, nx) && in != sum_out)
-            return fail(RET_ERR_INVALID_ARG, "sum_out overlaps x or residual");
-    }
-    if (overlaps(y, ny, sum_out, nx)) return fail(RET_ERR_INVALID_ARG, "y overlaps sum_out");
-    const void* small[2] = {mean, rstd};
-    for (const void* m : small)
-        if (overlaps(m, 4 * rows, y, ny) || overlaps(m, 4 * rows, sum_out, nx) || overlaps(m, 4 * rows, x, nx) ||
-            overlaps(m, 4 * rows, residual, nx))
-            return fail(RET_ERR_INVALID_ARG, "mean or rstd overlaps another buffer");
-    if (overlaps(mean, 4 * rows, rstd, 4 * rows)) return fail(RET_ERR_INVALID_ARG, "mean overlaps rstd");
+    const size_t nx = (size_t)rows * D * esize(x_dt), nr = (size_t)rows * 4, nd = (size_t)D * 4;
+    // outputs may take an input's place; workgroups write while others still read
+    const Buf w[] = {{"y", y, (size_t)rows * D * esize(y_dt), 3u}, {"sum_out", sum_out, nx, 3u}, {"mean", mean, nr},
+                     {"rstd", rstd, nr}};
+    const Buf r[] = {{"x", x, nx}, {"residual", residual, nx}, {"weight", weight, nd}, {"bias", bias, nd}};
+    const ret_status_t apart = check_apart(w, r);
+    if (apart != RET_OK) return apart;
     const int64_t wgs = (rows + k.fwd_rows - 1) / k.fwd_rows;
     if (wgs > 0x7fffffff) return fail(RET_ERR_UNSUPPORTED, "layer norm: %lld rows", (long long)rows);
     LnArgs A = {x, residual, sum_out, y, weight, bias, mean, rstd, rows, D, x_dt == RET_BF16, y_dt == RET_BF16, eps};

@@ -44,3 +44,20 @@ def _epb(lib, **kw):
 def test_epilogue_gradients(lib, kw):
     assert _epb(lib, **kw) == -1
     assert b"overlaps" in lib.ret_last_error()
+
+
+def _ln(lib, **kw):
+    a = dict(x=1 * M, res=2 * M, w=3 * M, b=4 * M, y=5 * M, sum=6 * M, mean=7 * M, rstd=8 * M, rows=4, D=64, xt=1, yt=1,
+             eps=1e-5)
+    a.update(kw)
+    return lib.ret_layer_norm_fwd(*list(a.values()), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(y=3 * M), dict(y=4 * M + 16), dict(sum=3 * M), dict(sum=4 * M), dict(mean=3 * M), dict(rstd=4 * M),
+    dict(mean=M), dict(rstd=2 * M), dict(y=6 * M), dict(y=M + 16), dict(sum=2 * M, y=2 * M), dict(y=2 * M, yt=0),
+    dict(mean=8 * M),
+], ids=str)
+def test_layer_norm(lib, kw):
+    assert _ln(lib, **kw) == -1
+    assert b"overlaps" in lib.ret_last_error()
