@@ -150,13 +150,14 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     const Opts op = resolve(opts);
     const Plan p = make_plan(s, kn, in_dt, false, op);
     const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
+    const unsigned eg = esize(gate_dt);
     // state_out may be state_in (r[6]): every kernel that reads the latter has read it before the former is written,
     // except within a segment chain's first launches, which precede it
     const Buf w[] = {{"o", o, T * H * dv * esize(out_dt)}, {"state_out", state_out, sb, 1u << 6},
                      {"the workspace", workspace, workspace_bytes}};
     const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
-                     {"g", g, T * H * esize(gate_dt)}, {"beta", beta, T * H * esize(gate_dt)},
-                     {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}};
+                     {"g", g, T * H * eg, 0, eg}, {"beta", beta, T * H * eg, 0, eg},
+                     {"lengths", lengths, (size_t)B * 4, 0, 4}, {"state_in", state_in, sb}};
     if ((st = check_apart(w, r)) != RET_OK) return st;
     if (!workspace || workspace_bytes < p.bytes)
         return fail(RET_ERR_WORKSPACE, "gated delta rule: workspace of %zu bytes, %zu needed",
@@ -212,14 +213,14 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
     const Plan p = make_plan(s, kn, in_dt, true, op);
-    const size_t T = (size_t)B * N, ei = esize(in_dt), eo = esize(out_dt), eg = esize(gate_dt);
-    const size_t sb = (size_t)B * H * dk * dv * 4;
+    const size_t T = (size_t)B * N, ei = esize(in_dt), eo = esize(out_dt), sb = (size_t)B * H * dk * dv * 4;
+    const unsigned eg = esize(gate_dt);
     const Buf w[] = {{"dq", dq, T * Hk * dk * eo}, {"dk", dk_out, T * Hk * dk * eo}, {"dv", dv_out, T * H * dv * eo},
-                     {"dg", dg, T * H * eg}, {"dbeta", dbeta, T * H * eg}, {"dstate_in", dstate_in, sb},
+                     {"dg", dg, T * H * eg, 0, eg}, {"dbeta", dbeta, T * H * eg, 0, eg}, {"dstate_in", dstate_in, sb},
                      {"the workspace", workspace, workspace_bytes}};
     const Buf r[] = {{"q", q, T * Hk * dk * ei}, {"k", k, T * Hk * dk * ei}, {"v", v, T * H * dv * ei},
-                     {"g", g, T * H * eg}, {"beta", beta, T * H * eg}, {"dout", dout, T * H * dv * ei},
-                     {"lengths", lengths, (size_t)B * 4}, {"state_in", state_in, sb}, {"dstate_out", dstate_out, sb}};
+                     {"g", g, T * H * eg, 0, eg}, {"beta", beta, T * H * eg, 0, eg}, {"dout", dout, T * H * dv * ei},
+                     {"lengths", lengths, (size_t)B * 4, 0, 4}, {"state_in", state_in, sb}, {"dstate_out", dstate_out, sb}};
     if ((st = check_apart(w, r)) != RET_OK) return st;
     if (!workspace || workspace_bytes < p.bytes)
         return fail(RET_ERR_WORKSPACE, "gated delta gradients: workspace of %zu bytes, %zu needed",
@@ -278,9 +279,10 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
         return fail(RET_ERR_UNSUPPORTED, "gated delta step: d_k=%d not in {16,32,64,128,256} or d_v=%d not a multiple of 16",
                     dk, dv);
     const size_t ei = esize(in_dt), ng = (size_t)B * H * esize(gate_dt);
+    const unsigned eg = esize(gate_dt);
     const Buf w[] = {{"o", o, (size_t)B * H * dv * esize(out_dt)}, {"state", state, (size_t)B * H * dk * dv * 4}};
     const Buf r[] = {{"q", q, (size_t)B * Hk * dk * ei}, {"k", k, (size_t)B * Hk * dk * ei},
-                     {"v", v, (size_t)B * H * dv * ei}, {"g", g, ng}, {"beta", beta, ng}};
+                     {"v", v, (size_t)B * H * dv * ei}, {"g", g, ng, 0, eg}, {"beta", beta, ng, 0, eg}};
     if ((st = check_apart(w, r)) != RET_OK) return st;
     DeltaStepArgs A = {q, k, v, g, beta, state, o, B, H, Hk, dv, out_dt == RET_BF16, gate_dt == RET_BF16,
                        scale_of(scale, dk)};

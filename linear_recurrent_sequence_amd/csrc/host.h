@@ -64,15 +64,15 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 // One buffer of a call. over (written ones): bit j set where it may take the place of the j-th read buffer, that is have
-// its start and size.
+// its start and size. align: 16 bytes, or an element's where kernels access it one element at a time.
 struct Buf {
     const char* name;
     const void* p;
     size_t bytes;
-    unsigned over = 0;
+    unsigned over = 0, align = 16;
 };
 
-// Every written buffer apart from every other buffer of the call, but for the places it may take; all 16-byte aligned.
+// Every written buffer apart from every other buffer of the call, but for the places it may take; all aligned.
 template <int NW, int NR>
 ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR]) {
     for (int i = 0; i < NW; ++i) {
@@ -85,9 +85,9 @@ ret_status_t check_apart(const Buf (&w)[NW], const Buf (&r)[NR]) {
                 return fail(RET_ERR_INVALID_ARG, "%s overlaps %s", w[i].name, r[j].name);
     }
     for (const Buf& b : w)
-        if (!aligned16(b.p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", b.name);
+        if ((uintptr_t)b.p % b.align) return fail(RET_ERR_INVALID_ARG, "%s must be %u-byte aligned", b.name, b.align);
     for (const Buf& b : r)
-        if (!aligned16(b.p)) return fail(RET_ERR_INVALID_ARG, "%s must be 16-byte aligned", b.name);
+        if ((uintptr_t)b.p % b.align) return fail(RET_ERR_INVALID_ARG, "%s must be %u-byte aligned", b.name, b.align);
     return RET_OK;
 }
 
