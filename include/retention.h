@@ -414,8 +414,9 @@ ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gat
  * over the last axis of x [rows, D] (biased variance, statistics in fp32). residual, sum_out: as x, or NULL; sum_out
  * receives s, the stream the next block adds to. weight, bias: device float[D], NULL means 1 and 0. mean, rstd: device
  * float[rows], or NULL; the gradients want them. x_dt, y_dt: F32 or BF16 each. y and sum_out may take the place of x or
- * residual (same start and dtype); no other overlap. Pointers 16-byte aligned; rows = 0 does nothing; 1 <= D <= 16384
- * (rows with D a multiple of 8 move as 16-byte vectors). Kernel: "ret_layer_norm".
+ * residual (same start and dtype); no other overlap. Pointers 16-byte aligned (mean and rstd 4: a slice of the rows'
+ * statistics will do); rows = 0 does nothing; 1 <= D <= 16384 (rows with D a multiple of 8 move as 16-byte vectors).
+ * Kernel: "ret_layer_norm".
  */
 ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float* weight, const float* bias, void* y,
                                 void* sum_out, float* mean, float* rstd, int64_t rows, int D, ret_dtype_t x_dt,

@@ -291,8 +291,8 @@ ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float
     if (rows == 0) return RET_OK;
     const size_t nx = (size_t)rows * D * esize(x_dt), nr = (size_t)rows * 4, nd = (size_t)D * 4;
     // outputs may take an input's place; workgroups write while others still read
-    const Buf w[] = {{"y", y, (size_t)rows * D * esize(y_dt), 3u}, {"sum_out", sum_out, nx, 3u}, {"mean", mean, nr},
-                     {"rstd", rstd, nr}};
+    const Buf w[] = {{"y", y, (size_t)rows * D * esize(y_dt), 3u}, {"sum_out", sum_out, nx, 3u}, {"mean", mean, nr, 0, 4},
+                     {"rstd", rstd, nr, 0, 4}};
     const Buf r[] = {{"x", x, nx}, {"residual", residual, nx}, {"weight", weight, nd}, {"bias", bias, nd}};
     const ret_status_t apart = check_apart(w, r);
     if (apart != RET_OK) return apart;
@@ -335,7 +335,7 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
     const Buf w[] = {{"dx", dx, n * esize(dx_dt), 1u << 0 | 1u << 1 | 1u << 2}, {"dweight", dweight, nd},
                      {"dbias", dbias, nd}, {"the workspace", workspace, cols ? workspace_bytes : 0}};
     const Buf r[] = {{"dy", dy, n * esize(dy_dt)}, {"x", x, n * esize(x_dt)}, {"dsum", dsum, n * esize(dx_dt)},
-                     {"weight", weight, nd}, {"mean", mean, nr}, {"rstd", rstd, nr}};
+                     {"weight", weight, nd}, {"mean", mean, nr, 0, 4}, {"rstd", rstd, nr, 0, 4}};
     const ret_status_t apart = check_apart(w, r);
     if (apart != RET_OK) return apart;
     hipStream_t s = (hipStream_t)stream;
