@@ -463,7 +463,8 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
  * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_full".
  *
  * ret_gated_delta_step computes one token of every sequence, the state updated in place; d_k in {16, 32, 64, 128, 256},
- * d_v a multiple of 16, fp32 arithmetic for either input dtype. Kernel: "ret_delta_step".
+ * d_v a multiple of 16, B*H <= 131072 and otherwise the limits above; fp32 arithmetic for either input dtype. Kernel:
+ * "ret_delta_step".
  */
 size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
                                        const ret_options_t* opts);

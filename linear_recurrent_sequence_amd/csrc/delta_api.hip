@@ -17,8 +17,11 @@ struct Shape {
     int B, N, H, Hk, dk, dv;
 };
 
+// B H at most: a sequence's kernels have up to B H workgroups along the grid's y, a step's along x (that many are tested).
+constexpr int kSeqMaxBH = 65535, kStepMaxBH = 1 << 17;
+
 // Sizes, dtypes and head counts of any of the calls; N = 1 for a step.
-ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, ret_dtype_t gate_dt) {
+ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, ret_dtype_t gate_dt, int max_bh) {
     if (s.B <= 0 || s.N <= 0 || s.H <= 0 || s.Hk <= 0 || s.dk <= 0 || s.dv <= 0)
         return fail(RET_ERR_INVALID_ARG, "sizes must be positive (B=%d N=%d H=%d Hk=%d dk=%d dv=%d)", s.B, s.N, s.H,
                     s.Hk, s.dk, s.dv);
@@ -27,7 +30,8 @@ ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, 
     if (in_dt == RET_F32 && (out_dt != RET_F32 || gate_dt != RET_F32))
         return fail(RET_ERR_INVALID_ARG, "F32 input requires F32 output and gates");
     if (s.H % s.Hk) return fail(RET_ERR_INVALID_ARG, "H=%d is not a multiple of Hk=%d", s.H, s.Hk);
-    if ((long long)s.B * s.H > 65535) return fail(RET_ERR_UNSUPPORTED, "B*H=%lld exceeds 65535", (long long)s.B * s.H);
+    if ((long long)s.B * s.H > max_bh)
+        return fail(RET_ERR_UNSUPPORTED, "B*H=%lld exceeds %d", (long long)s.B * s.H, max_bh);
     // a chunk of one head is addressed with 32-bit byte offsets
     const long long w = (long long)s.H * (s.dk > s.dv ? s.dk : s.dv);
     if (w * kDeltaC * 4 >= 1LL << 30)
@@ -129,7 +133,8 @@ size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int 
                                        const ret_options_t* opts) {
     const Shape s = {B, N, H, Hk, dk, dv};
     DeltaKernels k;
-    if (check_shape(s, in_dt, RET_F32, RET_F32) != RET_OK || !delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
+    if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
+    if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
     return make_plan(s, k, in_dt, false, resolve(opts)).bytes;
 }
 
@@ -139,7 +144,7 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
                                  float* state_out, void* workspace, size_t workspace_bytes, void* stream,
                                  const ret_options_t* opts) {
     const Shape s = {B, N, H, Hk, dk, dv};
-    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt, kSeqMaxBH);
     if (st != RET_OK) return st;
     if (!q || !k || !v || !g || !beta || !o) return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/o pointer");
     if (!isfinite(scale)) return fail(RET_ERR_INVALID_ARG, "scale is not finite");
@@ -191,7 +196,8 @@ size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, 
                                            const ret_options_t* opts) {
     const Shape s = {B, N, H, Hk, dk, dv};
     DeltaKernels k;
-    if (check_shape(s, in_dt, RET_F32, RET_F32) != RET_OK || !delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
+    if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
+    if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
     return make_plan(s, k, in_dt, true, resolve(opts)).bytes;
 }
 
@@ -202,7 +208,7 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
                                  const float* dstate_out, float* dstate_in, void* workspace, size_t workspace_bytes,
                                  void* stream, const ret_options_t* opts) {
     const Shape s = {B, N, H, Hk, dk, dv};
-    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt, kSeqMaxBH);
     if (st != RET_OK) return st;
     if (!q || !k || !v || !g || !beta || !dout || !dq || !dk_out || !dv_out || !dg || !dbeta)
         return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/dout or gradient pointer");
@@ -269,7 +275,7 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
                                   ret_dtype_t out_dt, ret_dtype_t gate_dt, float scale, void* stream,
                                   const ret_options_t* opts) {
     const Shape s = {B, 1, H, Hk, dk, dv};
-    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt);
+    ret_status_t st = check_shape(s, in_dt, out_dt, gate_dt, kStepMaxBH);
     if (st != RET_OK) return st;
     if (!q || !k || !v || !g || !beta || !o || !state)
         return fail(RET_ERR_INVALID_ARG, "null q/k/v/g/beta/o/state pointer");
