@@ -26,8 +26,9 @@ COMMON = [
     "-Wall", "-Wno-unused-function", "-Wno-unused-result",
 ]
 # per-source additions: the wide-head kernel and the gated delta rule's keep their MFMA accumulators in architectural
-# registers (the latter's states are operands and accumulators in turn; and with accumulators in AGPRs this compiler has
-# merged two of delta_prep's LDS stores into one with a wrong offset)
+# registers: the latter's states are operands and accumulators in turn. It also keeps AGPRs out of small LDS stores, of
+# which this compiler merges some wrongly when others have a VGPR as their value (an offset divided by the element's size
+# twice: delta_prep once stored a tile's element 204 at 51); tests/test_codegen.py looks for them in the built library
 VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA = {"chunk_wide.hip": VGPR_FORM, "delta_fwd.hip": VGPR_FORM, "delta_bwd.hip": VGPR_FORM}
 NOISE = "'-packed-fp32-ops' is not a recognized feature"
