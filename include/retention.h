@@ -399,7 +399,7 @@ ret_status_t ret_chunkwise_fwd_noalloc(const void* q, const void* k, const void*
  * overlap (RET_ERR_INVALID_ARG). workspace: ret_msr_epilogue_bwd_workspace_bytes device bytes when dweight or dbias is
  * wanted (RET_ERR_WORKSPACE if short), of any content; calls sharing one must not overlap in time. The sums are added
  * in a fixed order: the same call gives the same bits. Pointers 16-byte aligned; supported: d_v in {16, 32, 64, 128,
- * 256, 512}. Kernels: "ret_msr_epilogue_bwd", "ret_column_sums". opts: the timer, or NULL.
+ * 256, 512}, H * d_v < 2^27. Kernels: "ret_msr_epilogue_bwd", "ret_column_sums". opts: the timer, or NULL.
  */
 size_t ret_msr_epilogue_bwd_workspace_bytes(int64_t rows, int H, int dv);
 ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gate, const float* gn_weight,

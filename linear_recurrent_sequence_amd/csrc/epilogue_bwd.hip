@@ -100,6 +100,9 @@ int epi_bwd_strips(int64_t rows, int C) {
 
 size_t esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
 
+// H d_v below this: the column sums take 32 work-items a channel, and a launch fewer than 2^32.
+constexpr int64_t kEpiBwdMaxC = 1 << 27;
+
 }  // namespace
 
 epi_bwd_kernel_t epi_bwd_kernel_get(int dv) {
@@ -121,7 +124,7 @@ using namespace ret;
 extern "C" {
 
 size_t ret_msr_epilogue_bwd_workspace_bytes(int64_t rows, int H, int dv) {
-    if (rows < 0 || H <= 0 || !epi_bwd_kernel_get(dv) || (int64_t)H * dv > 0x3fffffff) return 0;
+    if (rows < 0 || H <= 0 || !epi_bwd_kernel_get(dv) || (int64_t)H * dv >= kEpiBwdMaxC) return 0;
     const size_t n = (size_t)epi_bwd_strips(rows, H * dv) * 2 * H * dv * sizeof(float);
     return n ? n : 16;
 }
@@ -140,7 +143,7 @@ ret_status_t ret_msr_epilogue_bwd(const void* dy, const void* o, const void* gat
     if (!(eps >= 0.f) || eps > 3e38f) return fail(RET_ERR_INVALID_ARG, "eps=%g must be finite and >= 0", eps);
     const epi_bwd_kernel_t fn = epi_bwd_kernel_get(dv);
     if (!fn) return fail(RET_ERR_UNSUPPORTED, "epilogue gradients: d_v=%d not in {16,32,64,128,256,512}", dv);
-    if ((int64_t)H * dv > 0x3fffffff || rows > (int64_t)1 << 40)
+    if ((int64_t)H * dv >= kEpiBwdMaxC || rows > (int64_t)1 << 40)
         return fail(RET_ERR_UNSUPPORTED, "epilogue gradients: rows=%lld H=%d too large", (long long)rows, H);
     const bool cols = dweight || dbias;
     const size_t need = ret_msr_epilogue_bwd_workspace_bytes(rows, H, dv);
