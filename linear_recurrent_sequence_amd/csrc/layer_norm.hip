@@ -52,7 +52,9 @@ __global__ __launch_bounds__(THREADS) void layer_norm_kernel(LnArgs a) {
     __shared__ float red[2 * (THREADS / 64)];
     RowSum<L, THREADS> sum{red, 0};
     const int lane = threadIdx.x % L;
-    const long long row = (long long)blockIdx.x * (THREADS / L) + threadIdx.x / L;
+    const long long wg = (long long)blockIdx.y * gridDim.x + blockIdx.x;
+    if (wg * (THREADS / L) >= a.rows) return;  // the rest of the grid's last row
+    const long long row = wg * (THREADS / L) + threadIdx.x / L;
     const bool live = row < a.rows;
     const long long base = (live ? row : a.rows - 1) * a.D;  // idle groups read the last row
     float x[K][W], s = 0.f;
@@ -267,6 +269,8 @@ int ln_bwd_grid(int64_t rows, const LnKernels& k) {
     return (int)(g < 256 ? g : 256);
 }
 
+constexpr int64_t kLnGridX = 1 << 20;  // workgroups of the forward along x at most (of up to 1024 threads)
+
 bool good_dt(ret_dtype_t t) { return t == RET_F32 || t == RET_BF16; }
 size_t esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
 
@@ -297,12 +301,14 @@ ret_status_t ret_layer_norm_fwd(const void* x, const void* residual, const float
     const ret_status_t apart = check_apart(w, r);
     if (apart != RET_OK) return apart;
     const int64_t wgs = (rows + k.fwd_rows - 1) / k.fwd_rows;
-    if (wgs > 0x7fffffff) return fail(RET_ERR_UNSUPPORTED, "layer norm: %lld rows", (long long)rows);
+    // a launch of 2^32 work-items along one axis runs short without an error: the grid goes on along y
+    const int64_t gx = wgs < kLnGridX ? wgs : kLnGridX, gy = (wgs + gx - 1) / gx;
+    if (gy > 65535) return fail(RET_ERR_UNSUPPORTED, "layer norm: %lld rows", (long long)rows);
     LnArgs A = {x, residual, sum_out, y, weight, bias, mean, rstd, rows, D, x_dt == RET_BF16, y_dt == RET_BF16, eps};
     hipStream_t s = (hipStream_t)stream;
     const Opts op = resolve(opts);
     LaunchTimer tm("ret_layer_norm", s, op);
-    hipLaunchKernelGGL(k.fwd, dim3((unsigned)wgs), dim3(k.fwd_threads), 0, s, A);
+    hipLaunchKernelGGL(k.fwd, dim3((unsigned)gx, (unsigned)gy), dim3(k.fwd_threads), 0, s, A);
     tm.done();
     return launch_status("ret_layer_norm");
 }
