@@ -456,10 +456,11 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
  * token can reach the outputs of its own chunk's earlier tokens.
  * workspace: ret_gated_delta_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing
  * one must not overlap in time. Supported: d_k in {32, 64, 128, 256} (BF16) or {16, 32, 64, 128} (F32), d_v a multiple
- * of 16, B*H <= 65535, N >= 1, H * max(d_k, d_v) < 2^22, d_k * d_v < 2^28. Written buffers must not overlap other
- * buffers. Pointers 16-byte aligned; those of g, beta and lengths (and of dg and dbeta) like one of their elements, so
- * that one token's gates can be a slice of a sequence's. opts: segments (> 0: segments per sequence that run in
- * parallel, joined by their transitions) and timer.
+ * of 16, B*H <= 65535, N >= 1, H * max(d_k, d_v) < 2^22, d_k * d_v < 2^28, and no launch of 2^32 work-items (512 per
+ * sequence, value head, segment and 128 columns of d_v). Written buffers must not overlap other buffers. Pointers
+ * 16-byte aligned; those of g, beta and lengths (and of dg and dbeta) like one of their elements, so that one token's
+ * gates can be a slice of a sequence's. opts: segments (> 0: segments per sequence that run in parallel, joined by
+ * their transitions) and timer.
  * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_full".
  *
  * ret_gated_delta_step computes one token of every sequence, the state updated in place; d_k in {16, 32, 64, 128, 256},

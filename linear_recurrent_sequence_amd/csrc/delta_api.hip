@@ -51,7 +51,7 @@ struct Plan {
 Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bwd, const Opts& op) {
     const int nmats = bwd ? 3 : 2;
     Plan p;
-    p.nchunks = (s.N + kDeltaC - 1) / kDeltaC;
+    p.nchunks = s.N / kDeltaC + (s.N % kDeltaC != 0);
     const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
     int n = 1;
     if (op.segments > 0) n = op.segments;
@@ -119,7 +119,27 @@ ret_status_t launch(const char* name, delta_kernel_t fn, dim3 grid, hipStream_t 
     return launch_status(name);
 }
 
-unsigned blocks(int n, int per) { return (unsigned)((n + per - 1) / per); }
+unsigned long long blocks(long long n, int per) { return (unsigned long long)((n + per - 1) / per); }
+
+// Workgroups of the chains: a multiple of 8 segments (see DeltaBlock) times the column blocks of d_v, and in a local pass
+// of the transition's d_k.
+struct Grids {
+    unsigned long long units, nv, nk, scan_y;
+};
+// RET_ERR_UNSUPPORTED where one of the call's launches would not run whole.
+ret_status_t make_grids(const Shape& s, const Plan& p, const DeltaKernels& k, Grids* g) {
+    const unsigned long long heads = (unsigned long long)s.B * s.H;
+    *g = {blocks(heads * p.nseg, 8) * 8, blocks(s.dv, k.cols), blocks(s.dk, k.cols), blocks(s.dv, kScanCols)};
+    const dim3 chunks = prep_grid(p, s);  // delta_prep's; delta_grad's is no larger
+    const int threads = k.grad_threads > kThreads ? k.grad_threads : kThreads;
+    const bool split = p.nseg > 1;
+    if (!grid_fits(chunks.x, chunks.y, chunks.z, threads) ||
+        !grid_fits(g->units * (g->nv + (split ? g->nk : 0)), 1, 1, k.threads) ||
+        (split && !grid_fits(heads, g->scan_y, 1, k.scan_threads)))
+        return fail(RET_ERR_UNSUPPORTED, "gated delta rule: B=%d N=%d H=%d d_v=%d in %d segments exceed a launch", s.B, s.N,
+                    s.H, s.dv, p.nseg);
+    return RET_OK;
+}
 
 }  // namespace
 
@@ -135,7 +155,9 @@ size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int 
     DeltaKernels k;
     if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
     if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
-    return make_plan(s, k, in_dt, false, resolve(opts)).bytes;
+    const Plan p = make_plan(s, k, in_dt, false, resolve(opts));
+    Grids G;
+    return make_grids(s, p, k, &G) == RET_OK ? p.bytes : 0;
 }
 
 ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,
@@ -154,6 +176,8 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
     const Plan p = make_plan(s, kn, in_dt, false, op);
+    Grids G;
+    if ((st = make_grids(s, p, kn, &G)) != RET_OK) return st;
     const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
     const unsigned eg = esize(gate_dt);
     // state_out may be state_in (r[6]): every kernel that reads the latter has read it before the former is written,
@@ -179,17 +203,14 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
     A.state_in = state_in;
     A.state_out = state_out;
     hipStream_t str = (hipStream_t)stream;
+    const dim3 scan(B * H, (unsigned)G.scan_y), chain((unsigned)(G.units * G.nv));
     if ((st = launch("ret_delta_prep", kn.prep, prep_grid(p, s), str, op, A)) != RET_OK) return st;
-    const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local", kn.local, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
-            RET_OK)
-            return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
-            RET_OK)
-            return st;
+        const dim3 local((unsigned)(G.units * (G.nv + G.nk)));
+        if ((st = launch("ret_delta_local", kn.local, local, str, op, A, kn.threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, scan, str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
-    return launch("ret_delta_full", out_dt == RET_BF16 ? kn.full : kn.full_f32, dim3(units * nc), str, op, A, kn.threads);
+    return launch("ret_delta_full", out_dt == RET_BF16 ? kn.full : kn.full_f32, chain, str, op, A, kn.threads);
 }
 
 size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, int dv, ret_dtype_t in_dt,
@@ -198,7 +219,9 @@ size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, 
     DeltaKernels k;
     if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
     if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
-    return make_plan(s, k, in_dt, true, resolve(opts)).bytes;
+    const Plan p = make_plan(s, k, in_dt, true, resolve(opts));
+    Grids G;
+    return make_grids(s, p, k, &G) == RET_OK ? p.bytes : 0;
 }
 
 ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -219,6 +242,8 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
     const Plan p = make_plan(s, kn, in_dt, true, op);
+    Grids G;
+    if ((st = make_grids(s, p, kn, &G)) != RET_OK) return st;
     const size_t T = (size_t)B * N, ei = esize(in_dt), eo = esize(out_dt), sb = (size_t)B * H * dk * dv * 4;
     const unsigned eg = esize(gate_dt);
     const Buf w[] = {{"dq", dq, T * Hk * dk * eo}, {"dk", dk_out, T * Hk * dk * eo}, {"dv", dv_out, T * H * dv * eo},
@@ -249,24 +274,19 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
     A.dg = dg;
     A.dbeta = dbeta;
     hipStream_t str = (hipStream_t)stream;
+    const dim3 scan(B * H, (unsigned)G.scan_y), chain((unsigned)(G.units * G.nv));
     if ((st = launch("ret_delta_prep", kn.bprep, prep_grid(p, s), str, op, A)) != RET_OK) return st;
-    const unsigned nc = blocks(dv, kn.cols), units = blocks(B * H * p.nseg, 8) * 8;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local", kn.blocal, dim3(units * (nc + blocks(dk, kn.cols))), str, op, A, kn.threads)) !=
-            RET_OK)
-            return st;
-        if ((st = launch("ret_delta_scan", kn.scan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
-            RET_OK)
-            return st;
+        const dim3 local((unsigned)(G.units * (G.nv + G.nk)));
+        if ((st = launch("ret_delta_local", kn.blocal, local, str, op, A, kn.threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.scan, scan, str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_states", kn.states, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
+    if ((st = launch("ret_delta_states", kn.states, chain, str, op, A, kn.threads)) != RET_OK) return st;
     if (p.nseg > 1) {
-        if ((st = launch("ret_delta_local_bwd", kn.rlocal, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
-        if ((st = launch("ret_delta_scan", kn.rscan, dim3(B * H, blocks(dv, kScanCols)), str, op, A, kn.scan_threads)) !=
-            RET_OK)
-            return st;
+        if ((st = launch("ret_delta_local_bwd", kn.rlocal, chain, str, op, A, kn.threads)) != RET_OK) return st;
+        if ((st = launch("ret_delta_scan", kn.rscan, scan, str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_full_bwd", kn.rfull, dim3(units * nc), str, op, A, kn.threads)) != RET_OK) return st;
+    if ((st = launch("ret_delta_full_bwd", kn.rfull, chain, str, op, A, kn.threads)) != RET_OK) return st;
     return launch("ret_delta_grad", H > Hk ? kn.grad_group : kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
 }
 
@@ -284,6 +304,10 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
     if (!fn || dv % 16)
         return fail(RET_ERR_UNSUPPORTED, "gated delta step: d_k=%d not in {16,32,64,128,256} or d_v=%d not a multiple of 16",
                     dk, dv);
+    const unsigned long long col_blocks = blocks(dv, 64);
+    const int threads = dk >= 32 ? 2 * dk : 64;
+    if (!grid_fits(B * H, col_blocks, 1, threads))
+        return fail(RET_ERR_UNSUPPORTED, "gated delta step: B=%d H=%d d_v=%d exceed a launch", B, H, dv);
     const size_t ei = esize(in_dt), ng = (size_t)B * H * esize(gate_dt);
     const unsigned eg = esize(gate_dt);
     const Buf w[] = {{"o", o, (size_t)B * H * dv * esize(out_dt)}, {"state", state, (size_t)B * H * dk * dv * 4}};
@@ -294,7 +318,7 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
                        scale_of(scale, dk)};
     hipStream_t str = (hipStream_t)stream;
     LaunchTimer tm("ret_delta_step", str, resolve(opts));
-    hipLaunchKernelGGL(fn, dim3(B * H, blocks(dv, 64)), dim3(dk >= 32 ? 2 * dk : 64), 0, str, A);
+    hipLaunchKernelGGL(fn, dim3(B * H, (unsigned)col_blocks), dim3(threads), 0, str, A);
     tm.done();
     return launch_status("ret_delta_step");
 }

@@ -54,6 +54,12 @@ struct LaunchTimer {
 
 ret_status_t launch_status(const char* what);
 
+// Whether a launch runs whole: one of 2^32 work-items or more along x runs short without an error, and y and z have their
+// own limit.
+inline bool grid_fits(unsigned long long x, unsigned long long y, unsigned long long z, int threads) {
+    return x * (unsigned)threads < 1ull << 32 && y <= 65535 && z <= 65535;
+}
+
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 // Whether the byte ranges [a, a + na) and [b, b + nb) share a byte (null ranges share none).

@@ -40,3 +40,36 @@ def test_layer_norm_of_more_rows_than_one_launch_axis_takes():
     tol = 64 * 2.0 ** -24 * (1 + last.abs().max() / last.std(1, unbiased=False).min()) * ref.abs().max()
     assert float((y[-9:].double().cpu() - ref).abs().max()) <= float(tol)
     assert float((mean[-9:].double().cpu() - last.mean(1)).abs().max()) <= 64 * 2.0 ** -24 * float(last.abs().max())
+
+
+def _delta(lib, bwd=False, B=1, N=1, H=1, dk=32, dv=16, dt=1, segments=0, ws=None):
+    """The call with buffers far apart and no workspace: -3 where all checks before that pass."""
+    from linear_recurrent_sequence_amd import retention
+    opts = retention._options({"segments": segments})
+    shape = (B, N, H, H, dk, dv, dt, dt, 0, 0.0)
+    if bwd:
+        return lib.ret_gated_delta_bwd(*[T * i for i in range(1, 12)], *shape, None, None, None, None, None, 0, None, opts)
+    return lib.ret_gated_delta_fwd(*[T * i for i in range(1, 7)], *shape, None, None, None, None, 0, None, opts)
+
+
+@pytest.mark.parametrize("bwd", [False, True])
+def test_delta_calls_refuse_what_a_launch_does_not_hold(lib, bwd):
+    query = lib.ret_gated_delta_bwd_workspace_bytes if bwd else lib.ret_gated_delta_workspace_bytes
+    # 60000 heads of 139 blocks of 128 columns, 512 threads each: 0.994 x 2^32 work-items; one block more
+    assert _delta(lib, bwd, B=300, H=200, dv=139 * 128) == -3
+    assert _delta(lib, bwd, B=300, H=200, dv=140 * 128) == -2 and b"launch" in lib.ret_last_error()
+    assert query(300, 1, 200, 200, 32, 140 * 128, 1, None) == 0 < query(300, 1, 200, 200, 32, 139 * 128, 1, None)
+    # the segment scan has d_v / 32 workgroups along y
+    assert _delta(lib, bwd, N=512, dv=1 << 21) == -3
+    assert _delta(lib, bwd, N=512, dv=1 << 21, segments=2) == -2
+    assert _delta(lib, bwd, N=512, dv=(1 << 21) - 32, segments=2) == -3
+    # chunks of tokens
+    for N in (2 ** 31 - 1, 2 ** 31 - 64, 2 ** 30):
+        assert _delta(lib, bwd, N=N) == -2 and query(1, N, 1, 1, 32, 16, 1, None) == 0
+
+
+def test_delta_step_refuses_what_a_launch_does_not_hold(lib):
+    step = lambda dv, state=7 * T: lib.ret_gated_delta_step(*[T * i for i in range(1, 7)], state, 1, 1, 1, 16, dv,  # noqa: E731
+                                                            1, 1, 0, 0.0, None, None)
+    assert step((1 << 22) - 16, None) == -1  # a missing state comes first
+    assert step((1 << 22) - 16) == -2
