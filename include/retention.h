@@ -346,7 +346,7 @@ ret_status_t ret_recurrent_step_positions_ex(const void* q, const void* k, const
  * sum before token 0 ([B, H, d_k] fp32 device, or NULL = zeros); z_out: the key sum after the last token (or
  * NULL; may equal z_in). pos0 >= 0. The workspace is required: ret_chunkwise_normalized_workspace_bytes (0 for
  * an unsupported shape) bytes, zero-filled before first use like the chunkwise workspace. Supported: as
- * ret_chunkwise_fwd. RET_ERR_INVALID_ARG also for norm outside 0..7 and misaligned z buffers,
+ * ret_chunkwise_fwd, B*N*H*d_v < 2^35. RET_ERR_INVALID_ARG also for norm outside 0..7 and misaligned z buffers,
  * RET_ERR_WORKSPACE for a missing or short workspace. Kernels: the chunkwise kernels, then "ret_norm_zseg",
  * "ret_segment_scan", "ret_norm_rows" and "ret_norm_scale" (the output scaled in place).
  */

@@ -1269,6 +1269,9 @@ ret_status_t ret_chunkwise_normalized_fwd(const void* q, const void* k, const vo
     if (!norm_layout(B, N, H, dk, dv, chunk, in_dt, op, &L))
         return fail(RET_ERR_UNSUPPORTED, "normalized chunkwise form: unsupported d_k=%d d_v=%d chunk=%d", dk, dv,
                     chunk);
+    const long long groups = (long long)B * N * H * dv / 8;  // of outputs, a work-item each
+    if (!grid_fits((groups + 255) / 256, 1, 1, 256))
+        return fail(RET_ERR_UNSUPPORTED, "normalized chunkwise form: B*N*H*d_v=%lld exceeds a launch", groups * 8);
     if (!workspace || workspace_bytes < L.total)
         return fail(RET_ERR_WORKSPACE, "the normalized chunkwise form needs a workspace of %zu bytes (got %zu)",
                     L.total, workspace_bytes);
@@ -1318,7 +1321,6 @@ ret_status_t ret_chunkwise_normalized_fwd(const void* q, const void* k, const vo
         tm.done();
         if ((st = launch_status("ret_norm_rows")) != RET_OK) return st;
     }
-    const long long groups = (long long)B * N * H * dv / 8;
     LaunchTimer tm("ret_norm_scale", s, op);
     hipLaunchKernelGGL(nk.scale, dim3((unsigned)((groups + 255) / 256)), dim3(256), 0, s, A);
     tm.done();

@@ -73,3 +73,14 @@ def test_delta_step_refuses_what_a_launch_does_not_hold(lib):
                                                             1, 1, 0, 0.0, None, None)
     assert step((1 << 22) - 16, None) == -1  # a missing state comes first
     assert step((1 << 22) - 16) == -2
+
+
+def test_normalized_form_refuses_what_a_launch_does_not_hold(lib):
+    """2^35 outputs, 68 GB in bf16: 8 a work-item."""
+    import ctypes
+    H = 64
+    gamma = (ctypes.c_float * H)(*[0.9] * H)
+    call = lambda N: lib.ret_chunkwise_normalized_fwd(T, 2 * T, 3 * T, 4 * T, 1, N, H, 64, 512, 1, 1, gamma, None, 0,  # noqa: E731
+                                                      64, 7, None, None, None, None, None, 0, None, None)
+    assert call((1 << 20) - 64) == -3  # nothing but the workspace is missing
+    assert call(1 << 20) == -2 and b"launch" in lib.ret_last_error()
