@@ -756,8 +756,8 @@ def _delta_qkv(q, k, v, g, beta, step=False):
 def _delta_scale(scale):
     if scale is None:
         return 0.0
-    if float(scale) == 0.0:
-        raise ValueError("scale must not be zero")
+    if ctypes.c_float(scale).value == 0.0:  # as the library gets it: there 0 stands for 1 / sqrt(d_k)
+        raise ValueError("scale must not be zero in float32")
     return float(scale)
 
 
