@@ -28,6 +28,7 @@
 #pragma once
 
 #include "chunk_bf16.h"
+#include "delta_step.h"
 
 namespace ret {
 
@@ -84,9 +85,6 @@ __device__ __forceinline__ int delta_len(const DeltaArgs& a, int b) {
     if (!a.lengths) return a.N;
     const int n = a.lengths[b];
     return n < 0 ? 0 : n > a.N ? a.N : n;
-}
-__device__ __forceinline__ float gate_at(const void* p, long long i, int bf16) {
-    return bf16 ? bf16_to_f32(((const uint16_t*)p)[i]) : ((const float*)p)[i];
 }
 
 // Between LDS accesses of one wave whose lanes read what other lanes wrote: the accesses before are complete, and the

@@ -1,6 +1,5 @@
 // Entry points of the gated delta rule: argument checks, segment plan, workspace layout, launches.
 #include "delta.h"
-#include "delta_step.h"
 #include "host.h"
 
 #include <math.h>

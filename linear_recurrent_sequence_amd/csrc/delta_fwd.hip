@@ -438,10 +438,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
         if constexpr (FULL) {
             typename D::Fm fpt[F::COUNT];
 #pragma unroll
-            for (int f = 0; f < F::COUNT; ++f) {
-                
-                fpt[f] = D::mat_frag(sp, f, lane);
-            }
+            for (int f = 0; f < F::COUNT; ++f) fpt[f] = D::mat_frag(sp, f, lane);
 #pragma unroll
             for (int m = 0; m < 4; ++m) o[m] *= a.scale * sf[p][16 * m + n16];
             keep_order();

@@ -32,12 +32,12 @@ __global__ __launch_bounds__(DK >= 32 ? DK * 2 : 64) void delta_step_kernel(Delt
     float q[RPT], k[RPT], v[4];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        q[i] = gate_value(a.q, qrow + i, sizeof(st) == 2);
-        k[i] = gate_value(a.k, qrow + i, sizeof(st) == 2);
+        q[i] = gate_at(a.q, qrow + i, sizeof(st) == 2);
+        k[i] = gate_at(a.k, qrow + i, sizeof(st) == 2);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = gate_value(a.v, (long long)bh * a.dv + cc + j, sizeof(st) == 2);
-    const float alpha = expf(gate_value(a.g, bh, a.gate_bf16)), beta = gate_value(a.beta, bh, a.gate_bf16);
+    for (int j = 0; j < 4; ++j) v[j] = gate_at(a.v, (long long)bh * a.dv + cc + j, sizeof(st) == 2);
+    const float alpha = expf(gate_at(a.g, bh, a.gate_bf16)), beta = gate_at(a.beta, bh, a.gate_bf16);
     f32x4_t x = {0.f, 0.f, 0.f, 0.f}, z = {0.f, 0.f, 0.f, 0.f};
     float qk = 0.f;
 #pragma unroll
