@@ -450,10 +450,11 @@ ret_status_t ret_layer_norm_bwd(const void* dy, const void* x, const float* weig
  * ret_gated_delta_fwd computes a whole sequence in chunks of 64 tokens. state_in (NULL: zeros), state_out (NULL: not
  * wanted; may equal state_in): the state before token 0 and after the last token, so that a sequence can be resumed or
  * handed to ret_gated_delta_step. lengths (device int32[B], or NULL): sequence b has lengths[b] tokens (0 .. N, other
- * values are taken as the nearest of these); inputs past them are not used, outputs past them are zero, and state_out is
- * the state after lengths[b] tokens. Products accumulate in fp32; on BF16 input everything the kernels compute and
- * multiply again (the state among it) is split in two bf16 parts, so results carry about 2^-17. A NaN or infinity of a
- * token can reach the outputs of its own chunk's earlier tokens.
+ * values are taken as the nearest of these); inputs past them are not used, outputs past them are zero, and state_out
+ * is the state after lengths[b] tokens. Products accumulate in fp32; on BF16 input everything the kernels compute and
+ * multiply again (the state among it) is split in two bf16 parts, which leaves an error of about 6e-6 in the 2-norm of
+ * the outputs (before their own rounding) and of the state, 5e-7 on F32 input. A NaN or infinity of a token can reach
+ * the outputs of its own chunk's earlier tokens.
  * workspace: ret_gated_delta_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing
  * one must not overlap in time. Supported: d_k in {32, 64, 128, 256} (BF16) or {16, 32, 64, 128} (F32), d_v a multiple
  * of 16, B*H <= 65535, N >= 1, H * max(d_k, d_v) < 2^22, d_k * d_v < 2^28, and no launch of 2^32 work-items (512 per
@@ -480,13 +481,16 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
                                   const ret_options_t* opts);
 
 /*
- * Gradients of ret_gated_delta_fwd: with dout = dL/do [B, N, H, d_v] in in_dt and, optionally, dstate_out = dL/dstate_out
- * [B, H, d_k, d_v] fp32, writes dq, dk [B, N, Hk, d_k] (summed over the value heads that share a key head), dv
- * [B, N, H, d_v] in out_dt, dg, dbeta [B, N, H] in gate_dt and, unless NULL, dstate_in. The other arguments are the
- * forward call's. Gradients of the padding past lengths[b] are zero. dq, dk, dbeta and dg come from states and writes
- * stored as BF16 on BF16 input, whatever out_dt and gate_dt (a relative 2^-8); dv and dstate_in carry 2^-17 like the
- * forward. workspace: ret_gated_delta_bwd_workspace_bytes (it holds the state entering and the state gradient leaving
- * every chunk of 64 tokens). Same limits as the forward. Sums have one order: the same call gives the same bits.
+ * Gradients of ret_gated_delta_fwd: with dout = dL/do [B, N, H, d_v] in in_dt and, optionally, dstate_out =
+ * dL/dstate_out [B, H, d_k, d_v] fp32, writes dq, dk [B, N, Hk, d_k] (summed over the value heads that share a key
+ * head), dv [B, N, H, d_v] in out_dt, dg, dbeta [B, N, H] in gate_dt and, unless NULL, dstate_in. The other arguments
+ * are the forward call's. Gradients of the padding past lengths[b] are zero. On BF16 input dq, dk, dbeta and dg come
+ * from states and writes rounded to BF16, whatever out_dt and gate_dt: F32 outputs and gates do not make them more
+ * precise. Their error is about 0.003 of the tensor's 2-norm with a BF16 output's own rounding (tested up to 0.0051);
+ * dg's, a difference of sums, up to 0.008 (tested up to 0.011). Single values that are small beside the rest can be off
+ * by more than themselves. dv and dstate_in are as precise as the forward's results. workspace:
+ * ret_gated_delta_bwd_workspace_bytes (it holds the state entering and the state gradient leaving every chunk of 64
+ * tokens). Same limits as the forward. Sums have one order: the same call gives the same bits.
  * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_states", "ret_delta_local_bwd",
  * "ret_delta_full_bwd", "ret_delta_grad".
  */

@@ -20,11 +20,14 @@
 // heads 708 us, one 577 then).
 //
 // Precision. Products run on bf16 MFMA for bf16 inputs. What the kernels compute themselves (S, R, E, T, P) is split in
-// two bf16 parts, x = hi + lo + e with |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two products where the
-// other side is an input, which is exact): the carried state keeps fp32-like accuracy over any number of chunks, where a
-// single rounding of E and S would leave 2^-9 in it. What leaves a chain for the gradients' per-chunk kernel (S_0, dS_C,
-// E, dU) is stored in the input's type: at d_k = 256, d_v = 512 these are 512 KB of a chunk's 830 in bf16. F32 inputs run
-// on the fp32 MFMA.
+// two bf16 parts, x = hi + lo + e with |lo| <= 2^-8 |x| and |e| <= 2^-17 |x|, and multiplied as hi.hi + hi.lo + lo.hi (two
+// products where the other side is an input, which is exact). A term of two split operands is off by 2^-15 of itself at
+// worst: 2^-17 for each split and 2^-16 for the lo.lo left out; sums of them, whose errors are independent, come to 4e-6 to
+// 6e-6 of outputs and states in the 2-norm, over any number of chunks (fp32 inputs: 2e-7 to 5e-7), where a single rounding of
+// E and S would leave up to 2^-8 of each term. What leaves a chain for the gradients' per-chunk kernel (S_0, dS_C, E, dU) is
+// rounded once to the input's type, for the traffic's sake: at d_k = 256, d_v = 512 these are 512 KB of a chunk's 830 in
+// bf16, and that kernel is bound by them. It costs dq, dk, dg and dbeta an error of 0.002 to 0.008 in the 2-norm, whatever the
+// type they are asked for in (dv and the gradient of the state do not pass that way). F32 inputs run on the fp32 MFMA.
 #pragma once
 
 #include "chunk_bf16.h"

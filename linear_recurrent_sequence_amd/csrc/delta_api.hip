@@ -42,7 +42,13 @@ ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt, 
 
 float scale_of(float scale, int dk) { return scale == 0.f ? (float)(1.0 / sqrt((double)dk)) : scale; }
 
-// Segments per sequence.
+// Segments per sequence, by default
+//   - one workgroup of the full pass per CU, two where rows are short, rounded down: more go in a second round (129 heads of
+//     1024 tokens, 128 x 128: one segment 98 us, two 165; gradients 291 and 412);
+//   - at least 4 chunks a segment. Segments of 2, 3, 4 and 6 chunks take, for 4 heads of 2048 tokens, 169, 137, 120 and 123 us
+//     at d_k = 256 and 68, 62, 62 and 69 at 128; for 4 x 1024 tokens of 8 heads at 128, 70, -, 60 and 69. Where few heads leave
+//     the card idle 2 would be better (1024 tokens of 8 heads of 64: 31 us, 35 at 4 chunks; fp32, 4 heads of 128: 94 and 131),
+//     and so would one segment be than two for 8 to 11 chunks of bf16 (512 tokens of 8 heads of 64: 29 us and 32).
 struct Plan {
     int nchunks, nseg, seg_chunks;
     size_t mats, fac, segE, segM, segF, s0t, ds1t, et, dut, bytes;  // byte offsets of the parts, and their end
@@ -54,8 +60,8 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     const long long units = (long long)s.B * s.H * ((s.dv + k.cols - 1) / k.cols);
     int n = 1;
     if (op.segments > 0) n = op.segments;
-    else n = (int)((s.dk * esize(in_dt) >= 256 ? 256 : 512) / units);  // one or two workgroups per CU
-    if (op.segments <= 0 && n > p.nchunks / 4) n = p.nchunks / 4;  // at least 4 chunks a segment
+    else n = (int)((s.dk * esize(in_dt) >= 256 ? 256 : 512) / units);
+    if (op.segments <= 0 && n > p.nchunks / 4) n = p.nchunks / 4;
     if (n > p.nchunks) n = p.nchunks;
     if (n < 1) n = 1;
     p.seg_chunks = (p.nchunks + n - 1) / n;
@@ -78,7 +84,9 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     }
     return p;
 }
-// delta_prep: the value heads of a key head share a workgroup unless the card takes one for each at once.
+// delta_prep: the value heads of a key head share a workgroup unless the card takes one for each at once. 8 value heads of
+// 2 key heads at d_k = 128, shared and one each: 512 of them 32 and 18 us, 2048 38 and 34, 4096 51 and 60; at d_k = 256 32
+// and 18, 41 and 55, 74 and 100.
 dim3 prep_grid(const Plan& p, const Shape& s) {
     return dim3(p.nchunks, s.B * s.Hk, (long long)p.nchunks * s.B * s.H <= 512 ? s.H / s.Hk : 1);
 }

@@ -26,7 +26,7 @@ typedef double f64;
 // state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise dS_C of
 // each chunk and dU, as blocks, and dV; the first segment leaves dstate_in. Built as the forward's chain: requests a chunk
 // ahead between the products of K dS, K in two buffers, Q's product before the second barrier. 10 us a step at d_k = 256,
-// 7 at 128, by the same measure as the forward's; 8192 tokens, 16 heads, d_k = 256, d_v = 512: 233 us local, 315 us full.
+// 7 at 128, by the same measure as the forward's; 8192 tokens, 16 heads, d_k = 256, d_v = 512: 242 us local, 336 us full.
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, int NW, bool LOCAL>
 __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
@@ -366,10 +366,12 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 // dq and dk added up in registers: no atomics, one order). Wave w owns tokens 16 (w % 4) .. + 15 and 64 columns of d_k
 // (all of a shorter one). Every product has its accumulator rows along d_k (or j) and columns along tokens: per-token
 // factors are one value per lane and a lane holds 4 consecutive values of its token's row. d_v is walked in blocks of 32.
-// Bound by HBM: 830 KB a chunk at d_k = 256, d_v = 512, 1.7 GB in 445 us, 3.8 TB/s (one workgroup of 16 waves per CU;
-// with 8 waves 545 us, their sums spilled); 190 us for 4 x 4096 tokens of 16 heads at d_k = d_v = 128 (at the copy rate
-// 141). X and Z go on in the input's type, like what the chains stored: dq, dk, dbeta and dg of bf16 input
-// carry two to four roundings of 2^-9, 0.003 of the 2-norm with the output's own 0.0017.
+// Bound by HBM: 830 KB a chunk at d_k = 256, d_v = 512, 1.7 GB in 470 us, 3.6 TB/s (one workgroup of 16 waves per CU;
+// with 8 waves, whose sums spilled, 100 us more); 199 us for 4 x 4096 tokens of 16 heads at d_k = d_v = 128 (at the copy
+// rate 141). The sums of grouped heads spill 66 registers at d_k = 256 (8 key heads for the 16: 549 us) and 9 at 128 in fp32
+// (8192 tokens of 8 heads: 142 us, and 148 ungrouped). X and Z go on in the input's type, like what the chains stored, so
+// that a term of dq, dk, dbeta and dg of bf16 input carries two to four roundings of up to 2^-8 each: 0.003 in the 2-norm
+// with the output's own 0.0017. dg is a difference of such sums, 0.003 as a rule and up to 0.008 where they nearly cancel.
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, int NW, bool GROUP>
 __global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <= 128 ? 2 : 1))

@@ -22,8 +22,8 @@ typedef double f64;
 // then twice the block rule [[X, 0], [A, Y]]^-1 = [[X', 0], [-Y' A X', Y']] with fp32 MFMA.
 //
 // A workgroup's steps wait for each other (gates, inverse, products: eight barriers), so what counts is how many share a
-// CU: the fp32 matrices lie where the rows were. 8192 chunks at d_k = 128: 109 us, 32 KB read and 26 KB written each,
-// 4.4 TB/s; the copy rate would give 93.
+// CU: the fp32 matrices lie where the rows were. 8192 chunks at d_k = 128: 114 us, 33 KB read and 26 KB written each,
+// 4.2 TB/s; the copy rate would give 95.
 // ---------------------------------------------------------------------------------------------------
 constexpr int kTriLD = 68;  // row pitch of the fp32 matrices in LDS
 
@@ -280,7 +280,7 @@ void delta_prep_kernel(DeltaArgs a) {
 // the store 1300, the state 2700, barriers and staging 3500. MFMA issue is 6000, 1 MB of fragments out of LDS 8000. Rows
 // read 8 bytes at a time cost 2300 more. Eight waves rather than four halve the staging per column; more workgroups per CU
 // (128 registers) cost more in spills than they hid (local pass at d_k = 128 200 -> 222 us). Full pass, one workgroup per
-// CU: 77 us for 16 chunks at d_k = 128, 277 us for 43 at 256; local pass 159 us for 32 at 256; states 214 for 32 at 256,
+// CU: 86 us for 16 chunks at d_k = 128, 284 us for 43 at 256; local pass 167 us for 32 at 256; states 221 for 32 at 256,
 // of which 670 MB of states and E at the copy rate are 131.
 // ---------------------------------------------------------------------------------------------------
 enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };

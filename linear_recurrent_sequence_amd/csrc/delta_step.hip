@@ -1,8 +1,8 @@
 // One token of the gated delta rule with the state updated in place. With S read once,
 //     x = S^T k,  z = S^T q,  u = beta (v - alpha x),  S <- alpha S + k u^T,  o = scale (alpha z + (q.k) u),
 // so both sums over the state come from the same read and one exchange between the waves; the state is read and written
-// once, which is all the traffic there is. Measured: 128 sequences of 16 heads of 128 x 256, 98 us (5.5 TB/s); one sequence
-// of 8 heads of 64 x 64, 3.4 us.
+// once, which is all the traffic there is. Measured: 128 sequences of 16 heads of 128 x 256, 99 us (5.4 TB/s); one sequence
+// of 8 heads of 64 x 64, 3.5 us.
 #include "delta_step.h"
 
 #include "kernels.h"

@@ -9,7 +9,7 @@
 // walks rows; the 16 waves of a workgroup own the same channels and different rows. Each lane keeps the weight and bias
 // sums of its channels in registers; they are added up through LDS at the end and left as one partial row per
 // workgroup, which the column-sum kernel of the layer norm adds in a fixed order. Measured in bf16 with a gate: 8192 rows
-// of 16 heads of 512, 122 us and 5 for the column sums (5.3 TB/s), 16384 rows of 8 heads of 64, 19 and 4 (84 MB, part of
+// of 16 heads of 512, 128 us and 5 for the column sums (5.0 TB/s), 16384 rows of 8 heads of 64, 20 and 4 (84 MB, part of
 // it from the last-level cache).
 #include "host.h"
 #include "rows.h"

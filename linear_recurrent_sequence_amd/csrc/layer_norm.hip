@@ -3,13 +3,15 @@
 //   forward:  s = x + residual (rounded to x's dtype), xh = (s - mean s) rstd, y = w xh + b
 //   gradient: a = w dy, dx = rstd (a - mean a - xh mean(a xh)) + dsum, dw = sum_rows dy xh, db = sum_rows dy
 //
-// A row is held in the registers of L lanes (8 or 16 values each, so that D up to 16384 needs no second read): both
-// kernels read each tensor once and are bound by HBM. Rows whose length is a multiple of 8 move as 16-byte vectors,
-// others value by value. Statistics are fp32: mean first, then the squared differences from it, both from registers.
+// A row is held in the registers of L lanes (4 to 16 values each, so that D up to 16384 needs no second read): both
+// kernels read each tensor once. Rows whose length is a multiple of 8 move as 16-byte vectors and are bound by HBM, others
+// value by value. Statistics are fp32: mean first, then the squared differences from it, both from registers.
 // L <= 64 reduces within a wave (no barrier); wider rows add their waves' sums through LDS. Measured: forward, 128 rows of
-// 4096 in bf16 with the residual 4.7 us (launch and one round trip), 16384 rows of 1001 in fp32 32.5 us (4.0 TB/s; rows
-// that are not 16-byte aligned move 4 bytes a lane); gradients, 8192 rows of 4096 in bf16 57 us and 5 for the column sums
-// (4.4 TB/s over both).
+// 4096 in bf16 with the residual 5.1 us (launch and one round trip), 8192 of them 57 (4.7 TB/s), 16384 rows of 1001 in fp32
+// 35 us (3.7 TB/s), in bf16 30 (2.2); gradients, 8192 rows of 4096 in bf16 58 us and 5 for the column sums (4.3 TB/s
+// over both). Gradients of rows of more than 256 values whose number is no multiple of 8 are bound by their 16 values a lane,
+// of which the compiler spills 46 to 76 registers, and by 2- and 4-byte accesses: 16384 rows of 1001 93 us in fp32 (2.1
+// TB/s) and 137 in bf16 (0.7), 8192 of 4097 in bf16 260; 4 values a lane do not spill (65536 rows of 250 in fp32, 49 us).
 //
 // The weight's gradients are sums over rows. A workgroup walks the rows with a stride of the grid, keeps the sums of its
 // own columns in registers, adds up its row groups through LDS at the end and leaves one partial row of sums; a second
