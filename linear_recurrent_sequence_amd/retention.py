@@ -258,6 +258,14 @@ def _same_device(*ts):
 
 
 _IO = (torch.float32, torch.bfloat16)
+_INT = 2 ** 31 - 1
+
+
+def _int_sizes(*ts):
+    """Sizes reach the library as C ints, to which ctypes cuts them without an error."""
+    for t in ts:
+        if t.numel() > _INT and max(t.shape) > _INT:
+            raise ValueError("sizes must be below 2^31, got %s" % (tuple(t.shape),))
 
 
 def _qkv(q, k, v, step=False):
@@ -270,6 +278,15 @@ def _qkv(q, k, v, step=False):
     _shape(v, "v", tuple(q.shape[:-1]) + (v.shape[-1],), (q.dtype,))
     if q.dtype not in _IO or k.dtype != q.dtype:
         raise ValueError("q, k, v must share one dtype (float32 or bfloat16)")
+    _int_sizes(q, v)
+
+
+def _heads(o):
+    """(H, d_v) of a tensor [..., H, d_v]; the axes before them are rows, which have 64 bits."""
+    H, dv = o.shape[-2], o.shape[-1]
+    if H > _INT or dv > _INT:
+        raise ValueError("sizes must be below 2^31, got %s" % (tuple(o.shape),))
+    return H, dv
 
 
 def _gamma(gamma, H):
@@ -408,7 +425,7 @@ def ret_msr_epilogue(o, y, gate=None, gn_weight=None, gn_bias=None, eps=1e-5, st
     lib = load()
     if o.dim() < 2 or tuple(y.shape) != tuple(o.shape) or (gate is not None and tuple(gate.shape) != tuple(o.shape)):
         raise ValueError("o, y (and gate) must share one shape [..., H, d_v]")
-    H, dv = o.shape[-2], o.shape[-1]
+    H, dv = _heads(o)
     rows = o.numel() // (H * dv) if H * dv else 0
     for name, t in (("gn_weight", gn_weight), ("gn_bias", gn_bias)):
         if t is not None and (t.dtype != torch.float32 or t.numel() != H * dv):
@@ -620,7 +637,7 @@ def _rows_workspace(nbytes, device):
 
 def msr_epilogue_bwd_workspace(o):
     """A workspace of ret_msr_epilogue_bwd_workspace_bytes for o [..., H, d_v]."""
-    H, dv = o.shape[-2], o.shape[-1]
+    H, dv = _heads(o)
     rows = o.numel() // (H * dv) if H * dv else 0
     nbytes = load().ret_msr_epilogue_bwd_workspace_bytes(rows, H, dv)
     if nbytes == 0:
@@ -643,7 +660,7 @@ def ret_msr_epilogue_bwd(dy, o, do, gate=None, dgate=None, gn_weight=None, gn_bi
         raise ValueError("o must be float32 or bfloat16, got %s" % o.dtype)
     if dgate is not None and gate is None:
         raise ValueError("dgate without a gate")
-    H, dv = o.shape[-2], o.shape[-1]
+    H, dv = _heads(o)
     rows = o.numel() // (H * dv) if H * dv else 0
     for name, t in (("gn_weight", gn_weight), ("gn_bias", gn_bias), ("dweight", dweight), ("dbias", dbias)):
         _shape(t, name, (H * dv,), (torch.float32,))
@@ -666,6 +683,8 @@ def _norm_rows(x):
     if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.dtype not in _IO:
         raise ValueError("x must be a float32 or bfloat16 tensor [..., D]")
     D = x.shape[-1]
+    if D > _INT:
+        raise ValueError("sizes must be below 2^31, got %s" % (tuple(x.shape),))
     return (x.numel() // D if D else 0), D
 
 
@@ -751,6 +770,7 @@ def _delta_qkv(q, k, v, g, beta, step=False):
         _shape(t, name, v.shape[:-1], _IO)
     if g.dtype != beta.dtype:
         raise ValueError("g and beta must share one dtype")
+    _int_sizes(q, v)
 
 
 def _delta_scale(scale):
@@ -769,6 +789,7 @@ def _delta_lengths(lengths, B):
 
 def gated_delta_workspace(q, v, options=None):
     """A workspace of ret_gated_delta_workspace_bytes for these shapes."""
+    _int_sizes(q, v)
     B, N, Hk, dk = q.shape
     H, dv = v.shape[2], v.shape[3]
     nbytes = load().ret_gated_delta_workspace_bytes(B, N, H, Hk, dk, dv, _dt(q), _options(options))
@@ -807,6 +828,7 @@ def ret_gated_delta_fwd(q, k, v, g, beta, o, scale=None, lengths=None, state_in=
 
 def gated_delta_bwd_workspace(q, v, options=None):
     """A workspace of ret_gated_delta_bwd_workspace_bytes for these shapes."""
+    _int_sizes(q, v)
     B, N, Hk, dk = q.shape
     H, dv = v.shape[2], v.shape[3]
     nbytes = load().ret_gated_delta_bwd_workspace_bytes(B, N, H, Hk, dk, dv, _dt(q), _options(options))
