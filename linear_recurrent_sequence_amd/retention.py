@@ -615,6 +615,8 @@ def _launch(t, stream, workspace, make):
             with guard:
                 workspace = make()
     else:
+        if stream.device != t.device:
+            raise ValueError("the stream is on %s, the tensors are on %s" % (stream.device, t.device))
         sp = stream.cuda_stream
         if workspace is None and make is not None:
             with torch.cuda.stream(stream):
