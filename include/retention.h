@@ -484,13 +484,15 @@ ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, c
  * Gradients of ret_gated_delta_fwd: with dout = dL/do [B, N, H, d_v] in in_dt and, optionally, dstate_out =
  * dL/dstate_out [B, H, d_k, d_v] fp32, writes dq, dk [B, N, Hk, d_k] (summed over the value heads that share a key
  * head), dv [B, N, H, d_v] in out_dt, dg, dbeta [B, N, H] in gate_dt and, unless NULL, dstate_in. The other arguments
- * are the forward call's. Gradients of the padding past lengths[b] are zero. On BF16 input dq, dk, dbeta and dg come
- * from states and writes rounded to BF16, whatever out_dt and gate_dt: F32 outputs and gates do not make them more
- * precise. Their error is about 0.003 of the tensor's 2-norm with a BF16 output's own rounding (tested up to 0.0051);
- * dg's, a difference of sums, up to 0.008 (tested up to 0.011). Single values that are small beside the rest can be off
- * by more than themselves. dv and dstate_in are as precise as the forward's results. workspace:
+ * are the forward call's. Gradients of the padding past lengths[b] are zero. On BF16 input with BF16 outputs and gates,
+ * dq, dk, dbeta and dg come from states and writes rounded once to BF16: their error is about 0.003 of the tensor's
+ * 2-norm with their own rounding (tested up to 0.0051); dg's, a difference of sums, up to 0.008 (tested up to 0.011),
+ * and single values that are small beside the rest can be off by more than themselves. With F32 outputs or gates these
+ * are kept in two BF16 parts, at a sixth to a third more time: 1e-5 (tested up to 2e-5), dg 2e-5 (8e-5), before a BF16
+ * output's own rounding. dv and dstate_in are as precise as the forward's results. workspace:
  * ret_gated_delta_bwd_workspace_bytes (it holds the state entering and the state gradient leaving every chunk of 64
- * tokens). Same limits as the forward. Sums have one order: the same call gives the same bits.
+ * tokens, on BF16 input room for both parts). Same limits as the forward. Sums have one order: the same call gives the
+ * same bits.
  * Kernels: "ret_delta_prep", "ret_delta_local", "ret_delta_scan", "ret_delta_states", "ret_delta_local_bwd",
  * "ret_delta_full_bwd", "ret_delta_grad".
  */

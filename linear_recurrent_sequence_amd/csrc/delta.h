@@ -24,10 +24,12 @@
 // products where the other side is an input, which is exact). A term of two split operands is off by 2^-15 of itself at
 // worst: 2^-17 for each split and 2^-16 for the lo.lo left out; sums of them, whose errors are independent, come to 4e-6 to
 // 6e-6 of outputs and states in the 2-norm, over any number of chunks (fp32 inputs: 2e-7 to 5e-7), where a single rounding of
-// E and S would leave up to 2^-8 of each term. What leaves a chain for the gradients' per-chunk kernel (S_0, dS_C, E, dU) is
-// rounded once to the input's type, for the traffic's sake: at d_k = 256, d_v = 512 these are 512 KB of a chunk's 830 in
-// bf16, and that kernel is bound by them. It costs dq, dk, dg and dbeta an error of 0.002 to 0.008 in the 2-norm, whatever the
-// type they are asked for in (dv and the gradient of the state do not pass that way). F32 inputs run on the fp32 MFMA.
+// E and S would leave up to 2^-8 of each term. What leaves a chain for the gradients' per-chunk kernel (S_0, dS_C, E, dU) goes
+// by the types of the gradients that come of it. All in bf16: rounded once, for the traffic's sake (at d_k = 256, d_v = 512
+// S_0 and dS_C are 512 KB of a chunk's 830, and that kernel is bound by them); it costs dq, dk and dbeta an error of 0.002 to
+// 0.003 in the 2-norm where their own rounding is 0.0017, dg up to 0.008. Outputs or gates in fp32: in two bf16 parts, errors
+// below 1e-5, dg's 2e-5; 8192 tokens of 16 heads, 256 x 512, 1920 us for 1450, 4 x 4096 tokens, 128 x 128, 878 for 650. dv
+// and the gradient of the state do not pass that way. F32 inputs run on the fp32 MFMA.
 #pragma once
 
 #include "chunk_bf16.h"
@@ -60,6 +62,7 @@ struct DeltaArgs {
     // in the input type, as blocks of 16 columns (of d_v) x 16 TPS rows: [B*H][nchunks][dv/16][rows/(16 TPS)][1 KB]
     void *s0t, *ds1t;            // states entering and their gradients leaving the chunks (rows: d_k)
     void *et, *dut;              // E and dU (rows: the chunk's tokens)
+    long long state_lo, rows_lo; // elements from a state's, or E's or dU's, high part to its low one, where there are two
     const void* dout;            // [B, N, H, dv]
     const float* dstate_out;     // [B, H, dk, dv] or null (zeros)
     float* dstate_in;            // or null
@@ -208,6 +211,10 @@ struct DOps<BF16> {
     // of a lane's part to row n16 of an LDS tile (the block transposed: its rows become columns c0 ..)
     __device__ static __forceinline__ void blk_store(st* p, int i, int lane, const f32x4_t* x) {
         *reinterpret_cast<bf16x8_t*>(p + (i * 64 + lane) * 8) = acc_pair(x[0], x[1]);
+    }
+    // the low part of the same block
+    __device__ static __forceinline__ void blk_store_lo(st* p, int i, int lane, const f32x4_t* x) {
+        *reinterpret_cast<bf16x8_t*>(p + (i * 64 + lane) * 8) = split(x[0], x[1]).lo;
     }
     template <class Tile>
     __device__ static __forceinline__ void blk_lds(st* lds, int row, int c0, int g4, u32x4_t x) {
@@ -433,12 +440,13 @@ struct DOut {
 struct DeltaKernels {
     delta_kernel_t prep, local, full, full_f32, scan;  // full_f32: F32 output
     delta_kernel_t bprep, blocal, states, rlocal, rscan, rfull, grad, grad_group;  // gradients (grad_group: H > Hk)
+    delta_kernel_t states2, rfull2, grad2, grad_group2;  // the same with what the chains store in two parts (BF16 input)
     int cols, threads; // columns of d_v (or of a transition) and threads per workgroup of the chains
-    int grad_threads, scan_threads;
+    int grad_threads, grad2_threads, scan_threads;
 };
 // d_k in {32, 64, 128, 256} for bf16 and {16, 32, 64, 128} for fp32; false otherwise.
 bool delta_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);
-// The gradients' own kernels (rlocal, rfull, grad, grad_threads) of a supported shape.
+// The gradients' own kernels (rlocal, rfull, grad, their two-part forms and the threads) of a supported shape.
 void delta_bwd_kernels_get(bool bf16_in, int dk, int dv, DeltaKernels* out);
 
 }  // namespace ret

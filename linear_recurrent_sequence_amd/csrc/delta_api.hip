@@ -52,8 +52,11 @@ float scale_of(float scale, int dk) { return scale == 0.f ? (float)(1.0 / sqrt((
 struct Plan {
     int nchunks, nseg, seg_chunks;
     size_t mats, fac, segE, segM, segF, s0t, ds1t, et, dut, bytes;  // byte offsets of the parts, and their end
+    size_t state, rows;                                             // bytes of one part of s0t or ds1t, of et or dut
 };
-Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bwd, const Opts& op) {
+// parts: 0 for the forward; for the gradients, in how many the chains store what the per-chunk kernel reads.
+Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, int parts, const Opts& op) {
+    const bool bwd = parts > 0;
     const int nmats = bwd ? 3 : 2;
     Plan p;
     p.nchunks = s.N / kDeltaC + (s.N % kDeltaC != 0);
@@ -73,14 +76,14 @@ Plan make_plan(const Shape& s, const DeltaKernels& k, ret_dtype_t in_dt, bool bw
     p.segM = p.segE + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dv * sizeof(float)) : 0);
     p.segF = p.segM + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dk * sizeof(float)) : 0);
     p.s0t = p.ds1t = p.et = p.dut = p.bytes = p.segF;
+    p.state = round256(bh * p.nchunks * s.dk * s.dv * esize(in_dt));
+    p.rows = round256(bh * p.nchunks * kDeltaC * s.dv * esize(in_dt));
     if (bwd) {
-        const size_t state = round256(bh * p.nchunks * s.dk * s.dv * esize(in_dt));
-        const size_t rows = round256(bh * p.nchunks * kDeltaC * s.dv * esize(in_dt));
         p.s0t = p.segF + (p.nseg > 1 ? round256(bh * p.nseg * s.dk * s.dv * sizeof(float)) : 0);
-        p.ds1t = p.s0t + state;
-        p.et = p.ds1t + state;
-        p.dut = p.et + rows;
-        p.bytes = p.dut + rows;
+        p.ds1t = p.s0t + parts * p.state;
+        p.et = p.ds1t + parts * p.state;
+        p.dut = p.et + parts * p.rows;
+        p.bytes = p.dut + parts * p.rows;
     }
     return p;
 }
@@ -113,6 +116,8 @@ void fill(DeltaArgs& A, const Shape& s, const Plan& p, bool bwd, void* workspace
     A.ds1t = (char*)workspace + p.ds1t;
     A.et = (char*)workspace + p.et;
     A.dut = (char*)workspace + p.dut;
+    A.state_lo = p.state / 2;  // bf16 elements
+    A.rows_lo = p.rows / 2;
     A.out_bf16 = out_dt == RET_BF16;
     A.gate_bf16 = gate_dt == RET_BF16;
     A.scale = scale_of(scale, s.dk);
@@ -162,7 +167,7 @@ size_t ret_gated_delta_workspace_bytes(int B, int N, int H, int Hk, int dk, int 
     DeltaKernels k;
     if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
     if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
-    const Plan p = make_plan(s, k, in_dt, false, resolve(opts));
+    const Plan p = make_plan(s, k, in_dt, 0, resolve(opts));
     Grids G;
     return make_grids(s, p, k, &G) == RET_OK ? p.bytes : 0;
 }
@@ -182,7 +187,7 @@ ret_status_t ret_gated_delta_fwd(const void* q, const void* k, const void* v, co
         return fail(RET_ERR_UNSUPPORTED, "gated delta rule: unsupported d_k=%d d_v=%d for %s input", dk, dv,
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
-    const Plan p = make_plan(s, kn, in_dt, false, op);
+    const Plan p = make_plan(s, kn, in_dt, 0, op);
     Grids G;
     if ((st = make_grids(s, p, kn, &G)) != RET_OK) return st;
     const size_t T = (size_t)B * N, ei = esize(in_dt), sb = (size_t)B * H * dk * dv * 4;
@@ -226,7 +231,7 @@ size_t ret_gated_delta_bwd_workspace_bytes(int B, int N, int H, int Hk, int dk, 
     DeltaKernels k;
     if (check_shape(s, in_dt, RET_F32, RET_F32, kSeqMaxBH) != RET_OK) return 0;
     if (!delta_kernels_get(in_dt == RET_BF16, dk, dv, &k)) return 0;
-    const Plan p = make_plan(s, k, in_dt, true, resolve(opts));
+    const Plan p = make_plan(s, k, in_dt, in_dt == RET_BF16 ? 2 : 1, resolve(opts));
     Grids G;
     return make_grids(s, p, k, &G) == RET_OK ? p.bytes : 0;
 }
@@ -248,7 +253,9 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
         return fail(RET_ERR_UNSUPPORTED, "gated delta gradients: unsupported d_k=%d d_v=%d for %s input", dk, dv,
                     in_dt == RET_F32 ? "F32" : "BF16");
     const Opts op = resolve(opts);
-    const Plan p = make_plan(s, kn, in_dt, true, op);
+    // gradients in fp32 from bf16 input: their type holds more than one rounding of the chains' states leaves
+    const bool two = in_dt == RET_BF16 && (out_dt == RET_F32 || gate_dt == RET_F32);
+    const Plan p = make_plan(s, kn, in_dt, two ? 2 : 1, op);
     Grids G;
     if ((st = make_grids(s, p, kn, &G)) != RET_OK) return st;
     const size_t T = (size_t)B * N, ei = esize(in_dt), eo = esize(out_dt), sb = (size_t)B * H * dk * dv * 4;
@@ -288,13 +295,15 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
         if ((st = launch("ret_delta_local", kn.blocal, local, str, op, A, kn.threads)) != RET_OK) return st;
         if ((st = launch("ret_delta_scan", kn.scan, scan, str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_states", kn.states, chain, str, op, A, kn.threads)) != RET_OK) return st;
+    if ((st = launch("ret_delta_states", two ? kn.states2 : kn.states, chain, str, op, A, kn.threads)) != RET_OK) return st;
     if (p.nseg > 1) {
         if ((st = launch("ret_delta_local_bwd", kn.rlocal, chain, str, op, A, kn.threads)) != RET_OK) return st;
         if ((st = launch("ret_delta_scan", kn.rscan, scan, str, op, A, kn.scan_threads)) != RET_OK) return st;
     }
-    if ((st = launch("ret_delta_full_bwd", kn.rfull, chain, str, op, A, kn.threads)) != RET_OK) return st;
-    return launch("ret_delta_grad", H > Hk ? kn.grad_group : kn.grad, dim3(p.nchunks, B * Hk), str, op, A, kn.grad_threads);
+    if ((st = launch("ret_delta_full_bwd", two ? kn.rfull2 : kn.rfull, chain, str, op, A, kn.threads)) != RET_OK) return st;
+    const delta_kernel_t grad = H > Hk ? two ? kn.grad_group2 : kn.grad_group : two ? kn.grad2 : kn.grad;
+    const int threads = two ? kn.grad2_threads : kn.grad_threads;
+    return launch("ret_delta_grad", grad, dim3(p.nchunks, B * Hk), str, op, A, threads);
 }
 
 ret_status_t ret_gated_delta_step(const void* q, const void* k, const void* v, const void* g, const void* beta, void* o,

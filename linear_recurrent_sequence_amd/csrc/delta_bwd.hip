@@ -24,11 +24,11 @@ typedef double f64;
 // ---------------------------------------------------------------------------------------------------
 // The chain from the right: one segment of one head, 16 columns per wave, dS in accumulators. LOCAL: the gradient of the
 // state entering the segment from a zero one leaving it (the last segment: from dstate_out), into segF. Otherwise dS_C of
-// each chunk and dU, as blocks, and dV; the first segment leaves dstate_in. Built as the forward's chain: requests a chunk
+// each chunk and dU, as blocks (TWO: in two parts), and dV; the first segment leaves dstate_in. Built as the forward's chain: requests a chunk
 // ahead between the products of K dS, K in two buffers, Q's product before the second barrier. 10 us a step at d_k = 256,
 // 7 at 128, by the same measure as the forward's; 8192 tokens, 16 heads, d_k = 256, d_v = 512: 242 us local, 336 us full.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NW, bool LOCAL>
+template <class E, int DK, int NW, bool LOCAL, bool TWO>
 __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
@@ -151,7 +151,10 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
             st* out = (st*)a.ds1t + (unit * a.dv + col0) * DK;
             if (active)
 #pragma unroll
-                for (int t = 0; t < DT / D::TPS; ++t) D::blk_store(out, t, lane, &S[D::TPS * t]);
+                for (int t = 0; t < DT / D::TPS; ++t) {
+                    D::blk_store(out, t, lane, &S[D::TPS * t]);
+                    if constexpr (TWO) D::blk_store_lo(out + a.state_lo, t, lane, &S[D::TPS * t]);
+                }
         }
         // W = exp(G_C - G) K dS + Pr^T dO
         f32x4_t x[4];
@@ -237,7 +240,10 @@ __global__ __launch_bounds__(64 * NW) void delta_rchain_kernel(DeltaArgs a) {
             if (active) {
                 st* out = (st*)a.dut + (unit * a.dv + col0) * kDeltaC;
 #pragma unroll
-                for (int s = 0; s < NS; ++s) D::blk_store(out, s, lane, &u[D::TPS * s]);
+                for (int s = 0; s < NS; ++s) {
+                    D::blk_store(out, s, lane, &u[D::TPS * s]);
+                    if constexpr (TWO) D::blk_store_lo(out + a.rows_lo, s, lane, &u[D::TPS * s]);
+                }
                 const bool rows = sizeof(st) == 2 && a.out_bf16;
                 wave_fence();  // the last reads of dO come before
 #pragma unroll
@@ -337,6 +343,35 @@ struct GBlocks {
     }
 };
 
+// Blocks of E and of dU in two parts: segments of four arrays in one order (E's high and low, dU's high and low part), so that
+// every thread moves the same number of them.
+template <class E, int R, int VB, int NT>
+struct GQuad {
+    typedef typename E::st st;
+    typedef DOps<E> D;
+    static constexpr int PER = R / (16 * D::TPS), SEGS = VB / 16 * PER * 64, NP = 4 * SEGS / NT;
+    static_assert(4 * SEGS % NT == 0 && SEGS % 64 == 0, "whole waves per array");
+    typedef typename D::template Tile<R> Tile;
+    u32x4_t x[NP];
+    __device__ static __forceinline__ int array(int w, int i) { return (64 * w + i * NT) / SEGS; }
+    __device__ __forceinline__ void load(const st* e, const st* u, long long lo, int cols, int lane, int w) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int k = array(w, i), s = 64 * w + i * NT - k * SEGS + lane;
+            const st* p = (k & 2 ? u : e) + (k & 1 ? lo : 0);
+            x[i] = buf_load16(bytes_rsrc(p, cols * R * (int)sizeof(st)), 16 * s, 0);
+        }
+    }
+    __device__ __forceinline__ void store(st* lds, int lane, int w) const {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int k = array(w, i), blk = w + i * NT / 64 - k * SEGS / 64;
+            const int row = blk / PER * 16 + (lane & 15), c0 = blk % PER * 16 * D::TPS;
+            D::template blk_lds<Tile>(lds + k * VB * Tile::LD, row, c0, 4 * (lane >> 4), x[i]);
+        }
+    }
+};
+
 // sum of the products of two operand fragments
 __device__ __forceinline__ float frag_dot(bf16x8_t a, bf16x8_t b) {
     const u32x4_t x = __builtin_bit_cast(u32x4_t, a), y = __builtin_bit_cast(u32x4_t, b);
@@ -351,6 +386,78 @@ __device__ __forceinline__ float frag_dot(bf16x8_t a, bf16x8_t b) {
 __device__ __forceinline__ float frag_dot(f32x4_t a, f32x4_t b) {
     return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
+__device__ __forceinline__ void unpack8(bf16x8_t a, float* f) {
+    const u32x4_t x = __builtin_bit_cast(u32x4_t, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(x[i] << 16);
+        f[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ float frag_dot(const DOps<BF16>::Fb& a, const DOps<BF16>::Fb& b) {
+    float ah[8], al[8], bh[8], bl[8], s = 0.f;
+    unpack8(a.hi, ah);
+    unpack8(a.lo, al);
+    unpack8(b.hi, bh);
+    unpack8(b.lo, bl);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += (ah[i] + al[i]) * (bh[i] + bl[i]);
+    return s;
+}
+
+// What the chains stored and the matrices X and Z as operands: one part in the input's type, or (TWO) two bf16 parts, the
+// low one `lo` elements behind the high one. mma adds a product, of operands in two parts all but that of the low ones.
+template <class E, bool TWO>
+struct GOps {
+    typedef typename E::st st;
+    typedef DOps<E> D;
+    typedef typename D::Fa F;
+    template <class Tile>
+    __device__ static __forceinline__ F rows(const st* X, int, int r0, int k0, int lane) {
+        return Tile::rows(X, r0, k0, lane);
+    }
+    template <class Tile>
+    __device__ static __forceinline__ F cols(const st* X, int, int k0, int n0, int lane) {
+        return Tile::cols(X, k0, n0, lane);
+    }
+    __device__ static __forceinline__ void mma(f32x4_t& acc, const F& a, const F& b) { D::mma_aa(acc, a, b); }
+    __device__ static __forceinline__ void store(st* p, int, f32x4_t x) { store4(p, x); }
+};
+template <>
+struct GOps<BF16, true> {
+    typedef uint16_t st;
+    typedef DOps<BF16> D;
+    typedef D::Fb F;
+    template <class Tile>
+    __device__ static __forceinline__ F rows(const st* X, int lo, int r0, int k0, int lane) {
+        return {Tile::rows(X, r0, k0, lane), Tile::rows(X + lo, r0, k0, lane)};
+    }
+    template <class Tile>
+    __device__ static __forceinline__ F cols(const st* X, int lo, int k0, int n0, int lane) {
+        return {Tile::cols(X, k0, n0, lane), Tile::cols(X + lo, k0, n0, lane)};
+    }
+    __device__ static __forceinline__ void mma(f32x4_t& acc, const F& a, const F& b) {
+        D::mfma1(acc, a.lo, b.hi);
+        D::mfma1(acc, a.hi, b.lo);
+        D::mfma1(acc, a.hi, b.hi);
+    }
+    __device__ static __forceinline__ void mma(f32x4_t& acc, const F& a, bf16x8_t b) {
+        D::mfma1(acc, a.lo, b);
+        D::mfma1(acc, a.hi, b);
+    }
+    __device__ static __forceinline__ void mma(f32x4_t& acc, bf16x8_t a, const F& b) {
+        D::mfma1(acc, a, b.lo);
+        D::mfma1(acc, a, b.hi);
+    }
+    __device__ static __forceinline__ void store(st* p, int lo, f32x4_t x) {
+        const uint2 u = make_uint2(pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]));
+        const f32x4_t h = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xffff0000u)};
+        *reinterpret_cast<uint2*>(p) = u;
+        store4(p + lo, x - h);
+    }
+};
+
 __device__ __forceinline__ f32x4_t lds4(const uint16_t* p) {
     const uint2 u = *reinterpret_cast<const uint2*>(p);
     return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
@@ -372,24 +479,32 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 // (8192 tokens of 8 heads: 142 us, and 148 ungrouped). X and Z go on in the input's type, like what the chains stored, so
 // that a term of dq, dk, dbeta and dg of bf16 input carries two to four roundings of up to 2^-8 each: 0.003 in the 2-norm
 // with the output's own 0.0017. dg is a difference of such sums, 0.003 as a rule and up to 0.008 where they nearly cancel.
+// TWO (gates or outputs in fp32, whose type holds more): all of these in two bf16 parts, twice the bytes of the chains'
+// arrays; dO, which then does not fit the LDS, is read as fragments. 720 us at d_k = 256 (8 waves with twice the registers:
+// 16 would spill 87 of theirs), 350 at 128, 65 for 8 x 2048 tokens of 8 heads of 64 (42 in one part). Grouped heads spill
+// 114 registers at d_k = 256 and 17 at 64: 892 us for 8 key heads of the 16, 69 for 2 of the 8. X's diagonal stands with q in dq
+// and with k in Kw, so that it cancels in dg: in one part exactly (24-bit products), in two it is left to the end.
 // ---------------------------------------------------------------------------------------------------
-template <class E, int DK, int NW, bool GROUP>
+template <class E, int DK, int NW, bool GROUP, bool TWO>
 __global__ __launch_bounds__(64 * NW, (NW == 4 && DK * sizeof(typename E::st) <= 128 ? 2 : 1))
 void delta_grad_kernel(DeltaArgs a) {
     typedef typename E::st st;
     typedef DOps<E> D;
-    constexpr int NT = 64 * NW, HF = NW / 4, DH = DK / HF, DT = DH / 16, NS = kDeltaC / D::KS, VB = 32;
+    typedef GOps<E, TWO> G;
+    constexpr int NT = 64 * NW, HF = NW / 4, DH = DK / HF, DT = DH / 16, NS = kDeltaC / D::KS, VB = 32, P = TWO ? 2 : 1;
     typedef typename D::template Tile<DK> TK;
     typedef typename D::template Tile<VB> TO;
     typedef typename D::template Tile<kDeltaC> TC;
-    constexpr int kStage = 2 * VB * TK::LD + kDeltaC * TO::LD + 2 * VB * TC::LD, kXZ = 2 * kDeltaC * TC::LD;
+    // one part of: S_0 or dS_C, dO, E or dU, X or Z
+    constexpr int kS = VB * TK::LD, kO = TWO ? 0 : kDeltaC * TO::LD, kE = VB * TC::LD, kX = kDeltaC * TC::LD;
+    constexpr int kStage = 2 * P * (kS + kE) + kO, kXZ = 2 * P * kX;
     __shared__ __align__(16) st sk[kDeltaC * TK::LD];
     __shared__ __align__(16) st sq[kDeltaC * TK::LD];
     __shared__ __align__(16) st buf[kStage > kXZ ? kStage : kXZ];
     __shared__ f64 sG[kDeltaC];
-    __shared__ float sF[256], sDg[HF][kDeltaC], sDb[kDeltaC], sR[2][NW];
-    st *sS = buf, *sD = sS + VB * TK::LD, *sO = sD + VB * TK::LD, *sE = sO + kDeltaC * TO::LD, *sU = sE + VB * TC::LD;
-    st *sX = buf, *sZ = buf + kDeltaC * TC::LD;
+    __shared__ float sF[256], sDg[HF][kDeltaC], sDb[kDeltaC], sR[2][NW], sXd[TWO ? kDeltaC : 1];
+    st *sS = buf, *sD = sS + P * kS, *sO = sD + P * kS, *sE = sO + kO, *sU = sE + P * kE;
+    st *sX = buf, *sZ = buf + P * kX;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n16 = lane & 15;
     const int g4 = 4 * (lane >> 4), tw = w & 3, hf = w >> 2, dk0 = hf * DH, i = 16 * tw + n16;  // this lane's token
     const int c = blockIdx.x, b = blockIdx.y / a.Hk, hk = blockIdx.y % a.Hk;
@@ -425,9 +540,11 @@ void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) M[0][j] = M[kM2][j] = zero;
         float dot = 0.f;
-        GBlocks<E, DK, VB, NT, true> rs, rd;
+        GBlocks<E, DK, VB, NT, true> rs[P], rd[P];
         GRows<E, kDeltaC, VB, NT> ro;
         GBlocks<E, kDeltaC, VB, NT, false> re, ru;
+        GQuad<E, kDeltaC, VB, TWO ? NT : 64> reu;
+        u32x4_t xo;  // this lane's part of dO's rows as a fragment
         const st* sp = (const st*)a.s0t + unit * a.dv * DK;
         const st* dp = (const st*)a.ds1t + unit * a.dv * DK;
         const st* ep = (const st*)a.et + unit * a.dv * kDeltaC;
@@ -435,11 +552,22 @@ void delta_grad_kernel(DeltaArgs a) {
         const st* op = (const st*)a.dout + (((long long)b * a.N + t0) * a.H + h) * a.dv;
         auto fetch = [&](int v0) {
             const int nv = min(VB, a.dv - v0);
-            rs.load(sp + (long long)v0 * DK, nv, tid);
-            rd.load(dp + (long long)v0 * DK, nv, tid);
-            ro.load(op + v0, a.H * a.dv, live, nv, tid);
-            re.load(ep + v0 * kDeltaC, nv, tid);
-            ru.load(up + v0 * kDeltaC, nv, tid);
+#pragma unroll
+            for (int p = 0; p < P; ++p) rs[p].load(sp + p * a.state_lo + (long long)v0 * DK, nv, tid);
+#pragma unroll
+            for (int p = 0; p < P; ++p) rd[p].load(dp + p * a.state_lo + (long long)v0 * DK, nv, tid);
+            if constexpr (TWO) {
+                const rsrc_t r = bytes_rsrc(op + v0, ((live - 1) * a.H * a.dv + nv) * (int)sizeof(st));
+                const int at = i < live ? (i * a.H * a.dv + g4) * (int)sizeof(st) : 0x40000000;
+                const u32x2_t x = __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0);
+                const u32x2_t y = __builtin_amdgcn_raw_buffer_load_b64(r, nv > 16 ? at + 16 * (int)sizeof(st) : 0x40000000, 0, 0);
+                xo = u32x4_t{x[0], x[1], y[0], y[1]};
+                reu.load(ep + v0 * kDeltaC, up + v0 * kDeltaC, a.rows_lo, nv, lane, w);
+            } else {
+                ro.load(op + v0, a.H * a.dv, live, nv, tid);
+                re.load(ep + v0 * kDeltaC, nv, tid);
+                ru.load(up + v0 * kDeltaC, nv, tid);
+            }
         };
         fetch(0);
         const float* f = a.fac + unit * kDeltaFac;
@@ -448,33 +576,43 @@ void delta_grad_kernel(DeltaArgs a) {
         if (tid < kDeltaC) sG[tid] = reinterpret_cast<const f64*>(f + 256)[tid];
         for (int v0 = 0; v0 < a.dv; v0 += VB) {
             __syncthreads();
-            rs.store(sS, tid);
-            rd.store(sD, tid);
-            ro.store(sO, tid);
-            re.store(sE, tid);
-            ru.store(sU, tid);
+#pragma unroll
+            for (int p = 0; p < P; ++p) rs[p].store(sS + p * kS, tid);
+#pragma unroll
+            for (int p = 0; p < P; ++p) rd[p].store(sD + p * kS, tid);
+            u32x4_t xo0;
+            if constexpr (TWO) {
+                xo0 = xo;
+                reu.store(sE, lane, w);
+            } else {
+                ro.store(sO, tid);
+                re.store(sE, tid);
+                ru.store(sU, tid);
+            }
             __syncthreads();
             fetch(min(v0 + VB, (a.dv - 1) / VB * VB));  // unconditional: see the forward chain
 #pragma unroll
             for (int s = 0; s < VB / D::KS; ++s) {
-                const typename D::Fa fo = TO::rows(sO, 16 * tw, s * D::KS, lane);
-                const typename D::Fa fu = TC::cols(sU, s * D::KS, 16 * tw, lane);
-                const typename D::Fa fe = TC::cols(sE, s * D::KS, 16 * tw, lane);
+                typename D::Fa fo;
+                if constexpr (TWO) fo = __builtin_bit_cast(typename D::Fa, xo0);
+                else fo = TO::rows(sO, 16 * tw, s * D::KS, lane);
+                const typename G::F fu = G::template cols<TC>(sU, kE, s * D::KS, 16 * tw, lane);
+                const typename G::F fe = G::template cols<TC>(sE, kE, s * D::KS, 16 * tw, lane);
 #pragma unroll
                 for (int t = 0; t < DT; ++t) {
-                    const typename D::Fa fs = TK::cols(sS, s * D::KS, dk0 + 16 * t, lane);
-                    const typename D::Fa fd = TK::cols(sD, s * D::KS, dk0 + 16 * t, lane);
-                    D::mma_aa(Dq[t], fs, fo);
-                    D::mma_aa(Dr[t], fs, fu);
-                    D::mma_aa(Du[t], fd, fe);
+                    const typename G::F fs = G::template cols<TK>(sS, kS, s * D::KS, dk0 + 16 * t, lane);
+                    const typename G::F fd = G::template cols<TK>(sD, kS, s * D::KS, dk0 + 16 * t, lane);
+                    G::mma(Dq[t], fs, fo);
+                    G::mma(Dr[t], fs, fu);
+                    G::mma(Du[t], fd, fe);
                     if ((t & 3) == tw) dot += frag_dot(fs, fd);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (j > tw) continue;
-                    const typename D::Fa fj = TC::cols(sE, s * D::KS, 16 * j, lane);
-                    if (hf == 0) D::mma_aa(M[0][j], fj, fo);
-                    if (hf == HF - 1) D::mma_aa(M[kM2][j], fj, fu);
+                    const typename G::F fj = G::template cols<TC>(sE, kE, s * D::KS, 16 * j, lane);
+                    if (hf == 0) G::mma(M[0][j], fj, fo);
+                    if (hf == HF - 1) G::mma(M[kM2][j], fj, fu);
                 }
             }
         }
@@ -498,28 +636,36 @@ void delta_grad_kernel(DeltaArgs a) {
                 if (jj > i) continue;
                 const float d = __builtin_amdgcn_exp2f((float)(sG[i] - sG[jj])) * sF[192 + jj];
                 x[e] = a.scale * d * M[0][j][e];
+                if constexpr (TWO) {
+                    if (jj == i) {
+                        if (hf == 0) sXd[i] = x[e];
+                        x[e] = 0.f;
+                    }
+                }
                 if (jj < i) z[e] = -d * be * M[kM2][j][e];
                 else if (hf == HF - 1) sDb[i] = M[kM2][j][e];
             }
-            if (hf == 0) store4(sX + TC::off(i, 16 * j + g4), x);
-            if (hf == HF - 1) store4(sZ + TC::off(i, 16 * j + g4), z);
+            if (hf == 0) G::store(sX + TC::off(i, 16 * j + g4), kX, x);
+            if (hf == HF - 1) G::store(sZ + TC::off(i, 16 * j + g4), kX, z);
         }
         __syncthreads();
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
             const bool lower = s * D::KS <= 16 * tw + 15, upper = (s + 1) * D::KS > 16 * tw;
-            const typename D::Fa fx = TC::rows(sX, 16 * tw, s * D::KS, lane), fz = TC::rows(sZ, 16 * tw, s * D::KS, lane);
-            const typename D::Fa gx = TC::cols(sX, s * D::KS, 16 * tw, lane), gz = TC::cols(sZ, s * D::KS, 16 * tw, lane);
+            const typename G::F fx = G::template rows<TC>(sX, kX, 16 * tw, s * D::KS, lane);
+            const typename G::F fz = G::template rows<TC>(sZ, kX, 16 * tw, s * D::KS, lane);
+            const typename G::F gx = G::template cols<TC>(sX, kX, s * D::KS, 16 * tw, lane);
+            const typename G::F gz = G::template cols<TC>(sZ, kX, s * D::KS, 16 * tw, lane);
 #pragma unroll
             for (int t = 0; t < DT; ++t) {
                 const typename D::Fa fk = TK::cols(sk, s * D::KS, dk0 + 16 * t, lane);
                 if (lower) {
-                    D::mma_aa(Dq[t], fk, fx);
-                    D::mma_aa(Dr[t], fk, fz);
+                    G::mma(Dq[t], fk, fx);
+                    G::mma(Dr[t], fk, fz);
                 }
                 if (upper) {
-                    D::mma_aa(Du[t], TK::cols(sq, s * D::KS, dk0 + 16 * t, lane), gx);
-                    D::mma_aa(Du[t], fk, gz);
+                    G::mma(Du[t], TK::cols(sq, s * D::KS, dk0 + 16 * t, lane), gx);
+                    G::mma(Du[t], fk, gz);
                 }
             }
         }
@@ -529,6 +675,10 @@ void delta_grad_kernel(DeltaArgs a) {
             const f32x4_t kv = lds4(sk + TK::off(i, dk0 + 16 * t + g4)), qv = lds4(sq + TK::off(i, dk0 + 16 * t + g4));
             dg += dot4(qv, Dq[t]) + dot4(kv, Dr[t] - Du[t]);
             Dr[t] += Du[t];
+            if constexpr (TWO) {
+                Dq[t] += sXd[i] * kv;
+                Dr[t] += sXd[i] * qv;
+            }
             if constexpr (GROUP) {
                 tq[t] += Dq[t];
                 tk[t] += Dr[t];
@@ -589,15 +739,24 @@ void delta_grad_kernel(DeltaArgs a) {
 template <class E, int DK>
 void pick(int dv, DeltaKernels* o) {
     constexpr int NW = DK > 64 ? DK / 16 : 4;
+    constexpr bool B16 = sizeof(typename E::st) == 2;
     if (dv <= 64) {  // as the forward's
-        o->rlocal = delta_rchain_kernel<E, DK, 4, true>;
-        o->rfull = delta_rchain_kernel<E, DK, 4, false>;
+        o->rlocal = delta_rchain_kernel<E, DK, 4, true, false>;
+        o->rfull = delta_rchain_kernel<E, DK, 4, false, false>;
+        if constexpr (B16) o->rfull2 = delta_rchain_kernel<E, DK, 4, false, true>;
     } else {
-        o->rlocal = delta_rchain_kernel<E, DK, 8, true>;
-        o->rfull = delta_rchain_kernel<E, DK, 8, false>;
+        o->rlocal = delta_rchain_kernel<E, DK, 8, true, false>;
+        o->rfull = delta_rchain_kernel<E, DK, 8, false, false>;
+        if constexpr (B16) o->rfull2 = delta_rchain_kernel<E, DK, 8, false, true>;
     }
-    o->grad = delta_grad_kernel<E, DK, NW, false>;
-    o->grad_group = delta_grad_kernel<E, DK, NW, true>;
+    o->grad = delta_grad_kernel<E, DK, NW, false, false>;
+    o->grad_group = delta_grad_kernel<E, DK, NW, true, false>;
+    if constexpr (B16) {
+        constexpr int NW2 = NW < 8 ? NW : 8;
+        o->grad2 = delta_grad_kernel<E, DK, NW2, false, true>;
+        o->grad_group2 = delta_grad_kernel<E, DK, NW2, true, true>;
+        o->grad2_threads = 64 * NW2;
+    }
     o->grad_threads = 64 * NW;
 }
 

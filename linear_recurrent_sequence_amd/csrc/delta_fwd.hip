@@ -268,7 +268,7 @@ void delta_prep_kernel(DeltaArgs a) {
 //   kFull: outputs of the input's type; kFullF32: BF16 input, F32 output. After the last segment the state.
 //   kLocal / kLocalRaw (with Ts / with T): the segment's end state from zero (columns of V; segment 0 starts from state_in)
 //     into segE, or its transition (columns of the identity, V = 0) into segM.
-//   kStates (with T): the states entering the chunks and E, for the gradients.
+//   kStates (with T): the states entering the chunks and E, for the gradients; kStates2: both in two parts.
 // A step: Y = K S and Q S, between their products the requests for everything the next chunk needs, into registers; R; O
 // from Q S and P T; E; the state; then the registers go to LDS. K has two buffers, so that nothing but the first barrier
 // of a chunk stands between its steps; the second one (after Q S) frees Q's and makes the matrices visible. A wave
@@ -283,7 +283,7 @@ void delta_prep_kernel(DeltaArgs a) {
 // CU: 86 us for 16 chunks at d_k = 128, 284 us for 43 at 256; local pass 167 us for 32 at 256; states 221 for 32 at 256,
 // of which 670 MB of states and E at the copy rate are 131.
 // ---------------------------------------------------------------------------------------------------
-enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4 };
+enum { kFull = 0, kFullF32 = 1, kLocal = 2, kLocalRaw = 3, kStates = 4, kStates2 = 5 };
 template <class E, int DK, int NW, int MODE>
 __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     typedef typename E::st st;
@@ -295,7 +295,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
     typedef typename VRows::Tile VTile;
     typedef TriFrags<D::KS> F;
     constexpr bool LOCAL = MODE == kLocal || MODE == kLocalRaw, FULL = MODE == kFull || MODE == kFullF32;
-    constexpr bool RAW = MODE == kLocalRaw || MODE == kStates;
+    constexpr bool STATES = MODE == kStates || MODE == kStates2, RAW = MODE == kLocalRaw || STATES;
     constexpr bool OUT16 = MODE == kFull && sizeof(st) == 2;
     typedef typename std::conditional<OUT16, uint16_t, float>::type out_t;
     constexpr int DT = DK / 16, NS = F::NS, KN = DK / D::KS, TB = DT < 4 ? DT : 4;
@@ -388,11 +388,14 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
         if constexpr (FULL) rp.store(sp);
         from(min(c + 1, cend - 1));
         const st* K = sk[p];
-        if constexpr (MODE == kStates) {
+        if constexpr (STATES) {
             st* out = (st*)a.s0t + (((long long)bh * a.nchunks + c) * a.dv + col0) * DK;
             if (active)
 #pragma unroll
-                for (int t = 0; t < DT / D::TPS; ++t) D::blk_store(out, t, lane, &S[D::TPS * t]);
+                for (int t = 0; t < DT / D::TPS; ++t) {
+                    D::blk_store(out, t, lane, &S[D::TPS * t]);
+                    if constexpr (MODE == kStates2) D::blk_store_lo(out + a.state_lo, t, lane, &S[D::TPS * t]);
+                }
         }
         // Y = K S and O^T = (Q S)^T: there a lane holds 4 columns of token 16 m + n16
         f32x4_t y[4], o[4];
@@ -468,11 +471,14 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
 #pragma unroll
         for (int s = 0; s < NS; ++s) tri<E, false, false>(u, ft, fr[s], s);
         keep_order();
-        if constexpr (MODE == kStates) {
+        if constexpr (STATES) {
             st* out = (st*)a.et + (((long long)bh * a.nchunks + c) * a.dv + col0) * kDeltaC;
             if (active)
 #pragma unroll
-                for (int s = 0; s < NS; ++s) D::blk_store(out, s, lane, &u[D::TPS * s]);
+                for (int s = 0; s < NS; ++s) {
+                    D::blk_store(out, s, lane, &u[D::TPS * s]);
+                    if constexpr (MODE == kStates2) D::blk_store_lo(out + a.rows_lo, s, lane, &u[D::TPS * s]);
+                }
         }
         if constexpr (RAW)
 #pragma unroll
@@ -511,7 +517,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(DeltaArgs a) {
             for (int m = 0; m < 4; ++m) out.put((out_t*)nullptr, m, zero);
         }
     }
-    if constexpr (MODE == kStates) return;
+    if constexpr (STATES) return;
     float* out = nullptr;
     if (LOCAL) out = (trans ? a.segM : a.segE) + ((long long)bh * a.nseg + seg) * DK * width;
     else if (seg == a.nseg - 1 && a.state_out) out = a.state_out + (long long)bh * DK * a.dv;
@@ -646,6 +652,7 @@ void pick_waves(DeltaKernels* o) {
     o->full = delta_chain_kernel<E, DK, NW, kFull>;
     o->full_f32 = delta_chain_kernel<E, DK, NW, sizeof(typename E::st) == 2 ? kFullF32 : kFull>;
     o->states = delta_chain_kernel<E, DK, NW, kStates>;
+    if constexpr (sizeof(typename E::st) == 2) o->states2 = delta_chain_kernel<E, DK, NW, kStates2>;
     o->scan = delta_scan_kernel<E, DK, false>;
     o->rscan = delta_scan_kernel<E, DK, true>;
     o->scan_threads = 64 * scan_waves<DK>();

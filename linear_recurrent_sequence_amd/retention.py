@@ -842,8 +842,9 @@ def gated_delta_bwd_workspace(q, v, options=None):
 def ret_gated_delta_bwd(q, k, v, g, beta, dout, dq, dk, dv, dg, dbeta, scale=None, lengths=None, state_in=None,
                         dstate_out=None, dstate_in=None, workspace=None, stream=None, options=None):
     """dq, dk, dv, dg, dbeta (and dstate_in) <- gradients of sum(dout o) (+ sum(dstate_out state_out)) of
-    ret_gated_delta_fwd on the same inputs. dq, dk, dv share one dtype; dg, dbeta have that of g and beta. Without a
-    workspace one is allocated for the call."""
+    ret_gated_delta_fwd on the same inputs. dq, dk, dv share one dtype; dg, dbeta have that of g and beta. bfloat16 inputs
+    with float32 gates or gradients take a more precise and slower path. Without a workspace one is allocated for the
+    call."""
     lib = load()
     _delta_qkv(q, k, v, g, beta)
     B, N, Hk, d_k = q.shape
