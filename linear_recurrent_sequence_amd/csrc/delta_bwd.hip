@@ -481,8 +481,8 @@ __device__ __forceinline__ float dot4(f32x4_t a, f32x4_t b) {
 // with the output's own 0.0017. dg is a difference of such sums, 0.003 as a rule and up to 0.008 where they nearly cancel.
 // TWO (gates or outputs in fp32, whose type holds more): all of these in two bf16 parts, twice the bytes of the chains'
 // arrays; dO, which then does not fit the LDS, is read as fragments. 720 us at d_k = 256 (8 waves with twice the registers:
-// 16 would spill 87 of theirs), 350 at 128, 65 for 8 x 2048 tokens of 8 heads of 64 (42 in one part). Grouped heads spill
-// 114 registers at d_k = 256 and 17 at 64: 892 us for 8 key heads of the 16, 69 for 2 of the 8. X's diagonal stands with q in dq
+// 16 would spill 87 of theirs), 350 at 128, 67 for 8 x 2048 tokens of 8 heads of 64 (42 in one part). Grouped heads spill
+// 114 registers at d_k = 256 and 17 at 64: 908 us for 8 key heads of the 16, 76 for 2 of the 8. X's diagonal stands with q in dq
 // and with k in Kw, so that it cancels in dg: in one part exactly (24-bit products), in two it is left to the end.
 // ---------------------------------------------------------------------------------------------------
 template <class E, int DK, int NW, bool GROUP, bool TWO>
