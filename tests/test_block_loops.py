@@ -1,5 +1,5 @@
-"""Sizes at which the block's kernels go round more than once: several value heads per workgroup of the chunk matrices,
-rows and partial sums past one round of the grid, default plans of many segments. Tolerances as derived in
+"""Sizes at which the block's kernels loop more than once: several value heads per workgroup of the chunk matrices,
+rows and partial sums past one pass of the grid, default plans of many segments. Tolerances as derived in
 test_block_norms.py, test_gated_delta.py and test_gated_delta_grad.py."""
 import numpy as np
 import pytest
@@ -29,7 +29,7 @@ def R():
     ("f32", "f32", 1, 2500, 2, 1, 32, 48), ("bf16", "f32", 1, 2500, 1, 1, 64, 64), ("bf16", "f32", 1, 2777, 2, 2, 128, 80)])
 def test_delta_rule(R, dtype, gates, B, N, H, Hk, dk, dv):
     import torch
-    print_case("gated_delta_rounds", dtype, gates, B, N, H, Hk, dk, dv)
+    print_case("gated_delta_loops", dtype, gates, B, N, H, Hk, dk, dv)
     x = inputs(N, B, N, H, Hk, dk, dv, dtype, gates)
     gen = torch.Generator().manual_seed(1)
     dout = torch.randn(B, N, H, dv, generator=gen).to(x["q"].dtype)
@@ -49,7 +49,7 @@ def test_delta_rule(R, dtype, gates, B, N, H, Hk, dk, dv):
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_layer_norm_gradients(R, rows, D, kind):
     import torch
-    print_case("layer_norm_rounds", rows, D, kind)
+    print_case("layer_norm_loops", rows, D, kind)
     t = torch.float32 if kind == "f32" else torch.bfloat16
     g = torch.Generator().manual_seed(D)
     x, dy = (torch.randn(rows, D, generator=g) + 0.5).to(t), torch.randn(rows, D, generator=g).to(t)
@@ -80,7 +80,7 @@ def test_layer_norm_gradients(R, rows, D, kind):
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_epilogue_gradients(R, rows, H, dv, kind):
     import torch
-    print_case("epilogue_rounds", rows, H, dv, kind)
+    print_case("epilogue_loops", rows, H, dv, kind)
     t = torch.float32 if kind == "f32" else torch.bfloat16
     g = torch.Generator().manual_seed(dv)
     dy, o = (torch.randn(rows, H, dv, generator=g).to(t) for _ in range(2))
