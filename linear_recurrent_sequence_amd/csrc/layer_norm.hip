@@ -23,31 +23,6 @@ namespace ret {
 
 namespace {
 
-// Sum over the L lanes of a row group, left in every one of them. red: 2 slots of THREADS / 64 floats, used in turn so
-// that one barrier per sum is enough (a slot is written again only after the other slot's barrier).
-template <int L, int THREADS>
-struct RowSum {
-    float* red;
-    int slot;
-    __device__ __forceinline__ float operator()(float v) {
-        if constexpr (L <= 64) {
-            return lanes_sum<L>(v);
-        } else {
-            constexpr int NW = THREADS / 64, GW = L / 64;
-            v = lanes_sum<64>(v);
-            const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-            float* r = red + slot * NW;
-            slot ^= 1;
-            if ((threadIdx.x & 63) == 0) r[w] = v;
-            __syncthreads();
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < GW; ++i) s += r[w / GW * GW + i];
-            return s;
-        }
-    }
-};
-
 // W consecutive columns per vector, K vectors per lane, L lanes per row.
 template <int W, int L, int K, int THREADS>
 __global__ __launch_bounds__(THREADS) void layer_norm_kernel(LnArgs a) {

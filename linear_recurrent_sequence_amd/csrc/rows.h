@@ -52,6 +52,31 @@ __device__ __forceinline__ void row_store(void* p, long long i, bool bf16, const
     }
 }
 
+// Sum over the L lanes of a row group, left in every one of them. red: 2 slots of THREADS / 64 floats, used in turn so
+// that one barrier per sum is enough (a slot is written again only after the other slot's barrier).
+template <int L, int THREADS>
+struct RowSum {
+    float* red;
+    int slot;
+    __device__ __forceinline__ float operator()(float v) {
+        if constexpr (L <= 64) {
+            return lanes_sum<L>(v);
+        } else {
+            constexpr int NW = THREADS / 64, GW = L / 64;
+            v = lanes_sum<64>(v);
+            const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+            float* r = red + slot * NW;
+            slot ^= 1;
+            if ((threadIdx.x & 63) == 0) r[w] = v;
+            __syncthreads();
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < GW; ++i) s += r[w / GW * GW + i];
+            return s;
+        }
+    }
+};
+
 // Column sums left by `parts` workgroups, partial [parts][2][cols] fp32, added up in a fixed order: sums over the
 // first half into out0, over the second into out1 (either may be null).
 struct ColSumArgs {
@@ -62,6 +87,17 @@ struct ColSumArgs {
 typedef void (*colsum_kernel_t)(ColSumArgs);
 colsum_kernel_t colsum_kernel_get();
 constexpr int kColSumCols = 64, kColSumThreads = 1024;  // columns (of the 2 * cols) and threads per workgroup
+
+// Sums of partial rows, partial [parts][n] fp32, added up in a fixed order: columns below n0 into out0, the n1 after them
+// into out1, the rest into out2 (each may be null).
+struct PartSumArgs {
+    const float* partial;
+    float *out0, *out1, *out2;
+    long long n, n0, n1;
+    int parts;
+};
+typedef void (*part_sum_kernel_t)(PartSumArgs);
+part_sum_kernel_t part_sum_kernel_get();  // kColSumCols columns a workgroup of kColSumThreads
 
 // Layer norm of rows of D values, with an optional residual added first, and its gradients.
 struct LnArgs {

@@ -1,0 +1,249 @@
+// Selective scan over sequences, forward. Bound by the vector units: per token, channel and state one exp2 (a quarter of the
+// rate of the other instructions) and four products or sums where the states are reached in one pass.
+//
+// full: a workgroup walks the chunks of its segment, NW waves a chunk, each its own T tokens. A wave computes its decays once,
+// keeps them in 64 registers a lane, and from them the state its tokens leave if they start from zero; the waves exchange
+// these with the products of their decays, each forms the state entering its tokens, and goes over them again with the
+// decays it kept (three products a state more, where a second exp2 would cost the time of four). Few sequences of few channels
+// do not fill the card: they are split into segments, whose states from zero (local) are joined by their decays,
+// exp(A sum dt) (join), before full starts from them.
+#include "scan.h"
+
+namespace ret {
+
+namespace {
+
+// The states that a segment leaves if it starts from zero, and the sum of its steps. Its waves take neighbouring runs of
+// seg_tokens / NW tokens.
+template <class E, int S>
+__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_local_kernel(ScanArgs a) {
+    typedef ScanShape<S> P;
+    constexpr int SL = P::SL, T = P::T;
+    __shared__ float bc[P::NW][T * S];
+    __shared__ float ex[P::NW][2][64 * SL];
+    __shared__ float sums[P::NW][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
+    ScanPos at;
+    if (!scan_pos(a, &at) || at.seg == a.nseg - 1) return;  // nothing follows the last segment
+    const int d = at.cb * kScanCh + (lane >> 2), dc = d < a.D ? d : a.D - 1;
+    const int g = __builtin_amdgcn_readfirstlane(dc / (a.D / a.G));  // one for the whole wave
+    const int n = scan_length(a.lengths, at.b, a.N), run = a.seg_tokens / P::NW;
+    const int t0 = at.seg * a.seg_tokens + w * run, t1 = t0 + run < n ? t0 + run : n;
+    const long long row0 = (long long)at.b * a.N;
+    const float bias = a.bias ? a.bias[dc] : 0.f;
+    float A2[SL], h[SL], total = 0.f;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+        A2[j] = decay_rate(a.A[(long long)dc * S + q * SL + j]);
+        h[j] = 0.f;
+    }
+    float* Bs = bc[w];
+    ScanBlock<E, S> x;
+    if (t0 < t1) x.load(a, row0, n, t0, q, lane, dc, g, false);
+    for (int t = t0; t < t1; t += T) {
+        float du[P::TL], dt[P::TL];
+        x.steps(a, bias, n, t, q, du);
+#pragma unroll
+        for (int i = 0; i < P::TL; ++i) total += dt[i] = x.dt[i];
+        *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{x.b[0], x.b[1], x.b[2], x.b[3]};
+        if (t + T < t1) x.load(a, row0, n, t + T, q, lane, dc, g, false);
+        lds_order();
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            float B[SL];
+            lds_vec<SL>(Bs + k * S + q * SL, B);
+            const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
+#pragma unroll
+            for (int j = 0; j < SL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(dk * A2[j]), h[j], uk * B[j]);
+        }
+        lds_order();
+    }
+    total = lanes_sum<4>(total);
+    float p[SL];
+#pragma unroll
+    for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
+    ex_put<SL>(ex[w][0], lane, h);
+    ex_put<SL>(ex[w][1], lane, p);
+    sums[w][lane] = total;
+    __syncthreads();
+    if (w != 0) return;
+#pragma unroll
+    for (int v = 1; v < P::NW; ++v) {
+        float hv[SL], pv[SL];
+        ex_get<SL>(ex[v][0], lane, hv);
+        ex_get<SL>(ex[v][1], lane, pv);
+#pragma unroll
+        for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
+        total += sums[v][lane];
+    }
+    if (d >= a.D) return;
+    const long long seg = ((long long)at.b * a.nseg + at.seg) * a.D + d;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) a.seg_h[seg * S + q * SL + j] = h[j];
+    if (q == 0) a.seg_dt[seg] = total;
+}
+
+// Segments' states from zero -> the states entering them, in place.
+template <int S>
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
+    const long long per = (long long)a.D * S, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= per) return;
+    const int b = blockIdx.y, d = (int)(i / S);
+    const float A2 = decay_rate(a.A[i]);
+    float h = a.state_in ? a.state_in[b * per + i] : 0.f;
+    float* hp = a.seg_h + (long long)b * a.nseg * per + i;
+    const float* sp = a.seg_dt + (long long)b * a.nseg * a.D + d;
+    constexpr int U = 8;
+    for (int k = 0; k < a.nseg; k += U) {
+        float x[U], p[U];
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+            const int s = k + e < a.nseg - 1 ? k + e : 0;
+            x[e] = hp[s * per];
+            p[e] = sp[(long long)s * a.D];
+        }
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+            if (k + e >= a.nseg) break;
+            hp[(k + e) * per] = h;
+            h = fmaf(__builtin_amdgcn_exp2f(p[e] * A2), h, x[e]);
+        }
+    }
+}
+
+template <class E, class O, int S>
+__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_full_kernel(ScanArgs a) {
+    typedef ScanShape<S> P;
+    constexpr int SL = P::SL, T = P::T, TL = P::TL;
+    __shared__ float bc[P::NW][2][T * S];
+    __shared__ float ex[2][P::NW][2][64 * SL];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
+    ScanPos at;
+    if (!scan_pos(a, &at)) return;
+    const int d = at.cb * kScanCh + (lane >> 2), dc = d < a.D ? d : a.D - 1;
+    const int g = __builtin_amdgcn_readfirstlane(dc / (a.D / a.G));
+    const int n = scan_length(a.lengths, at.b, a.N);
+    const int s0 = at.seg * a.seg_tokens, s1 = a.N - s0 < a.seg_tokens ? a.N : s0 + a.seg_tokens;
+    const long long row0 = (long long)at.b * a.N;
+    const float bias = a.bias ? a.bias[dc] : 0.f, skip = a.skip ? a.skip[dc] : 0.f;
+    float A2[SL], run[SL];
+    const long long st = ((long long)at.b * a.D + dc) * S + q * SL;
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+        A2[j] = decay_rate(a.A[(long long)dc * S + q * SL + j]);
+        run[j] = 0.f;
+    }
+    if (a.nseg > 1) state_get<SL>(a.seg_h + (((long long)at.b * a.nseg + at.seg) * a.D + dc) * S + q * SL, run);
+    else if (a.state_in) state_get<SL>(a.state_in + st, run);
+    float *Bs = bc[w][0], *Cs = bc[w][1];
+    typedef typename O::st ost;
+    ost* y = (ost*)a.y;
+    // tokens past the sequence's length: zeros
+    const int live1 = s1 < n ? s1 : n;
+    for (int t = (live1 > s0 ? live1 : s0) + (int)(threadIdx.x / kScanCh); t < s1; t += P::THREADS / kScanCh) {
+        const int dz = at.cb * kScanCh + (int)(threadIdx.x % kScanCh);
+        if (dz < a.D) store_out(y + (row0 + t) * a.D + dz, 0.f);
+    }
+    ScanBlock<E, S> x;
+    if (s0 < live1) x.load(a, row0, n, s0 + w * T, q, lane, dc, g, true);
+    int parity = 0;
+    for (int c0 = s0; c0 < live1; c0 += P::CH, parity ^= 1) {
+        const int t0 = c0 + w * T;
+        float du[TL], dt[TL], u[TL], z[TL], total = 0.f;
+        x.steps(a, bias, n, t0, q, du);
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            dt[i] = x.dt[i];
+            u[i] = x.u[i];
+            z[i] = a.z ? x.z[i] : 0.f;
+            total += dt[i];
+        }
+        *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{x.b[0], x.b[1], x.b[2], x.b[3]};
+        *reinterpret_cast<f32x4_t*>(Cs + 4 * lane) = f32x4_t{x.c[0], x.c[1], x.c[2], x.c[3]};
+        if (c0 + P::CH < live1) x.load(a, row0, n, t0 + P::CH, q, lane, dc, g, true);
+        lds_order();
+        float al[T][SL], h[SL];
+#pragma unroll
+        for (int j = 0; j < SL; ++j) h[j] = 0.f;
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            float B[SL];
+            lds_vec<SL>(Bs + k * S + q * SL, B);
+            const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                al[k][j] = __builtin_amdgcn_exp2f(dk * A2[j]);
+                h[j] = fmaf(al[k][j], h[j], uk * B[j]);
+            }
+        }
+        total = lanes_sum<4>(total);
+        float p[SL];
+#pragma unroll
+        for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
+        ex_put<SL>(ex[parity][w][0], lane, h);
+        ex_put<SL>(ex[parity][w][1], lane, p);
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < P::NW; ++v) {
+            if (v == w)
+#pragma unroll
+                for (int j = 0; j < SL; ++j) h[j] = run[j];
+            float hv[SL], pv[SL];
+            ex_get<SL>(ex[parity][v][0], lane, hv);
+            ex_get<SL>(ex[parity][v][1], lane, pv);
+#pragma unroll
+            for (int j = 0; j < SL; ++j) run[j] = fmaf(pv[j], run[j], hv[j]);
+        }
+        float yp[T];
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            float B[SL], C[SL];
+            lds_vec<SL>(Bs + k * S + q * SL, B);
+            lds_vec<SL>(Cs + k * S + q * SL, C);
+            const float uk = quad_of(du[k / 4], k % 4);
+            yp[k] = 0.f;
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                h[j] = fmaf(al[k][j], h[j], uk * B[j]);
+                yp[k] = fmaf(C[j], h[j], yp[k]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            float o = quad_sums(yp[4 * i], yp[4 * i + 1], yp[4 * i + 2], yp[4 * i + 3], q);
+            const int t = t0 + 4 * i + q;
+            o = fmaf(skip, u[i], o);
+            if (a.z) o *= swish_hw(z[i]);
+            if (t < live1 && d < a.D) store_out(y + (row0 + t) * a.D + d, o);
+        }
+        lds_order();
+    }
+    if (w == 0 && a.state_out && at.seg == a.nseg - 1 && d < a.D)
+#pragma unroll
+        for (int j = 0; j < SL; ++j) a.state_out[st + j] = run[j];
+}
+
+template <class E, class O, int S>
+bool pick(ScanKernels* o) {
+    *o = {scan_local_kernel<E, S>, scan_join_kernel<S>, scan_full_kernel<E, O, S>, ScanShape<S>::CH, ScanShape<S>::THREADS};
+    return true;
+}
+template <class E, class O>
+bool of_states(int S, ScanKernels* o) {
+    switch (S) {
+        case 8: return pick<E, O, 8>(o);
+        case 16: return pick<E, O, 16>(o);
+        case 32: return pick<E, O, 32>(o);
+        case 64: return pick<E, O, 64>(o);
+        default: return false;
+    }
+}
+
+}  // namespace
+
+bool scan_kernels_get(bool bf16_in, bool bf16_out, int S, ScanKernels* o) {
+    if (!bf16_in) return of_states<F32, F32>(S, o);
+    return bf16_out ? of_states<BF16, BF16>(S, o) : of_states<BF16, F32>(S, o);
+}
+
+}  // namespace ret

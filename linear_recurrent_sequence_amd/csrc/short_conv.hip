@@ -1,0 +1,451 @@
+// Short causal convolution per channel, with the activation fused: forward, gradients and one token.
+//
+//   x~ = the W - 1 inputs before the sequence (the state, or zeros), then x
+//   pre_t = bias + sum_{j < W} w[j] x~_{t - W + 1 + j},  y_t = act(pre_t),  act the identity or silu
+//   dpre_t = dy_t act'(pre_t),  dx~_t = sum_j w[j] dpre_{t + W - 1 - j},  dw[j] = sum_t dpre_t x~_{t - W + 1 + j}
+//
+// A thread owns V neighbouring channels and walks a strip of tokens with the last W - 1 inputs (and, for the gradients, the
+// last W dpre) in registers, so that a strip reads its tokens once and W - 1 (2 W - 2) more of its neighbours'. Each kernel
+// reads and writes its tensors once and is bound by HBM. The gradients' sums over tokens stay in registers over a
+// workgroup's strips, meet in LDS and leave one partial row per workgroup, added up in a fixed order by a second kernel.
+#include "host.h"
+#include "rows.h"
+
+namespace ret {
+
+namespace {
+
+constexpr int kConvStrip = 32;   // tokens of a strip of the forward
+constexpr int kConvBwdStrip = 64;
+constexpr int kConvWaves = 4;    // waves of a workgroup, each its own strips of the same 64 V channels
+constexpr int kConvAhead = 8;     // tokens whose loads are in flight
+constexpr int kConvBwdAhead = 4;
+
+struct ConvArgs {
+    const void* x;          // rows of ld elements
+    const float *w, *bias;  // [D][W], [D] or null
+    const void* state_in;   // [B][W - 1][D], x's dtype, or null
+    void* y;                // [B][N][D]
+    void* state_out;        // as state_in, or null
+    const int32_t* lengths;
+    long long ld;
+    int B, N, D, silu, strips, cblocks;
+};
+struct ConvBwdArgs {
+    const void *dy, *x;
+    const float *w, *bias;
+    const void* state_in;
+    const void* dstate_out;  // [B][W - 1][D], dx's dtype, or null
+    void *dx, *dstate_in;
+    float* partial;          // [parts][(W + 1) D]: dw, then dbias; or null
+    const int32_t* lengths;
+    long long ld;
+    int B, N, D, silu, strips, cblocks, parts;
+};
+struct ConvStepArgs {
+    const void* x;
+    const float *w, *bias;
+    void *state, *y;
+    long long ld;
+    int B, D, silu, cblocks;
+};
+
+__device__ __forceinline__ float sigmoid_hw(float x) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+
+__device__ __forceinline__ int length_of(const int32_t* lengths, int b, int N) {
+    if (!lengths) return N;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > N ? N : n;
+}
+
+// V channels' weights [V][W] as w[j][v], and biases.
+template <int V, int W>
+__device__ __forceinline__ void load_weights(const float* w, const float* bias, long long c, int D, float (&o)[W][V],
+                                             float (&b)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) o[j][v] = c < D ? w[(c + v) * W + j] : 0.f;
+        b[v] = bias && c < D ? bias[c + v] : 0.f;
+    }
+}
+
+// Token t of x~ (t >= 1 - W) for V channels from c; zeros from n on.
+template <int V, bool XB>
+__device__ __forceinline__ void load_x(const void* x, const void* state, long long row0, long long ld, long long srow0,
+                                       int D, long long c, int W, int t, int n, float* f) {
+    if (t >= 0 && t < n) {
+        row_load<V>(x, (row0 + t) * ld + c, XB, f);
+    } else if (t < 0 && state) {
+        row_load<V>(state, (srow0 + W - 1 + t) * D + c, XB, f);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = 0.f;
+    }
+}
+
+template <int V, int W, bool XB, bool YB>
+__global__ __launch_bounds__(64 * kConvWaves) void conv_fwd_kernel(ConvArgs a) {
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cb = blockIdx.x % a.cblocks, rest = blockIdx.x / a.cblocks;
+    const int groups = (a.strips + kConvWaves - 1) / kConvWaves;
+    const int b = rest / groups, strip = rest % groups * kConvWaves + wv;
+    const long long c = ((long long)cb * 64 + lane) * V;
+    if (strip >= a.strips || c >= a.D) return;
+    const int n = length_of(a.lengths, b, a.N), t0 = strip * kConvStrip;
+    const int t1 = a.N - t0 < kConvStrip ? a.N : t0 + kConvStrip;
+    const long long row0 = (long long)b * a.N, srow0 = (long long)b * (W - 1);
+    float w[W][V], bias[V], x[W - 1 + kConvAhead][V];
+    load_weights<V, W>(a.w, a.bias, c, a.D, w, bias);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i)
+        load_x<V, XB>(a.x, a.state_in, row0, a.ld, srow0, a.D, c, W, t0 - (W - 1) + i, n, x[i]);
+    if (strip == 0 && a.state_out) {
+        // the last W - 1 of x~ before token n; what of the old state stays is read before anything is written
+        float s[W - 1][V];
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+            load_x<V, XB>(a.x, a.state_in, row0, a.ld, srow0, a.D, c, W, n - (W - 1) + i, n, s[i]);
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) row_store<V>(a.state_out, (srow0 + i) * a.D + c, XB, s[i]);
+    }
+    for (int t = t0; t < t1; t += kConvAhead) {
+#pragma unroll
+        for (int i = 0; i < kConvAhead; ++i)
+            load_x<V, XB>(a.x, nullptr, row0, a.ld, srow0, a.D, c, W, t + i, n, x[W - 1 + i]);
+#pragma unroll
+        for (int i = 0; i < kConvAhead; ++i) {
+            if (t + i >= t1) break;
+            float y[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                y[v] = bias[v];
+#pragma unroll
+                for (int j = 0; j < W; ++j) y[v] += w[j][v] * x[i + j][v];
+                if (a.silu) y[v] *= sigmoid_hw(y[v]);
+                if (t + i >= n) y[v] = 0.f;
+            }
+            row_store<V>(a.y, (row0 + t + i) * a.D + c, YB, y);
+        }
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[i][v] = x[kConvAhead + i][v];
+    }
+}
+
+// Strips of a workgroup's waves: part p takes strips (p kConvWaves + wave), then every parts kConvWaves further, over all
+// sequences. A strip yields dx of tokens t0 - (W - 1) .. t1 - W: with dpre from t0 on that needs the W - 1 dpre before t0,
+// computed again; the last strip of a sequence goes on to the end of dx with dpre of zero, the first starts in the state.
+template <int V, int W, bool XB, bool YB>
+__global__ __launch_bounds__(64 * kConvWaves) void conv_bwd_kernel(ConvBwdArgs a) {
+    __shared__ float meet[kConvWaves - 1][64][V];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cb = blockIdx.x % a.cblocks, part = blockIdx.x / a.cblocks;
+    const long long c = ((long long)cb * 64 + lane) * V;
+    const bool in = c < a.D;
+    float w[W][V], bias[V], dw[W][V], db[V];
+    load_weights<V, W>(a.w, a.bias, c, a.D, w, bias);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        db[v] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
+    }
+    const long long all = (long long)a.B * a.strips;
+    for (long long id = (long long)part * kConvWaves + wv; in && id < all; id += (long long)a.parts * kConvWaves) {
+        const int b = (int)(id / a.strips), strip = (int)(id % a.strips);
+        const int n = length_of(a.lengths, b, a.N), t0 = strip * kConvBwdStrip;
+        const bool last = strip == a.strips - 1;
+        const int t1 = last ? a.N : t0 + kConvBwdStrip;
+        const int from = strip == 0 ? 0 : t0 - (W - 1), to = last ? a.N + W - 1 : t1;  // tokens of dpre
+        const long long row0 = (long long)b * a.N, srow0 = (long long)b * (W - 1);
+        float x[W - 1 + kConvBwdAhead][V], g[W - 1 + kConvBwdAhead][V];  // x~ and dpre; the W - 1 before token t first
+#pragma unroll
+        for (int i = 0; i < W - 1; ++i) {
+            load_x<V, XB>(a.x, a.state_in, row0, a.ld, srow0, a.D, c, W, from - (W - 1) + i, n, x[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[i][v] = 0.f;
+        }
+        for (int t = from; t < to; t += kConvBwdAhead) {
+#pragma unroll
+            for (int i = 0; i < kConvBwdAhead; ++i) {
+                load_x<V, XB>(a.x, nullptr, row0, a.ld, srow0, a.D, c, W, t + i, n, x[W - 1 + i]);
+                if (t + i < n && t + i < to) {
+                    row_load<V>(a.dy, (row0 + t + i) * a.D + c, XB, g[W - 1 + i]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) g[W - 1 + i][v] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kConvBwdAhead; ++i) {
+                const int at = t + i;
+                if (at >= to) break;
+                float d[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    if (a.silu) {
+                        float pre = bias[v];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) pre += w[j][v] * x[i + j][v];
+                        const float s = sigmoid_hw(pre);
+                        if (at < n) g[W - 1 + i][v] *= s * (1.f + pre * (1.f - s));
+                    }
+                    const float dp = g[W - 1 + i][v];
+                    if (at >= t0) {
+                        db[v] += dp;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][v] += dp * x[i + j][v];
+                    }
+                    d[v] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) d[v] += w[j][v] * g[W - 1 + i - j][v];
+                }
+                const int o = at - (W - 1);  // the token that has all its dpre now
+                if (strip != 0 && at < t0) continue;  // the strip before yields it
+                if (o < n && a.dstate_out && o >= n - (W - 1)) {
+                    float s[V];
+                    row_load<V>(a.dstate_out, (srow0 + o - (n - (W - 1))) * a.D + c, YB, s);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) d[v] += s[v];
+                }
+                if (o >= 0) {
+                    if (o >= n)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) d[v] = 0.f;
+                    row_store<V>(a.dx, (row0 + o) * a.D + c, YB, d);
+                } else if (a.dstate_in) {
+                    row_store<V>(a.dstate_in, (srow0 + o + W - 1) * a.D + c, YB, d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < W - 1; ++i)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    x[i][v] = x[kConvBwdAhead + i][v];
+                    g[i][v] = g[kConvBwdAhead + i][v];
+                }
+        }
+    }
+    if (!a.partial) return;
+    float* out = a.partial + (long long)part * (W + 1) * a.D;
+#pragma unroll
+    for (int j = 0; j <= W; ++j) {
+        float(&mine)[V] = j < W ? dw[j < W ? j : 0] : db;
+        __syncthreads();
+        if (wv > 0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) meet[wv - 1][lane][v] = mine[v];
+        __syncthreads();
+        if (wv == 0 && in)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float s = mine[v];
+#pragma unroll
+                for (int i = 0; i < kConvWaves - 1; ++i) s += meet[i][lane][v];
+                if (j < W) out[(c + v) * W + j] = s;
+                else out[(long long)W * a.D + c + v] = s;
+            }
+    }
+}
+
+template <int V, int W, bool XB, bool YB>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvStepArgs a) {
+    const int b = blockIdx.x / a.cblocks;
+    const long long c = ((long long)(blockIdx.x % a.cblocks) * 256 + threadIdx.x) * V;
+    if (c >= a.D) return;
+    float w[W][V], bias[V], x[W][V];
+    const long long srow0 = (long long)b * (W - 1);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) row_load<V>(a.state, (srow0 + i) * a.D + c, XB, x[i]);
+    row_load<V>(a.x, b * a.ld + c, XB, x[W - 1]);
+    load_weights<V, W>(a.w, a.bias, c, a.D, w, bias);
+    float y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        y[v] = bias[v];
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[v] += w[j][v] * x[j][v];
+        if (a.silu) y[v] *= sigmoid_hw(y[v]);
+    }
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) row_store<V>(a.state, (srow0 + i) * a.D + c, XB, x[i + 1]);
+    row_store<V>(a.y, (long long)b * a.D + c, YB, y);
+}
+
+typedef void (*conv_fwd_t)(ConvArgs);
+typedef void (*conv_bwd_t)(ConvBwdArgs);
+typedef void (*conv_step_t)(ConvStepArgs);
+struct ConvKernels {
+    conv_fwd_t fwd;
+    conv_bwd_t bwd;
+    conv_step_t step;
+};
+
+template <int V, int W>
+ConvKernels conv_of_types(bool xb, bool yb) {
+    if (!xb) return {conv_fwd_kernel<V, W, false, false>, conv_bwd_kernel<V, W, false, false>, conv_step_kernel<V, W, false, false>};
+    if (yb) return {conv_fwd_kernel<V, W, true, true>, conv_bwd_kernel<V, W, true, true>, conv_step_kernel<V, W, true, true>};
+    return {conv_fwd_kernel<V, W, true, false>, conv_bwd_kernel<V, W, true, false>, conv_step_kernel<V, W, true, false>};
+}
+
+// vec: 8 channels a thread as 16-byte vectors, where every row starts on 16 bytes; else channel by channel.
+ConvKernels conv_kernels_get(int W, bool vec, bool xb, bool yb) {
+    if (W == 2) return vec ? conv_of_types<8, 2>(xb, yb) : conv_of_types<1, 2>(xb, yb);
+    if (W == 3) return vec ? conv_of_types<8, 3>(xb, yb) : conv_of_types<1, 3>(xb, yb);
+    return vec ? conv_of_types<8, 4>(xb, yb) : conv_of_types<1, 4>(xb, yb);
+}
+
+size_t esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
+
+ret_status_t check_conv(const void* x, const void* w, const void* y, int B, int N, int D, int W, int64_t* ld,
+                        ret_dtype_t in_dt, ret_dtype_t out_dt, int act) {
+    if (!x || !w || !y) return fail(RET_ERR_INVALID_ARG, "null x/weight/output pointer");
+    if (B <= 0 || N <= 0 || D <= 0)
+        return fail(RET_ERR_INVALID_ARG, "sizes must be positive (B=%d N=%d D=%d)", B, N, D);
+    for (ret_dtype_t t : {in_dt, out_dt})
+        if (t != RET_F32 && t != RET_BF16) return fail(RET_ERR_INVALID_ARG, "bad dtype %d", (int)t);
+    if (in_dt == RET_F32 && out_dt != RET_F32) return fail(RET_ERR_INVALID_ARG, "F32 input requires F32 output");
+    if (act != RET_ACT_NONE && act != RET_ACT_SILU) return fail(RET_ERR_INVALID_ARG, "bad activation %d", act);
+    if (W < 2 || W > 4) return fail(RET_ERR_UNSUPPORTED, "short convolution: width %d is not 2, 3 or 4", W);
+    if (*ld == 0) *ld = D;
+    if (*ld < D) return fail(RET_ERR_INVALID_ARG, "rows of x (%lld apart) are shorter than D=%d", (long long)*ld, D);
+    if ((long long)B * N > 1LL << 40 || *ld > 1LL << 32 || D > 1 << 28)
+        return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d N=%d D=%d ld=%lld too large", B, N, D, (long long)*ld);
+    return RET_OK;
+}
+
+bool conv_vec(const void* x, int D, int64_t ld) { return D % 8 == 0 && ld % 8 == 0 && aligned16(x); }
+
+int64_t conv_parts(int B, int N, int64_t cblocks) {
+    const int64_t strips = (int64_t)B * ((N + kConvBwdStrip - 1) / kConvBwdStrip);
+    const int64_t most = (strips + kConvWaves - 1) / kConvWaves, want = (1024 + cblocks - 1) / cblocks;
+    return most < want ? most : want;
+}
+
+int64_t conv_cblocks(int D, bool vec) {
+    const int per = vec ? 512 : 64;
+    return (D + per - 1) / per;
+}
+
+}  // namespace
+
+}  // namespace ret
+
+using namespace ret;
+
+extern "C" {
+
+ret_status_t ret_short_conv_fwd(const void* x, int64_t x_ld, const float* weight, const float* bias, void* y, int B, int N,
+                                int D, int W, ret_dtype_t in_dt, ret_dtype_t out_dt, int act, const int32_t* lengths,
+                                const void* state_in, void* state_out, void* stream, const ret_options_t* opts) {
+    ret_status_t st = check_conv(x, weight, y, B, N, D, W, &x_ld, in_dt, out_dt, act);
+    if (st != RET_OK) return st;
+    const bool vec = conv_vec(x, D, x_ld);
+    const int64_t strips = (N + kConvStrip - 1) / kConvStrip, cblocks = conv_cblocks(D, vec);
+    const unsigned long long wgs = (unsigned long long)cblocks * ((strips + kConvWaves - 1) / kConvWaves) * B;
+    if (!grid_fits(wgs, 1, 1, 64 * kConvWaves))
+        return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d N=%d D=%d exceed a launch", B, N, D);
+    const size_t rows = (size_t)B * N, e = esize(in_dt), sb = (size_t)B * (W - 1) * D * e;
+    const Buf w[] = {{"y", y, rows * D * esize(out_dt)}, {"state_out", state_out, sb, 1u << 3}};
+    const Buf r[] = {{"x", x, ((rows - 1) * x_ld + D) * e, 0, (unsigned)e}, {"weight", weight, (size_t)D * W * 4},
+                     {"bias", bias, (size_t)D * 4}, {"state_in", state_in, sb}, {"lengths", lengths, (size_t)B * 4, 0, 4}};
+    if ((st = check_apart(w, r)) != RET_OK) return st;
+    ConvArgs A = {x, weight, bias, state_in, y, state_out, lengths, x_ld, B, N, D, act == RET_ACT_SILU, (int)strips,
+                  (int)cblocks};
+    hipStream_t s = (hipStream_t)stream;
+    const Opts op = resolve(opts);
+    LaunchTimer tm("ret_short_conv", s, op);
+    hipLaunchKernelGGL(conv_kernels_get(W, vec, in_dt == RET_BF16, out_dt == RET_BF16).fwd, dim3((unsigned)wgs),
+                       dim3(64 * kConvWaves), 0, s, A);
+    tm.done();
+    return launch_status("ret_short_conv");
+}
+
+size_t ret_short_conv_bwd_workspace_bytes(int B, int N, int D, int W) {
+    if (B <= 0 || N <= 0 || D <= 0 || W < 2 || W > 4) return 0;
+    // either kernel's (x may be a slice that the vectors do not take)
+    int64_t parts = conv_parts(B, N, conv_cblocks(D, false));
+    if (D % 8 == 0) {
+        const int64_t v = conv_parts(B, N, conv_cblocks(D, true));
+        if (v > parts) parts = v;
+    }
+    return (size_t)parts * (W + 1) * D * sizeof(float);
+}
+
+ret_status_t ret_short_conv_bwd(const void* dy, const void* x, int64_t x_ld, const float* weight, const float* bias,
+                                void* dx, float* dweight, float* dbias, int B, int N, int D, int W, ret_dtype_t in_dt,
+                                ret_dtype_t out_dt, int act, const int32_t* lengths, const void* state_in,
+                                const void* dstate_out, void* dstate_in, void* workspace, size_t workspace_bytes,
+                                void* stream, const ret_options_t* opts) {
+    ret_status_t st = check_conv(x, weight, dx, B, N, D, W, &x_ld, in_dt, out_dt, act);
+    if (st != RET_OK) return st;
+    if (!dy) return fail(RET_ERR_INVALID_ARG, "null dy pointer");
+    const bool vec = conv_vec(x, D, x_ld);
+    const int64_t strips = (N + kConvBwdStrip - 1) / kConvBwdStrip, cblocks = conv_cblocks(D, vec);
+    const int64_t parts = conv_parts(B, N, cblocks);
+    if (!grid_fits((unsigned long long)cblocks * parts, 1, 1, 64 * kConvWaves))
+        return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d N=%d D=%d exceed a launch", B, N, D);
+    const bool cols = dweight || dbias;
+    const size_t need = ret_short_conv_bwd_workspace_bytes(B, N, D, W);
+    if (cols && (!workspace || workspace_bytes < need))
+        return fail(RET_ERR_WORKSPACE, "short convolution gradients: workspace of %zu bytes, %zu needed",
+                    workspace ? workspace_bytes : 0, need);
+    const size_t rows = (size_t)B * N, e = esize(in_dt), eo = esize(out_dt), sn = (size_t)B * (W - 1) * D;
+    const Buf w[] = {{"dx", dx, rows * D * eo}, {"dweight", dweight, (size_t)D * W * 4}, {"dbias", dbias, (size_t)D * 4},
+                     {"dstate_in", dstate_in, sn * eo}, {"the workspace", workspace, cols ? workspace_bytes : 0}};
+    const Buf r[] = {{"dy", dy, rows * D * e}, {"x", x, ((rows - 1) * x_ld + D) * e, 0, (unsigned)e},
+                     {"weight", weight, (size_t)D * W * 4}, {"bias", bias, (size_t)D * 4}, {"state_in", state_in, sn * e},
+                     {"dstate_out", dstate_out, sn * eo}, {"lengths", lengths, (size_t)B * 4, 0, 4}};
+    if ((st = check_apart(w, r)) != RET_OK) return st;
+    ConvBwdArgs A = {dy, x, weight, bias, state_in, dstate_out, dx, dstate_in, cols ? (float*)workspace : nullptr, lengths,
+                     x_ld, B, N, D, act == RET_ACT_SILU, (int)strips, (int)cblocks, (int)parts};
+    hipStream_t s = (hipStream_t)stream;
+    const Opts op = resolve(opts);
+    {
+        LaunchTimer tm("ret_short_conv_bwd", s, op);
+        hipLaunchKernelGGL(conv_kernels_get(W, vec, in_dt == RET_BF16, out_dt == RET_BF16).bwd,
+                           dim3((unsigned)(cblocks * parts)), dim3(64 * kConvWaves), 0, s, A);
+        tm.done();
+        if ((st = launch_status("ret_short_conv_bwd")) != RET_OK) return st;
+    }
+    if (!cols) return RET_OK;
+    const long long n = (long long)(W + 1) * D;
+    PartSumArgs P = {(const float*)workspace, dweight, dbias, nullptr, n, (long long)W * D, D, (int)parts};
+    LaunchTimer tm("ret_column_sums", s, op);
+    hipLaunchKernelGGL(part_sum_kernel_get(), dim3((unsigned)((n + kColSumCols - 1) / kColSumCols)), dim3(kColSumThreads),
+                       0, s, P);
+    tm.done();
+    return launch_status("ret_column_sums");
+}
+
+ret_status_t ret_short_conv_step(const void* x, int64_t x_ld, const float* weight, const float* bias, void* y, void* state,
+                                 int B, int D, int W, ret_dtype_t in_dt, ret_dtype_t out_dt, int act, void* stream,
+                                 const ret_options_t* opts) {
+    ret_status_t st = check_conv(x, weight, y, B, 1, D, W, &x_ld, in_dt, out_dt, act);
+    if (st != RET_OK) return st;
+    if (!state) return fail(RET_ERR_INVALID_ARG, "null state pointer");
+    const bool vec = conv_vec(x, D, x_ld);
+    const int per = vec ? 2048 : 256;
+    const unsigned long long cblocks = (D + per - 1) / per;
+    if (!grid_fits(cblocks * B, 1, 1, 256))
+        return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d D=%d exceed a launch", B, D);
+    const size_t e = esize(in_dt);
+    const Buf w[] = {{"y", y, (size_t)B * D * esize(out_dt)}, {"state", state, (size_t)B * (W - 1) * D * e}};
+    const Buf r[] = {{"x", x, ((size_t)(B - 1) * x_ld + D) * e, 0, (unsigned)e}, {"weight", weight, (size_t)D * W * 4},
+                     {"bias", bias, (size_t)D * 4}};
+    if ((st = check_apart(w, r)) != RET_OK) return st;
+    ConvStepArgs A = {x, weight, bias, state, y, x_ld, B, D, act == RET_ACT_SILU, (int)cblocks};
+    hipStream_t s = (hipStream_t)stream;
+    const Opts op = resolve(opts);
+    LaunchTimer tm("ret_short_conv_step", s, op);
+    hipLaunchKernelGGL(conv_kernels_get(W, vec, in_dt == RET_BF16, out_dt == RET_BF16).step,
+                       dim3((unsigned)(cblocks * B)), dim3(256), 0, s, A);
+    tm.done();
+    return launch_status("ret_short_conv_step");
+}
+
+}  // extern "C"

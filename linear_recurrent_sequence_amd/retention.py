@@ -20,6 +20,7 @@ from . import build as _build
 
 RET_F32, RET_BF16 = 0, 1
 RET_NORM_SCALE, RET_NORM_DECAY, RET_NORM_SCORES = 1, 2, 4
+RET_ACT_NONE, RET_ACT_SILU = 0, 1
 _STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported", -3: "workspace", -4: "hip error"}
 
 _lib = None
@@ -198,6 +199,31 @@ def load(build_if_missing: bool = True):
     lib.ret_gated_delta_bwd_workspace_bytes.restype = sz
     lib.ret_gated_delta_bwd.argtypes = [vp] * 11 + [i32] * 9 + [fl, vp, vp, vp, vp, vp, sz, vp, op]
     lib.ret_gated_delta_bwd.restype = i32
+    lib.ret_rms_norm_fwd.argtypes = [vp] * 8 + [i32, i64, i32, i32, i32, fl, vp, op]
+    lib.ret_rms_norm_fwd.restype = i32
+    lib.ret_rms_norm_bwd_workspace_bytes.argtypes = [i64, i32]
+    lib.ret_rms_norm_bwd_workspace_bytes.restype = sz
+    lib.ret_rms_norm_bwd.argtypes = [vp] * 7 + [i64, i32, i32, i32, i32, vp, sz, vp, op]
+    lib.ret_rms_norm_bwd.restype = i32
+    lib.ret_short_conv_fwd.argtypes = [vp, i64] + [vp] * 3 + [i32] * 7 + [vp, vp, vp, vp, op]
+    lib.ret_short_conv_fwd.restype = i32
+    lib.ret_short_conv_bwd_workspace_bytes.argtypes = [i32] * 4
+    lib.ret_short_conv_bwd_workspace_bytes.restype = sz
+    lib.ret_short_conv_bwd.argtypes = [vp, vp, i64] + [vp] * 5 + [i32] * 7 + [vp] * 5 + [sz, vp, op]
+    lib.ret_short_conv_bwd.restype = i32
+    lib.ret_short_conv_step.argtypes = [vp, i64] + [vp] * 4 + [i32] * 6 + [vp, op]
+    lib.ret_short_conv_step.restype = i32
+    scan = [vp, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp]
+    lib.ret_selective_scan_workspace_bytes.argtypes = [i32] * 6 + [op]
+    lib.ret_selective_scan_workspace_bytes.restype = sz
+    lib.ret_selective_scan_fwd.argtypes = scan + [vp] + [i32] * 8 + [vp, vp, vp, vp, sz, vp, op]
+    lib.ret_selective_scan_fwd.restype = i32
+    lib.ret_selective_scan_step.argtypes = scan + [vp, vp] + [i32] * 7 + [vp, op]
+    lib.ret_selective_scan_step.restype = i32
+    lib.ret_selective_scan_bwd_workspace_bytes.argtypes = [i32] * 6
+    lib.ret_selective_scan_bwd_workspace_bytes.restype = sz
+    lib.ret_selective_scan_bwd.argtypes = scan + [vp] * 9 + [i32] * 8 + [vp] * 5 + [sz, vp, op]
+    lib.ret_selective_scan_bwd.restype = i32
     lib.ret_options_default.argtypes = [op]
     lib.ret_options_default.restype = None
     lib.ret_timer_create.restype = vp
@@ -895,3 +921,357 @@ def ret_gated_delta_step(q, k, v, g, beta, o, state, scale=None, stream=None, op
                                       _delta_scale(scale), sp, _options(options))
     _check("ret_gated_delta_step", st)
     return o
+
+
+# ---- root-mean-square norm, short convolution, selective scan ----
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _rms_scales(x, group):
+    """The shape of the scales of x [..., D]: one a row, or one for every `group` columns."""
+    return tuple(x.shape[:-1]) + (1 if not group else -(-x.shape[-1] // group),)
+
+
+def ret_rms_norm_fwd(x, y=None, weight=None, eps=1e-5, residual=None, sum_out=None, rstd=None, y8=None, scales=None,
+                     group=None, stream=None, options=None):
+    """y (or y8, or both) <- root-mean-square norm of s = x (+ residual) over the last axis; sum_out <- s; rstd <- the rows'
+    statistic (float32, the shape of x without its last axis). weight: float32 [D] or None. y8 (float8_e4m3fn or uint8, the
+    shape of x) holds y / scales in e4m3; scales float32 [..., 1] with group None, [..., ceil(D / group)] with a group of 32, 64
+    or 128 columns."""
+    lib = load()
+    rows, D = _norm_rows(x)
+    if y is None and y8 is None:
+        raise ValueError("y or y8 must be a tensor")
+    if (y8 is None) != (scales is None):
+        raise ValueError("y8 and scales go together")
+    if group not in (None, 32, 64, 128):
+        raise ValueError("group must be None, 32, 64 or 128, got %r" % (group,))
+    _shape(y, "y", x.shape, _IO)
+    _shape(y8, "y8", x.shape, _E4M3)
+    _shape(scales, "scales", _rms_scales(x, group), (torch.float32,))
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        _shape(t, name, x.shape, (x.dtype,))
+    _shape(weight, "weight", (D,), (torch.float32,))
+    _shape(rstd, "rstd", x.shape[:-1], (torch.float32,))
+    _same_device(x, y, weight, residual, sum_out, rstd, y8, scales)
+    _need_gpu(x, "x")
+    guard, sp, _ = _launch(x, stream, None, None)
+    with guard:
+        st = lib.ret_rms_norm_fwd(_dev(x, "x"), _dev(residual, "residual"), _dev(weight, "weight"), _dev(y, "y"),
+                                  _dev(sum_out, "sum_out"), _dev(rstd, "rstd"), _dev(y8, "y8"), _dev(scales, "scales"),
+                                  group or 0, rows, D, _dt(x), _dt(y) if y is not None else _dt(x), float(eps), sp,
+                                  _options(options))
+    _check("ret_rms_norm_fwd", st)
+    return y if y is not None else y8
+
+
+def rms_norm_bwd_workspace(x):
+    """A workspace of ret_rms_norm_bwd_workspace_bytes for x [..., D]."""
+    rows, D = _norm_rows(x)
+    nbytes = load().ret_rms_norm_bwd_workspace_bytes(rows, D)
+    if nbytes == 0:
+        raise ValueError("rms norm gradients: unsupported shape")
+    return _rows_workspace(nbytes, x.device)
+
+
+def ret_rms_norm_bwd(dy, x, rstd, dx, weight=None, dsum=None, dweight=None, workspace=None, stream=None, options=None):
+    """Gradients of ret_rms_norm_fwd: x is what was normalized (sum_out where there was a residual), rstd its statistic; dx
+    gets dsum (the gradient reaching the sum past the norm) added. dweight: float32 [D] or None. Without a workspace one is
+    allocated for the call."""
+    lib = load()
+    rows, D = _norm_rows(x)
+    for name, t in (("dy", dy), ("dx", dx), ("rstd", rstd)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+    _shape(dy, "dy", x.shape, _IO)
+    _shape(dx, "dx", x.shape, _IO)
+    _shape(dsum, "dsum", x.shape, (dx.dtype,))
+    _shape(rstd, "rstd", x.shape[:-1], (torch.float32,))
+    for name, t in (("weight", weight), ("dweight", dweight)):
+        _shape(t, name, (D,), (torch.float32,))
+    _same_device(dy, x, rstd, dx, weight, dsum, dweight, workspace)
+    _need_gpu(x, "x")
+    make = (lambda: rms_norm_bwd_workspace(x)) if dweight is not None else None
+    guard, sp, workspace = _launch(x, stream, workspace, make)
+    with guard:
+        st = lib.ret_rms_norm_bwd(_dev(dy, "dy"), _dev(x, "x"), _dev(weight, "weight"), _dev(rstd, "rstd"),
+                                  _dev(dsum, "dsum"), _dev(dx, "dx"), _dev(dweight, "dweight"), rows, D, _dt(x), _dt(dy),
+                                  _dt(dx), _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+    _check("ret_rms_norm_bwd", st)
+    return dx
+
+
+def _token_rows(t, name, inner):
+    """(pointer, elements from row to row) of a tensor [rows..., inner axes] whose rows lie evenly apart and are contiguous in
+    themselves: a slice of wider rows, or a whole tensor. inner: the number of axes within a row."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    width, ld, rows = 1, None, 1
+    for size, step in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
+        if size != 1 and step != width:
+            raise ValueError("%s must be contiguous within a row" % name)
+        width *= size
+    for size, step in zip(reversed(t.shape[:-inner]), reversed(t.stride()[:-inner])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = step
+        if step != ld * rows:
+            raise ValueError("the rows of %s must lie evenly apart" % name)
+        rows *= size
+    if ld is None:
+        ld = width
+    if ld < width:
+        raise ValueError("the rows of %s overlap" % name)
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _conv_x(x, weight, bias, nd):
+    """Shapes of x [B, N, D] (a step: [B, D]), weight [D, W] and bias [D]; W."""
+    if not isinstance(x, torch.Tensor) or x.dim() != nd or x.dtype not in _IO:
+        raise ValueError("x must be a float32 or bfloat16 %d-d tensor" % nd)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be a tensor [D, W]")
+    _int_sizes(x, weight)
+    _shape(weight, "weight", (x.shape[-1], weight.shape[1]), (torch.float32,))
+    _shape(bias, "bias", (x.shape[-1],), (torch.float32,))
+    return weight.shape[1]
+
+
+def ret_short_conv_fwd(x, weight, y, bias=None, silu=True, lengths=None, state_in=None, state_out=None, stream=None,
+                       options=None):
+    """y <- the short causal convolution of x [B,N,D] (whole, or a slice of wider rows) with weight [D,W] and bias [D]
+    (float32), through silu if wanted; state_in, state_out [B,W-1,D] in x's dtype: the inputs before the first token and the
+    last ones. lengths: int32 [B] tokens of each sequence on the device, or None."""
+    lib = load()
+    W = _conv_x(x, weight, bias, 3)
+    B, N, D = x.shape
+    if y is None:
+        raise ValueError("y must be a tensor")
+    _shape(y, "y", x.shape, _IO)
+    for name, s in (("state_in", state_in), ("state_out", state_out)):
+        _shape(s, name, (B, W - 1, D), (x.dtype,))
+    _delta_lengths(lengths, B)
+    _same_device(x, weight, y, bias, lengths, state_in, state_out)
+    _need_gpu(x, "x")
+    xp, ld = _token_rows(x, "x", 1)
+    guard, sp, _ = _launch(x, stream, None, None)
+    with guard:
+        st = lib.ret_short_conv_fwd(xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(y, "y"), B, N, D, W, _dt(x),
+                                    _dt(y), RET_ACT_SILU if silu else RET_ACT_NONE, _dev(lengths, "lengths"),
+                                    _dev(state_in, "state_in"), _dev(state_out, "state_out"), sp, _options(options))
+    _check("ret_short_conv_fwd", st)
+    return y
+
+
+def short_conv_bwd_workspace(x, weight):
+    """A workspace of ret_short_conv_bwd_workspace_bytes for x [B,N,D] and weight [D,W]."""
+    _int_sizes(x, weight)
+    nbytes = load().ret_short_conv_bwd_workspace_bytes(*x.shape, weight.shape[1])
+    if nbytes == 0:
+        raise ValueError("short convolution gradients: unsupported shape")
+    return _rows_workspace(nbytes, x.device)
+
+
+def ret_short_conv_bwd(dy, x, weight, dx, dweight=None, bias=None, dbias=None, silu=True, lengths=None, state_in=None,
+                       dstate_out=None, dstate_in=None, workspace=None, stream=None, options=None):
+    """dx, and dweight [D,W], dbias [D] (float32), dstate_in where given <- gradients of sum(dy y) (+ sum(dstate_out
+    state_out)) of ret_short_conv_fwd on the same inputs. The states' gradients have dx's dtype. Without a workspace one is
+    allocated for the call."""
+    lib = load()
+    W = _conv_x(x, weight, bias, 3)
+    B, N, D = x.shape
+    for name, t in (("dy", dy), ("dx", dx)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+    _shape(dy, "dy", x.shape, (x.dtype,))
+    _shape(dx, "dx", x.shape, _IO)
+    _shape(dweight, "dweight", weight.shape, (torch.float32,))
+    _shape(dbias, "dbias", (D,), (torch.float32,))
+    _shape(state_in, "state_in", (B, W - 1, D), (x.dtype,))
+    for name, s in (("dstate_out", dstate_out), ("dstate_in", dstate_in)):
+        _shape(s, name, (B, W - 1, D), (dx.dtype,))
+    _delta_lengths(lengths, B)
+    _same_device(dy, x, weight, dx, dweight, bias, dbias, lengths, state_in, dstate_out, dstate_in, workspace)
+    _need_gpu(x, "x")
+    xp, ld = _token_rows(x, "x", 1)
+    make = (lambda: short_conv_bwd_workspace(x, weight)) if dweight is not None or dbias is not None else None
+    guard, sp, workspace = _launch(x, stream, workspace, make)
+    with guard:
+        st = lib.ret_short_conv_bwd(_dev(dy, "dy"), xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(dx, "dx"),
+                                    _dev(dweight, "dweight"), _dev(dbias, "dbias"), B, N, D, W, _dt(x), _dt(dx),
+                                    RET_ACT_SILU if silu else RET_ACT_NONE, _dev(lengths, "lengths"),
+                                    _dev(state_in, "state_in"), _dev(dstate_out, "dstate_out"),
+                                    _dev(dstate_in, "dstate_in"), _dev(workspace, "workspace"), _nbytes(workspace), sp,
+                                    _options(options))
+    _check("ret_short_conv_bwd", st)
+    return dx
+
+
+def ret_short_conv_step(x, weight, y, state, bias=None, silu=True, stream=None, options=None):
+    """One token of the short convolution: x (whole, or a slice of wider rows), y [B,D]; state [B,W-1,D] in x's dtype, the
+    inputs before it, is moved on in place."""
+    lib = load()
+    W = _conv_x(x, weight, bias, 2)
+    B, D = x.shape
+    if y is None or state is None:
+        raise ValueError("y and state must be tensors")
+    _shape(y, "y", x.shape, _IO)
+    _shape(state, "state", (B, W - 1, D), (x.dtype,))
+    _same_device(x, weight, y, state, bias)
+    _need_gpu(x, "x")
+    xp, ld = _token_rows(x, "x", 1)
+    guard, sp, _ = _launch(x, stream, None, None)
+    with guard:
+        st = lib.ret_short_conv_step(xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(y, "y"),
+                                     _dev(state, "state"), B, D, W, _dt(x), _dt(y),
+                                     RET_ACT_SILU if silu else RET_ACT_NONE, sp, _options(options))
+    _check("ret_short_conv_step", st)
+    return y
+
+
+def _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias, step=False):
+    """Shapes and dtypes of u, dt, z [B, N, D], b, c [B, N, G, S], A [D, S], d_skip, dt_bias [D] (a step: no N axis); G, S."""
+    nd = 2 if step else 3
+    if not isinstance(u, torch.Tensor) or u.dim() != nd or u.dtype not in _IO:
+        raise ValueError("u must be a float32 or bfloat16 %d-d tensor" % nd)
+    if not isinstance(b, torch.Tensor) or b.dim() != nd + 1 or b.shape[:-2] != u.shape[:-1]:
+        raise ValueError("b must be a tensor [%s, G, S]" % ("B" if step else "B, N"))
+    G, S = b.shape[-2:]
+    D = u.shape[-1]
+    for name, t, shape in (("dt", dt, u.shape), ("b", b, b.shape), ("c", c, b.shape)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+        _shape(t, name, shape, (u.dtype,))
+    if A is None:
+        raise ValueError("A must be a tensor")
+    _shape(z, "z", u.shape, (u.dtype,))
+    _shape(A, "A", (D, S), (torch.float32,))
+    for name, t in (("d_skip", d_skip), ("dt_bias", dt_bias)):
+        _shape(t, name, (D,), (torch.float32,))
+    if G == 0 or D % G:
+        raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (D, G))
+    _int_sizes(u, b)
+    return G, S
+
+
+def selective_scan_workspace(u, b, options=None):
+    """A workspace of ret_selective_scan_workspace_bytes for u [B,N,D] and b [B,N,G,S]."""
+    _int_sizes(u, b)
+    B, N, D = u.shape
+    G, S = b.shape[-2:]
+    nbytes = load().ret_selective_scan_workspace_bytes(B, N, D, S, G, _dt(u), _options(options))
+    if nbytes == 0:
+        raise ValueError("selective scan: unsupported shape")
+    return _rows_workspace(nbytes, u.device)
+
+
+def _scan_args(u, dt, A, b, c, d_skip, z, dt_bias):
+    bp, ldb = _token_rows(b, "b", 2)
+    cp, ldc = _token_rows(c, "c", 2)
+    zp, ldz = _token_rows(z, "z", 1)
+    return (_dev(u, "u"), _dev(dt, "dt"), _dev(A, "A"), bp, ldb, cp, ldc, _dev(d_skip, "d_skip"), zp, ldz,
+            _dev(dt_bias, "dt_bias"))
+
+
+def ret_selective_scan_fwd(u, dt, A, b, c, y, d_skip=None, z=None, dt_bias=None, softplus=True, lengths=None,
+                           state_in=None, state_out=None, workspace=None, stream=None, options=None):
+    """y <- the selective scan over u, dt [B,N,D] with A [D,S] (float32), b, c [B,N,G,S], the skip d_skip [D], gated by
+    silu(z); step lengths softplus(dt + dt_bias), or dt + dt_bias without softplus. b, c and z may be slices of wider rows. From
+    state_in [B,D,S] (float32; None: zeros), the final state to state_out. lengths: int32 [B] tokens of each sequence on the
+    device, or None. Without a workspace one is allocated for the call."""
+    lib = load()
+    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias)
+    B, N, D = u.shape
+    if y is None:
+        raise ValueError("y must be a tensor")
+    _shape(y, "y", u.shape, _IO)
+    for name, s in (("state_in", state_in), ("state_out", state_out)):
+        _shape(s, name, (B, D, S), (torch.float32,))
+    _delta_lengths(lengths, B)
+    _same_device(u, dt, A, b, c, y, d_skip, z, dt_bias, lengths, state_in, state_out, workspace)
+    _need_gpu(u, "u")
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    guard, sp, workspace = _launch(u, stream, workspace, lambda: selective_scan_workspace(u, b, options))
+    with guard:
+        st = lib.ret_selective_scan_fwd(*args, _dev(y, "y"), B, N, D, S, G, _dt(u), _dt(y), 1 if softplus else 0,
+                                        _dev(lengths, "lengths"), _dev(state_in, "state_in"),
+                                        _dev(state_out, "state_out"), _dev(workspace, "workspace"), _nbytes(workspace),
+                                        sp, _options(options))
+    _check("ret_selective_scan_fwd", st)
+    return y
+
+
+def ret_selective_scan_step(u, dt, A, b, c, y, state, d_skip=None, z=None, dt_bias=None, softplus=True, stream=None,
+                            options=None):
+    """One token of the selective scan: u, dt, z, y [B,D], b, c [B,G,S]; state [B,D,S] (float32) is updated in place."""
+    lib = load()
+    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias, step=True)
+    B, D = u.shape
+    if y is None or state is None:
+        raise ValueError("y and state must be tensors")
+    _shape(y, "y", u.shape, _IO)
+    _shape(state, "state", (B, D, S), (torch.float32,))
+    _same_device(u, dt, A, b, c, y, state, d_skip, z, dt_bias)
+    _need_gpu(u, "u")
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    guard, sp, _ = _launch(u, stream, None, None)
+    with guard:
+        st = lib.ret_selective_scan_step(*args, _dev(y, "y"), _dev(state, "state"), B, D, S, G, _dt(u), _dt(y),
+                                         1 if softplus else 0, sp, _options(options))
+    _check("ret_selective_scan_step", st)
+    return y
+
+
+def selective_scan_bwd_workspace(u, b):
+    """A workspace of ret_selective_scan_bwd_workspace_bytes for u [B,N,D] and b [B,N,G,S]."""
+    _int_sizes(u, b)
+    B, N, D = u.shape
+    G, S = b.shape[-2:]
+    nbytes = load().ret_selective_scan_bwd_workspace_bytes(B, N, D, S, G, _dt(u))
+    if nbytes == 0:
+        raise ValueError("selective scan gradients: unsupported shape")
+    return _rows_workspace(nbytes, u.device)
+
+
+def ret_selective_scan_bwd(u, dt, A, b, c, dy, du, ddt, dA, db, dc, d_skip=None, dd_skip=None, z=None, dz=None,
+                           dt_bias=None, ddt_bias=None, softplus=True, lengths=None, state_in=None, dstate_out=None,
+                           dstate_in=None, workspace=None, stream=None, options=None):
+    """du, ddt, db, dc, and dA, dd_skip, ddt_bias (float32), dz, dstate_in where given <- gradients of sum(dy y) (+
+    sum(dstate_out state_out)) of ret_selective_scan_fwd on the same inputs. du, ddt, db, dc and dz share one dtype; db and dc
+    are summed over the channels of a group. Without a workspace one is allocated for the call."""
+    lib = load()
+    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias)
+    B, N, D = u.shape
+    for name, t in (("dy", dy), ("du", du), ("ddt", ddt), ("db", db), ("dc", dc)):
+        if t is None:
+            raise ValueError("%s must be a tensor" % name)
+    _shape(dy, "dy", u.shape, (u.dtype,))
+    _shape(du, "du", u.shape, _IO)
+    for name, t, shape in (("ddt", ddt, u.shape), ("dz", dz, u.shape), ("db", db, b.shape), ("dc", dc, b.shape)):
+        _shape(t, name, shape, (du.dtype,))
+    for name, t, shape in (("dA", dA, (D, S)), ("dd_skip", dd_skip, (D,)), ("ddt_bias", ddt_bias, (D,))):
+        _shape(t, name, shape, (torch.float32,))
+    if dz is not None and z is None:
+        raise ValueError("dz without z")
+    if dd_skip is not None and d_skip is None:
+        raise ValueError("dd_skip without d_skip")
+    for name, s in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
+        _shape(s, name, (B, D, S), (torch.float32,))
+    _delta_lengths(lengths, B)
+    _same_device(u, dt, A, b, c, dy, du, ddt, dA, db, dc, d_skip, dd_skip, z, dz, dt_bias, ddt_bias, lengths, state_in,
+                 dstate_out, dstate_in, workspace)
+    _need_gpu(u, "u")
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    guard, sp, workspace = _launch(u, stream, workspace, lambda: selective_scan_bwd_workspace(u, b))
+    with guard:
+        st = lib.ret_selective_scan_bwd(*args, _dev(dy, "dy"), _dev(du, "du"), _dev(ddt, "ddt"), _dev(dA, "dA"),
+                                        _dev(db, "db"), _dev(dc, "dc"), _dev(dd_skip, "dd_skip"), _dev(dz, "dz"),
+                                        _dev(ddt_bias, "ddt_bias"), B, N, D, S, G, _dt(u), _dt(du),
+                                        1 if softplus else 0, _dev(lengths, "lengths"), _dev(state_in, "state_in"),
+                                        _dev(dstate_out, "dstate_out"), _dev(dstate_in, "dstate_in"),
+                                        _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+    _check("ret_selective_scan_bwd", st)
+    return du, ddt, dA, db, dc
