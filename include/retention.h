@@ -587,10 +587,12 @@ ret_status_t ret_short_conv_bwd(const void* dy, const void* x, int64_t x_ld, con
  * ret_selective_scan_fwd computes whole sequences. state_in (NULL: zeros), state_out (NULL: not wanted; may equal state_in),
  * lengths: as in ret_gated_delta_fwd. A NaN or infinity reaches only later tokens of its sequence. workspace:
  * ret_selective_scan_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing one must not
- * overlap in time. Supported: S in {8, 16, 32, 64}, G = 1 or D / G a multiple of 16, D <= 2^26, B N <= 2^36, and no launch of
- * 2^32 work-items (512 a sequence, segment and 16 channels) or 65536 sequences. Written buffers must not overlap others.
+ * overlap in time. Supported: S in {8, 16, 32, 64}, G = 1 or D / G a multiple of 16, D and z_ld, b_ld, c_ld below 2^22, B N <=
+ * 2^36, and no launch of 2^32 work-items (512 a sequence, segment and 16 channels) or 65536 sequences. Written buffers must not overlap others.
  * Pointers: A and the states 16-byte aligned, the others like one of their elements. opts: segments (> 0: segments per sequence
- * that run in parallel) and timer. Kernels: "ret_scan_local", "ret_scan_join", "ret_scan_full".
+ * that run in parallel), variant (1: waves that walk their tokens one by one, 2: workgroups that do chunks of 128 tokens, 32 and
+ * 16 at 32 and 64 states) and timer. Kernels: "ret_scan_local", "ret_scan_join", "ret_scan_walk",
+ * "ret_scan_chunks".
  *
  * ret_selective_scan_step computes one token of every sequence, the state updated in place. Kernel: "ret_scan_step".
  */
@@ -613,8 +615,8 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
  * writes du, ddt [B, N, D] (ddt: that of dt before dt_bias and softplus), db, dc [B, N, G, S] (summed over the channels of a
  * group) in out_dt, contiguous, and, unless NULL, dz (out_dt), dA float[D, S], dd_skip, ddt_bias float[D] and dstate_in. The
  * other arguments are the forward call's. Gradients of the padding past lengths[b] are zero. workspace:
- * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 2048 / S tokens (1024 / S
- * where S > 16), partial sums of db and dc over up to 512 channels and of dA over a chunk). Same limits as the forward. Sums
+ * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 128 tokens (32 and 16 at 32 and
+ * 64 states), partial sums of db and dc over up to 512 channels and of dA over a chunk). Same limits as the forward. Sums
  * have one order: the same call gives the same bits. opts: the timer. Kernels: "ret_scan_local_bwd", "ret_scan_join_bwd",
  * "ret_scan_grad", "ret_scan_sum_bc", "ret_column_sums".
  */

@@ -6,8 +6,8 @@
 
 namespace ret {
 
-// W consecutive values at element offset i. W = 8: 16-byte vectors, for arrays whose rows are all 16-byte aligned;
-// W = 1: any offset.
+// W consecutive values at element offset i. W = 8: 16-byte vectors, for arrays whose rows are all 16-byte aligned; W = 4: half
+// of such a vector in bf16; W = 1: any offset.
 template <int W>
 __device__ __forceinline__ void row_load(const void* p, long long i, bool bf16, float* f) {
     if constexpr (W == 8) {
@@ -26,6 +26,18 @@ __device__ __forceinline__ void row_load(const void* p, long long i, bool bf16, 
                 for (int j = 0; j < 4; ++j) f[e + j] = x[j];
             }
         }
+    } else if constexpr (W == 4) {
+        if (bf16) {
+            const uint2 u = *reinterpret_cast<const uint2*>((const uint16_t*)p + i);
+            f[0] = __uint_as_float(u.x << 16);
+            f[1] = __uint_as_float(u.x & 0xffff0000u);
+            f[2] = __uint_as_float(u.y << 16);
+            f[3] = __uint_as_float(u.y & 0xffff0000u);
+        } else {
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>((const float*)p + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[j] = x[j];
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < W; ++e) f[e] = bf16 ? bf16_to_f32(((const uint16_t*)p)[i + e]) : ((const float*)p)[i + e];
@@ -43,6 +55,9 @@ __device__ __forceinline__ void row_store(void* p, long long i, bool bf16, const
             for (int e = 0; e < 8; e += 4)
                 *reinterpret_cast<f32x4_t*>((float*)p + i + e) = f32x4_t{f[e], f[e + 1], f[e + 2], f[e + 3]};
         }
+    } else if constexpr (W == 4) {
+        if (bf16) store4((uint16_t*)p + i, f32x4_t{f[0], f[1], f[2], f[3]});
+        else store4((float*)p + i, f32x4_t{f[0], f[1], f[2], f[3]});
     } else {
 #pragma unroll
         for (int e = 0; e < W; ++e) {

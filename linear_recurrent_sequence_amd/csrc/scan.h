@@ -5,9 +5,10 @@
 //     y_t = (sum_s C_t[g] h_t + D u_t) silu(z_t)
 //
 // Layout of every sequence kernel: a wave holds 16 channels, four neighbouring lanes a channel, each with SL = S / 4 of its
-// states, and T = 256 / S tokens at a time, so that the T SL decays a_t of a lane are 64 registers whatever S is. The values
-// per token and channel (u, delta, z, y) lie one in a lane: lane q of a channel's four holds tokens 4 i + q, and sums over
-// the states leave each token's in that lane. B and C of a wave's tokens are staged in its own part of the LDS, in fp32.
+// states, and T tokens at a time: 256 / S of them, at most 16, so that the T SL decays a_t of a lane are at most 64 registers.
+// The values per token and channel (u, delta, z, y) lie one in a lane: lane q of a channel's four holds tokens 4 i + q, and
+// sums over the states leave each token's in that lane. B and C of a wave's tokens are staged in its own part of the LDS, in
+// fp32.
 #pragma once
 
 #include "kernels.h"
@@ -17,15 +18,19 @@ namespace ret {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kScanCh = 16;  // channels of a wave
 
-template <int S>
-struct ScanShape {
-    static constexpr int SL = S / 4;            // states a lane
-    static constexpr int T = 256 / S;           // tokens of a wave's block
-    static constexpr int TL = T / 4;            // of which a lane holds the scalars
-    static constexpr int NW = S <= 16 ? 8 : 4;  // waves of a workgroup, neighbouring blocks of tokens
-    static constexpr int CH = NW * T;           // tokens of a workgroup's chunk
+template <int S_, int T_, int NW_>
+struct ScanTile {
+    static constexpr int S = S_;
+    static constexpr int SL = S / 4;   // states a lane
+    static constexpr int T = T_;       // tokens of a wave's block
+    static constexpr int TL = T / 4;   // of which a lane holds the scalars
+    static constexpr int NW = NW_;     // waves of a workgroup, neighbouring blocks of tokens
+    static constexpr int CH = NW * T;  // tokens of a workgroup's chunk
     static constexpr int THREADS = 64 * NW;
+    static_assert(T % 4 == 0 && T * S <= 256, "a wave stages its block's B and C four values a lane");
 };
+template <int S>
+struct ScanShape : ScanTile<S, S < 16 ? 16 : 256 / S, S <= 16 ? 8 : 4> {};
 
 struct ScanArgs {
     const void *u, *dt, *z, *b, *c;      // u, dt [B, N, D]; z rows of ldz; b, c rows of ldb, ldc with [G, S] in each
@@ -36,7 +41,9 @@ struct ScanArgs {
     void* y;                             // [B, N, D]
     float *seg_h, *seg_dt;               // [B][nseg][D][S], [B][nseg][D]
     long long ldz, ldb, ldc;
-    int B, N, D, G, nseg, seg_tokens, cblocks, softplus, bc_vec;
+    int B, N, D, G, nseg, seg_tokens;
+    int cblocks;                         // blocks of 16 channels (walk: of 64)
+    int softplus, bc_vec;                // bc_vec: b and c may be read four values at a time
 };
 
 // One value of either type as fp32.
@@ -56,24 +63,17 @@ __device__ __forceinline__ int scan_length(const int32_t* lengths, int b, int N)
 // turn): n is a multiple of 8.
 __device__ __forceinline__ long long xcd_order(long long id, long long n) { return (id & 7) * (n >> 3) + (id >> 3); }
 
-// log(1 + exp(x)) and its derivative. exp(-|x|) by the hardware 2^x with the rounding of |x| log2(e) made up for;
-// log(1 + e) = 2 atanh(e / (2 + e)) by its series, whose ninth term is below 2e-9 of the sum at e = 1.
+// log(1 + exp(x)) and its derivative. e = exp(-|x|) on the hardware 2^x: its argument's rounding makes it |x| units of 2^-24.
+// log(1 + e) = 2 atanh(r), r = e / (2 + e) <= 1/3: a polynomial of degree 4 in r^2 for atanh(r) / r, fitted for the least
+// largest error on [0, 1/9], which is 4e-9. A NaN comes through e; minus infinity gives 0.
 __device__ __forceinline__ void softplus(float x, float* value, float* slope) {
-    const float m = fabsf(x), t = m * kLog2e;
-    const float rest = fmaf(m, kLog2e, -t) + m * 1.925963033e-8f;  // log2(e) - kLog2e
-    float e = __builtin_amdgcn_exp2f(-t);
-    e = fmaf(e, -kLn2 * rest, e);
-    if (m > 87.f) e = 0.f;
+    const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
     const float r = e * __builtin_amdgcn_rcpf(2.f + e), w = r * r;
-    float p = fmaf(w, 1.f / 15.f, 1.f / 13.f);
-    p = fmaf(w, p, 1.f / 11.f);
-    p = fmaf(w, p, 1.f / 9.f);
-    p = fmaf(w, p, 1.f / 7.f);
-    p = fmaf(w, p, 1.f / 5.f);
-    p = fmaf(w, p, 1.f / 3.f);
+    float p = fmaf(w, 0.14095773673944728f, 0.13978833207656793f);
+    p = fmaf(w, p, 0.2001255710881801f);
+    p = fmaf(w, p, 0.33333155074914933f);
     p = fmaf(w, p, 1.f);
-    *value = (x > 0.f ? x : 0.f) + 2.f * r * p;
-    if (x != x) *value = x;
+    *value = fmaf(2.f * r, p, x > 0.f ? x : 0.f);
     const float s = __builtin_amdgcn_rcpf(1.f + e);
     *slope = x > 0.f ? s : e * s;
 }
@@ -89,10 +89,10 @@ __device__ __forceinline__ float decay_rate(float A) {
     return r < -3.4e38f ? -3.4e38f : r > 3.4e38f ? 3.4e38f : r;
 }
 
-// The value that lane K of every four holds.
+// The value that lane K of every four holds. In the form that the compiler can make a part of the instruction that uses it.
 template <int K>
 __device__ __forceinline__ float quad_of(float v) {
-    return dpp_mov<K * 0x55>(v);
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), K * 0x55, 0xf, 0xf, true));
 }
 __device__ __forceinline__ float quad_of(float v, int k) {  // k a constant after unrolling
     return k == 0 ? quad_of<0>(v) : k == 1 ? quad_of<1>(v) : k == 2 ? quad_of<2>(v) : quad_of<3>(v);
@@ -105,76 +105,130 @@ __device__ __forceinline__ float quad_sums(float v0, float v1, float v2, float v
     return (high ? b : a) + dpp_mov<0x4e>(high ? a : b);
 }
 
-// Four neighbouring values.
+// Values as they lie in memory, so that a load is not waited for before its values are used. off: bytes.
 template <class E>
-__device__ __forceinline__ void load4(const void* p, long long i, bool vec, float* f) {
-    typedef typename E::st st;
-    if (vec) {
-        if constexpr (sizeof(st) == 2) {
-            const uint2 w = *reinterpret_cast<const uint2*>((const uint16_t*)p + i);
-            f[0] = __uint_as_float(w.x << 16);
-            f[1] = __uint_as_float(w.x & 0xffff0000u);
-            f[2] = __uint_as_float(w.y << 16);
-            f[3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
-            const f32x4_t w = *reinterpret_cast<const f32x4_t*>((const float*)p + i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = w[e];
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = at<E>(p, i + e);
+struct Raw;
+template <>
+struct Raw<BF16> {
+    typedef uint32_t one;  // a bf16 value in the low half
+    typedef uint2 four;
+    static __device__ __forceinline__ one get(const char* p, uint32_t off) { return *(const uint16_t*)(p + off); }
+    static __device__ __forceinline__ float value(one r) { return __uint_as_float(r << 16); }
+    static __device__ __forceinline__ four get4(const char* p, uint32_t off, bool vec) {
+        const uint16_t* q = (const uint16_t*)(p + off);
+        if (vec) return *reinterpret_cast<const uint2*>(q);
+        return make_uint2(q[0] | (uint32_t)q[1] << 16, q[2] | (uint32_t)q[3] << 16);
     }
-}
+    static __device__ __forceinline__ f32x4_t values(four w) {
+        return f32x4_t{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u)};
+    }
+};
+template <>
+struct Raw<F32> {
+    typedef float one;
+    typedef f32x4_t four;
+    static __device__ __forceinline__ one get(const char* p, uint32_t off) { return *(const float*)(p + off); }
+    static __device__ __forceinline__ float value(one r) { return r; }
+    static __device__ __forceinline__ four get4(const char* p, uint32_t off, bool vec) {
+        const float* q = (const float*)(p + off);
+        if (vec) return *reinterpret_cast<const f32x4_t*>(q);
+        return f32x4_t{q[0], q[1], q[2], q[3]};
+    }
+    static __device__ __forceinline__ f32x4_t values(four w) { return w; }
+};
 
-// Reads u and dt of the lane's tokens (any in-range row where a token is past the end).
-template <class E, int S>
-__device__ __forceinline__ void load_scalars(const void* p, long long row0, long long ld, int N, int t0, int q, int d,
-                                             float (&f)[ScanShape<S>::TL]) {
-#pragma unroll
-    for (int i = 0; i < ScanShape<S>::TL; ++i) {
-        const int t = t0 + 4 * i + q;
-        f[i] = at<E>(p, (row0 + (t < N ? t : N - 1)) * ld + d);
+// Where a wave's block of tokens lies in an array of rows: one address for the wave and 24-bit products for its lanes, so that
+// rows of at most kScanMaxLd elements have 32-bit offsets. Tokens past the end are read as the last one; whoever uses them
+// leaves those from n on out.
+constexpr int64_t kScanMaxLd = (1 << 22) - 1;
+struct ScanRows {
+    long long row;  // of the block's first token
+    int last;       // the last token of the block that there is
+    __device__ __forceinline__ ScanRows(long long row0, int t0, int N) {
+        const int t = t0 < N ? t0 : N - 1;
+        row = row0 + t;
+        last = N - 1 - t;
     }
-}
-// The lane's part of B or C: 4 neighbouring values of the wave's [T][S], zero from token n on.
-template <class E, int S>
-__device__ __forceinline__ void load_bc(const void* p, long long row0, long long ld, int N, int n, int t0, int g, int lane,
-                                        bool vec, float (&f)[4]) {
-    const int t = t0 + 4 * lane / S;
-    load4<E>(p, (row0 + (t < N ? t : N - 1)) * ld + g * S + 4 * lane % S, vec, f);
-    if (t >= n)
+    template <class E>
+    __device__ __forceinline__ const char* base(const void* p, long long ld) const {
+        return (const char*)p + row * ld * (int)sizeof(typename E::st);
+    }
+    template <class E>
+    __device__ __forceinline__ uint32_t off(int k, long long ld, int col) const {
+        const uint32_t e = sizeof(typename E::st);
+        return __umul24(k < last ? k : last, (uint32_t)ld * e) + col * e;
+    }
+};
+// The lane's tokens 4 i + q of channel d.
+template <class E, class P>
+__device__ __forceinline__ void load_scalars(const ScanRows& r, const void* p, long long ld, int q, int d,
+                                             typename Raw<E>::one (&f)[P::TL]) {
+    const char* base = r.base<E>(p, ld);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = 0.f;
+    for (int i = 0; i < P::TL; ++i) f[i] = Raw<E>::get(base, r.off<E>(4 * i + q, ld, d));
+}
+// Outputs of the lane's tokens 4 i + q of channel d, those before `end` tokens of the block.
+template <class O, class P>
+__device__ __forceinline__ void store_scalars(void* p, long long row, long long D, int end, int q, int d,
+                                              const float (&f)[P::TL]) {
+    typedef typename O::st st;
+    char* base = (char*)p + row * D * (int)sizeof(st);
+#pragma unroll
+    for (int i = 0; i < P::TL; ++i)
+        if (4 * i + q < end)
+            store_out((st*)(base + (__umul24(4 * i + q, (uint32_t)D * (uint32_t)sizeof(st)) + d * (uint32_t)sizeof(st))), f[i]);
+}
+// The lane's four values of the block's [T][S] of b or c ...
+template <class E, class P>
+__device__ __forceinline__ typename Raw<E>::four load_bc(const ScanRows& r, const void* p, long long ld, int g, int lane,
+                                                         bool vec) {
+    return Raw<E>::get4(r.base<E>(p, ld), r.off<E>(4 * lane / P::S, ld, g * P::S + 4 * lane % P::S), vec);
+}
+// ... to LDS in fp32, zeros from token n on.
+template <class E, class P>
+__device__ __forceinline__ void put_bc(float* lds, typename Raw<E>::four r, int n, int t0, int lane) {
+    const f32x4_t v = Raw<E>::values(r);
+    if (4 * lane < P::T * P::S)
+        *reinterpret_cast<f32x4_t*>(lds + 4 * lane) = t0 + 4 * lane / P::S < n ? v : f32x4_t{0.f, 0.f, 0.f, 0.f};
 }
 
 // Keeps a wave's LDS accesses on either side of it in order: they are carried out in the order they are issued.
 __device__ __forceinline__ void lds_order() { __asm__ volatile("" ::: "memory"); }
 
-// A wave's block: dt and dt u of the lane's tokens (0 from token n on: such a token changes nothing), B and C to LDS.
+// A wave's block of tokens: loaded one block ahead, then steps().
 template <class E, int S>
 struct ScanBlock {
     typedef ScanShape<S> P;
-    float u[P::TL], dt[P::TL], z[P::TL], b[4], c[4];
-    __device__ __forceinline__ void load(const ScanArgs& a, long long row0, int n, int t0, int q, int lane, int d, int g,
-                                         bool out) {
-        load_scalars<E, S>(a.u, row0, a.D, a.N, t0, q, d, u);
-        load_scalars<E, S>(a.dt, row0, a.D, a.N, t0, q, d, dt);
-        if (out && a.z) load_scalars<E, S>(a.z, row0, a.ldz, a.N, t0, q, d, z);
-        load_bc<E, S>(a.b, row0, a.ldb, a.N, n, t0, g, lane, a.bc_vec, b);
-        if (out) load_bc<E, S>(a.c, row0, a.ldc, a.N, n, t0, g, lane, a.bc_vec, c);
+    typedef Raw<E> R;
+    typename R::one u[P::TL], dt[P::TL], z[P::TL];
+    typename R::four b, c;
+    __device__ __forceinline__ void load(const ScanArgs& a, long long row0, int t0, int q, int lane, int d, int g, bool out) {
+        const ScanRows r(row0, t0, a.N);
+        load_scalars<E, P>(r, a.u, a.D, q, d, u);
+        load_scalars<E, P>(r, a.dt, a.D, q, d, dt);
+        if (out && a.z) load_scalars<E, P>(r, a.z, a.ldz, q, d, z);
+        b = load_bc<E, P>(r, a.b, a.ldb, g, lane, a.bc_vec);
+        if (out) c = load_bc<E, P>(r, a.c, a.ldc, g, lane, a.bc_vec);
     }
-    // dt becomes the length of the step, du its product with u
-    __device__ __forceinline__ void steps(const ScanArgs& a, float bias, int n, int t0, int q, float (&du)[P::TL]) {
+    // The lane's step lengths, and their products with u; 0 from token n on: such a token changes nothing.
+    __device__ __forceinline__ void steps(const ScanArgs& a, float bias, int n, int t0, int q, float (&step)[P::TL],
+                                          float (&us)[P::TL], float (&du)[P::TL]) const {
+        float s;
 #pragma unroll
         for (int i = 0; i < P::TL; ++i) {
-            float v = dt[i] + bias, s;
-            if (a.softplus) softplus(v, &v, &s);
-            const bool live = t0 + 4 * i + q < n;
-            dt[i] = live ? v : 0.f;
-            u[i] = live ? u[i] : 0.f;
-            du[i] = dt[i] * u[i];
+            us[i] = R::value(u[i]);
+            step[i] = R::value(dt[i]) + bias;
         }
+        if (a.softplus)
+#pragma unroll
+            for (int i = 0; i < P::TL; ++i) softplus(step[i], &step[i], &s);
+        if (t0 + P::T > n)
+#pragma unroll
+            for (int i = 0; i < P::TL; ++i)
+                if (t0 + 4 * i + q >= n) step[i] = us[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < P::TL; ++i) du[i] = step[i] * us[i];
     }
 };
 
@@ -193,6 +247,14 @@ __device__ __forceinline__ void lds_vec(const float* p, float (&f)[SL]) {
         }
     }
 }
+// GT tokens of a wave's [T][S] in LDS from token k: the lane's states. Read one group ahead of its use, with an lds_order()
+// after each group: the compiler would otherwise ask for all of a block at once and run out of registers.
+template <int S, int GT>
+__device__ __forceinline__ void lds_group(const float* p, int k, int q, float (&f)[GT][S / 4]) {
+#pragma unroll
+    for (int e = 0; e < GT; ++e) lds_vec<S / 4>(p + (k + e) * S + q * (S / 4), f[e]);
+}
+
 // Values of a lane in an exchange buffer: [SL / 4][64][4] (SL = 2: [64][2]), so that a wave's accesses are contiguous.
 template <int SL>
 __device__ __forceinline__ void ex_put(float* p, int lane, const float (&f)[SL]) {
@@ -222,6 +284,12 @@ __device__ __forceinline__ void state_get(const float* p, float (&f)[SL]) {  // 
     for (int j = 0; j < SL; ++j) f[j] = p[j];
 }
 
+template <int SL>
+__device__ __forceinline__ void state_put(float* p, const float (&f)[SL]) {
+#pragma unroll
+    for (int j = 0; j < SL; ++j) p[j] = f[j];
+}
+
 struct ScanPos {
     int cb, seg, b;
 };
@@ -236,9 +304,10 @@ __device__ __forceinline__ bool scan_pos(const ScanArgs& a, ScanPos* p) {
 
 typedef void (*scan_kernel_t)(ScanArgs);
 struct ScanKernels {
-    scan_kernel_t local, join, full;
-    int chunk, threads;  // tokens of a workgroup's chunk and threads of local and full
+    scan_kernel_t local, join, walk, chunks;  // local and walk: 4 waves a workgroup, each its own block of 16 channels
+    int block, chunk, threads;                // tokens of a wave's block; tokens of a chunk and threads of chunks
 };
+constexpr int kWalkWaves = 4;
 bool scan_kernels_get(bool bf16_in, bool bf16_out, int S, ScanKernels* o);
 
 }  // namespace ret

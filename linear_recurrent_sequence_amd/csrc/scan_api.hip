@@ -1,6 +1,8 @@
 // Entry points of the selective scan: argument checks, segment plan, workspace layout, launches.
 #include <string.h>
 
+#include <algorithm>
+
 #include "host.h"
 #include "rows.h"
 #include "scan_bwd.h"
@@ -29,7 +31,7 @@ ret_status_t check_shape(const Shape& s, ret_dtype_t in_dt, ret_dtype_t out_dt) 
     if (s.G > 1 && s.D / s.G % kScanCh)
         return fail(RET_ERR_UNSUPPORTED, "selective scan: groups of %d channels are not a multiple of %d", s.D / s.G,
                     kScanCh);
-    if ((long long)s.B * s.N > 1LL << 36 || s.D > 1 << 26 || s.N > INT32_MAX - 1024)
+    if ((long long)s.B * s.N > 1LL << 36 || s.D > kScanMaxLd || s.N > INT32_MAX - 1024)
         return fail(RET_ERR_UNSUPPORTED, "selective scan: B=%d N=%d D=%d too large", s.B, s.N, s.D);
     return RET_OK;
 }
@@ -46,8 +48,8 @@ ret_status_t check_rows(const Shape& s, Rows* r) {
     if (r->z < s.D || r->b < gs || r->c < gs)
         return fail(RET_ERR_INVALID_ARG, "rows of z, b or c (%lld, %lld, %lld apart) are shorter than they are wide",
                     (long long)r->z, (long long)r->b, (long long)r->c);
-    if (r->z > 1LL << 32 || r->b > 1LL << 32 || r->c > 1LL << 32)
-        return fail(RET_ERR_UNSUPPORTED, "rows of z, b or c too far apart");
+    if (r->z > kScanMaxLd || r->b > kScanMaxLd || r->c > kScanMaxLd)
+        return fail(RET_ERR_UNSUPPORTED, "rows of z, b or c are more than %lld elements apart", (long long)kScanMaxLd);
     return RET_OK;
 }
 size_t span(size_t rows, int64_t ld, int64_t width, size_t e) { return ((rows - 1) * ld + width) * e; }
@@ -57,22 +59,43 @@ bool vectors(const void* b, const void* c, const Rows& r, ret_dtype_t dt) {
     return (uintptr_t)b % a == 0 && (uintptr_t)c % a == 0 && r.b % 4 == 0 && r.c % 4 == 0;
 }
 
-// Segments a sequence. One where the sequences' blocks of 16 channels fill the card; more cost the segments' local pass.
+// How a sequence is cut up. Measured nanoseconds a token (bf16, with gate and skip), w the sequences' blocks of 16 channels:
+// waves that walk a sequence whole take `walk` each and, all together, walk_all w; workgroups on chunks take `chunk` while the
+// card holds them all (chunk_wgs), more in proportion; segments, which go over the tokens twice and start three kernels, take
+// 22 us and seg_all w. The least of the three. Examples at 16 states, us (walk, chunks, segments): 512 tokens of 8192 channels
+// 65, 38, 47; 8192 of 1024 992, 247, 84; 8192 of 4096 1012, 257, 260; 4 x 512 of 8192 100, 138, 142.
+struct Cost {
+    float walk, walk_all, chunk, chunk_wgs, seg_all;
+};
+constexpr Cost kCost[4] = {{99.f, 0.070f, 23.f, 310.f, 0.085f},   // 8 states
+                           {122.f, 0.095f, 30.f, 230.f, 0.117f},  // 16
+                           {200.f, 0.149f, 78.f, 400.f, 0.186f},  // 32
+                           {370.f, 0.258f, 155.f, 378.f, 0.325f}};  // 64
+constexpr int kSegWaves = 8192, kSegLeast = 64;  // waves that the segments are for (8 a SIMD), tokens of a segment at least
+
 struct Plan {
-    int nchunks, nseg, seg_chunks, cblocks;
+    bool walk;
+    int nseg, seg_tokens, cblocks, wblocks;
     size_t seg_dt, bytes;
 };
-Plan make_plan(const Shape& s, int chunk, const Opts& op) {
+Plan make_plan(const Shape& s, const ScanKernels& k, const Opts& op) {
     Plan p;
     p.cblocks = (s.D + kScanCh - 1) / kScanCh;
-    p.nchunks = (s.N + chunk - 1) / chunk;
-    const long long units = (long long)s.B * p.cblocks;
-    long long n = op.segments > 0 ? op.segments : 512 / units;
-    if (op.segments <= 0 && n > p.nchunks / 2) n = p.nchunks / 2;
-    if (n > p.nchunks) n = p.nchunks;
+    p.wblocks = (p.cblocks + kWalkWaves - 1) / kWalkWaves;
+    const double w = (double)s.B * p.cblocks;
+    const Cost& c = kCost[s.S == 8 ? 0 : s.S == 16 ? 1 : s.S == 32 ? 2 : 3];
+    const double walk = s.N * std::max<double>(c.walk, c.walk_all * w);
+    const double chunk = s.N * (double)c.chunk * std::max(1.0, w / c.chunk_wgs);
+    const double seg = 22000.0 + s.N * c.seg_all * w;
+    const bool split = op.segments > 1 || (op.segments == 0 && seg < std::min(walk, chunk));
+    p.walk = op.variant == 1 || (op.variant != 2 && (split || walk <= chunk));
+    const int unit = p.walk ? k.block : k.chunk, units = (s.N + unit - 1) / unit;
+    long long n = op.segments > 0 ? op.segments : split ? std::min<long long>((long long)(kSegWaves / w), s.N / kSegLeast) : 1;
+    if (n > units) n = units;
     if (n < 1) n = 1;
-    p.seg_chunks = (int)((p.nchunks + n - 1) / n);
-    p.nseg = (p.nchunks + p.seg_chunks - 1) / p.seg_chunks;
+    const int per = (int)((units + n - 1) / n);
+    p.seg_tokens = per * unit;
+    p.nseg = (units + per - 1) / per;
     const size_t ds = (size_t)s.B * p.nseg * s.D;
     p.seg_dt = p.nseg > 1 ? round256(ds * s.S * 4) : 0;
     p.bytes = p.seg_dt + (p.nseg > 1 ? round256(ds * 4) : 256);
@@ -82,7 +105,7 @@ Plan make_plan(const Shape& s, int chunk, const Opts& op) {
 // Chunks of the gradients, and blocks of channels that a workgroup does one after another: the more, the smaller the partial
 // sums of dB and dC, while about four workgroups a CU are left.
 struct BwdPlan {
-    int nchunks, run, blocks_g, parts_g, cblocks;
+    int nchunks, blocks_g, parts_g, cblocks;
     size_t seg_g, seg_dt, part_a, part_bc, bytes;
 };
 BwdPlan make_bwd_plan(const Shape& s, int chunk) {
@@ -95,8 +118,6 @@ BwdPlan make_bwd_plan(const Shape& s, int chunk) {
     run = run < 1 ? 1 : run > 32 ? 32 : run;
     if (run > p.blocks_g) run = p.blocks_g;
     p.parts_g = (int)((p.blocks_g + run - 1) / run);
-    p.run = (p.blocks_g + p.parts_g - 1) / p.parts_g;
-    p.parts_g = (p.blocks_g + p.run - 1) / p.run;
     const size_t dk = (size_t)s.B * p.nchunks * s.D;
     p.seg_g = round256(dk * s.S * 4);
     p.seg_dt = p.seg_g + round256(dk * s.S * 4);
@@ -109,23 +130,24 @@ BwdPlan make_bwd_plan(const Shape& s, int chunk) {
 unsigned long long by8(unsigned long long n) { return (n + 7) / 8 * 8; }
 
 struct Grids {
-    unsigned long long units, join, grad, bc;
+    unsigned long long local, units, join, grad, bc;
 };
 ret_status_t fits(const Shape& s, bool ok) {
     if (ok) return RET_OK;
     return fail(RET_ERR_UNSUPPORTED, "selective scan: B=%d N=%d D=%d S=%d exceed a launch", s.B, s.N, s.D, s.S);
 }
-ret_status_t fwd_grids(const Shape& s, const Plan& p, int threads, Grids* g) {
-    g->units = by8((unsigned long long)p.cblocks * p.nseg * s.B);
+ret_status_t fwd_grids(const Shape& s, const Plan& p, const ScanKernels& k, Grids* g) {
+    g->local = by8((unsigned long long)p.wblocks * p.nseg * s.B);
+    g->units = p.walk ? g->local : by8((unsigned long long)p.cblocks * p.nseg * s.B);
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
-    return fits(s, grid_fits(g->units, 1, 1, threads) && (p.nseg == 1 || grid_fits(g->join, s.B, 1, 256)));
+    return fits(s, grid_fits(g->local, 1, 1, 64 * kWalkWaves) && grid_fits(g->units, 1, 1, p.walk ? 64 * kWalkWaves : k.threads) &&
+                       (p.nseg == 1 || grid_fits(g->join, s.B, 1, 256)));
 }
 ret_status_t bwd_grids(const Shape& s, const BwdPlan& p, int threads, Grids* g) {
-    g->units = by8((unsigned long long)p.cblocks * p.nchunks * s.B);
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
     g->grad = by8((unsigned long long)p.parts_g * s.G * p.nchunks * s.B);
     g->bc = ((unsigned long long)s.B * s.N * 2 * s.S + 255) / 256;
-    return fits(s, grid_fits(g->units, 1, 1, threads) && grid_fits(g->join, s.B, 2, 256) &&
+    return fits(s, grid_fits(g->join, s.B, 2, 256) &&
                        grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc, s.G, 1, 256) &&
                        grid_fits(((unsigned long long)s.D * (s.S + 2) + kColSumCols - 1) / kColSumCols, 1, 1, kColSumThreads) &&
                        (long long)p.nchunks * s.B <= INT32_MAX / 2);
@@ -153,8 +175,8 @@ size_t ret_selective_scan_workspace_bytes(int B, int N, int D, int S, int G, ret
     ScanKernels k;
     Grids g;
     if (check_shape(s, in_dt, RET_F32) != RET_OK || !scan_kernels_get(in_dt == RET_BF16, false, S, &k)) return 0;
-    const Plan p = make_plan(s, k.chunk, resolve(opts));
-    return fwd_grids(s, p, k.threads, &g) == RET_OK ? p.bytes : 0;
+    const Plan p = make_plan(s, k, resolve(opts));
+    return fwd_grids(s, p, k, &g) == RET_OK ? p.bytes : 0;
 }
 
 ret_status_t ret_selective_scan_fwd(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,
@@ -171,9 +193,9 @@ ret_status_t ret_selective_scan_fwd(const void* u, const void* dt, const float* 
     ScanKernels k;
     scan_kernels_get(in_dt == RET_BF16, out_dt == RET_BF16, S, &k);
     const Opts op = resolve(opts);
-    const Plan p = make_plan(s, k.chunk, op);
+    const Plan p = make_plan(s, k, op);
     Grids g;
-    if ((st = fwd_grids(s, p, k.threads, &g)) != RET_OK) return st;
+    if ((st = fwd_grids(s, p, k, &g)) != RET_OK) return st;
     const size_t rows = (size_t)B * N, e = esize(in_dt), sb = (size_t)B * D * S * 4, gs = (size_t)G * S;
     const unsigned ei = e, eo = esize(out_dt);
     const bool split = p.nseg > 1;
@@ -195,14 +217,16 @@ ret_status_t ret_selective_scan_fwd(const void* u, const void* dt, const float* 
     a.state_in = state_in, a.state_out = state_out, a.y = y;
     a.seg_h = (float*)workspace, a.seg_dt = (float*)((char*)workspace + p.seg_dt);
     a.ldz = ld.z, a.ldb = ld.b, a.ldc = ld.c;
-    a.B = B, a.N = N, a.D = D, a.G = G, a.nseg = p.nseg, a.seg_tokens = p.seg_chunks * k.chunk, a.cblocks = p.cblocks;
+    a.B = B, a.N = N, a.D = D, a.G = G, a.nseg = p.nseg, a.seg_tokens = p.seg_tokens, a.cblocks = p.wblocks;
     a.softplus = softplus != 0, a.bc_vec = vectors(b, c, ld, in_dt);
     hipStream_t sm = (hipStream_t)stream;
     if (split) {
-        if ((st = launch("ret_scan_local", k.local, dim3((unsigned)g.units), k.threads, sm, op, a)) != RET_OK) return st;
+        if ((st = launch("ret_scan_local", k.local, dim3((unsigned)g.local), 64 * kWalkWaves, sm, op, a)) != RET_OK) return st;
         if ((st = launch("ret_scan_join", k.join, dim3((unsigned)g.join, B), 256, sm, op, a)) != RET_OK) return st;
     }
-    return launch("ret_scan_full", k.full, dim3((unsigned)g.units), k.threads, sm, op, a);
+    if (p.walk) return launch("ret_scan_walk", k.walk, dim3((unsigned)g.units), 64 * kWalkWaves, sm, op, a);
+    a.cblocks = p.cblocks;
+    return launch("ret_scan_chunks", k.chunks, dim3((unsigned)g.units), k.threads, sm, op, a);
 }
 
 ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,
@@ -217,7 +241,11 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
     if (!u || !dt || !A || !b || !c || !y || !state) return fail(RET_ERR_INVALID_ARG, "null u/dt/A/b/c/y/state pointer");
     const int per = 1024 / S;
     const unsigned long long blocks = (D + per - 1) / per;
-    if ((st = fits(s, grid_fits(blocks * B, 1, 1, 256))) != RET_OK) return st;
+    // several sequences a workgroup while enough workgroups are left
+    int seqs = 1;
+    while (seqs < kScanStepSeqs && blocks * ((B + 2 * seqs - 1) / (2 * seqs)) >= kScanStepWgs) seqs *= 2;
+    const unsigned long long wgs = blocks * ((B + seqs - 1) / seqs);
+    if ((st = fits(s, grid_fits(wgs, 1, 1, 256))) != RET_OK) return st;
     const size_t n = (size_t)B * D, e = esize(in_dt), gs = (size_t)G * S;
     const unsigned ei = e, eo = esize(out_dt);
     const Buf w[] = {{"y", y, n * eo, 0, eo}, {"state", state, n * S * 4}};
@@ -226,10 +254,10 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
                      {"d_skip", d_skip, (size_t)D * 4, 0, 4}, {"z", z, z ? span(B, ld.z, D, e) : 0, 0, ei},
                      {"dt_bias", dt_bias, (size_t)D * 4, 0, 4}};
     if ((st = check_apart(w, r)) != RET_OK) return st;
-    ScanStepArgs a = {u, dt, z, b, c, A, d_skip, dt_bias, state, y, ld.z, ld.b, ld.c, B, D, G, (int)blocks, softplus != 0,
+    ScanStepArgs a = {u, dt, z, b, c, A, d_skip, dt_bias, state, y, ld.z, ld.b, ld.c, B, D, G, (int)blocks, seqs, softplus != 0,
                       vectors(b, c, ld, in_dt)};
     return launch("ret_scan_step", scan_step_kernel_get(in_dt == RET_BF16, out_dt == RET_BF16, S),
-                  dim3((unsigned)(blocks * B)), 256, (hipStream_t)stream, resolve(opts), a);
+                  dim3((unsigned)wgs), 256, (hipStream_t)stream, resolve(opts), a);
 }
 
 size_t ret_selective_scan_bwd_workspace_bytes(int B, int N, int D, int S, int G, ret_dtype_t in_dt) {
@@ -238,7 +266,7 @@ size_t ret_selective_scan_bwd_workspace_bytes(int B, int N, int D, int S, int G,
     Grids g;
     if (check_shape(s, in_dt, RET_F32) != RET_OK || !scan_bwd_kernels_get(in_dt == RET_BF16, false, S, &k)) return 0;
     const BwdPlan p = make_bwd_plan(s, k.chunk);
-    return bwd_grids(s, p, k.threads, &g) == RET_OK ? p.bytes : 0;
+    return bwd_grids(s, p, 64 * k.waves, &g) == RET_OK ? p.bytes : 0;
 }
 
 ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,
@@ -261,7 +289,7 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     const Opts op = resolve(opts);
     const BwdPlan p = make_bwd_plan(s, k.chunk);
     Grids g;
-    if ((st = bwd_grids(s, p, k.threads, &g)) != RET_OK) return st;
+    if ((st = bwd_grids(s, p, 64 * k.waves, &g)) != RET_OK) return st;
     const size_t rows = (size_t)B * N, e = esize(in_dt), sb = (size_t)B * D * S * 4, gs = (size_t)G * S, nd = (size_t)D * 4;
     const unsigned ei = e, eo = esize(out_dt);
     const Buf w[] = {{"du", du, rows * D * eo, 0, eo}, {"ddt", ddt, rows * D * eo, 0, eo}, {"dA", dA, nd * S, 0, 4},
@@ -288,11 +316,11 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     a.dy = dy, a.dstate_out = dstate_out, a.dstate_in = dstate_in;
     a.seg_g = (float*)((char*)workspace + p.seg_g);
     a.part_a = (float*)((char*)workspace + p.part_a), a.part_bc = (float*)((char*)workspace + p.part_bc);
-    a.du = du, a.ddt = ddt, a.dz = dz, a.db = db, a.dc = dc, a.run = p.run, a.parts_g = p.parts_g;
+    a.du = du, a.ddt = ddt, a.dz = dz, a.db = db, a.dc = dc, a.parts_g = p.parts_g;
     hipStream_t sm = (hipStream_t)stream;
-    if ((st = launch("ret_scan_local_bwd", k.local, dim3((unsigned)g.units), k.threads, sm, op, a)) != RET_OK) return st;
+    if ((st = launch("ret_scan_local_bwd", k.local, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
     if ((st = launch("ret_scan_join_bwd", k.join, dim3((unsigned)g.join, B, 2), 256, sm, op, a)) != RET_OK) return st;
-    if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)g.grad), k.threads, sm, op, a)) != RET_OK) return st;
+    if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
     if ((st = launch("ret_scan_sum_bc", k.sum_bc, dim3((unsigned)g.bc, G), 256, sm, op, a)) != RET_OK) return st;
     if (!dA && !dd_skip && !ddt_bias) return RET_OK;
     const long long n = (long long)D * (S + 2);

@@ -14,12 +14,12 @@ struct ScanBwdArgs {
     float* part_bc;                            // [parts][B N][2][S]: sums over a workgroup's channels of dB, dC
     float* part_a;                             // [B nseg][D (S + 2)]: dA, dskip, dbias
     void *du, *ddt, *dz, *db, *dc;             // dz or null
-    int run, parts_g;                          // channel blocks a workgroup, parts a group of channels
+    int parts_g;                               // parts a group of channels, each every parts_g-th block of 16
 };
 typedef void (*scan_bwd_kernel_t)(ScanBwdArgs);
 struct ScanBwdKernels {
     scan_bwd_kernel_t local, join, grad, sum_bc;
-    int chunk, threads;
+    int chunk, waves;
 };
 bool scan_bwd_kernels_get(bool bf16_in, bool bf16_out, int S, ScanBwdKernels* o);
 

@@ -9,7 +9,7 @@
 // waves' blocks joined through LDS both ways, the states kept in 64 more, then the tokens in reverse.
 //
 // dB and dC are sums over all channels. A wave adds its 16 channels up by halving exchanges, 8 values at a time (16
-// instructions for 8 values where separate sums would take 32), keeps one register for each of its 16 groups of 8 over the
+// instructions for 8 values where separate sums would take 32), keeps one register for each of its groups of 8 over the
 // `run` blocks of channels that its workgroup does one after another, and leaves them as partial sums for sum_bc. Every sum
 // has one order.
 #include "scan_bwd.h"
@@ -17,6 +17,9 @@
 namespace ret {
 
 namespace {
+
+template <int S>
+struct GradShape : ScanShape<S> {};
 
 // Sums of 8 values over the lanes of equal q (lane & 3): after the exchanges the lanes of equal bits 3..5 hold value
 // 4 bit5 + 2 bit4 + bit3, the two of them that differ in bit 2 each a half of the sum.
@@ -37,120 +40,189 @@ __device__ __forceinline__ float halving_sums(const float (&v)[8], int lane) {
     return (high ? t[1] : t[0]) + dpp_mov<0x128>(high ? t[0] : t[1]);  // row_ror:8
 }
 
-// What both kernels do with a block: steps and gradients before the gate.
+// A wave's block of 16 channels, loaded ahead.
 template <class E, int S>
 struct GradBlock {
-    typedef ScanShape<S> P;
-    float u[P::TL], dt[P::TL], z[P::TL], dy[P::TL];
-    __device__ __forceinline__ void load(const ScanBwdArgs& a, long long row0, int t0, int q, int d) {
-        load_scalars<E, S>(a.f.u, row0, a.f.D, a.f.N, t0, q, d, u);
-        load_scalars<E, S>(a.f.dt, row0, a.f.D, a.f.N, t0, q, d, dt);
-        load_scalars<E, S>(a.dy, row0, a.f.D, a.f.N, t0, q, d, dy);
-        if (a.f.z) load_scalars<E, S>(a.f.z, row0, a.f.ldz, a.f.N, t0, q, d, z);
+    typedef GradShape<S> P;
+    typedef Raw<E> R;
+    typename R::one u[P::TL], dt[P::TL], z[P::TL], dy[P::TL];
+    float A[P::SL], bias;
+    __device__ __forceinline__ void load(const ScanBwdArgs& a, const ScanRows& r, int q, int d) {
+        load_scalars<E, P>(r, a.f.u, a.f.D, q, d, u);
+        load_scalars<E, P>(r, a.f.dt, a.f.D, q, d, dt);
+        load_scalars<E, P>(r, a.dy, a.f.D, q, d, dy);
+        if (a.f.z) load_scalars<E, P>(r, a.f.z, a.f.ldz, q, d, z);
+        state_get<P::SL>(a.f.A + (long long)d * S + q * P::SL, A);
+        bias = a.f.bias ? a.f.bias[d] : 0.f;
     }
 };
 
-template <class E, int S>
-__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_local_bwd_kernel(ScanBwdArgs a) {
-    typedef ScanShape<S> P;
-    constexpr int SL = P::SL, T = P::T, TL = P::TL;
-    __shared__ float bc[P::NW][2][T * S];
-    __shared__ float ex[P::NW][3][64 * SL];
-    __shared__ float sums[P::NW][64];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
-    ScanPos at;
-    if (!scan_pos(a.f, &at)) return;
-    const int d = at.cb * kScanCh + (lane >> 2), D = a.f.D, dc = d < D ? d : D - 1;
-    const int g = __builtin_amdgcn_readfirstlane(dc / (D / a.f.G));
-    const int n = scan_length(a.f.lengths, at.b, a.f.N), c0 = at.seg * P::CH, t0 = c0 + w * T;
-    const long long row0 = (long long)at.b * a.f.N, seg = ((long long)at.b * a.f.nseg + at.seg) * D + d;
-    if (c0 >= n) {  // nothing in it: neither a state nor a gradient changes
-        if (w == 0 && d < D) {
+// The decays of a wave's block, and what it leaves of a state from zero (h) and of a gradient behind it from zero (G).
+template <int S>
+__device__ __forceinline__ void grad_local(const float* Bs, const float* Cs, int q, const float (&A2)[S / 4],
+                                           const float (&dt)[GradShape<S>::TL], const float (&du)[GradShape<S>::TL],
+                                           const float (&dp)[GradShape<S>::TL], float (&al)[GradShape<S>::T][S / 4],
+                                           float (&h)[S / 4], float (&G)[S / 4]) {
+    constexpr int SL = S / 4, T = GradShape<S>::T, GT = SL >= 16 ? 1 : 16 / SL;
+    float v[2][GT][SL];
 #pragma unroll
-            for (int j = 0; j < SL; ++j) a.f.seg_h[seg * S + q * SL + j] = a.seg_g[seg * S + q * SL + j] = 0.f;
-            if (q == 0) a.f.seg_dt[seg] = 0.f;
-        }
-        return;
-    }
-    GradBlock<E, S> x;
-    x.load(a, row0, t0, q, dc);
-    float *Bs = bc[w][0], *Cs = bc[w][1], v[4];
-    load_bc<E, S>(a.f.b, row0, a.f.ldb, a.f.N, n, t0, g, lane, a.f.bc_vec, v);
-    *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{v[0], v[1], v[2], v[3]};
-    load_bc<E, S>(a.f.c, row0, a.f.ldc, a.f.N, n, t0, g, lane, a.f.bc_vec, v);
-    *reinterpret_cast<f32x4_t*>(Cs + 4 * lane) = f32x4_t{v[0], v[1], v[2], v[3]};
-    const float bias = a.f.bias ? a.f.bias[dc] : 0.f;
-    float A2[SL], h[SL], G[SL], total = 0.f, du[TL];
-#pragma unroll
-    for (int j = 0; j < SL; ++j) {
-        A2[j] = decay_rate(a.f.A[(long long)dc * S + q * SL + j]);
-        h[j] = G[j] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < TL; ++i) {
-        const bool live = t0 + 4 * i + q < n;
-        float s, step = x.dt[i] + bias;
-        if (a.f.softplus) softplus(step, &step, &s);
-        total += x.dt[i] = live ? step : 0.f;
-        du[i] = live ? x.dt[i] * x.u[i] : 0.f;
-        x.dy[i] = live ? a.f.z ? x.dy[i] * swish_hw(x.z[i]) : x.dy[i] : 0.f;
-    }
-    lds_order();
-    float al[T][SL];
+    for (int j = 0; j < SL; ++j) h[j] = G[j] = 0.f;
+    lds_group<S, GT>(Bs, 0, q, v[0]);
 #pragma unroll
     for (int k = 0; k < T; ++k) {
-        float B[SL];
-        lds_vec<SL>(Bs + k * S + q * SL, B);
-        const float dk = quad_of(x.dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
+        if (k % GT == 0) {
+            if (k + GT < T) lds_group<S, GT>(Bs, k + GT, q, v[(k / GT + 1) & 1]);
+            else lds_group<S, GT>(Cs, T - GT, q, v[(k / GT + 1) & 1]);
+        }
+        const float(&B)[SL] = v[k / GT & 1][k % GT];
+        const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
             al[k][j] = __builtin_amdgcn_exp2f(dk * A2[j]);
             h[j] = fmaf(al[k][j], h[j], uk * B[j]);
         }
+        if (k % GT == GT - 1) lds_order();
     }
 #pragma unroll
     for (int k = T - 1; k >= 0; --k) {
-        float C[SL];
-        lds_vec<SL>(Cs + k * S + q * SL, C);
-        const float yk = quad_of(x.dy[k / 4], k % 4);
+        // group k / GT in reverse, the buffer after the last of the ones above
+        const int g = (T / GT + (T - 1 - k) / GT) & 1;
+        if (k % GT == GT - 1 && k >= GT) lds_group<S, GT>(Cs, k + 1 - 2 * GT, q, v[g ^ 1]);
+        const float(&C)[SL] = v[g][k % GT];
+        const float yk = quad_of(dp[k / 4], k % 4);
 #pragma unroll
         for (int j = 0; j < SL; ++j) G[j] = fmaf(C[j], yk, G[j]) * al[k][j];
+        if (k % GT == 0) lds_order();
     }
-    total = lanes_sum<4>(total);
-    float p[SL];
-#pragma unroll
-    for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
-    ex_put<SL>(ex[w][0], lane, h);
-    ex_put<SL>(ex[w][1], lane, p);
-    ex_put<SL>(ex[w][2], lane, G);
-    sums[w][lane] = total;
-    __syncthreads();
-    if (w > 1 || d >= D) return;
-    if (w == 0) {
-#pragma unroll
-        for (int v = 1; v < P::NW; ++v) {
-            float hv[SL], pv[SL];
-            ex_get<SL>(ex[v][0], lane, hv);
-            ex_get<SL>(ex[v][1], lane, pv);
-#pragma unroll
-            for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
-            total += sums[v][lane];
+}
+
+// Workgroup -> part, chunk and sequence with neighbouring parts on one XCD. A part is every parts_g-th block of 16 channels of
+// a group, so that the workgroups that run at the same time share the 128-byte lines of the rows in their L2: taken as runs of
+// neighbouring blocks, a line was gone before the next of its four blocks asked for it (3 times the reads from HBM).
+struct GradPos {
+    int part, chunk, b, g, cb0, cb1, step;
+};
+__device__ __forceinline__ bool grad_pos(const ScanBwdArgs& a, GradPos* p) {
+    const int parts = a.parts_g * a.f.G, blocks_g = (a.f.D / a.f.G + kScanCh - 1) / kScanCh;
+    const long long id = xcd_order(blockIdx.x, gridDim.x);
+    p->part = (int)(id % parts);
+    p->chunk = (int)(id / parts % a.f.nseg);
+    p->b = (int)(id / parts / a.f.nseg);
+    p->g = p->part / a.parts_g;
+    p->step = a.parts_g;
+    p->cb0 = p->g * blocks_g + p->part % a.parts_g;
+    p->cb1 = (p->g + 1) * blocks_g;
+    return p->b < a.f.B;
+}
+
+template <class E, int S>
+__global__ __launch_bounds__(GradShape<S>::THREADS) void scan_local_bwd_kernel(ScanBwdArgs a) {
+    typedef GradShape<S> P;
+    typedef Raw<E> R;
+    constexpr int SL = P::SL, T = P::T, TL = P::TL;
+    __shared__ float bc[P::NW][2][T * S];
+    __shared__ float ex[2][P::NW][3][64 * SL];
+    __shared__ float sums[2][P::NW][64];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3, D = a.f.D;
+    GradPos at;
+    if (!grad_pos(a, &at)) return;
+    const int n = scan_length(a.f.lengths, at.b, a.f.N), c0 = at.chunk * P::CH, t0 = c0 + w * T;
+    const long long row0 = (long long)at.b * a.f.N, seg0 = ((long long)at.b * a.f.nseg + at.chunk) * D;
+    if (c0 >= n) {  // nothing in it: neither a state nor a gradient changes
+        for (int cb = at.cb0; cb < at.cb1; cb += at.step) {
+            const int d0 = cb * kScanCh, cols = D - d0 < kScanCh ? D - d0 : kScanCh;
+            for (int i = threadIdx.x; i < cols * S; i += P::THREADS)
+                a.f.seg_h[(seg0 + d0) * S + i] = a.seg_g[(seg0 + d0) * S + i] = 0.f;
+            if ((int)threadIdx.x < cols) a.f.seg_dt[seg0 + d0 + threadIdx.x] = 0.f;
         }
+        return;
+    }
+    const ScanRows rows(row0, t0, a.f.N);
+    float *Bs = bc[w][0], *Cs = bc[w][1];
+    put_bc<E, P>(Bs, load_bc<E, P>(rows, a.f.b, a.f.ldb, at.g, lane, a.f.bc_vec), n, t0, lane);
+    put_bc<E, P>(Cs, load_bc<E, P>(rows, a.f.c, a.f.ldc, at.g, lane, a.f.bc_vec), n, t0, lane);
+    GradBlock<E, S> x;
+    {
+        const int d = at.cb0 * kScanCh + (lane >> 2);
+        x.load(a, rows, q, d < D ? d : D - 1);
+    }
+    int parity = 0;
+    for (int cb = at.cb0, turn = 0; cb < at.cb1; cb += at.step, parity ^= 1, turn = (turn + 2) % P::NW) {
+        const int d = cb * kScanCh + (lane >> 2);
+        float A2[SL], h[SL], G[SL], total = 0.f, dt[TL], du[TL], dp[TL], u[TL], s;
 #pragma unroll
-        for (int j = 0; j < SL; ++j) a.f.seg_h[seg * S + q * SL + j] = h[j];
-        if (q == 0) a.f.seg_dt[seg] = total;
-    } else {
-        ex_get<SL>(ex[P::NW - 1][2], lane, G);
+        for (int j = 0; j < SL; ++j) A2[j] = decay_rate(x.A[j]);
 #pragma unroll
-        for (int v = P::NW - 2; v >= 0; --v) {
-            float gv[SL], pv[SL];
-            ex_get<SL>(ex[v][2], lane, gv);
-            ex_get<SL>(ex[v][1], lane, pv);
-#pragma unroll
-            for (int j = 0; j < SL; ++j) G[j] = fmaf(pv[j], G[j], gv[j]);
+        for (int i = 0; i < TL; ++i) {
+            u[i] = R::value(x.u[i]);
+            dt[i] = R::value(x.dt[i]) + x.bias;
+            dp[i] = R::value(x.dy[i]);
         }
+        if (a.f.softplus)
 #pragma unroll
-        for (int j = 0; j < SL; ++j) a.seg_g[seg * S + q * SL + j] = G[j];
+            for (int i = 0; i < TL; ++i) softplus(dt[i], &dt[i], &s);
+        if (a.f.z)
+#pragma unroll
+            for (int i = 0; i < TL; ++i) dp[i] *= swish_hw(R::value(x.z[i]));
+        if (t0 + T > n)
+#pragma unroll
+            for (int i = 0; i < TL; ++i)
+                if (t0 + 4 * i + q >= n) dt[i] = u[i] = dp[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            total += dt[i];
+            du[i] = dt[i] * u[i];
+        }
+        if (cb + at.step < at.cb1) {
+            const int e = d + at.step * kScanCh;
+            x.load(a, rows, q, e < D ? e : D - 1);
+        }
+        lds_order();
+        float al[T][SL];
+        grad_local<S>(Bs, Cs, q, A2, dt, du, dp, al, h, G);
+        total = lanes_sum<4>(total);
+        float p[SL];
+#pragma unroll
+        for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
+        ex_put<SL>(ex[parity][w][0], lane, h);
+        ex_put<SL>(ex[parity][w][1], lane, p);
+        ex_put<SL>(ex[parity][w][2], lane, G);
+        sums[parity][w][lane] = total;
+        __syncthreads();
+        // the waves take turns: two of them join the waves' parts, the states forward and the gradients back
+        if (w == turn) {
+#pragma unroll
+            for (int j = 0; j < SL; ++j) h[j] = 0.f;
+            total = 0.f;
+#pragma unroll
+            for (int v = 0; v < P::NW; ++v) {
+                float hv[SL], pv[SL];
+                ex_get<SL>(ex[parity][v][0], lane, hv);
+                ex_get<SL>(ex[parity][v][1], lane, pv);
+#pragma unroll
+                for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
+                total += sums[parity][v][lane];
+            }
+            if (d < D) {
+#pragma unroll
+                for (int j = 0; j < SL; ++j) a.f.seg_h[(seg0 + d) * S + q * SL + j] = h[j];
+                if (q == 0) a.f.seg_dt[seg0 + d] = total;
+            }
+        } else if (w == turn + 1) {
+#pragma unroll
+            for (int j = 0; j < SL; ++j) G[j] = 0.f;
+#pragma unroll
+            for (int v = P::NW - 1; v >= 0; --v) {
+                float gv[SL], pv[SL];
+                ex_get<SL>(ex[parity][v][2], lane, gv);
+                ex_get<SL>(ex[parity][v][1], lane, pv);
+#pragma unroll
+                for (int j = 0; j < SL; ++j) G[j] = fmaf(pv[j], G[j], gv[j]);
+            }
+            if (d < D)
+#pragma unroll
+                for (int j = 0; j < SL; ++j) a.seg_g[(seg0 + d) * S + q * SL + j] = G[j];
+        }
     }
 }
 
@@ -203,24 +275,25 @@ __global__ __launch_bounds__(256) void scan_join_bwd_kernel(ScanBwdArgs a) {
     }
 }
 
-// blockIdx.x -> (part, chunk, b) with neighbouring parts on one XCD; a part is `run` blocks of channels of one group.
 template <class E, class O, int S>
-__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBwdArgs a) {
-    typedef ScanShape<S> P;
+__global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBwdArgs a) {
+    typedef GradShape<S> P;
+    typedef Raw<E> R;
     typedef typename O::st ost;
     constexpr int SL = P::SL, T = P::T, TL = P::TL, NW = P::NW;
     __shared__ float bc[NW][2][T * S];
     __shared__ float ex[NW][3][64 * SL];
     __shared__ float red[NW][64 * SL];
     __shared__ float red2[NW][2][kScanCh];
+    // 64 decays and 64 states a lane leave no room for the rest: the states of the first half of the tokens wait in LDS
+    constexpr int HL = T * SL == 64 ? T / 2 : 0;
+    __shared__ float hs[NW][HL ? HL : 1][HL ? 64 * SL : 1];
+    constexpr int NA = T * SL / 4;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
-    const int parts = a.parts_g * a.f.G, D = a.f.D, N = a.f.N;
-    const long long id = xcd_order(blockIdx.x, gridDim.x);
-    const int part = (int)(id % parts), chunk = (int)(id / parts % a.f.nseg), b = (int)(id / parts / a.f.nseg);
-    if (b >= a.f.B) return;
-    const int g = part / a.parts_g, blocks_g = (D / a.f.G + kScanCh - 1) / kScanCh;
-    const int cb0 = g * blocks_g + part % a.parts_g * a.run;
-    const int cb1 = cb0 + a.run < (g + 1) * blocks_g ? cb0 + a.run : (g + 1) * blocks_g;
+    const int D = a.f.D, N = a.f.N;
+    GradPos pos;
+    if (!grad_pos(a, &pos)) return;
+    const int part = pos.part, chunk = pos.chunk, b = pos.b, g = pos.g, cb0 = pos.cb0, cb1 = pos.cb1;
     const int n = scan_length(a.f.lengths, b, N), c0 = chunk * P::CH, t0 = c0 + w * T;
     const long long row0 = (long long)b * N;
     float* out_bc = a.part_bc + ((long long)part * a.f.B * N + row0) * 2 * S;
@@ -228,91 +301,82 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBw
     ost *du_p = (ost*)a.du, *ddt_p = (ost*)a.ddt, *dz_p = (ost*)a.dz;
     if (c0 >= n) {  // padding: zeros
         const int rows = N - c0 < P::CH ? N - c0 : P::CH;
-        const int d0 = cb0 * kScanCh, cols = (cb1 * kScanCh < D ? cb1 * kScanCh : D) - d0;
-        for (int i = threadIdx.x; i < rows * cols; i += P::THREADS) {
-            const long long o = (row0 + c0 + i / cols) * D + d0 + i % cols;
-            store_out(du_p + o, 0.f);
-            store_out(ddt_p + o, 0.f);
-            if (dz_p) store_out(dz_p + o, 0.f);
+        for (int cb = cb0; cb < cb1; cb += pos.step) {
+            const int d0 = cb * kScanCh, cols = D - d0 < kScanCh ? D - d0 : kScanCh;
+            for (int i = threadIdx.x; i < rows * kScanCh; i += P::THREADS) {
+                if (i % kScanCh >= cols) continue;
+                const long long o = (row0 + c0 + i / kScanCh) * D + d0 + i % kScanCh;
+                store_out(du_p + o, 0.f);
+                store_out(ddt_p + o, 0.f);
+                if (dz_p) store_out(dz_p + o, 0.f);
+            }
+            for (int i = threadIdx.x; i < cols * S; i += P::THREADS) out_a[(long long)d0 * S + i] = 0.f;
+            if ((int)threadIdx.x < cols)
+                out_a[(long long)D * S + d0 + threadIdx.x] = out_a[(long long)D * (S + 1) + d0 + threadIdx.x] = 0.f;
         }
         for (int i = threadIdx.x; i < rows * 2 * S; i += P::THREADS) out_bc[(long long)c0 * 2 * S + i] = 0.f;
-        for (int i = threadIdx.x; i < cols * S; i += P::THREADS) out_a[(long long)d0 * S + i] = 0.f;
-        for (int i = threadIdx.x; i < cols; i += P::THREADS)
-            out_a[(long long)D * S + d0 + i] = out_a[(long long)D * (S + 1) + d0 + i] = 0.f;
         return;
     }
     float *Bs = bc[w][0], *Cs = bc[w][1];
     {
-        float v[4];
-        load_bc<E, S>(a.f.b, row0, a.f.ldb, N, n, t0, g, lane, a.f.bc_vec, v);
-        *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{v[0], v[1], v[2], v[3]};
-        load_bc<E, S>(a.f.c, row0, a.f.ldc, N, n, t0, g, lane, a.f.bc_vec, v);
-        *reinterpret_cast<f32x4_t*>(Cs + 4 * lane) = f32x4_t{v[0], v[1], v[2], v[3]};
+        const ScanRows rows(row0, t0, N);
+        put_bc<E, P>(Bs, load_bc<E, P>(rows, a.f.b, a.f.ldb, g, lane, a.f.bc_vec), n, t0, lane);
+        put_bc<E, P>(Cs, load_bc<E, P>(rows, a.f.c, a.f.ldc, g, lane, a.f.bc_vec), n, t0, lane);
     }
     lds_order();
-    float acc[16];
+    constexpr int GT = SL >= 4 ? 1 : 2;  // tokens of B and C read at a time
+    char *du_row = (char*)(du_p + (row0 + t0) * D), *ddt_row = (char*)(ddt_p + (row0 + t0) * D);
+    char* dz_row = (char*)(dz_p + (row0 + t0) * D);
+    float acc[NA];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+    for (int i = 0; i < NA; ++i) acc[i] = 0.f;
+    const ScanRows rows(row0, t0, N);
+    const float* seg_h = a.f.seg_h + ((long long)b * a.f.nseg + chunk) * D * S;
+    const float* seg_g = a.seg_g + ((long long)b * a.f.nseg + chunk) * D * S;
     GradBlock<E, S> x;
     {
         const int d = cb0 * kScanCh + (lane >> 2);
-        x.load(a, row0, t0, q, d < D ? d : D - 1);
+        x.load(a, rows, q, d < D ? d : D - 1);
     }
-    for (int cb = cb0; cb < cb1; ++cb) {
+    for (int cb = cb0; cb < cb1; cb += pos.step) {
         const int d = cb * kScanCh + (lane >> 2), dc = d < D ? d : D - 1;
         const bool own = d < D;
-        const long long seg = (((long long)b * a.f.nseg + chunk) * D + dc) * S + q * SL;
+        const float skip = a.f.skip && own ? a.f.skip[d] : 0.f;
         float A2[SL], hin[SL], gin[SL];
-        state_get<SL>(a.f.seg_h + seg, hin);
-        state_get<SL>(a.seg_g + seg, gin);
+        state_get<SL>(seg_h + (long long)dc * S + q * SL, hin);
+        state_get<SL>(seg_g + (long long)dc * S + q * SL, gin);
 #pragma unroll
-        for (int j = 0; j < SL; ++j) A2[j] = decay_rate(a.f.A[(long long)dc * S + q * SL + j]);
-        const float bias = a.f.bias ? a.f.bias[dc] : 0.f, skip = a.f.skip ? a.f.skip[dc] : 0.f;
+        for (int j = 0; j < SL; ++j) A2[j] = decay_rate(x.A[j]);
         float u[TL], dt[TL], du[TL], slope[TL], dp[TL], dzf[TL], total = 0.f;  // dzf: dy silu'(z)
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
-            const bool live = own && t0 + 4 * i + q < n;
-            float step = x.dt[i] + bias;
+            u[i] = R::value(x.u[i]);
+            dt[i] = R::value(x.dt[i]) + x.bias;
+            dp[i] = R::value(x.dy[i]);
             slope[i] = 1.f;
-            if (a.f.softplus) softplus(step, &step, &slope[i]);
-            if (!live) slope[i] = 0.f;
-            total += dt[i] = live ? step : 0.f;
-            u[i] = live ? x.u[i] : 0.f;
-            du[i] = dt[i] * u[i];
-            dp[i] = live ? x.dy[i] : 0.f;
             dzf[i] = 0.f;
-            if (a.f.z && live) {
-                const float s = sigmoid_of(x.z[i]);
-                dzf[i] = dp[i] * (s * (1.f + x.z[i] * (1.f - s)));
-                dp[i] *= x.z[i] * s;
-            }
         }
-        if (cb + 1 < cb1) {
-            const int e = d + kScanCh;
-            x.load(a, row0, t0, q, e < D ? e : D - 1);
+        if (a.f.softplus)
+#pragma unroll
+            for (int i = 0; i < TL; ++i) softplus(dt[i], &dt[i], &slope[i]);
+        if (a.f.z)
+#pragma unroll
+            for (int i = 0; i < TL; ++i) {
+                const float z = R::value(x.z[i]), s = sigmoid_of(z);
+                dzf[i] = dp[i] * (s * (1.f + z * (1.f - s)));
+                dp[i] *= z * s;
+            }
+        if (t0 + T > n || (cb + 1) * kScanCh > D)
+#pragma unroll
+            for (int i = 0; i < TL; ++i)
+                if (!own || t0 + 4 * i + q >= n) dt[i] = u[i] = dp[i] = dzf[i] = slope[i] = 0.f;
+#pragma unroll
+        for (int i = 0; i < TL; ++i) {
+            total += dt[i];
+            du[i] = dt[i] * u[i];
         }
         float al[T][SL], h[SL], G[SL];
-#pragma unroll
-        for (int j = 0; j < SL; ++j) h[j] = G[j] = 0.f;
-#pragma unroll
-        for (int k = 0; k < T; ++k) {
-            float B[SL];
-            lds_vec<SL>(Bs + k * S + q * SL, B);
-            const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
-#pragma unroll
-            for (int j = 0; j < SL; ++j) {
-                al[k][j] = __builtin_amdgcn_exp2f(dk * A2[j]);
-                h[j] = fmaf(al[k][j], h[j], uk * B[j]);
-            }
-        }
-#pragma unroll
-        for (int k = T - 1; k >= 0; --k) {
-            float C[SL];
-            lds_vec<SL>(Cs + k * S + q * SL, C);
-            const float yk = quad_of(dp[k / 4], k % 4);
-#pragma unroll
-            for (int j = 0; j < SL; ++j) G[j] = fmaf(C[j], yk, G[j]) * al[k][j];
-        }
+        grad_local<S>(Bs, Cs, q, A2, dt, du, dp, al, h, G);
         total = lanes_sum<4>(total);
         float p[SL];
 #pragma unroll
@@ -321,61 +385,101 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBw
         ex_put<SL>(ex[w][1], lane, p);
         ex_put<SL>(ex[w][2], lane, G);
         __syncthreads();
-        for (int v = 0; v < w; ++v) {
-            float hv[SL], pv[SL];
-            ex_get<SL>(ex[v][0], lane, hv);
-            ex_get<SL>(ex[v][1], lane, pv);
+        // half of the waves' parts in registers at a time
 #pragma unroll
-            for (int j = 0; j < SL; ++j) hin[j] = fmaf(pv[j], hin[j], hv[j]);
-        }
-        for (int v = NW - 1; v > w; --v) {
-            float gv[SL], pv[SL];
-            ex_get<SL>(ex[v][2], lane, gv);
-            ex_get<SL>(ex[v][1], lane, pv);
+        for (int v0 = 0; v0 < NW; v0 += NW / 2) {
+            float hv[NW / 2][SL], pv[NW / 2][SL];
 #pragma unroll
-            for (int j = 0; j < SL; ++j) gin[j] = fmaf(pv[j], gin[j], gv[j]);
+            for (int e = 0; e < NW / 2; ++e) {
+                if (v0 + e == NW - 1) continue;
+                ex_get<SL>(ex[v0 + e][0], lane, hv[e]);
+                ex_get<SL>(ex[v0 + e][1], lane, pv[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < NW / 2; ++e)
+                if (v0 + e < NW - 1 && v0 + e < w)
+#pragma unroll
+                    for (int j = 0; j < SL; ++j) hin[j] = fmaf(pv[e][j], hin[j], hv[e][j]);
         }
-        float hh[T][SL], yp[T];
+#pragma unroll
+        for (int v0 = NW / 2; v0 >= 0; v0 -= NW / 2) {
+            float gv[NW / 2][SL], pv[NW / 2][SL];
+#pragma unroll
+            for (int e = 0; e < NW / 2; ++e) {
+                if (v0 + e == 0) continue;
+                ex_get<SL>(ex[v0 + e][2], lane, gv[e]);
+                ex_get<SL>(ex[v0 + e][1], lane, pv[e]);
+            }
+#pragma unroll
+            for (int e = NW / 2 - 1; e >= 0; --e)
+                if (v0 + e > 0 && v0 + e > w)
+#pragma unroll
+                    for (int j = 0; j < SL; ++j) gin[j] = fmaf(pv[e][j], gin[j], gv[e][j]);
+        }
+        lds_order();
+        float hh[T - HL][SL], hk[SL], yp[4], b2[2][GT][SL], c2[2][GT][SL];
+        lds_group<S, GT>(Bs, 0, q, b2[0]);
+        lds_group<S, GT>(Cs, 0, q, c2[0]);
 #pragma unroll
         for (int k = 0; k < T; ++k) {
-            float B[SL], C[SL];
-            lds_vec<SL>(Bs + k * S + q * SL, B);
-            lds_vec<SL>(Cs + k * S + q * SL, C);
+            const int gk = k / GT & 1;
+            if (k % GT == 0 && k + GT < T) {
+                lds_group<S, GT>(Bs, k + GT, q, b2[gk ^ 1]);
+                lds_group<S, GT>(Cs, k + GT, q, c2[gk ^ 1]);
+            }
             const float uk = quad_of(du[k / 4], k % 4);
-            yp[k] = 0.f;
+            yp[k % 4] = 0.f;
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
-                hh[k][j] = fmaf(al[k][j], k ? hh[k ? k - 1 : 0][j] : hin[j], uk * B[j]);
-                yp[k] = fmaf(C[j], hh[k][j], yp[k]);
+                hk[j] = fmaf(al[k][j], k ? hk[j] : hin[j], uk * b2[gk][k % GT][j]);
+                yp[k % 4] = fmaf(c2[gk][k % GT][j], hk[j], yp[k % 4]);
+                if (k >= HL) hh[k >= HL ? k - HL : 0][j] = hk[j];
             }
+            if constexpr (HL > 0)
+                if (k < HL) ex_put<SL>(hs[w][k < HL ? k : 0], lane, hk);
+            if (k % 4 == 3) {
+                const float dz = fmaf(skip, u[k / 4], quad_sums(yp[0], yp[1], yp[2], yp[3], q)) * dzf[k / 4];
+                if (dz_p && own && t0 + k - 3 + q < N)
+                    store_out((ost*)(dz_row + (__umul24(k - 3 + q, (uint32_t)D * (uint32_t)sizeof(ost)) +
+                                               d * (uint32_t)sizeof(ost))), dz);
+            }
+            if (k % GT == GT - 1) lds_order();
         }
-        if (dz_p)
-#pragma unroll
-            for (int i = 0; i < TL; ++i) {
-                float y = quad_sums(yp[4 * i], yp[4 * i + 1], yp[4 * i + 2], yp[4 * i + 3], q);
-                y = fmaf(skip, u[i], y);
-                const int t = t0 + 4 * i + q;
-                if (t < N && own) store_out(dz_p + (row0 + t) * D + d, dzf[i] * y);
-            }
-        float dA[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
+        // in reverse, from the group that the loop above read last
+        constexpr int last = (T / GT - 1) & 1;
+        float dA[SL], hn[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
 #pragma unroll
         for (int j = 0; j < SL; ++j) dA[j] = 0.f;
 #pragma unroll
         for (int k = T - 1; k >= 0; --k) {
-            float B[SL], C[SL];
-            lds_vec<SL>(Bs + k * S + q * SL, B);
-            lds_vec<SL>(Cs + k * S + q * SL, C);
+            const int gk = (last + (T - 1 - k) / GT) & 1;
+            if (k % GT == GT - 1 && k >= GT) {
+                lds_group<S, GT>(Bs, k + 1 - 2 * GT, q, b2[gk ^ 1]);
+                lds_group<S, GT>(Cs, k + 1 - 2 * GT, q, c2[gk ^ 1]);
+            }
+            const float(&B)[SL] = b2[gk][k % GT];
+            const float(&C)[SL] = c2[gk][k % GT];
             const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4), yk = quad_of(dp[k / 4], k % 4);
             s1[k % 4] = s2[k % 4] = 0.f;
+            // hk: the state after this token; hp: before it, asked for from LDS one token ahead of its use
+            float hp[SL];
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                hp[j] = k == 0 ? hin[j] : k > HL ? hh[k > HL ? k - 1 - HL : 0][j] : hn[j];
+                if (k == T - 1) hk[j] = hh[T - 1 - HL][j];
+            }
+            if constexpr (HL > 0)
+                if (k > 1 && k - 2 < HL) ex_get<SL>(hs[w][k > 1 && k - 2 < HL ? k - 2 : 0], lane, hn);
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
                 gin[j] = fmaf(C[j], yk, gin[j]);
                 const int at = SL == 2 ? 2 * (k & 1) + j : j & 3;
                 v[at] = uk * gin[j];
-                v[4 + at] = yk * hh[k][j];
+                v[4 + at] = yk * hk[j];
                 s1[k % 4] = fmaf(gin[j], B[j], s1[k % 4]);
                 gin[j] *= al[k][j];
-                const float along = gin[j] * (k ? hh[k ? k - 1 : 0][j] : hin[j]);
+                const float along = gin[j] * hp[j];
+                hk[j] = hp[j];
                 s2[k % 4] = fmaf(A2[j], along, s2[k % 4]);
                 dA[j] = fmaf(dk, along, dA[j]);
                 if constexpr (SL >= 4)
@@ -384,15 +488,22 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBw
             if constexpr (SL == 2)
                 if (k % 2 == 0) acc[k / 2] += halving_sums(v, lane);
             if (k % 4 == 0) {
-                const int i = k / 4, t = t0 + 4 * i + q;
+                const int i = k / 4;
                 const float gb = quad_sums(s1[0], s1[1], s1[2], s1[3], q), ak = quad_sums(s2[0], s2[1], s2[2], s2[3], q);
-                const float ddt = fmaf(kLn2, ak, u[i] * gb) * slope[i];
+                // 0 from token n on, as dp, dt and slope are
+                const float x1 = fmaf(skip, dp[i], dt[i] * gb), x2 = fmaf(kLn2, ak, u[i] * gb) * slope[i];
                 dskip = fmaf(dp[i], u[i], dskip);
-                dbias += ddt;
-                if (t < N && own) {
-                    store_out(du_p + (row0 + t) * D + d, t < n ? fmaf(skip, dp[i], dt[i] * gb) : 0.f);
-                    store_out(ddt_p + (row0 + t) * D + d, t < n ? ddt : 0.f);
+                dbias += x2;
+                if (own && t0 + k + q < N) {
+                    const uint32_t o = __umul24(k + q, (uint32_t)D * (uint32_t)sizeof(ost)) + d * (uint32_t)sizeof(ost);
+                    store_out((ost*)(du_row + o), x1);
+                    store_out((ost*)(ddt_row + o), x2);
                 }
+            }
+            if (k % GT == 0) lds_order();
+            if (k == T / 2 && cb + pos.step < cb1) {  // half of the decays and states are done with: room for the next channels
+                const int e = d + pos.step * kScanCh;
+                x.load(a, rows, q, e < D ? e : D - 1);
             }
         }
         dskip = lanes_sum<4>(dskip);
@@ -420,12 +531,12 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBw
         }
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        acc[i] += dpp_mov<0x12c>(acc[i]);  // row_ror:12, the value of lane + 4: whole where bit 2 is clear
+    for (int i = 0; i < NA; ++i) {
+        const float sum = acc[i] + dpp_mov<0x12c>(acc[i]);  // row_ror:12, the value of lane + 4: whole where bit 2 is clear
         const int hi = lane >> 5, mid = lane >> 4 & 1, lo = lane >> 3 & 1;
         const int k = SL == 2 ? 2 * i + mid : i / (SL / 4 ? SL / 4 : 1);
         const int s = SL == 2 ? 2 * q + lo : q * SL + i % (SL / 4 ? SL / 4 : 1) * 4 + 2 * mid + lo;
-        if (!(lane & 4) && t0 + k < N) out_bc[(long long)(t0 + k) * 2 * S + hi * S + s] = t0 + k < n ? acc[i] : 0.f;
+        if (!(lane & 4) && t0 + k < N) out_bc[(long long)(t0 + k) * 2 * S + hi * S + s] = t0 + k < n ? sum : 0.f;
     }
 }
 
@@ -451,7 +562,7 @@ __global__ __launch_bounds__(256) void scan_sum_bc_kernel(ScanBwdArgs a) {
 template <class E, class O, int S>
 bool pick(ScanBwdKernels* o) {
     *o = {scan_local_bwd_kernel<E, S>, scan_join_bwd_kernel<S>, scan_grad_kernel<E, O, S>, scan_sum_bc_kernel<O, S>,
-          ScanShape<S>::CH, ScanShape<S>::THREADS};
+          GradShape<S>::CH, GradShape<S>::NW};
     return true;
 }
 template <class E, class O>

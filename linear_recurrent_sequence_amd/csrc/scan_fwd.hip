@@ -13,74 +13,91 @@ namespace ret {
 
 namespace {
 
-// The states that a segment leaves if it starts from zero, and the sum of its steps. Its waves take neighbouring runs of
-// seg_tokens / NW tokens.
-template <class E, int S>
-__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_local_kernel(ScanArgs a) {
+// A wave on its own: 16 channels of a segment, token by token. LOCAL: the states that the segment leaves if it starts from
+// zero, and the sum of its steps; else the outputs, from the state entering it.
+template <class E, class O, int S, bool LOCAL>
+__global__ __launch_bounds__(256) void scan_walk_kernel(ScanArgs a) {
     typedef ScanShape<S> P;
-    constexpr int SL = P::SL, T = P::T;
-    __shared__ float bc[P::NW][T * S];
-    __shared__ float ex[P::NW][2][64 * SL];
-    __shared__ float sums[P::NW][64];
+    constexpr int SL = P::SL, T = P::T, TL = P::TL;
+    __shared__ float bc[4][2][T * S];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
     ScanPos at;
-    if (!scan_pos(a, &at) || at.seg == a.nseg - 1) return;  // nothing follows the last segment
+    if (!scan_pos(a, &at) || (LOCAL && at.seg == a.nseg - 1)) return;  // nothing follows the last segment
+    at.cb = 4 * at.cb + w;
+    if (at.cb * kScanCh >= a.D) return;
     const int d = at.cb * kScanCh + (lane >> 2), dc = d < a.D ? d : a.D - 1;
     const int g = __builtin_amdgcn_readfirstlane(dc / (a.D / a.G));  // one for the whole wave
-    const int n = scan_length(a.lengths, at.b, a.N), run = a.seg_tokens / P::NW;
-    const int t0 = at.seg * a.seg_tokens + w * run, t1 = t0 + run < n ? t0 + run : n;
+    const int n = scan_length(a.lengths, at.b, a.N);
+    const int s0 = at.seg * a.seg_tokens, s1 = a.N - s0 < a.seg_tokens ? a.N : s0 + a.seg_tokens, e1 = s1 < n ? s1 : n;
     const long long row0 = (long long)at.b * a.N;
-    const float bias = a.bias ? a.bias[dc] : 0.f;
+    const float bias = a.bias ? a.bias[dc] : 0.f, skip = !LOCAL && a.skip ? a.skip[dc] : 0.f;
     float A2[SL], h[SL], total = 0.f;
+    const long long st = ((long long)at.b * a.D + dc) * S + q * SL;
 #pragma unroll
     for (int j = 0; j < SL; ++j) {
         A2[j] = decay_rate(a.A[(long long)dc * S + q * SL + j]);
         h[j] = 0.f;
     }
-    float* Bs = bc[w];
+    const long long seg = ((long long)at.b * a.nseg + at.seg) * a.D + dc;
+    if (!LOCAL) {
+        if (a.nseg > 1) state_get<SL>(a.seg_h + seg * S + q * SL, h);
+        else if (a.state_in) state_get<SL>(a.state_in + st, h);
+    }
+    float *Bs = bc[w][0], *Cs = bc[w][1];
+    typename O::st* y = (typename O::st*)a.y;
     ScanBlock<E, S> x;
-    if (t0 < t1) x.load(a, row0, n, t0, q, lane, dc, g, false);
-    for (int t = t0; t < t1; t += T) {
-        float du[P::TL], dt[P::TL];
-        x.steps(a, bias, n, t, q, du);
+    if (s0 < e1) x.load(a, row0, s0, q, lane, dc, g, !LOCAL);
+    for (int t0 = s0; t0 < e1; t0 += T) {
+        float du[TL], dt[TL], u[TL], z[TL];
+        x.steps(a, bias, n, t0, q, dt, u, du);
+        put_bc<E, P>(Bs, x.b, n, t0, lane);
+        if (!LOCAL) put_bc<E, P>(Cs, x.c, n, t0, lane);
 #pragma unroll
-        for (int i = 0; i < P::TL; ++i) total += dt[i] = x.dt[i];
-        *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{x.b[0], x.b[1], x.b[2], x.b[3]};
-        if (t + T < t1) x.load(a, row0, n, t + T, q, lane, dc, g, false);
+        for (int i = 0; i < TL; ++i) {
+            if (LOCAL) total += dt[i];
+            else z[i] = a.z ? swish_hw(Raw<E>::value(x.z[i])) : 1.f;
+        }
+        if (t0 + T < e1) x.load(a, row0, t0 + T, q, lane, dc, g, !LOCAL);
         lds_order();
+        float o[TL];
 #pragma unroll
-        for (int k = 0; k < T; ++k) {
-            float B[SL];
-            lds_vec<SL>(Bs + k * S + q * SL, B);
-            const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4);
+        for (int i = 0; i < TL; ++i) {
+            float yp[4];
 #pragma unroll
-            for (int j = 0; j < SL; ++j) h[j] = fmaf(__builtin_amdgcn_exp2f(dk * A2[j]), h[j], uk * B[j]);
+            for (int k = 0; k < 4; ++k) {
+                float B[SL], C[SL];
+                lds_vec<SL>(Bs + (4 * i + k) * S + q * SL, B);
+                if (!LOCAL) lds_vec<SL>(Cs + (4 * i + k) * S + q * SL, C);
+                const float dk = quad_of(dt[i], k), uk = quad_of(du[i], k);
+                yp[k] = 0.f;
+#pragma unroll
+                for (int j = 0; j < SL; ++j) {
+                    h[j] = fmaf(__builtin_amdgcn_exp2f(dk * A2[j]), h[j], uk * B[j]);
+                    if (!LOCAL) yp[k] = fmaf(C[j], h[j], yp[k]);
+                }
+            }
+            if (!LOCAL) o[i] = fmaf(skip, u[i], quad_sums(yp[0], yp[1], yp[2], yp[3], q)) * z[i];
         }
         lds_order();
+        if (LOCAL) continue;
+        if (d < a.D) store_scalars<O, P>(a.y, row0 + t0, a.D, e1 - t0, q, d, o);
     }
-    total = lanes_sum<4>(total);
-    float p[SL];
+    if (LOCAL) {
+        total = lanes_sum<4>(total);
+        if (d >= a.D) return;
 #pragma unroll
-    for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
-    ex_put<SL>(ex[w][0], lane, h);
-    ex_put<SL>(ex[w][1], lane, p);
-    sums[w][lane] = total;
-    __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int v = 1; v < P::NW; ++v) {
-        float hv[SL], pv[SL];
-        ex_get<SL>(ex[v][0], lane, hv);
-        ex_get<SL>(ex[v][1], lane, pv);
-#pragma unroll
-        for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
-        total += sums[v][lane];
+        for (int j = 0; j < SL; ++j) a.seg_h[seg * S + q * SL + j] = h[j];
+        if (q == 0) a.seg_dt[seg] = total;
+        return;
     }
-    if (d >= a.D) return;
-    const long long seg = ((long long)at.b * a.nseg + at.seg) * a.D + d;
+    // tokens past the sequence's length: zeros
+    for (int t = (e1 > s0 ? e1 : s0) + (lane >> 4); t < s1; t += 4) {
+        const int dz = at.cb * kScanCh + (lane & 15);
+        if (dz < a.D) store_out(y + (row0 + t) * a.D + dz, 0.f);
+    }
+    if (a.state_out && at.seg == a.nseg - 1 && d < a.D)
 #pragma unroll
-    for (int j = 0; j < SL; ++j) a.seg_h[seg * S + q * SL + j] = h[j];
-    if (q == 0) a.seg_dt[seg] = total;
+        for (int j = 0; j < SL; ++j) a.state_out[st + j] = h[j];
 }
 
 // Segments' states from zero -> the states entering them, in place.
@@ -111,8 +128,9 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanArgs a) {
     }
 }
 
+// A workgroup on 16 channels of a segment, NW blocks of T tokens at a time.
 template <class E, class O, int S>
-__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_full_kernel(ScanArgs a) {
+__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_chunks_kernel(ScanArgs a) {
     typedef ScanShape<S> P;
     constexpr int SL = P::SL, T = P::T, TL = P::TL;
     __shared__ float bc[P::NW][2][T * S];
@@ -136,31 +154,23 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_full_kernel(ScanAr
     if (a.nseg > 1) state_get<SL>(a.seg_h + (((long long)at.b * a.nseg + at.seg) * a.D + dc) * S + q * SL, run);
     else if (a.state_in) state_get<SL>(a.state_in + st, run);
     float *Bs = bc[w][0], *Cs = bc[w][1];
-    typedef typename O::st ost;
-    ost* y = (ost*)a.y;
-    // tokens past the sequence's length: zeros
+    typename O::st* y = (typename O::st*)a.y;
     const int live1 = s1 < n ? s1 : n;
-    for (int t = (live1 > s0 ? live1 : s0) + (int)(threadIdx.x / kScanCh); t < s1; t += P::THREADS / kScanCh) {
-        const int dz = at.cb * kScanCh + (int)(threadIdx.x % kScanCh);
-        if (dz < a.D) store_out(y + (row0 + t) * a.D + dz, 0.f);
-    }
     ScanBlock<E, S> x;
-    if (s0 < live1) x.load(a, row0, n, s0 + w * T, q, lane, dc, g, true);
+    if (s0 < live1) x.load(a, row0, s0 + w * T, q, lane, dc, g, true);
     int parity = 0;
     for (int c0 = s0; c0 < live1; c0 += P::CH, parity ^= 1) {
         const int t0 = c0 + w * T;
         float du[TL], dt[TL], u[TL], z[TL], total = 0.f;
-        x.steps(a, bias, n, t0, q, du);
+        x.steps(a, bias, n, t0, q, dt, u, du);
+        put_bc<E, P>(Bs, x.b, n, t0, lane);
+        put_bc<E, P>(Cs, x.c, n, t0, lane);
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
-            dt[i] = x.dt[i];
-            u[i] = x.u[i];
-            z[i] = a.z ? x.z[i] : 0.f;
+            z[i] = a.z ? swish_hw(Raw<E>::value(x.z[i])) : 1.f;
             total += dt[i];
         }
-        *reinterpret_cast<f32x4_t*>(Bs + 4 * lane) = f32x4_t{x.b[0], x.b[1], x.b[2], x.b[3]};
-        *reinterpret_cast<f32x4_t*>(Cs + 4 * lane) = f32x4_t{x.c[0], x.c[1], x.c[2], x.c[3]};
-        if (c0 + P::CH < live1) x.load(a, row0, n, t0 + P::CH, q, lane, dc, g, true);
+        if (c0 + P::CH < live1) x.load(a, row0, t0 + P::CH, q, lane, dc, g, true);
         lds_order();
         float al[T][SL], h[SL];
 #pragma unroll
@@ -194,29 +204,31 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_full_kernel(ScanAr
 #pragma unroll
             for (int j = 0; j < SL; ++j) run[j] = fmaf(pv[j], run[j], hv[j]);
         }
-        float yp[T];
-#pragma unroll
-        for (int k = 0; k < T; ++k) {
-            float B[SL], C[SL];
-            lds_vec<SL>(Bs + k * S + q * SL, B);
-            lds_vec<SL>(Cs + k * S + q * SL, C);
-            const float uk = quad_of(du[k / 4], k % 4);
-            yp[k] = 0.f;
-#pragma unroll
-            for (int j = 0; j < SL; ++j) {
-                h[j] = fmaf(al[k][j], h[j], uk * B[j]);
-                yp[k] = fmaf(C[j], h[j], yp[k]);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
-            float o = quad_sums(yp[4 * i], yp[4 * i + 1], yp[4 * i + 2], yp[4 * i + 3], q);
-            const int t = t0 + 4 * i + q;
-            o = fmaf(skip, u[i], o);
-            if (a.z) o *= swish_hw(z[i]);
-            if (t < live1 && d < a.D) store_out(y + (row0 + t) * a.D + d, o);
+            float yp[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float B[SL], C[SL];
+                lds_vec<SL>(Bs + (4 * i + k) * S + q * SL, B);
+                lds_vec<SL>(Cs + (4 * i + k) * S + q * SL, C);
+                const float uk = quad_of(du[i], k);
+                yp[k] = 0.f;
+#pragma unroll
+                for (int j = 0; j < SL; ++j) {
+                    h[j] = fmaf(al[4 * i + k][j], h[j], uk * B[j]);
+                    yp[k] = fmaf(C[j], h[j], yp[k]);
+                }
+            }
+            z[i] *= fmaf(skip, u[i], quad_sums(yp[0], yp[1], yp[2], yp[3], q));
         }
+        if (d < a.D) store_scalars<O, P>(a.y, row0 + t0, a.D, live1 - t0, q, d, z);
         lds_order();
+    }
+    // tokens past the sequence's length: zeros
+    for (int t = (live1 > s0 ? live1 : s0) + (int)(threadIdx.x / kScanCh); t < s1; t += P::THREADS / kScanCh) {
+        const int dz = at.cb * kScanCh + (int)(threadIdx.x % kScanCh);
+        if (dz < a.D) store_out(y + (row0 + t) * a.D + dz, 0.f);
     }
     if (w == 0 && a.state_out && at.seg == a.nseg - 1 && d < a.D)
 #pragma unroll
@@ -225,7 +237,9 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_full_kernel(ScanAr
 
 template <class E, class O, int S>
 bool pick(ScanKernels* o) {
-    *o = {scan_local_kernel<E, S>, scan_join_kernel<S>, scan_full_kernel<E, O, S>, ScanShape<S>::CH, ScanShape<S>::THREADS};
+    typedef ScanShape<S> P;
+    *o = {scan_walk_kernel<E, O, S, true>, scan_join_kernel<S>, scan_walk_kernel<E, O, S, false>, scan_chunks_kernel<E, O, S>,
+          P::T, P::CH, P::THREADS};
     return true;
 }
 template <class E, class O>

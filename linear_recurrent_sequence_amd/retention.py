@@ -925,6 +925,48 @@ def ret_gated_delta_step(q, k, v, g, beta, o, state, scale=None, stream=None, op
 
 # ---- root-mean-square norm, short convolution, selective scan ----
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+_F32 = (torch.float32,)
+
+
+def _arg(t, name, shape, dtypes, dev):
+    """The address of t, a contiguous tensor of that shape and one of those dtypes on GPU `dev`; None passes. One look at a
+    tensor for all of it: a call of ten tensors takes 4 us less than with a check at a time."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise ValueError("%s must be a tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("all tensors must be on one GPU: %s is on %s" % (name, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows_arg(t, name, shape, dtypes, dev, inner):
+    """(address, elements from row to row, 0 where contiguous) of a tensor that may be a slice of wider rows (_token_rows)."""
+    if t is None or t.is_contiguous():
+        return _arg(t, name, shape, dtypes, dev), 0
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev:
+        _arg(t.contiguous(), name, shape, dtypes, dev)  # says what is wrong
+    return _token_rows(t, name, inner)
+
+
+def _gpu_of(t, name):
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    return dev
+
+
+def _workspace(ws, dev):
+    """(address, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    return _arg(ws, "workspace", ws.shape, (ws.dtype,), dev), ws.numel() * ws.element_size()
 
 
 def _rms_scales(x, group):
@@ -946,20 +988,14 @@ def ret_rms_norm_fwd(x, y=None, weight=None, eps=1e-5, residual=None, sum_out=No
         raise ValueError("y8 and scales go together")
     if group not in (None, 32, 64, 128):
         raise ValueError("group must be None, 32, 64 or 128, got %r" % (group,))
-    _shape(y, "y", x.shape, _IO)
-    _shape(y8, "y8", x.shape, _E4M3)
-    _shape(scales, "scales", _rms_scales(x, group), (torch.float32,))
-    for name, t in (("residual", residual), ("sum_out", sum_out)):
-        _shape(t, name, x.shape, (x.dtype,))
-    _shape(weight, "weight", (D,), (torch.float32,))
-    _shape(rstd, "rstd", x.shape[:-1], (torch.float32,))
-    _same_device(x, y, weight, residual, sum_out, rstd, y8, scales)
-    _need_gpu(x, "x")
+    dev, xt, lead = _gpu_of(x, "x"), (x.dtype,), x.shape[:-1]
+    args = (_arg(x, "x", x.shape, xt, dev), _arg(residual, "residual", x.shape, xt, dev),
+            _arg(weight, "weight", (D,), _F32, dev), _arg(y, "y", x.shape, _IO, dev),
+            _arg(sum_out, "sum_out", x.shape, xt, dev), _arg(rstd, "rstd", lead, _F32, dev),
+            _arg(y8, "y8", x.shape, _E4M3, dev), _arg(scales, "scales", _rms_scales(x, group), _F32, dev))
     guard, sp, _ = _launch(x, stream, None, None)
     with guard:
-        st = lib.ret_rms_norm_fwd(_dev(x, "x"), _dev(residual, "residual"), _dev(weight, "weight"), _dev(y, "y"),
-                                  _dev(sum_out, "sum_out"), _dev(rstd, "rstd"), _dev(y8, "y8"), _dev(scales, "scales"),
-                                  group or 0, rows, D, _dt(x), _dt(y) if y is not None else _dt(x), float(eps), sp,
+        st = lib.ret_rms_norm_fwd(*args, group or 0, rows, D, _dt(x), _dt(x if y is None else y), eps, sp,
                                   _options(options))
     _check("ret_rms_norm_fwd", st)
     return y if y is not None else y8
@@ -983,20 +1019,16 @@ def ret_rms_norm_bwd(dy, x, rstd, dx, weight=None, dsum=None, dweight=None, work
     for name, t in (("dy", dy), ("dx", dx), ("rstd", rstd)):
         if t is None:
             raise ValueError("%s must be a tensor" % name)
-    _shape(dy, "dy", x.shape, _IO)
-    _shape(dx, "dx", x.shape, _IO)
-    _shape(dsum, "dsum", x.shape, (dx.dtype,))
-    _shape(rstd, "rstd", x.shape[:-1], (torch.float32,))
-    for name, t in (("weight", weight), ("dweight", dweight)):
-        _shape(t, name, (D,), (torch.float32,))
-    _same_device(dy, x, rstd, dx, weight, dsum, dweight, workspace)
-    _need_gpu(x, "x")
+    dev = _gpu_of(x, "x")
+    args = (_arg(dy, "dy", x.shape, _IO, dev), _arg(x, "x", x.shape, (x.dtype,), dev),
+            _arg(weight, "weight", (D,), _F32, dev), _arg(rstd, "rstd", x.shape[:-1], _F32, dev),
+            _arg(dsum, "dsum", x.shape, (dx.dtype,), dev), _arg(dx, "dx", x.shape, _IO, dev),
+            _arg(dweight, "dweight", (D,), _F32, dev))
     make = (lambda: rms_norm_bwd_workspace(x)) if dweight is not None else None
     guard, sp, workspace = _launch(x, stream, workspace, make)
     with guard:
-        st = lib.ret_rms_norm_bwd(_dev(dy, "dy"), _dev(x, "x"), _dev(weight, "weight"), _dev(rstd, "rstd"),
-                                  _dev(dsum, "dsum"), _dev(dx, "dx"), _dev(dweight, "dweight"), rows, D, _dt(x), _dt(dy),
-                                  _dt(dx), _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+        st = lib.ret_rms_norm_bwd(*args, rows, D, _dt(x), _dt(dy), _dt(dx), *_workspace(workspace, dev), sp,
+                                  _options(options))
     _check("ret_rms_norm_bwd", st)
     return dx
 
@@ -1008,6 +1040,11 @@ def _token_rows(t, name, inner):
         return None, 0
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
+    st, sh = t.stride(), t.shape
+    if st[-1] == 1 and (inner == 1 or st[-2] == sh[-1]):  # as a projection's slices are
+        ld = st[-1 - inner]
+        if ld >= sh[-1] * (1 if inner == 1 else sh[-2]) and (len(sh) - inner == 1 or st[0] == ld * sh[1]):
+            return t.data_ptr(), ld
     width, ld, rows = 1, None, 1
     for size, step in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
         if size != 1 and step != width:
@@ -1025,18 +1062,16 @@ def _token_rows(t, name, inner):
         ld = width
     if ld < width:
         raise ValueError("the rows of %s overlap" % name)
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return t.data_ptr(), ld
 
 
-def _conv_x(x, weight, bias, nd):
-    """Shapes of x [B, N, D] (a step: [B, D]), weight [D, W] and bias [D]; W."""
+def _conv_width(x, weight, nd):
+    """W of weight [D, W] for x [B, N, D] (a step: [B, D])."""
     if not isinstance(x, torch.Tensor) or x.dim() != nd or x.dtype not in _IO:
         raise ValueError("x must be a float32 or bfloat16 %d-d tensor" % nd)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be a tensor [D, W]")
     _int_sizes(x, weight)
-    _shape(weight, "weight", (x.shape[-1], weight.shape[1]), (torch.float32,))
-    _shape(bias, "bias", (x.shape[-1],), (torch.float32,))
     return weight.shape[1]
 
 
@@ -1046,22 +1081,20 @@ def ret_short_conv_fwd(x, weight, y, bias=None, silu=True, lengths=None, state_i
     (float32), through silu if wanted; state_in, state_out [B,W-1,D] in x's dtype: the inputs before the first token and the
     last ones. lengths: int32 [B] tokens of each sequence on the device, or None."""
     lib = load()
-    W = _conv_x(x, weight, bias, 3)
+    W = _conv_width(x, weight, 3)
     B, N, D = x.shape
     if y is None:
         raise ValueError("y must be a tensor")
-    _shape(y, "y", x.shape, _IO)
-    for name, s in (("state_in", state_in), ("state_out", state_out)):
-        _shape(s, name, (B, W - 1, D), (x.dtype,))
     _delta_lengths(lengths, B)
-    _same_device(x, weight, y, bias, lengths, state_in, state_out)
-    _need_gpu(x, "x")
-    xp, ld = _token_rows(x, "x", 1)
+    dev, xt, state = _gpu_of(x, "x"), (x.dtype,), (B, W - 1, D)
+    args = (*_rows_arg(x, "x", x.shape, xt, dev, 1), _arg(weight, "weight", (D, W), _F32, dev),
+            _arg(bias, "bias", (D,), _F32, dev), _arg(y, "y", x.shape, _IO, dev))
+    states = (_arg(lengths, "lengths", (B,), (torch.int32,), dev), _arg(state_in, "state_in", state, xt, dev),
+              _arg(state_out, "state_out", state, xt, dev))
     guard, sp, _ = _launch(x, stream, None, None)
     with guard:
-        st = lib.ret_short_conv_fwd(xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(y, "y"), B, N, D, W, _dt(x),
-                                    _dt(y), RET_ACT_SILU if silu else RET_ACT_NONE, _dev(lengths, "lengths"),
-                                    _dev(state_in, "state_in"), _dev(state_out, "state_out"), sp, _options(options))
+        st = lib.ret_short_conv_fwd(*args, B, N, D, W, _dt(x), _dt(y), RET_ACT_SILU if silu else RET_ACT_NONE, *states,
+                                    sp, _options(options))
     _check("ret_short_conv_fwd", st)
     return y
 
@@ -1081,31 +1114,24 @@ def ret_short_conv_bwd(dy, x, weight, dx, dweight=None, bias=None, dbias=None, s
     state_out)) of ret_short_conv_fwd on the same inputs. The states' gradients have dx's dtype. Without a workspace one is
     allocated for the call."""
     lib = load()
-    W = _conv_x(x, weight, bias, 3)
+    W = _conv_width(x, weight, 3)
     B, N, D = x.shape
     for name, t in (("dy", dy), ("dx", dx)):
         if t is None:
             raise ValueError("%s must be a tensor" % name)
-    _shape(dy, "dy", x.shape, (x.dtype,))
-    _shape(dx, "dx", x.shape, _IO)
-    _shape(dweight, "dweight", weight.shape, (torch.float32,))
-    _shape(dbias, "dbias", (D,), (torch.float32,))
-    _shape(state_in, "state_in", (B, W - 1, D), (x.dtype,))
-    for name, s in (("dstate_out", dstate_out), ("dstate_in", dstate_in)):
-        _shape(s, name, (B, W - 1, D), (dx.dtype,))
     _delta_lengths(lengths, B)
-    _same_device(dy, x, weight, dx, dweight, bias, dbias, lengths, state_in, dstate_out, dstate_in, workspace)
-    _need_gpu(x, "x")
-    xp, ld = _token_rows(x, "x", 1)
+    dev, xt, ot, state = _gpu_of(x, "x"), (x.dtype,), (dx.dtype,), (B, W - 1, D)
+    args = (_arg(dy, "dy", x.shape, xt, dev), *_rows_arg(x, "x", x.shape, xt, dev, 1),
+            _arg(weight, "weight", (D, W), _F32, dev), _arg(bias, "bias", (D,), _F32, dev),
+            _arg(dx, "dx", x.shape, _IO, dev), _arg(dweight, "dweight", (D, W), _F32, dev),
+            _arg(dbias, "dbias", (D,), _F32, dev))
+    states = (_arg(lengths, "lengths", (B,), (torch.int32,), dev), _arg(state_in, "state_in", state, xt, dev),
+              _arg(dstate_out, "dstate_out", state, ot, dev), _arg(dstate_in, "dstate_in", state, ot, dev))
     make = (lambda: short_conv_bwd_workspace(x, weight)) if dweight is not None or dbias is not None else None
     guard, sp, workspace = _launch(x, stream, workspace, make)
     with guard:
-        st = lib.ret_short_conv_bwd(_dev(dy, "dy"), xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(dx, "dx"),
-                                    _dev(dweight, "dweight"), _dev(dbias, "dbias"), B, N, D, W, _dt(x), _dt(dx),
-                                    RET_ACT_SILU if silu else RET_ACT_NONE, _dev(lengths, "lengths"),
-                                    _dev(state_in, "state_in"), _dev(dstate_out, "dstate_out"),
-                                    _dev(dstate_in, "dstate_in"), _dev(workspace, "workspace"), _nbytes(workspace), sp,
-                                    _options(options))
+        st = lib.ret_short_conv_bwd(*args, B, N, D, W, _dt(x), _dt(dx), RET_ACT_SILU if silu else RET_ACT_NONE, *states,
+                                    *_workspace(workspace, dev), sp, _options(options))
     _check("ret_short_conv_bwd", st)
     return dx
 
@@ -1114,45 +1140,35 @@ def ret_short_conv_step(x, weight, y, state, bias=None, silu=True, stream=None, 
     """One token of the short convolution: x (whole, or a slice of wider rows), y [B,D]; state [B,W-1,D] in x's dtype, the
     inputs before it, is moved on in place."""
     lib = load()
-    W = _conv_x(x, weight, bias, 2)
+    W = _conv_width(x, weight, 2)
     B, D = x.shape
     if y is None or state is None:
         raise ValueError("y and state must be tensors")
-    _shape(y, "y", x.shape, _IO)
-    _shape(state, "state", (B, W - 1, D), (x.dtype,))
-    _same_device(x, weight, y, state, bias)
-    _need_gpu(x, "x")
-    xp, ld = _token_rows(x, "x", 1)
+    dev, xt = _gpu_of(x, "x"), (x.dtype,)
+    args = (*_rows_arg(x, "x", x.shape, xt, dev, 1), _arg(weight, "weight", (D, W), _F32, dev),
+            _arg(bias, "bias", (D,), _F32, dev), _arg(y, "y", x.shape, _IO, dev),
+            _arg(state, "state", (B, W - 1, D), xt, dev))
     guard, sp, _ = _launch(x, stream, None, None)
     with guard:
-        st = lib.ret_short_conv_step(xp, ld, _dev(weight, "weight"), _dev(bias, "bias"), _dev(y, "y"),
-                                     _dev(state, "state"), B, D, W, _dt(x), _dt(y),
-                                     RET_ACT_SILU if silu else RET_ACT_NONE, sp, _options(options))
+        st = lib.ret_short_conv_step(*args, B, D, W, _dt(x), _dt(y), RET_ACT_SILU if silu else RET_ACT_NONE, sp,
+                                     _options(options))
     _check("ret_short_conv_step", st)
     return y
 
 
-def _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias, step=False):
-    """Shapes and dtypes of u, dt, z [B, N, D], b, c [B, N, G, S], A [D, S], d_skip, dt_bias [D] (a step: no N axis); G, S."""
+def _scan_sizes(u, dt, A, b, c, step=False):
+    """G, S of b [B, N, G, S] for u [B, N, D] (a step: no N axis)."""
     nd = 2 if step else 3
     if not isinstance(u, torch.Tensor) or u.dim() != nd or u.dtype not in _IO:
         raise ValueError("u must be a float32 or bfloat16 %d-d tensor" % nd)
     if not isinstance(b, torch.Tensor) or b.dim() != nd + 1 or b.shape[:-2] != u.shape[:-1]:
         raise ValueError("b must be a tensor [%s, G, S]" % ("B" if step else "B, N"))
-    G, S = b.shape[-2:]
-    D = u.shape[-1]
-    for name, t, shape in (("dt", dt, u.shape), ("b", b, b.shape), ("c", c, b.shape)):
+    for name, t in (("dt", dt), ("A", A), ("c", c)):
         if t is None:
             raise ValueError("%s must be a tensor" % name)
-        _shape(t, name, shape, (u.dtype,))
-    if A is None:
-        raise ValueError("A must be a tensor")
-    _shape(z, "z", u.shape, (u.dtype,))
-    _shape(A, "A", (D, S), (torch.float32,))
-    for name, t in (("d_skip", d_skip), ("dt_bias", dt_bias)):
-        _shape(t, name, (D,), (torch.float32,))
-    if G == 0 or D % G:
-        raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (D, G))
+    G, S = b.shape[-2:]
+    if G == 0 or u.shape[-1] % G:
+        raise ValueError("the channels (%d) must be a multiple of the groups (%d)" % (u.shape[-1], G))
     _int_sizes(u, b)
     return G, S
 
@@ -1168,12 +1184,12 @@ def selective_scan_workspace(u, b, options=None):
     return _rows_workspace(nbytes, u.device)
 
 
-def _scan_args(u, dt, A, b, c, d_skip, z, dt_bias):
-    bp, ldb = _token_rows(b, "b", 2)
-    cp, ldc = _token_rows(c, "c", 2)
-    zp, ldz = _token_rows(z, "z", 1)
-    return (_dev(u, "u"), _dev(dt, "dt"), _dev(A, "A"), bp, ldb, cp, ldc, _dev(d_skip, "d_skip"), zp, ldz,
-            _dev(dt_bias, "dt_bias"))
+def _scan_args(u, dt, A, b, c, d_skip, z, dt_bias, dev):
+    D, t = u.shape[-1], (u.dtype,)
+    return (_arg(u, "u", u.shape, t, dev), _arg(dt, "dt", u.shape, t, dev), _arg(A, "A", (D, b.shape[-1]), _F32, dev),
+            *_rows_arg(b, "b", b.shape, t, dev, 2), *_rows_arg(c, "c", b.shape, t, dev, 2),
+            _arg(d_skip, "d_skip", (D,), _F32, dev), *_rows_arg(z, "z", u.shape, t, dev, 1),
+            _arg(dt_bias, "dt_bias", (D,), _F32, dev))
 
 
 def ret_selective_scan_fwd(u, dt, A, b, c, y, d_skip=None, z=None, dt_bias=None, softplus=True, lengths=None,
@@ -1183,23 +1199,19 @@ def ret_selective_scan_fwd(u, dt, A, b, c, y, d_skip=None, z=None, dt_bias=None,
     state_in [B,D,S] (float32; None: zeros), the final state to state_out. lengths: int32 [B] tokens of each sequence on the
     device, or None. Without a workspace one is allocated for the call."""
     lib = load()
-    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias)
+    G, S = _scan_sizes(u, dt, A, b, c)
     B, N, D = u.shape
     if y is None:
         raise ValueError("y must be a tensor")
-    _shape(y, "y", u.shape, _IO)
-    for name, s in (("state_in", state_in), ("state_out", state_out)):
-        _shape(s, name, (B, D, S), (torch.float32,))
     _delta_lengths(lengths, B)
-    _same_device(u, dt, A, b, c, y, d_skip, z, dt_bias, lengths, state_in, state_out, workspace)
-    _need_gpu(u, "u")
-    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    dev, state = _gpu_of(u, "u"), (B, D, S)
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias, dev) + (_arg(y, "y", u.shape, _IO, dev),)
+    states = (_arg(lengths, "lengths", (B,), (torch.int32,), dev), _arg(state_in, "state_in", state, _F32, dev),
+              _arg(state_out, "state_out", state, _F32, dev))
     guard, sp, workspace = _launch(u, stream, workspace, lambda: selective_scan_workspace(u, b, options))
     with guard:
-        st = lib.ret_selective_scan_fwd(*args, _dev(y, "y"), B, N, D, S, G, _dt(u), _dt(y), 1 if softplus else 0,
-                                        _dev(lengths, "lengths"), _dev(state_in, "state_in"),
-                                        _dev(state_out, "state_out"), _dev(workspace, "workspace"), _nbytes(workspace),
-                                        sp, _options(options))
+        st = lib.ret_selective_scan_fwd(*args, B, N, D, S, G, _dt(u), _dt(y), 1 if softplus else 0, *states,
+                                        *_workspace(workspace, dev), sp, _options(options))
     _check("ret_selective_scan_fwd", st)
     return y
 
@@ -1208,19 +1220,16 @@ def ret_selective_scan_step(u, dt, A, b, c, y, state, d_skip=None, z=None, dt_bi
                             options=None):
     """One token of the selective scan: u, dt, z, y [B,D], b, c [B,G,S]; state [B,D,S] (float32) is updated in place."""
     lib = load()
-    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias, step=True)
+    G, S = _scan_sizes(u, dt, A, b, c, step=True)
     B, D = u.shape
     if y is None or state is None:
         raise ValueError("y and state must be tensors")
-    _shape(y, "y", u.shape, _IO)
-    _shape(state, "state", (B, D, S), (torch.float32,))
-    _same_device(u, dt, A, b, c, y, state, d_skip, z, dt_bias)
-    _need_gpu(u, "u")
-    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    dev = _gpu_of(u, "u")
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias, dev)
+    args += (_arg(y, "y", u.shape, _IO, dev), _arg(state, "state", (B, D, S), _F32, dev))
     guard, sp, _ = _launch(u, stream, None, None)
     with guard:
-        st = lib.ret_selective_scan_step(*args, _dev(y, "y"), _dev(state, "state"), B, D, S, G, _dt(u), _dt(y),
-                                         1 if softplus else 0, sp, _options(options))
+        st = lib.ret_selective_scan_step(*args, B, D, S, G, _dt(u), _dt(y), 1 if softplus else 0, sp, _options(options))
     _check("ret_selective_scan_step", st)
     return y
 
@@ -1243,35 +1252,27 @@ def ret_selective_scan_bwd(u, dt, A, b, c, dy, du, ddt, dA, db, dc, d_skip=None,
     sum(dstate_out state_out)) of ret_selective_scan_fwd on the same inputs. du, ddt, db, dc and dz share one dtype; db and dc
     are summed over the channels of a group. Without a workspace one is allocated for the call."""
     lib = load()
-    G, S = _scan_inputs(u, dt, A, b, c, d_skip, z, dt_bias)
+    G, S = _scan_sizes(u, dt, A, b, c)
     B, N, D = u.shape
     for name, t in (("dy", dy), ("du", du), ("ddt", ddt), ("db", db), ("dc", dc)):
         if t is None:
             raise ValueError("%s must be a tensor" % name)
-    _shape(dy, "dy", u.shape, (u.dtype,))
-    _shape(du, "du", u.shape, _IO)
-    for name, t, shape in (("ddt", ddt, u.shape), ("dz", dz, u.shape), ("db", db, b.shape), ("dc", dc, b.shape)):
-        _shape(t, name, shape, (du.dtype,))
-    for name, t, shape in (("dA", dA, (D, S)), ("dd_skip", dd_skip, (D,)), ("ddt_bias", ddt_bias, (D,))):
-        _shape(t, name, shape, (torch.float32,))
     if dz is not None and z is None:
         raise ValueError("dz without z")
     if dd_skip is not None and d_skip is None:
         raise ValueError("dd_skip without d_skip")
-    for name, s in (("state_in", state_in), ("dstate_out", dstate_out), ("dstate_in", dstate_in)):
-        _shape(s, name, (B, D, S), (torch.float32,))
     _delta_lengths(lengths, B)
-    _same_device(u, dt, A, b, c, dy, du, ddt, dA, db, dc, d_skip, dd_skip, z, dz, dt_bias, ddt_bias, lengths, state_in,
-                 dstate_out, dstate_in, workspace)
-    _need_gpu(u, "u")
-    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias)
+    dev, state, ot = _gpu_of(u, "u"), (B, D, S), (du.dtype,)
+    args = _scan_args(u, dt, A, b, c, d_skip, z, dt_bias, dev)
+    args += (_arg(dy, "dy", u.shape, (u.dtype,), dev), _arg(du, "du", u.shape, _IO, dev),
+             _arg(ddt, "ddt", u.shape, ot, dev), _arg(dA, "dA", (D, S), _F32, dev), _arg(db, "db", b.shape, ot, dev),
+             _arg(dc, "dc", b.shape, ot, dev), _arg(dd_skip, "dd_skip", (D,), _F32, dev),
+             _arg(dz, "dz", u.shape, ot, dev), _arg(ddt_bias, "ddt_bias", (D,), _F32, dev))
+    states = (_arg(lengths, "lengths", (B,), (torch.int32,), dev), _arg(state_in, "state_in", state, _F32, dev),
+              _arg(dstate_out, "dstate_out", state, _F32, dev), _arg(dstate_in, "dstate_in", state, _F32, dev))
     guard, sp, workspace = _launch(u, stream, workspace, lambda: selective_scan_bwd_workspace(u, b))
     with guard:
-        st = lib.ret_selective_scan_bwd(*args, _dev(dy, "dy"), _dev(du, "du"), _dev(ddt, "ddt"), _dev(dA, "dA"),
-                                        _dev(db, "db"), _dev(dc, "dc"), _dev(dd_skip, "dd_skip"), _dev(dz, "dz"),
-                                        _dev(ddt_bias, "ddt_bias"), B, N, D, S, G, _dt(u), _dt(du),
-                                        1 if softplus else 0, _dev(lengths, "lengths"), _dev(state_in, "state_in"),
-                                        _dev(dstate_out, "dstate_out"), _dev(dstate_in, "dstate_in"),
-                                        _dev(workspace, "workspace"), _nbytes(workspace), sp, _options(options))
+        st = lib.ret_selective_scan_bwd(*args, B, N, D, S, G, _dt(u), _dt(du), 1 if softplus else 0, *states,
+                                        *_workspace(workspace, dev), sp, _options(options))
     _check("ret_selective_scan_bwd", st)
     return du, ddt, dA, db, dc
