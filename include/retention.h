@@ -512,9 +512,9 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
  * least one of y (y_dt) and y8 is wanted. y8 [rows, D] holds y in e4m3 (OCP, 1 byte a value) divided by its scale, rounded to
  * nearest even, for a product in 8 bits: y = y8 scale. group = 0: one scale a row, scales float[rows]; group = 32, 64 or 128:
  * one for every group columns, scales float[rows, ceil(D / group)]. scale = max |y| / 448 over its columns, at least 2^-126;
- * y is taken before its rounding to y_dt, and its quotient as the product with the rounded reciprocal of scale. A NaN makes
- * its scale NaN. y and sum_out may take the place of x or residual (same start and dtype); no other overlap. Pointers 16-byte
- * aligned (rstd and scales 4); rows = 0 does nothing; 1 <= D <= 16384. Kernel: "ret_rms_norm".
+ * y is taken before its rounding to y_dt. A NaN makes its scale NaN. y and sum_out may take the place of x or residual (same
+ * start and dtype); no other overlap. Pointers 16-byte aligned (rstd and scales 4); rows = 0 does nothing; 1 <= D <= 16384.
+ * Kernel: "ret_rms_norm".
  */
 ret_status_t ret_rms_norm_fwd(const void* x, const void* residual, const float* weight, void* y, void* sum_out,
                               float* rstd, void* y8, float* scales, int group, int64_t rows, int D, ret_dtype_t x_dt,
@@ -537,9 +537,9 @@ ret_status_t ret_rms_norm_bwd(const void* dy, const void* x, const float* weight
  * Short causal convolution along the tokens, channel by channel (before a selective scan, or before q, k and v of a gated
  * delta rule), with its activation:
  *     y_t[d] = act(bias[d] + sum_{j < W} weight[d][j] x_{t - W + 1 + j}[d])
- * x, y [B, N, D]; weight float[D, W], bias float[D] or NULL (0); act RET_ACT_NONE or RET_ACT_SILU. Tokens before the first are
- * state_in [B, W - 1, D] in in_dt, oldest first (NULL: zeros); state_out (as state_in, may equal it; NULL: not wanted) receives
- * the last W - 1 inputs. lengths (device int32[B], or NULL) as in ret_gated_delta_fwd: inputs past them are not used, outputs
+ * x, y [B, N, D]; weight float[D, W], bias float[D] or NULL (0); act RET_ACT_NONE or RET_ACT_SILU. Tokens before the first
+ * are state_in [B, W - 1, D] in in_dt, oldest first (NULL: zeros); state_out (as state_in, may equal it; NULL: not wanted)
+ * receives the last W - 1 inputs. lengths (device int32[B], or NULL) as in ret_gated_delta_fwd: inputs past them are not used, outputs
  * past them are zero, and state_out is the state after lengths[b] tokens. x_ld: elements from a token's row of x to the next
  * token's (0: D), so that x can be a slice of a wider projection's rows; sequence b starts at row b N.
  * dtypes: x and the states in in_dt, y in out_dt; pairs as in ret_chunkwise_fwd; arithmetic in fp32. Supported: W in
@@ -579,20 +579,22 @@ ret_status_t ret_short_conv_bwd(const void* dy, const void* x, int64_t x_ld, con
  *     dt_t = softplus(dt[t][d] + dt_bias[d]),  h_t[s] = exp(dt_t A[d][s]) h_{t-1}[s] + dt_t u_t b_t[g][s],
  *     y_t = (sum_s c_t[g][s] h_t[s] + d_skip[d] u_t) silu(z_t)
  * Layouts: u, dt, z, y [B, N, D], b, c [B, N, G, S], A float[D, S] (negative as a rule), d_skip, dt_bias float[D], states
- * [B, D, S] fp32; a step has no N axis. softplus = 0: dt + dt_bias is the step length itself. NULL d_skip, dt_bias: 0; NULL z:
- * no gate. z_ld, b_ld, c_ld: elements from a token's row to the next token's (0: contiguous), so that z, b and c can be slices
- * of wider projections' rows; sequence b starts at row b N. dtypes: u, dt, z, b, c in in_dt, y in out_dt; pairs as in
- * ret_chunkwise_fwd. All arithmetic is fp32, nothing is rounded before the output.
+ * [B, D, S] fp32; a step has no N axis. softplus = 0: dt + dt_bias is the step length itself. NULL d_skip, dt_bias: 0; NULL
+ * z: no gate. z_ld, b_ld, c_ld: elements from a token's row to the next token's (0: contiguous), so that z, b and c can be
+ * slices of wider projections' rows; sequence b starts at row b N. dtypes: u, dt, z, b, c in in_dt, y in out_dt; pairs as in
+ * ret_chunkwise_fwd. All arithmetic is fp32, nothing is rounded before the output. Tokens are joined by the products of their
+ * decays, which may vanish; where dt_t A > 0 makes the product over some tokens exceed fp32's range, states and outputs are
+ * not finite even if the states would be.
  *
  * ret_selective_scan_fwd computes whole sequences. state_in (NULL: zeros), state_out (NULL: not wanted; may equal state_in),
  * lengths: as in ret_gated_delta_fwd. A NaN or infinity reaches only later tokens of its sequence. workspace:
  * ret_selective_scan_workspace_bytes device bytes (0 for an unsupported shape), of any content; calls sharing one must not
- * overlap in time. Supported: S in {8, 16, 32, 64}, G = 1 or D / G a multiple of 16, D and z_ld, b_ld, c_ld below 2^22, B N <=
- * 2^36, and no launch of 2^32 work-items (512 a sequence, segment and 16 channels) or 65536 sequences. Written buffers must not overlap others.
- * Pointers: A and the states 16-byte aligned, the others like one of their elements. opts: segments (> 0: segments per sequence
- * that run in parallel), variant (1: waves that walk their tokens one by one, 2: workgroups that do chunks of 128 tokens, 32 and
- * 16 at 32 and 64 states) and timer. Kernels: "ret_scan_local", "ret_scan_join", "ret_scan_walk",
- * "ret_scan_chunks".
+ * overlap in time. Supported: S in {8, 16, 32, 64}, G = 1 or D / G a multiple of 16, D and z_ld, b_ld, c_ld below 2^22,
+ * B N <= 2^36, and no launch of 2^32 work-items (512 a sequence, segment and 16 channels) or, in segments, 65536 sequences.
+ * Written buffers must not overlap others. Pointers: A and the states 16-byte aligned, the others like one of their elements.
+ * opts: segments (> 0: segments per sequence that run in parallel), variant (1: waves that walk their tokens one by one, 2:
+ * workgroups that do chunks of 128 tokens, 32 and 16 at 32 and 64 states) and timer. Kernels: "ret_scan_local",
+ * "ret_scan_join", "ret_scan_walk", "ret_scan_chunks".
  *
  * ret_selective_scan_step computes one token of every sequence, the state updated in place. Kernel: "ret_scan_step".
  */
@@ -615,10 +617,10 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
  * writes du, ddt [B, N, D] (ddt: that of dt before dt_bias and softplus), db, dc [B, N, G, S] (summed over the channels of a
  * group) in out_dt, contiguous, and, unless NULL, dz (out_dt), dA float[D, S], dd_skip, ddt_bias float[D] and dstate_in. The
  * other arguments are the forward call's. Gradients of the padding past lengths[b] are zero. workspace:
- * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 128 tokens (32 and 16 at 32 and
- * 64 states), partial sums of db and dc over up to 512 channels and of dA over a chunk). Same limits as the forward. Sums
- * have one order: the same call gives the same bits. opts: the timer. Kernels: "ret_scan_local_bwd", "ret_scan_join_bwd",
- * "ret_scan_grad", "ret_scan_sum_bc", "ret_column_sums".
+ * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 128 tokens (32 and 16 at 32
+ * and 64 states), partial sums of db and dc over up to 512 channels and of dA over a chunk). Limits as the forward's in
+ * segments. Sums have one order: the same call gives the same bits. opts: the timer. Kernels: "ret_scan_local_bwd",
+ * "ret_scan_join_bwd", "ret_scan_grad", "ret_scan_sum_bc", "ret_column_sums".
  */
 size_t ret_selective_scan_bwd_workspace_bytes(int B, int N, int D, int S, int G, ret_dtype_t in_dt);
 ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,
