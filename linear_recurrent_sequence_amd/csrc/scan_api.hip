@@ -102,16 +102,25 @@ Plan make_plan(const Shape& s, const ScanKernels& k, const Opts& op) {
     return p;
 }
 
+// The gradients' local pass: from so many waves for each token of a chunk on, a wave does a chunk alone, which saves the join
+// of the 8 (32 and 64 states: 4) that share a chunk below. Together and alone, us, at 16 states and 512 x 512 tokens x channels
+// 8, 28; 2048 x 2048 26, 29; 4096 x 4096 91, 87; 2 x 2048 x 8192 190, 174; at 64 states 256 x 2048 24, 19; at 32 1024 x 2048
+// 26, 24.
+constexpr long long kLocalWaves = 40;
+
 // Chunks of the gradients, and blocks of channels that a workgroup does one after another: the more, the smaller the partial
 // sums of dB and dC, while about four workgroups a CU are left.
 struct BwdPlan {
-    int nchunks, blocks_g, parts_g, cblocks;
+    int nchunks, blocks_g, parts_g, cblocks, lblocks;
+    bool split;
     size_t seg_g, seg_dt, part_a, part_bc, bytes;
 };
-BwdPlan make_bwd_plan(const Shape& s, int chunk) {
+BwdPlan make_bwd_plan(const Shape& s, int chunk, int waves) {
     BwdPlan p;
     p.cblocks = (s.D + kScanCh - 1) / kScanCh;
     p.nchunks = (s.N + chunk - 1) / chunk;
+    p.split = (long long)s.B * p.nchunks * p.cblocks < kLocalWaves * chunk;
+    p.lblocks = p.split ? p.cblocks : (p.cblocks + waves - 1) / waves;
     p.blocks_g = (s.D / s.G + kScanCh - 1) / kScanCh;
     const long long units = (long long)s.B * p.nchunks * s.G * p.blocks_g;
     long long run = units / 1024;
@@ -145,10 +154,11 @@ ret_status_t fwd_grids(const Shape& s, const Plan& p, const ScanKernels& k, Grid
 }
 ret_status_t bwd_grids(const Shape& s, const BwdPlan& p, int threads, Grids* g) {
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
+    g->local = by8((unsigned long long)p.lblocks * p.nchunks * s.B);
     g->grad = by8((unsigned long long)p.parts_g * s.G * p.nchunks * s.B);
     g->bc = ((unsigned long long)s.B * s.N * 2 * s.S + 255) / 256;
     return fits(s, grid_fits(g->join, s.B, 2, 256) &&
-                       grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc, s.G, 1, 256) &&
+                       grid_fits(g->local, 1, 1, threads) && grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc, s.G, 1, 256) &&
                        grid_fits(((unsigned long long)s.D * (s.S + 2) + kColSumCols - 1) / kColSumCols, 1, 1, kColSumThreads) &&
                        (long long)p.nchunks * s.B <= INT32_MAX / 2);
 }
@@ -265,7 +275,7 @@ size_t ret_selective_scan_bwd_workspace_bytes(int B, int N, int D, int S, int G,
     ScanBwdKernels k;
     Grids g;
     if (check_shape(s, in_dt, RET_F32) != RET_OK || !scan_bwd_kernels_get(in_dt == RET_BF16, false, S, &k)) return 0;
-    const BwdPlan p = make_bwd_plan(s, k.chunk);
+    const BwdPlan p = make_bwd_plan(s, k.chunk, k.waves);
     return bwd_grids(s, p, 64 * k.waves, &g) == RET_OK ? p.bytes : 0;
 }
 
@@ -287,7 +297,7 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     ScanBwdKernels k;
     scan_bwd_kernels_get(in_dt == RET_BF16, out_dt == RET_BF16, S, &k);
     const Opts op = resolve(opts);
-    const BwdPlan p = make_bwd_plan(s, k.chunk);
+    const BwdPlan p = make_bwd_plan(s, k.chunk, k.waves);
     Grids g;
     if ((st = bwd_grids(s, p, 64 * k.waves, &g)) != RET_OK) return st;
     const size_t rows = (size_t)B * N, e = esize(in_dt), sb = (size_t)B * D * S * 4, gs = (size_t)G * S, nd = (size_t)D * 4;
@@ -311,14 +321,16 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     f.u = u, f.dt = dt, f.z = z, f.b = b, f.c = c, f.A = A, f.skip = d_skip, f.bias = dt_bias, f.lengths = lengths;
     f.state_in = state_in, f.seg_h = (float*)workspace, f.seg_dt = (float*)((char*)workspace + p.seg_dt);
     f.ldz = ld.z, f.ldb = ld.b, f.ldc = ld.c;
-    f.B = B, f.N = N, f.D = D, f.G = G, f.nseg = p.nchunks, f.seg_tokens = k.chunk, f.cblocks = p.cblocks;
+    f.B = B, f.N = N, f.D = D, f.G = G, f.nseg = p.nchunks, f.seg_tokens = k.chunk, f.cblocks = p.lblocks;
     f.softplus = softplus != 0, f.bc_vec = vectors(b, c, ld, in_dt);
     a.dy = dy, a.dstate_out = dstate_out, a.dstate_in = dstate_in;
     a.seg_g = (float*)((char*)workspace + p.seg_g);
     a.part_a = (float*)((char*)workspace + p.part_a), a.part_bc = (float*)((char*)workspace + p.part_bc);
     a.du = du, a.ddt = ddt, a.dz = dz, a.db = db, a.dc = dc, a.parts_g = p.parts_g;
     hipStream_t sm = (hipStream_t)stream;
-    if ((st = launch("ret_scan_local_bwd", k.local, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
+    if ((st = launch("ret_scan_local_bwd", p.split ? k.local_split : k.local, dim3((unsigned)g.local), 64 * k.waves, sm, op,
+                     a)) != RET_OK)
+        return st;
     if ((st = launch("ret_scan_join_bwd", k.join, dim3((unsigned)g.join, B, 2), 256, sm, op, a)) != RET_OK) return st;
     if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
     if ((st = launch("ret_scan_sum_bc", k.sum_bc, dim3((unsigned)g.bc, G), 256, sm, op, a)) != RET_OK) return st;

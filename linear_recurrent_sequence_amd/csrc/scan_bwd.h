@@ -18,7 +18,7 @@ struct ScanBwdArgs {
 };
 typedef void (*scan_bwd_kernel_t)(ScanBwdArgs);
 struct ScanBwdKernels {
-    scan_bwd_kernel_t local, join, grad, sum_bc;
+    scan_bwd_kernel_t local, local_split, join, grad, sum_bc;
     int chunk, waves;
 };
 bool scan_bwd_kernels_get(bool bf16_in, bool bf16_out, int S, ScanBwdKernels* o);

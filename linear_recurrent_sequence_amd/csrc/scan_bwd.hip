@@ -4,14 +4,20 @@
 //     dB = sum_d g dt u,  dC = sum_d dp h,  dskip = sum_t dp u,  dz = dy y silu'(z).
 //
 // Sequences are cut into the chunks of a workgroup (NW blocks of T tokens). local finds what each chunk does to a state
-// entering it and to a gradient leaving it (both from zero, one exp2 a state); join carries the states forward and the
-// gradients back over the chunks; grad does the chunks, all independent: decays once, kept in 64 registers a lane, the
-// waves' blocks joined through LDS both ways, the states kept in 64 more, then the tokens in reverse.
+// entering it and to a gradient leaving it (both from zero); join carries the states forward and the gradients back over the
+// chunks; grad does the chunks, all independent: decays once, kept in 64 registers a lane, the waves' blocks joined through
+// LDS both ways, the states kept in 64 more, then the tokens in reverse.
 //
 // dB and dC are sums over all channels. A wave adds its 16 channels up by halving exchanges, 8 values at a time (16
 // instructions for 8 values where separate sums would take 32), keeps one register for each of its groups of 8 over the
 // `run` blocks of channels that its workgroup does one after another, and leaves them as partial sums for sum_bc. Every sum
-// has one order.
+// has one order. Through LDS instead (each wave's products laid down and read back transposed, one add a value) grad took
+// 656 us where this takes 635.
+//
+// Bound by the vector units: grad has 28 instructions per token, channel and state of a wave's 16 x 4, which are 440 us of the
+// 635 that 2 x 2048 tokens of 8192 channels and 16 states take (two waves a SIMD, whose registers are full; waves of 8 tokens
+// with room for four joined twice as often and took as long); local has 11 and takes 172, join 14, the sums 16. The tensors'
+// bytes alone are 93.
 #include "scan_bwd.h"
 
 namespace ret {
@@ -20,6 +26,9 @@ namespace {
 
 template <int S>
 struct GradShape : ScanShape<S> {};
+
+// A sum is added to here, not when it is wanted: until then its terms, one a token, would take registers.
+__device__ __forceinline__ void sum_now(float& s) { __asm__ volatile("" : "+v"(s)); }
 
 // Sums of 8 values over the lanes of equal q (lane & 3): after the exchanges the lanes of equal bits 3..5 hold value
 // 4 bit5 + 2 bit4 + bit3, the two of them that differ in bit 2 each a half of the sum.
@@ -115,115 +124,105 @@ __device__ __forceinline__ bool grad_pos(const ScanBwdArgs& a, GradPos* p) {
     return p->b < a.f.B;
 }
 
-template <class E, int S>
+// What each chunk leaves of a state from zero (h) and of a gradient behind it from zero (G), in one walk along the tokens: with
+// P the product of the decays so far, h = a h + du B and G += P C dp. A wave walks a chunk on its own; where that leaves the
+// card idle (SPLIT) a workgroup's waves walk a block of it each and join them.
+template <class E, int S, bool SPLIT>
 __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_local_bwd_kernel(ScanBwdArgs a) {
     typedef GradShape<S> P;
-    typedef Raw<E> R;
-    constexpr int SL = P::SL, T = P::T, TL = P::TL;
-    __shared__ float bc[P::NW][2][T * S];
-    __shared__ float ex[2][P::NW][3][64 * SL];
-    __shared__ float sums[2][P::NW][64];
+    constexpr int SL = P::SL, T = P::T, TL = P::TL, NW = P::NW;
+    __shared__ float bc[NW][2][T * S];
+    __shared__ float ex[SPLIT ? NW : 1][3][SPLIT ? 64 * SL : 1];
+    __shared__ float sums[SPLIT ? NW : 1][64];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3, D = a.f.D;
-    GradPos at;
-    if (!grad_pos(a, &at)) return;
-    const int n = scan_length(a.f.lengths, at.b, a.f.N), c0 = at.chunk * P::CH, t0 = c0 + w * T;
-    const long long row0 = (long long)at.b * a.f.N, seg0 = ((long long)at.b * a.f.nseg + at.chunk) * D;
-    if (c0 >= n) {  // nothing in it: neither a state nor a gradient changes
-        for (int cb = at.cb0; cb < at.cb1; cb += at.step) {
-            const int d0 = cb * kScanCh, cols = D - d0 < kScanCh ? D - d0 : kScanCh;
-            for (int i = threadIdx.x; i < cols * S; i += P::THREADS)
-                a.f.seg_h[(seg0 + d0) * S + i] = a.seg_g[(seg0 + d0) * S + i] = 0.f;
-            if ((int)threadIdx.x < cols) a.f.seg_dt[seg0 + d0 + threadIdx.x] = 0.f;
-        }
-        return;
+    ScanPos at;
+    if (!scan_pos(a.f, &at)) return;
+    if (!SPLIT) {
+        at.cb = at.cb * NW + w;
+        if (at.cb * kScanCh >= D) return;
     }
-    const ScanRows rows(row0, t0, a.f.N);
+    const int d = at.cb * kScanCh + (lane >> 2), dc = d < D ? d : D - 1;
+    const int g = __builtin_amdgcn_readfirstlane(dc / (D / a.f.G));
+    const int n = scan_length(a.f.lengths, at.b, a.f.N), c0 = at.seg * P::CH, first = SPLIT ? c0 + w * T : c0;
+    const int c1 = n - first < (SPLIT ? T : P::CH) ? n : first + (SPLIT ? T : P::CH);
+    const long long row0 = (long long)at.b * a.f.N, seg = ((long long)at.b * a.f.nseg + at.seg) * D + d;
+    const float bias = a.f.bias ? a.f.bias[dc] : 0.f;
+    float A2[SL], h[SL], G[SL], p[SL], total = 0.f;
+    state_get<SL>(a.f.A + (long long)dc * S + q * SL, A2);
+#pragma unroll
+    for (int j = 0; j < SL; ++j) {
+        A2[j] = decay_rate(A2[j]);
+        h[j] = G[j] = 0.f;
+        p[j] = 1.f;
+    }
     float *Bs = bc[w][0], *Cs = bc[w][1];
-    put_bc<E, P>(Bs, load_bc<E, P>(rows, a.f.b, a.f.ldb, at.g, lane, a.f.bc_vec), n, t0, lane);
-    put_bc<E, P>(Cs, load_bc<E, P>(rows, a.f.c, a.f.ldc, at.g, lane, a.f.bc_vec), n, t0, lane);
-    GradBlock<E, S> x;
-    {
-        const int d = at.cb0 * kScanCh + (lane >> 2);
-        x.load(a, rows, q, d < D ? d : D - 1);
-    }
-    int parity = 0;
-    for (int cb = at.cb0, turn = 0; cb < at.cb1; cb += at.step, parity ^= 1, turn = (turn + 2) % P::NW) {
-        const int d = cb * kScanCh + (lane >> 2);
-        float A2[SL], h[SL], G[SL], total = 0.f, dt[TL], du[TL], dp[TL], u[TL], s;
-#pragma unroll
-        for (int j = 0; j < SL; ++j) A2[j] = decay_rate(x.A[j]);
-#pragma unroll
-        for (int i = 0; i < TL; ++i) {
-            u[i] = R::value(x.u[i]);
-            dt[i] = R::value(x.dt[i]) + x.bias;
-            dp[i] = R::value(x.dy[i]);
-        }
-        if (a.f.softplus)
-#pragma unroll
-            for (int i = 0; i < TL; ++i) softplus(dt[i], &dt[i], &s);
-        if (a.f.z)
-#pragma unroll
-            for (int i = 0; i < TL; ++i) dp[i] *= swish_hw(R::value(x.z[i]));
-        if (t0 + T > n)
-#pragma unroll
-            for (int i = 0; i < TL; ++i)
-                if (t0 + 4 * i + q >= n) dt[i] = u[i] = dp[i] = 0.f;
+    ScanBlock<E, S> x;
+    typename Raw<E>::one dy[TL];
+    auto load = [&](int t0) {
+        x.load(a.f, row0, t0, q, lane, dc, g, true);
+        load_scalars<E, P>(ScanRows(row0, t0, a.f.N), a.dy, D, q, dc, dy);
+    };
+    if (first < c1) load(first);
+    for (int t0 = first; t0 < c1; t0 += T) {
+        float dt[TL], du[TL], u[TL], dp[TL];
+        x.steps(a.f, bias, n, t0, q, dt, u, du);
+        put_bc<E, P>(Bs, x.b, n, t0, lane);
+        put_bc<E, P>(Cs, x.c, n, t0, lane);
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
+            dp[i] = Raw<E>::value(dy[i]);
+            if (a.f.z) dp[i] *= swish_hw(Raw<E>::value(x.z[i]));
+            if (t0 + 4 * i + q >= n) dp[i] = 0.f;
             total += dt[i];
-            du[i] = dt[i] * u[i];
         }
-        if (cb + at.step < at.cb1) {
-            const int e = d + at.step * kScanCh;
-            x.load(a, rows, q, e < D ? e : D - 1);
+        if (t0 + T < c1) load(t0 + T);
+        lds_order();
+#pragma unroll
+        for (int k = 0; k < T; ++k) {
+            float B[SL], C[SL];
+            lds_vec<SL>(Bs + k * S + q * SL, B);
+            lds_vec<SL>(Cs + k * S + q * SL, C);
+            const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4), yk = quad_of(dp[k / 4], k % 4);
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                const float al = __builtin_amdgcn_exp2f(dk * A2[j]);
+                h[j] = fmaf(al, h[j], uk * B[j]);
+                p[j] *= al;
+                G[j] = fmaf(p[j], C[j] * yk, G[j]);
+            }
         }
         lds_order();
-        float al[T][SL];
-        grad_local<S>(Bs, Cs, q, A2, dt, du, dp, al, h, G);
-        total = lanes_sum<4>(total);
-        float p[SL];
-#pragma unroll
-        for (int j = 0; j < SL; ++j) p[j] = __builtin_amdgcn_exp2f(total * A2[j]);
-        ex_put<SL>(ex[parity][w][0], lane, h);
-        ex_put<SL>(ex[parity][w][1], lane, p);
-        ex_put<SL>(ex[parity][w][2], lane, G);
-        sums[parity][w][lane] = total;
-        __syncthreads();
-        // the waves take turns: two of them join the waves' parts, the states forward and the gradients back
-        if (w == turn) {
-#pragma unroll
-            for (int j = 0; j < SL; ++j) h[j] = 0.f;
-            total = 0.f;
-#pragma unroll
-            for (int v = 0; v < P::NW; ++v) {
-                float hv[SL], pv[SL];
-                ex_get<SL>(ex[parity][v][0], lane, hv);
-                ex_get<SL>(ex[parity][v][1], lane, pv);
-#pragma unroll
-                for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
-                total += sums[parity][v][lane];
-            }
-            if (d < D) {
-#pragma unroll
-                for (int j = 0; j < SL; ++j) a.f.seg_h[(seg0 + d) * S + q * SL + j] = h[j];
-                if (q == 0) a.f.seg_dt[seg0 + d] = total;
-            }
-        } else if (w == turn + 1) {
-#pragma unroll
-            for (int j = 0; j < SL; ++j) G[j] = 0.f;
-#pragma unroll
-            for (int v = P::NW - 1; v >= 0; --v) {
-                float gv[SL], pv[SL];
-                ex_get<SL>(ex[parity][v][2], lane, gv);
-                ex_get<SL>(ex[parity][v][1], lane, pv);
-#pragma unroll
-                for (int j = 0; j < SL; ++j) G[j] = fmaf(pv[j], G[j], gv[j]);
-            }
-            if (d < D)
-#pragma unroll
-                for (int j = 0; j < SL; ++j) a.seg_g[(seg0 + d) * S + q * SL + j] = G[j];
-        }
     }
+    total = lanes_sum<4>(total);
+    if (!SPLIT) {
+        if (d >= D) return;
+        state_put<SL>(a.f.seg_h + seg * S + q * SL, h);
+        state_put<SL>(a.seg_g + seg * S + q * SL, G);
+        if (q == 0) a.f.seg_dt[seg] = total;
+        return;
+    }
+    ex_put<SL>(ex[w][0], lane, h);
+    ex_put<SL>(ex[w][1], lane, p);
+    ex_put<SL>(ex[w][2], lane, G);
+    sums[w][lane] = total;
+    __syncthreads();
+    if (w > 1 || d >= D) return;
+    // two waves join the waves' parts, the states forward and the gradients back
+#pragma unroll
+    for (int j = 0; j < SL; ++j) h[j] = 0.f;
+    total = 0.f;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) {
+        const int o = w ? NW - 1 - v : v;
+        float hv[SL], pv[SL];
+        ex_get<SL>(ex[o][w ? 2 : 0], lane, hv);
+        ex_get<SL>(ex[o][1], lane, pv);
+#pragma unroll
+        for (int j = 0; j < SL; ++j) h[j] = fmaf(pv[j], h[j], hv[j]);
+        total += sums[v][lane];
+    }
+    state_put<SL>((w ? a.seg_g : a.f.seg_h) + seg * S + q * SL, h);
+    if (w == 0 && q == 0) a.f.seg_dt[seg] = total;
 }
 
 // Chunks' states and gradients from zero -> the states entering and the gradients leaving the chunks, in place.
@@ -285,9 +284,6 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
     __shared__ float ex[NW][3][64 * SL];
     __shared__ float red[NW][64 * SL];
     __shared__ float red2[NW][2][kScanCh];
-    // 64 decays and 64 states a lane leave no room for the rest: the states of the first half of the tokens wait in LDS
-    constexpr int HL = T * SL == 64 ? T / 2 : 0;
-    __shared__ float hs[NW][HL ? HL : 1][HL ? 64 * SL : 1];
     constexpr int NA = T * SL / 4;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), q = lane & 3;
     const int D = a.f.D, N = a.f.N;
@@ -417,7 +413,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
                     for (int j = 0; j < SL; ++j) gin[j] = fmaf(pv[e][j], gin[j], gv[e][j]);
         }
         lds_order();
-        float hh[T - HL][SL], hk[SL], yp[4], b2[2][GT][SL], c2[2][GT][SL];
+        float hh[T][SL], yp[4], b2[2][GT][SL], c2[2][GT][SL];
         lds_group<S, GT>(Bs, 0, q, b2[0]);
         lds_group<S, GT>(Cs, 0, q, c2[0]);
 #pragma unroll
@@ -427,16 +423,16 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
                 lds_group<S, GT>(Bs, k + GT, q, b2[gk ^ 1]);
                 lds_group<S, GT>(Cs, k + GT, q, c2[gk ^ 1]);
             }
+            if (k == 1)  // the gradient entering from behind: its parts have come by now
+#pragma unroll
+                for (int j = 0; j < SL; ++j) sum_now(gin[j]);
             const float uk = quad_of(du[k / 4], k % 4);
             yp[k % 4] = 0.f;
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
-                hk[j] = fmaf(al[k][j], k ? hk[j] : hin[j], uk * b2[gk][k % GT][j]);
-                yp[k % 4] = fmaf(c2[gk][k % GT][j], hk[j], yp[k % 4]);
-                if (k >= HL) hh[k >= HL ? k - HL : 0][j] = hk[j];
+                hh[k][j] = fmaf(al[k][j], k ? hh[k ? k - 1 : 0][j] : hin[j], uk * b2[gk][k % GT][j]);
+                yp[k % 4] = fmaf(c2[gk][k % GT][j], hh[k][j], yp[k % 4]);
             }
-            if constexpr (HL > 0)
-                if (k < HL) ex_put<SL>(hs[w][k < HL ? k : 0], lane, hk);
             if (k % 4 == 3) {
                 const float dz = fmaf(skip, u[k / 4], quad_sums(yp[0], yp[1], yp[2], yp[3], q)) * dzf[k / 4];
                 if (dz_p && own && t0 + k - 3 + q < N)
@@ -447,7 +443,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
         }
         // in reverse, from the group that the loop above read last
         constexpr int last = (T / GT - 1) & 1;
-        float dA[SL], hn[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
+        float dA[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
 #pragma unroll
         for (int j = 0; j < SL; ++j) dA[j] = 0.f;
 #pragma unroll
@@ -461,32 +457,24 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
             const float(&C)[SL] = c2[gk][k % GT];
             const float dk = quad_of(dt[k / 4], k % 4), uk = quad_of(du[k / 4], k % 4), yk = quad_of(dp[k / 4], k % 4);
             s1[k % 4] = s2[k % 4] = 0.f;
-            // hk: the state after this token; hp: before it, asked for from LDS one token ahead of its use
-            float hp[SL];
-#pragma unroll
-            for (int j = 0; j < SL; ++j) {
-                hp[j] = k == 0 ? hin[j] : k > HL ? hh[k > HL ? k - 1 - HL : 0][j] : hn[j];
-                if (k == T - 1) hk[j] = hh[T - 1 - HL][j];
-            }
-            if constexpr (HL > 0)
-                if (k > 1 && k - 2 < HL) ex_get<SL>(hs[w][k > 1 && k - 2 < HL ? k - 2 : 0], lane, hn);
 #pragma unroll
             for (int j = 0; j < SL; ++j) {
                 gin[j] = fmaf(C[j], yk, gin[j]);
                 const int at = SL == 2 ? 2 * (k & 1) + j : j & 3;
                 v[at] = uk * gin[j];
-                v[4 + at] = yk * hk[j];
+                v[4 + at] = yk * hh[k][j];
                 s1[k % 4] = fmaf(gin[j], B[j], s1[k % 4]);
                 gin[j] *= al[k][j];
-                const float along = gin[j] * hp[j];
-                hk[j] = hp[j];
+                const float along = gin[j] * (k ? hh[k ? k - 1 : 0][j] : hin[j]);
                 s2[k % 4] = fmaf(A2[j], along, s2[k % 4]);
                 dA[j] = fmaf(dk, along, dA[j]);
                 if constexpr (SL >= 4)
-                    if (j % 4 == 3) acc[k * (SL / 4) + j / 4] += halving_sums(v, lane);
+                    if (j % 4 == 3) sum_now(acc[k * (SL / 4) + j / 4] += halving_sums(v, lane));
             }
             if constexpr (SL == 2)
-                if (k % 2 == 0) acc[k / 2] += halving_sums(v, lane);
+                if (k % 2 == 0) sum_now(acc[k / 2] += halving_sums(v, lane));
+#pragma unroll
+            for (int j = 0; j < SL; ++j) sum_now(dA[j]);
             if (k % 4 == 0) {
                 const int i = k / 4;
                 const float gb = quad_sums(s1[0], s1[1], s1[2], s1[3], q), ak = quad_sums(s2[0], s2[1], s2[2], s2[3], q);
@@ -494,6 +482,8 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
                 const float x1 = fmaf(skip, dp[i], dt[i] * gb), x2 = fmaf(kLn2, ak, u[i] * gb) * slope[i];
                 dskip = fmaf(dp[i], u[i], dskip);
                 dbias += x2;
+                sum_now(dskip);
+                sum_now(dbias);
                 if (own && t0 + k + q < N) {
                     const uint32_t o = __umul24(k + q, (uint32_t)D * (uint32_t)sizeof(ost)) + d * (uint32_t)sizeof(ost);
                     store_out((ost*)(du_row + o), x1);
@@ -503,7 +493,9 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
             if (k % GT == 0) lds_order();
             if (k == T / 2 && cb + pos.step < cb1) {  // half of the decays and states are done with: room for the next channels
                 const int e = d + pos.step * kScanCh;
-                x.load(a, rows, q, e < D ? e : D - 1);
+                int ql = q;  // the rows' offsets, made anew: kept from turn to turn they would take registers
+                __asm__ volatile("" : "+v"(ql));
+                x.load(a, rows, ql, e < D ? e : D - 1);
             }
         }
         dskip = lanes_sum<4>(dskip);
@@ -561,7 +553,7 @@ __global__ __launch_bounds__(256) void scan_sum_bc_kernel(ScanBwdArgs a) {
 
 template <class E, class O, int S>
 bool pick(ScanBwdKernels* o) {
-    *o = {scan_local_bwd_kernel<E, S>, scan_join_bwd_kernel<S>, scan_grad_kernel<E, O, S>, scan_sum_bc_kernel<O, S>,
+    *o = {scan_local_bwd_kernel<E, S, false>, scan_local_bwd_kernel<E, S, true>, scan_join_bwd_kernel<S>, scan_grad_kernel<E, O, S>, scan_sum_bc_kernel<O, S>,
           GradShape<S>::CH, GradShape<S>::NW};
     return true;
 }
