@@ -620,7 +620,7 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
  * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 128 tokens (32 and 16 at 32
  * and 64 states), partial sums of db and dc over up to 512 channels and of dA over a chunk). Limits as the forward's in
  * segments. Sums have one order: the same call gives the same bits. opts: the timer. Kernels: "ret_scan_local_bwd",
- * "ret_scan_join_bwd", "ret_scan_grad", "ret_scan_sum_bc", "ret_column_sums".
+ * "ret_scan_join_bwd", "ret_scan_grad", "ret_scan_sums".
  */
 size_t ret_selective_scan_bwd_workspace_bytes(int B, int N, int D, int S, int G, ret_dtype_t in_dt);
 ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,

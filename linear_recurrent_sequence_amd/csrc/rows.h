@@ -111,6 +111,38 @@ struct PartSumArgs {
     long long n, n0, n1;
     int parts;
 };
+// 64 columns per workgroup, the rows dealt to its 16 waves, 8 loads of a wave in flight.
+__device__ __forceinline__ void part_sums(const PartSumArgs& a, long long block) {
+    constexpr int NW = kColSumThreads / 64, U = 8;
+    __shared__ float part[kColSumThreads];
+    const long long c = block * kColSumCols + (threadIdx.x & 63);
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool in = c < a.n;
+    const float* p = a.partial + (in ? c : 0);
+    float s = 0.f;
+    for (int r = w; r < a.parts; r += NW * U) {
+        float x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int q = r + i * NW;
+            x[i] = p[(q < a.parts ? q : r) * a.n];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) s += r + i * NW < a.parts ? x[i] : 0.f;
+    }
+    part[threadIdx.x] = s;
+    __syncthreads();
+    if (w != 0 || !in) return;
+#pragma unroll
+    for (int i = 1; i < NW; ++i) s += part[threadIdx.x + 64 * i];
+    if (c < a.n0) {
+        if (a.out0) a.out0[c] = s;
+    } else if (c < a.n0 + a.n1) {
+        if (a.out1) a.out1[c - a.n0] = s;
+    } else {
+        if (a.out2) a.out2[c - a.n0 - a.n1] = s;
+    }
+}
 typedef void (*part_sum_kernel_t)(PartSumArgs);
 part_sum_kernel_t part_sum_kernel_get();  // kColSumCols columns a workgroup of kColSumThreads
 

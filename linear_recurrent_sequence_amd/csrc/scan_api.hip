@@ -139,7 +139,7 @@ BwdPlan make_bwd_plan(const Shape& s, int chunk, int waves) {
 unsigned long long by8(unsigned long long n) { return (n + 7) / 8 * 8; }
 
 struct Grids {
-    unsigned long long local, units, join, grad, bc;
+    unsigned long long local, units, join, grad, bc, cols;
 };
 ret_status_t fits(const Shape& s, bool ok) {
     if (ok) return RET_OK;
@@ -156,10 +156,11 @@ ret_status_t bwd_grids(const Shape& s, const BwdPlan& p, int threads, Grids* g) 
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
     g->local = by8((unsigned long long)p.lblocks * p.nchunks * s.B);
     g->grad = by8((unsigned long long)p.parts_g * s.G * p.nchunks * s.B);
-    g->bc = ((unsigned long long)s.B * s.N * 2 * s.S + 255) / 256;
+    g->bc = ((unsigned long long)s.B * s.N * 2 * s.S * s.G + kColSumThreads - 1) / kColSumThreads;
+    g->cols = ((unsigned long long)s.D * (s.S + 2) + kColSumCols - 1) / kColSumCols;
     return fits(s, grid_fits(g->join, s.B, 2, 256) &&
-                       grid_fits(g->local, 1, 1, threads) && grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc, s.G, 1, 256) &&
-                       grid_fits(((unsigned long long)s.D * (s.S + 2) + kColSumCols - 1) / kColSumCols, 1, 1, kColSumThreads) &&
+                       grid_fits(g->local, 1, 1, threads) &&
+                       grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc + g->cols, 1, 1, kColSumThreads) &&
                        (long long)p.nchunks * s.B <= INT32_MAX / 2);
 }
 
@@ -327,18 +328,16 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     a.seg_g = (float*)((char*)workspace + p.seg_g);
     a.part_a = (float*)((char*)workspace + p.part_a), a.part_bc = (float*)((char*)workspace + p.part_bc);
     a.du = du, a.ddt = ddt, a.dz = dz, a.db = db, a.dc = dc, a.parts_g = p.parts_g;
+    a.bc_blocks = (unsigned)g.bc;
+    a.cols = {a.part_a, dA, dd_skip, ddt_bias, (long long)D * (S + 2), (long long)D * S, D, B * p.nchunks};
+    const bool cols = dA || dd_skip || ddt_bias;
     hipStream_t sm = (hipStream_t)stream;
     if ((st = launch("ret_scan_local_bwd", p.split ? k.local_split : k.local, dim3((unsigned)g.local), 64 * k.waves, sm, op,
                      a)) != RET_OK)
         return st;
     if ((st = launch("ret_scan_join_bwd", k.join, dim3((unsigned)g.join, B, 2), 256, sm, op, a)) != RET_OK) return st;
     if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
-    if ((st = launch("ret_scan_sum_bc", k.sum_bc, dim3((unsigned)g.bc, G), 256, sm, op, a)) != RET_OK) return st;
-    if (!dA && !dd_skip && !ddt_bias) return RET_OK;
-    const long long n = (long long)D * (S + 2);
-    const PartSumArgs P = {a.part_a, dA, dd_skip, ddt_bias, n, (long long)D * S, D, B * p.nchunks};
-    return launch("ret_column_sums", part_sum_kernel_get(), dim3((unsigned)((n + kColSumCols - 1) / kColSumCols)),
-                  kColSumThreads, sm, op, P);
+    return launch("ret_scan_sums", k.sums, dim3((unsigned)(g.bc + (cols ? g.cols : 0))), kColSumThreads, sm, op, a);
 }
 
 }  // extern "C"

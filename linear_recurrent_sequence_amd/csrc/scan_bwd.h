@@ -1,6 +1,7 @@
 // Gradients of the selective scan: arguments and kernels.
 #pragma once
 
+#include "rows.h"
 #include "scan.h"
 
 namespace ret {
@@ -15,10 +16,12 @@ struct ScanBwdArgs {
     float* part_a;                             // [B nseg][D (S + 2)]: dA, dskip, dbias
     void *du, *ddt, *dz, *db, *dc;             // dz or null
     int parts_g;                               // parts a group of channels, each every parts_g-th block of 16
+    PartSumArgs cols;                          // dA, dskip and dbias from part_a
+    unsigned bc_blocks;                        // workgroups of sums for dB and dC, before those for cols
 };
 typedef void (*scan_bwd_kernel_t)(ScanBwdArgs);
 struct ScanBwdKernels {
-    scan_bwd_kernel_t local, local_split, join, grad, sum_bc;
+    scan_bwd_kernel_t local, local_split, join, grad, sums;
     int chunk, waves;
 };
 bool scan_bwd_kernels_get(bool bf16_in, bool bf16_out, int S, ScanBwdKernels* o);

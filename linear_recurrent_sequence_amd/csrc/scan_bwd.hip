@@ -339,10 +339,10 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
         const bool own = d < D;
         const float skip = a.f.skip && own ? a.f.skip[d] : 0.f;
         float A2[SL], hin[SL], gin[SL];
-        state_get<SL>(seg_h + (long long)dc * S + q * SL, hin);
-        state_get<SL>(seg_g + (long long)dc * S + q * SL, gin);
 #pragma unroll
         for (int j = 0; j < SL; ++j) A2[j] = decay_rate(x.A[j]);
+        state_get<SL>(seg_h + (long long)dc * S + q * SL, hin);
+        state_get<SL>(seg_g + (long long)dc * S + q * SL, gin);
         float u[TL], dt[TL], du[TL], slope[TL], dp[TL], dzf[TL], total = 0.f;  // dzf: dy silu'(z)
 #pragma unroll
         for (int i = 0; i < TL; ++i) {
@@ -532,18 +532,20 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
     }
 }
 
-// dB and dC from the parts of their group.
+// dB and dC from the parts of their group, and the sums of part_a.
 template <class O, int S>
-__global__ __launch_bounds__(256) void scan_sum_bc_kernel(ScanBwdArgs a) {
-    const long long rows = (long long)a.f.B * a.f.N, i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= rows * 2 * S) return;
-    const int g = blockIdx.y, which = (int)(i / S % 2), s = (int)(i % S);
-    const float* p = a.part_bc + (long long)g * a.parts_g * rows * 2 * S + i;
+__global__ __launch_bounds__(kColSumThreads) void scan_sums_kernel(ScanBwdArgs a) {
+    if (blockIdx.x >= a.bc_blocks) return part_sums(a.cols, blockIdx.x - a.bc_blocks);
+    const long long rows = (long long)a.f.B * a.f.N, per = rows * 2 * S;
+    const long long id = (long long)blockIdx.x * kColSumThreads + threadIdx.x, i = id % per;
+    const int g = (int)(id / per), which = (int)(i / S % 2), s = (int)(i % S);
+    if (g >= a.f.G) return;
+    const float* p = a.part_bc + (long long)g * a.parts_g * per + i;
     float t = 0.f;
     for (int k = 0; k < a.parts_g; k += 8) {
         float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = p[(k + e < a.parts_g ? k + e : k) * rows * 2 * S];
+        for (int e = 0; e < 8; ++e) x[e] = p[(k + e < a.parts_g ? k + e : k) * per];
 #pragma unroll
         for (int e = 0; e < 8; ++e) t += k + e < a.parts_g ? x[e] : 0.f;
     }
@@ -553,7 +555,8 @@ __global__ __launch_bounds__(256) void scan_sum_bc_kernel(ScanBwdArgs a) {
 
 template <class E, class O, int S>
 bool pick(ScanBwdKernels* o) {
-    *o = {scan_local_bwd_kernel<E, S, false>, scan_local_bwd_kernel<E, S, true>, scan_join_bwd_kernel<S>, scan_grad_kernel<E, O, S>, scan_sum_bc_kernel<O, S>,
+    *o = {scan_local_bwd_kernel<E, S, false>, scan_local_bwd_kernel<E, S, true>, scan_join_bwd_kernel<S>,
+          scan_grad_kernel<E, O, S>, scan_sums_kernel<O, S>,
           GradShape<S>::CH, GradShape<S>::NW};
     return true;
 }
