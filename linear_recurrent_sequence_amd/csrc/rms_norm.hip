@@ -6,7 +6,9 @@
 //
 // A row is held in the registers of L lanes (4 to 16 values each), as in layer_norm.hip, so that each tensor is read once;
 // the maxima of |y| come from the same registers. The weight's gradient leaves one partial row per workgroup, added up in a
-// fixed order by a second kernel.
+// fixed order by a second kernel. Bound by HBM: 8192 x 4096 bf16 with residual, in bf16 and in 8 bits with a scale for 128
+// columns, 57 us (5.3 TB/s, a large copy reaches 5.1); its gradients 45 us and 4.4 for the sums; 128 rows 4.7 us, of
+// which a launch is most.
 #include "host.h"
 #include "rows.h"
 

@@ -42,8 +42,9 @@ struct ScanArgs {
     float *seg_h, *seg_dt;               // [B][nseg][D][S], [B][nseg][D]
     long long ldz, ldb, ldc;
     int B, N, D, G, nseg, seg_tokens;
-    int cblocks;                         // blocks of 16 channels (walk: of 64)
+    int cblocks;                         // blocks of a workgroup's channels
     int softplus, bc_vec;                // bc_vec: b and c may be read four values at a time
+    int deal;                            // of workgroups to the XCDs: ScanDeal
 };
 
 // One value of either type as fp32.
@@ -293,13 +294,34 @@ __device__ __forceinline__ void state_put(float* p, const float (&f)[SL]) {
 struct ScanPos {
     int cb, seg, b;
 };
+// Workgroup -> unit of `units` (blocks of channels, or several) and number of its segment and sequence, by the XCDs:
+enum ScanDeal {
+    kDealRanges,  // a range of all, the units of a segment first
+    kDealUnits,   // a range of the units (a multiple of 8) with all their segments and sequences
+    kDealSegs,    // every eighth segment with all its units; an odd number a sequence, so that they begin on different XCDs
+};
+__host__ __device__ __forceinline__ int deal_segs(int deal, int nseg) { return deal == kDealSegs ? nseg | 1 : nseg; }
+__device__ __forceinline__ long long scan_order(int units, int deal, int* unit) {
+    const long long id = blockIdx.x, j = id >> 3;
+    if (deal == kDealUnits) {
+        const int u8 = units >> 3;
+        *unit = (int)(id & 7) * u8 + (int)(j % u8);
+        return j / u8;
+    }
+    if (deal == kDealSegs) {
+        *unit = (int)(j % units);
+        return j / units * 8 + (id & 7);
+    }
+    const long long o = xcd_order(id, gridDim.x);
+    *unit = (int)(o % units);
+    return o / units;
+}
 __device__ __forceinline__ bool scan_pos(const ScanArgs& a, ScanPos* p) {
-    const long long id = xcd_order(blockIdx.x, gridDim.x);
-    p->cb = (int)(id % a.cblocks);
-    const long long rest = id / a.cblocks;
-    p->seg = (int)(rest % a.nseg);
-    p->b = (int)(rest / a.nseg);
-    return p->b < a.B;
+    const long long rest = scan_order(a.cblocks, a.deal, &p->cb);
+    const int segs = deal_segs(a.deal, a.nseg);
+    p->seg = (int)(rest % segs);
+    p->b = (int)(rest / segs);
+    return p->b < a.B && p->seg < a.nseg;
 }
 
 typedef void (*scan_kernel_t)(ScanArgs);

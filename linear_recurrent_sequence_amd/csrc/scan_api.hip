@@ -136,32 +136,45 @@ BwdPlan make_bwd_plan(const Shape& s, int chunk, int waves) {
     return p;
 }
 
-unsigned long long by8(unsigned long long n) { return (n + 7) / 8 * 8; }
+// How workgroups are dealt to the 8 XCDs. Without lengths: each gets a range. With lengths that would leave the XCDs that have
+// the short sequences idle: where there are many segments they are dealt in turn; else the units of `channels` channels are, if
+// that leaves lines of 128 bytes in one piece. Ranges and dealt, us, at 16 states, 8192 channels and sequences of 2741, 1500, 900
+// and 100 tokens: forward 472, 410 (units; whole sequences take 475), gradients 2200, 1208 (segments; 2030 where only the units
+// of the local pass can be dealt; whole ones take 2167). 4096 and 500 tokens of 1024 channels forward 79, 58.
+constexpr long long kDealSegsLeast = 32;
+ScanDeal deal(const int32_t* lengths, long long segs, int units, int channels, size_t e) {
+    if (!lengths) return kDealRanges;
+    if (segs >= kDealSegsLeast) return kDealSegs;
+    return units % 8 == 0 && units / 8 * channels * e % 128 == 0 ? kDealUnits : kDealRanges;
+}
+unsigned long long deal_grid(ScanDeal d, int nseg, int B, int units) {
+    const unsigned long long segs = (unsigned long long)deal_segs(d, nseg) * B;
+    return d == kDealSegs ? (segs + 7) / 8 * 8 * units : (segs * units + 7) / 8 * 8;
+}
 
+// Grids and whether they fit; those that are dealt by deal() at their largest.
 struct Grids {
-    unsigned long long local, units, join, grad, bc, cols;
+    unsigned long long join, bc, cols;
 };
 ret_status_t fits(const Shape& s, bool ok) {
     if (ok) return RET_OK;
     return fail(RET_ERR_UNSUPPORTED, "selective scan: B=%d N=%d D=%d S=%d exceed a launch", s.B, s.N, s.D, s.S);
 }
 ret_status_t fwd_grids(const Shape& s, const Plan& p, const ScanKernels& k, Grids* g) {
-    g->local = by8((unsigned long long)p.wblocks * p.nseg * s.B);
-    g->units = p.walk ? g->local : by8((unsigned long long)p.cblocks * p.nseg * s.B);
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
-    return fits(s, grid_fits(g->local, 1, 1, 64 * kWalkWaves) && grid_fits(g->units, 1, 1, p.walk ? 64 * kWalkWaves : k.threads) &&
+    return fits(s, grid_fits(deal_grid(kDealSegs, p.nseg, s.B, p.wblocks), 1, 1, 64 * kWalkWaves) &&
+                       (p.walk || grid_fits(deal_grid(kDealSegs, p.nseg, s.B, p.cblocks), 1, 1, k.threads)) &&
                        (p.nseg == 1 || grid_fits(g->join, s.B, 1, 256)));
 }
 ret_status_t bwd_grids(const Shape& s, const BwdPlan& p, int threads, Grids* g) {
+    const long long segs = (long long)p.nchunks * s.B;
     g->join = ((unsigned long long)s.D * s.S + 255) / 256;
-    g->local = by8((unsigned long long)p.lblocks * p.nchunks * s.B);
-    g->grad = by8((unsigned long long)p.parts_g * s.G * p.nchunks * s.B);
     g->bc = ((unsigned long long)s.B * s.N * 2 * s.S * s.G + kColSumThreads - 1) / kColSumThreads;
     g->cols = ((unsigned long long)s.D * (s.S + 2) + kColSumCols - 1) / kColSumCols;
     return fits(s, grid_fits(g->join, s.B, 2, 256) &&
-                       grid_fits(g->local, 1, 1, threads) &&
-                       grid_fits(g->grad, 1, 1, threads) && grid_fits(g->bc + g->cols, 1, 1, kColSumThreads) &&
-                       (long long)p.nchunks * s.B <= INT32_MAX / 2);
+                       grid_fits(deal_grid(kDealSegs, p.nchunks, s.B, p.lblocks), 1, 1, threads) &&
+                       grid_fits(deal_grid(kDealSegs, p.nchunks, s.B, p.parts_g * s.G), 1, 1, threads) &&
+                       grid_fits(g->bc + g->cols, 1, 1, kColSumThreads) && segs <= INT32_MAX / 2);
 }
 
 template <class K, class A>
@@ -230,14 +243,19 @@ ret_status_t ret_selective_scan_fwd(const void* u, const void* dt, const float* 
     a.ldz = ld.z, a.ldb = ld.b, a.ldc = ld.c;
     a.B = B, a.N = N, a.D = D, a.G = G, a.nseg = p.nseg, a.seg_tokens = p.seg_tokens, a.cblocks = p.wblocks;
     a.softplus = softplus != 0, a.bc_vec = vectors(b, c, ld, in_dt);
+    const long long segs = (long long)p.nseg * B;
+    const ScanDeal dl = deal(lengths, segs, p.wblocks, kWalkWaves * kScanCh, e);
+    const dim3 waves((unsigned)deal_grid(dl, p.nseg, B, p.wblocks));
+    a.deal = dl;
     hipStream_t sm = (hipStream_t)stream;
     if (split) {
-        if ((st = launch("ret_scan_local", k.local, dim3((unsigned)g.local), 64 * kWalkWaves, sm, op, a)) != RET_OK) return st;
+        if ((st = launch("ret_scan_local", k.local, waves, 64 * kWalkWaves, sm, op, a)) != RET_OK) return st;
         if ((st = launch("ret_scan_join", k.join, dim3((unsigned)g.join, B), 256, sm, op, a)) != RET_OK) return st;
     }
-    if (p.walk) return launch("ret_scan_walk", k.walk, dim3((unsigned)g.units), 64 * kWalkWaves, sm, op, a);
-    a.cblocks = p.cblocks;
-    return launch("ret_scan_chunks", k.chunks, dim3((unsigned)g.units), k.threads, sm, op, a);
+    if (p.walk) return launch("ret_scan_walk", k.walk, waves, 64 * kWalkWaves, sm, op, a);
+    const ScanDeal dc = deal(lengths, segs, p.cblocks, kScanCh, e);
+    a.cblocks = p.cblocks, a.deal = dc;
+    return launch("ret_scan_chunks", k.chunks, dim3((unsigned)deal_grid(dc, p.nseg, B, p.cblocks)), k.threads, sm, op, a);
 }
 
 ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float* A, const void* b, int64_t b_ld,
@@ -324,6 +342,10 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     f.ldz = ld.z, f.ldb = ld.b, f.ldc = ld.c;
     f.B = B, f.N = N, f.D = D, f.G = G, f.nseg = p.nchunks, f.seg_tokens = k.chunk, f.cblocks = p.lblocks;
     f.softplus = softplus != 0, f.bc_vec = vectors(b, c, ld, in_dt);
+    const long long segs = (long long)p.nchunks * B;
+    const ScanDeal dl = deal(lengths, segs, p.lblocks, p.split ? kScanCh : k.waves * kScanCh, e);
+    const ScanDeal dg = deal(lengths, segs, p.parts_g * G, kScanCh, e);
+    f.deal = dl, a.deal_parts = dg;
     a.dy = dy, a.dstate_out = dstate_out, a.dstate_in = dstate_in;
     a.seg_g = (float*)((char*)workspace + p.seg_g);
     a.part_a = (float*)((char*)workspace + p.part_a), a.part_bc = (float*)((char*)workspace + p.part_bc);
@@ -332,11 +354,13 @@ ret_status_t ret_selective_scan_bwd(const void* u, const void* dt, const float* 
     a.cols = {a.part_a, dA, dd_skip, ddt_bias, (long long)D * (S + 2), (long long)D * S, D, B * p.nchunks};
     const bool cols = dA || dd_skip || ddt_bias;
     hipStream_t sm = (hipStream_t)stream;
-    if ((st = launch("ret_scan_local_bwd", p.split ? k.local_split : k.local, dim3((unsigned)g.local), 64 * k.waves, sm, op,
-                     a)) != RET_OK)
+    if ((st = launch("ret_scan_local_bwd", p.split ? k.local_split : k.local,
+                     dim3((unsigned)deal_grid(dl, p.nchunks, B, p.lblocks)), 64 * k.waves, sm, op, a)) != RET_OK)
         return st;
     if ((st = launch("ret_scan_join_bwd", k.join, dim3((unsigned)g.join, B, 2), 256, sm, op, a)) != RET_OK) return st;
-    if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)g.grad), 64 * k.waves, sm, op, a)) != RET_OK) return st;
+    if ((st = launch("ret_scan_grad", k.grad, dim3((unsigned)deal_grid(dg, p.nchunks, B, p.parts_g * G)), 64 * k.waves, sm, op,
+                     a)) != RET_OK)
+        return st;
     return launch("ret_scan_sums", k.sums, dim3((unsigned)(g.bc + (cols ? g.cols : 0))), kColSumThreads, sm, op, a);
 }
 

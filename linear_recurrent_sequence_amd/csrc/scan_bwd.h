@@ -17,6 +17,7 @@ struct ScanBwdArgs {
     void *du, *ddt, *dz, *db, *dc;             // dz or null
     int parts_g;                               // parts a group of channels, each every parts_g-th block of 16
     PartSumArgs cols;                          // dA, dskip and dbias from part_a
+    int deal_parts;                            // of grad's workgroups to the XCDs
     unsigned bc_blocks;                        // workgroups of sums for dB and dC, before those for cols
 };
 typedef void (*scan_bwd_kernel_t)(ScanBwdArgs);

@@ -113,15 +113,15 @@ struct GradPos {
 };
 __device__ __forceinline__ bool grad_pos(const ScanBwdArgs& a, GradPos* p) {
     const int parts = a.parts_g * a.f.G, blocks_g = (a.f.D / a.f.G + kScanCh - 1) / kScanCh;
-    const long long id = xcd_order(blockIdx.x, gridDim.x);
-    p->part = (int)(id % parts);
-    p->chunk = (int)(id / parts % a.f.nseg);
-    p->b = (int)(id / parts / a.f.nseg);
+    const long long rest = scan_order(parts, a.deal_parts, &p->part);
+    const int segs = deal_segs(a.deal_parts, a.f.nseg);
+    p->chunk = (int)(rest % segs);
+    p->b = (int)(rest / segs);
     p->g = p->part / a.parts_g;
     p->step = a.parts_g;
     p->cb0 = p->g * blocks_g + p->part % a.parts_g;
     p->cb1 = (p->g + 1) * blocks_g;
-    return p->b < a.f.B;
+    return p->b < a.f.B && p->chunk < a.f.nseg;
 }
 
 // What each chunk leaves of a state from zero (h) and of a gradient behind it from zero (G), in one walk along the tokens: with

@@ -1,12 +1,20 @@
-// Selective scan over sequences, forward. Bound by the vector units: per token, channel and state one exp2 (a quarter of the
-// rate of the other instructions) and four products or sums where the states are reached in one pass.
+// Selective scan over sequences, forward. Bound by the vector units: per token, channel and state one exp2 (about twice the time
+// of the other instructions) and four products or sums where the states are reached in one pass, 24 cycles of a SIMD for 64 of
+// them; the tensors' bytes take half of that time at 16 states.
 //
-// full: a workgroup walks the chunks of its segment, NW waves a chunk, each its own T tokens. A wave computes its decays once,
-// keeps them in 64 registers a lane, and from them the state its tokens leave if they start from zero; the waves exchange
+// walk: a wave takes 16 channels along the tokens with their states in registers; one pass, for as many waves as there are
+// blocks of channels. 4 x 2741 tokens of 8192 channels (16 states, bf16, gated): 470 us, 2 waves a SIMD, each of them 185
+// cycles a token where 124 are left when 8 share the SIMD.
+//
+// chunks: a workgroup walks the chunks of its sequence, NW waves a chunk, each its own T tokens. A wave computes its decays
+// once, keeps them in 64 registers a lane, and from them the state its tokens leave if they start from zero; the waves exchange
 // these with the products of their decays, each forms the state entering its tokens, and goes over them again with the
-// decays it kept (three products a state more, where a second exp2 would cost the time of four). Few sequences of few channels
-// do not fill the card: they are split into segments, whose states from zero (local) are joined by their decays,
-// exp(A sum dt) (join), before full starts from them.
+// decays it kept (three products a state more, where a second exp2 would cost the time of four). A token takes 30 ns where a
+// walking wave takes 122, but three times the instructions: for few blocks of channels. 64 tokens of 128 channels 7.6 us.
+//
+// Few, long sequences are cut into segments: local, a walk, leaves each segment's state from zero; join carries the states
+// over the segments by their decays, exp(A sum dt); then the walk starts from them. 65536 tokens of 1024 channels: 219 + 15 +
+// 244 us; the two passes are within 1.3 of the cycles above.
 #include "scan.h"
 
 namespace ret {

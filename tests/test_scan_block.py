@@ -263,6 +263,42 @@ def test_plans_agree(R, shape, kernels):
         assert ((h - outs[0][1]).abs() <= k * hs + 1e-30).all()
 
 
+@pytest.mark.parametrize("shape", [(3, 200, 512, 16), (2, 700, 1024, 16), (1, 5000, 512, 16), (5, 1000, 48, 8), (40, 20, 256, 32)],
+                         ids=str)
+def test_lengths_of_whole_sequences(R, shape):
+    """Lengths change which part of the card does what, and nothing else: with those of whole sequences every output is that of
+    the call without, bit for bit, and with others each sequence's is the same wherever in the batch it stands."""
+    import torch
+    B, N, D, S = shape
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(torch.bfloat16)  # noqa: E731
+    t = dict(u=r(B, N, D), dt=r(B, N, D), b=r(B, N, 1, S), c=r(B, N, 1, S), z=r(B, N, D), dy=r(B, N, D),
+             h0=r(B, D, S).float(), dh=r(B, D, S).float())
+    A, bias = -1 - torch.rand((D, S), generator=gen, device="cuda"), torch.full((D,), -3.0, device="cuda")
+
+    def call(t, lengths):
+        e = torch.empty_like
+        o = {k: e(t[k]) for k in ("u", "dt", "b", "c", "z", "dy", "h0", "dh")}
+        dA, db = e(A), e(bias)
+        R.ret_selective_scan_fwd(t["u"], t["dt"], A, t["b"], t["c"], o["dy"], z=t["z"], dt_bias=bias, lengths=lengths,
+                                 state_in=t["h0"], state_out=o["h0"])
+        R.ret_selective_scan_bwd(t["u"], t["dt"], A, t["b"], t["c"], t["dy"], o["u"], o["dt"], dA, o["b"], o["c"], z=t["z"],
+                                 dz=o["z"], dt_bias=bias, ddt_bias=db, lengths=lengths, state_in=t["h0"],
+                                 dstate_out=t["dh"], dstate_in=o["dh"])
+        return o, (dA, db)
+    print_case("lengths", B, N, D, S)
+    want, sums = call(t, None)
+    got, sums2 = call(t, torch.full((B,), N, dtype=torch.int32, device="cuda"))
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    assert torch.equal(sums[0], sums2[0]) and torch.equal(sums[1], sums2[1])
+    lengths = torch.tensor([[0, 1, N, N // 3, 17][i % 5] for i in range(B)], dtype=torch.int32, device="cuda")
+    one, _ = call(t, lengths)
+    two, _ = call({k: v.flip(0) for k, v in t.items()}, lengths.flip(0))
+    for k in want:
+        assert torch.equal(one[k], two[k].flip(0)), k
+
+
 def test_channels_apart(R):
     """A call's channels are those of calls on parts of them, bit for bit, and db and dc the parts' sums: each adds its channels
     in an order of its own, at most D roundings apart."""
