@@ -58,26 +58,30 @@ __device__ __forceinline__ uint32_t lanes_umax(uint32_t v, int n = L) {
     return v;
 }
 
-__device__ __forceinline__ float scale_of_max(uint32_t m) {
-    const float s = __uint_as_float(m) / kE4m3Max;
+// f: what a value is multiplied by for the one of y; m: the largest of the values.
+__device__ __forceinline__ float scale_of_max(uint32_t m, float f) {
+    const float s = __uint_as_float(m) * f / kE4m3Max;
     return s < kMinScale ? kMinScale : s;  // NaN stays
 }
 
-// W values (hi + lo) / scale in e4m3, rounded to nearest even. lo is what hi's two products lost, and the quotient is corrected by
-// its remainder, so that only the errors of rstd and scale decide which way a value next to a border between two of the format's
-// goes. With hi times the rounded reciprocal of scale more values fell on the other side than in a plain form that divides (the
-// error of all values was over 1.5 times as large); the time is the same, HBM bounds it.
+// W values (hi + lo) f / scale in e4m3, rounded to nearest even, where scale is m f / 448: 448 (hi + lo) / m, the quotient in two
+// parts, so that f has no part in it and only the rounding of m decides which way a value next to a border between two of the
+// format's goes. With y and scale as they are rounded one of 500000 values fell on the other side in every second call; the
+// time is the same, HBM bounds it.
 template <int W>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* hi, const float* lo, float scale) {
-    const float inv = 1.f / scale;
-    const float back = scale <= 3.4e38f ? scale : 0.f;  // an infinite scale has no remainder
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float* hi, const float* lo, float scale, uint32_t m, float f) {
+    const float top = __uint_as_float(m);
+    const bool plain = !(scale > kMinScale && scale <= 3.4e38f && top > 1e-30f);  // no quotient by m
+    const float inv = 1.f / (plain ? scale : top), inv448 = kE4m3Max * inv;
     float q[W];
 #pragma unroll
     for (int e = 0; e < W; ++e) {
-        q[e] = hi[e] * inv;
-        const float rest = fmaf(-q[e], back, hi[e]) + lo[e];
-        if (back != 0.f) q[e] = fmaf(rest, inv, q[e]);
+        const float t = hi[e] * inv;
+        q[e] = fmaf(kE4m3Max, t, (fmaf(-t, top, hi[e]) + lo[e]) * inv448);
     }
+    if (plain)
+#pragma unroll
+        for (int e = 0; e < W; ++e) q[e] = hi[e] * f * inv;
     if constexpr (W == 8) {
         uint2 u = make_uint2(0, 0);
         u.x = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], u.x, false);
@@ -132,29 +136,33 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(RmsArgs a) {
         for (int i = threadIdx.x; i < NG * G; i += THREADS) gtop[i] = 0;  // before the barriers below
     const float rstd = 1.f / sqrtf(sum(s2) * (1.f / (float)a.D) + a.eps);
     if (live && lane == 0 && a.rstd) a.rstd[row] = rstd;
+    // 8 bits: y = w s p2 f with p2 the power of two in rstd, so that only the product with w rounds; lo is what it loses
+    const bool normal = rstd > kMinScale && rstd < 3e38f;
+    const float p2 = normal ? __uint_as_float(__float_as_uint(rstd) & 0x7f800000u) : rstd;
+    const float f = normal ? __uint_as_float((__float_as_uint(rstd) & 0x007fffffu) | 0x3f800000u) : 1.f;
     uint32_t m = 0, mk[K];
-    float lo[Q ? K : 1][W];  // what the two products of a value lose
+    float lo[Q ? K : 1][W];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
         const int c = (k * L + lane) * W;
         mk[k] = 0;
         if (c >= a.D) continue;
         if (live && a.sum) row_store<W>(a.sum, base + c, a.x_bf16, x[k]);
-        float w[W];
+        float w[W], y[W];
         if (a.weight) row_load<W>(a.weight, c, false, w);
 #pragma unroll
         for (int e = 0; e < W; ++e) {
-            const float xh = x[k][e] * rstd;
-            if constexpr (Q) lo[k][e] = fmaf(x[k][e], rstd, -xh);
-            x[k][e] = xh;
-            if (a.weight) {
-                x[k][e] = xh * w[e];
-                if constexpr (Q) lo[k][e] = fmaf(lo[k][e], w[e], fmaf(xh, w[e], -x[k][e]));
+            const float v = x[k][e], xh = v * rstd;
+            y[e] = a.weight ? xh * w[e] : xh;
+            if constexpr (Q) {
+                const float u = v * p2;
+                x[k][e] = a.weight ? u * w[e] : u;
+                lo[k][e] = a.weight ? fmaf(u, w[e], -x[k][e]) : 0.f;
+                mk[k] = umax(mk[k], __float_as_uint(x[k][e]) & 0x7fffffffu);
             }
-            if constexpr (Q) mk[k] = umax(mk[k], __float_as_uint(x[k][e]) & 0x7fffffffu);
         }
         m = umax(m, mk[k]);
-        if (live && a.y) row_store<W>(a.y, base + c, a.y_bf16, x[k]);
+        if (live && a.y) row_store<W>(a.y, base + c, a.y_bf16, y);
     }
     if constexpr (!Q) return;
     if (a.group == 0) {
@@ -169,13 +177,13 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(RmsArgs a) {
 #pragma unroll
             for (int i = 0; i < GW; ++i) m = umax(m, top[w / GW * GW + i]);
         }
-        const float scale = scale_of_max(m);
+        const float scale = scale_of_max(m, f);
         if (!live) return;
         if (lane == 0) a.scales[row] = scale;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + lane) * W;
-            if (c < a.D) store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale);
+            if (c < a.D) store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale, m, f);
         }
         return;
     }
@@ -184,10 +192,11 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(RmsArgs a) {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int c = (k * L + lane) * W;
-            const float scale = scale_of_max(lanes_umax<16>(mk[k], a.group / 8));
+            const uint32_t g = lanes_umax<16>(mk[k], a.group / 8);
+            const float scale = scale_of_max(g, f);
             if (!live || c >= a.D) continue;
             if (c % a.group == 0) a.scales[row * a.ngroups + c / a.group] = scale;
-            store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale);
+            store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale, g, f);
         }
     } else {
         if constexpr (L <= 64) __syncthreads();  // gtop is zero (rows of more lanes have had a barrier in their sums)
@@ -202,9 +211,10 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(RmsArgs a) {
         for (int k = 0; k < K; ++k) {
             const int c = k * L + lane;
             if (c >= a.D) continue;
-            const float scale = scale_of_max(gtop[grp * NG + c / a.group]);
+            const uint32_t g = gtop[grp * NG + c / a.group];
+            const float scale = scale_of_max(g, f);
             if (c % a.group == 0) a.scales[row * a.ngroups + c / a.group] = scale;
-            store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale);
+            store_e4m3<W>(a.y8 + base + c, x[k], lo[Q ? k : 0], scale, g, f);
         }
     }
 }

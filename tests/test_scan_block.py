@@ -164,6 +164,22 @@ def test_8_bits_stand_for_the_norm(R):
         assert (off <= (2 ** -4 + 2 ** -8) * y.float().abs() + 2 ** -10 * k).all()
 
 
+def test_8_bits_are_the_quotients(R):
+    """Without a weight the values are exact but for their last rounding: the quotient comes in two parts, off by 2^-46 of itself
+    before fp32 and e4m3 round it, so that 64 bits lead elsewhere only where it is that near to a border of both."""
+    import torch
+    for dtype, rows, D, group in ((torch.bfloat16, 256, 4096, None), (torch.float32, 64, 1001, 32), (torch.float32, 999, 256, 64)):
+        gen = torch.Generator(device="cuda").manual_seed(D)
+        x = torch.randn((rows, D), generator=gen, device="cuda").to(dtype)
+        g = group or D
+        y8, scales = torch.empty_like(x, dtype=torch.float8_e4m3fn), torch.empty((rows, -(-D // g)), device="cuda")
+        print_case("quotients", rows, D, group)
+        R.ret_rms_norm_fwd(x, y8=y8, scales=scales, group=group)
+        for i, part in enumerate(x.double().split(g, 1)):
+            want = (448 * part / part.abs().amax(1, keepdim=True)).float().to(torch.float8_e4m3fn)
+            assert torch.equal(y8[:, i * g:(i + 1) * g].float(), want.float()), (D, i)
+
+
 def test_captured_graphs(R):
     """A prompt, a step and the gradients, captured, replayed several times with eager work between, bit for bit the eager
     results; two graphs that share a workspace, in turn."""
