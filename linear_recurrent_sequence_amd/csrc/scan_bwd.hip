@@ -16,7 +16,7 @@
 //
 // Bound by the vector units: grad has 28 instructions per token, channel and state of a wave's 16 x 4, which are 440 us of the
 // 635 that 2 x 2048 tokens of 8192 channels and 16 states take (two waves a SIMD, whose registers are full; waves of 8 tokens
-// with room for four joined twice as often and took as long); local has 11 and takes 172, join 14, the sums 16. The tensors'
+// with room for four joined twice as often and took as long); local has 11 and takes 172, join 14, the sums 13. The tensors'
 // bytes alone are 93.
 #include "scan_bwd.h"
 
