@@ -291,6 +291,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
     if (!grad_pos(a, &pos)) return;
     const int part = pos.part, chunk = pos.chunk, b = pos.b, g = pos.g, cb0 = pos.cb0, cb1 = pos.cb1;
     const int n = scan_length(a.f.lengths, b, N), c0 = chunk * P::CH, t0 = c0 + w * T;
+    const int live = n - t0;  // tokens of the wave's block before n
     const long long row0 = (long long)b * N;
     float* out_bc = a.part_bc + ((long long)part * a.f.B * N + row0) * 2 * S;
     float* out_a = a.part_a + ((long long)b * a.f.nseg + chunk) * D * (S + 2);
@@ -434,16 +435,46 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
                 yp[k % 4] = fmaf(c2[gk][k % GT][j], hh[k][j], yp[k % 4]);
             }
             if (k % 4 == 3) {
-                const float dz = fmaf(skip, u[k / 4], quad_sums(yp[0], yp[1], yp[2], yp[3], q)) * dzf[k / 4];
+                float dz = fmaf(skip, u[k / 4], quad_sums(yp[0], yp[1], yp[2], yp[3], q)) * dzf[k / 4];
+                if (k - 3 + q >= live) dz = 0.f;
                 if (dz_p && own && t0 + k - 3 + q < N)
                     store_out((ost*)(dz_row + (__umul24(k - 3 + q, (uint32_t)D * (uint32_t)sizeof(ost)) +
                                                d * (uint32_t)sizeof(ost))), dz);
             }
             if (k % GT == GT - 1) lds_order();
         }
+        float dA[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
+        // Tokens from n on have steps of 0, but the last state and its gradient pass over them: what is not finite, or
+        // overflows with A, would come into dA. So the last state's one product, in dC of token n - 1, is added here, and the
+        // states from there on become 0.
+        if (live < T) {
+            float yk = 0.f;
+#pragma unroll
+            for (int k = 0; k < T; ++k)
+                if (k == live - 1) yk = quad_of(dp[k / 4], k % 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+                const float dc = yk * hh[T - 1][j];
+                if constexpr (SL == 2) v[4 + j] = live & 1 ? dc : 0.f, v[6 + j] = live & 1 ? 0.f : dc;
+                else v[4 + j % 4] = dc;
+                if (SL == 2 ? j == 0 : j % 4 != 3) continue;
+                const float sum = halving_sums(v, lane);
+#pragma unroll
+                for (int k = 0; k < T; ++k)
+                    if (k == live - 1) acc[SL == 2 ? k / 2 : k * (SL / 4) + j / 4] += sum;
+            }
+#pragma unroll
+            for (int j = 0; j < SL; ++j) {
+#pragma unroll
+                for (int k = 0; k < T; ++k)
+                    if (k >= live - 1) hh[k][j] = 0.f;
+                if (live <= 0) hin[j] = gin[j] = 0.f;
+            }
+        }
         // in reverse, from the group that the loop above read last
         constexpr int last = (T / GT - 1) & 1;
-        float dA[SL], s1[4], s2[4], v[8], dskip = 0.f, dbias = 0.f;
 #pragma unroll
         for (int j = 0; j < SL; ++j) dA[j] = 0.f;
 #pragma unroll
@@ -478,8 +509,8 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
             if (k % 4 == 0) {
                 const int i = k / 4;
                 const float gb = quad_sums(s1[0], s1[1], s1[2], s1[3], q), ak = quad_sums(s2[0], s2[1], s2[2], s2[3], q);
-                // 0 from token n on, as dp, dt and slope are
-                const float x1 = fmaf(skip, dp[i], dt[i] * gb), x2 = fmaf(kLn2, ak, u[i] * gb) * slope[i];
+                float x1 = fmaf(skip, dp[i], dt[i] * gb), x2 = fmaf(kLn2, ak, u[i] * gb) * slope[i];
+                if (k + q >= live) x1 = x2 = 0.f;
                 dskip = fmaf(dp[i], u[i], dskip);
                 dbias += x2;
                 sum_now(dskip);
