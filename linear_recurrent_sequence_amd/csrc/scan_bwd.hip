@@ -508,7 +508,9 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
             for (int j = 0; j < SL; ++j) sum_now(dA[j]);
             if (k % 4 == 0) {
                 const int i = k / 4;
-                const float gb = quad_sums(s1[0], s1[1], s1[2], s1[3], q), ak = quad_sums(s2[0], s2[1], s2[2], s2[3], q);
+                const float gb = quad_sums(s1[0], s1[1], s1[2], s1[3], q);
+                float ak = quad_sums(s2[0], s2[1], s2[2], s2[3], q);
+                if (slope[i] == 0.f) ak = 0.f;  // a step below fp32's range: A times what stays may be outside of it
                 float x1 = fmaf(skip, dp[i], dt[i] * gb), x2 = fmaf(kLn2, ak, u[i] * gb) * slope[i];
                 if (k + q >= live) x1 = x2 = 0.f;
                 dskip = fmaf(dp[i], u[i], dskip);

@@ -124,3 +124,30 @@ def test_states_that_are_not_finite(R, S, bad, value):
     o = _gradients(R, x, dy, dS, h0, lengths, torch.float32)
     _padding(o, lengths)
     _compare(o, x, dy, dS, h0, lengths, torch.float32)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("S", [8, 16, 32, 64])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_steps_that_underflow(R, S, kind):
+    """Steps of exp(-200) and exp(-180), 0 in fp32 as their derivatives, of channels without memory: the state stays as it is,
+    and its product with the rate, which is outside of fp32, has no part in the step's gradient. In 64 bits that is
+    3e38 exp(-180) = 2e-40 times a state and its gradient: nothing beside what close() allows for fp32's range."""
+    import torch
+    print_case("steps_that_underflow", S, kind)
+    tin = torch.float32 if kind == "f32" else torch.bfloat16
+    B, N, D, G, lengths = 2, 150, 20, 1, [150, 90]
+    gen = torch.Generator().manual_seed(S)
+    x = scan_inputs(B, N, D, S, G, tin, 73)
+    x["A"][1], x["A"][7], x["A"][19, ::2] = -1e38, -3e38, -2e38
+    for d in (1, 7, 19):
+        x["dt_bias"][d] = 0.0
+        x["dt"][:, 20:45, d], x["dt"][:, 80:, d] = -200.0, -180.0
+    h0, dS, dy = rand(gen, B, D, S), rand(gen, B, D, S, scale=10.0), rand(gen, B, N, D, dtype=tin)
+    o = _gradients(R, x, dy, dS, h0, lengths, tin)
+    _padding(o, lengths)
+    assert torch.isfinite(o["ddt"]).all() and torch.isfinite(o["dbias"]).all()
+    _compare(o, x, dy, dS, h0, lengths, tin)
+    x["A"][7] = float("-inf")
+    same = _gradients(R, x, dy, dS, h0, lengths, tin)
+    assert all(torch.equal(o[k], same[k]) for k in NAMES)
