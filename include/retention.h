@@ -508,7 +508,8 @@ ret_status_t ret_gated_delta_bwd(const void* q, const void* k, const void* v, co
 /*
  * Root-mean-square norm, the pre-norm without a mean, with the residual stream's addition and an output in 8 bits:
  *     s = x + residual (rounded to x_dt; s = x without one),  y = w (.) s rstd,  rstd = 1 / sqrt(mean(s^2) + eps)
- * over the last axis of x [rows, D]; the statistic in fp32. residual, weight, sum_out, rstd as in ret_layer_norm_fwd. At
+ * over the last axis of x [rows, D]; the statistic in fp32, of any finite values (a row whose squares leave the range is scaled
+ * first; where the root is below 2^-128, rstd is infinite). residual, weight, sum_out, rstd as in ret_layer_norm_fwd. At
  * least one of y (y_dt) and y8 is wanted. y8 [rows, D] holds y in e4m3 (OCP, 1 byte a value) divided by its scale, rounded to
  * nearest even, for a product in 8 bits: y = y8 scale. group = 0: one scale a row, scales float[rows]; group = 32, 64 or 128:
  * one for every group columns, scales float[rows, ceil(D / group)]. scale = max |y| / 448 over its columns, at least 2^-126;

@@ -18,6 +18,9 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: its reciprocal is finite
+// Mean squares below are formed again of larger values: a square of less than 2^-126 is rounded by up to 2^-150, which is 2^-30
+// of this.
+constexpr float kMinSquare = 0x1p-120f;
 
 struct RmsArgs {
     const void *x, *res;  // [rows][D], one dtype
@@ -134,7 +137,20 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(RmsArgs a) {
     }
     if constexpr (NG > 1)
         for (int i = threadIdx.x; i < NG * G; i += THREADS) gtop[i] = 0;  // before the barriers below
-    const float rstd = 1.f / sqrtf(sum(s2) * (1.f / (float)a.D) + a.eps);
+    static_assert(L <= 64 || L == THREADS, "a row's barriers are the workgroup's");
+    const float inv = 1.f / (float)a.D, ms = sum(s2) * inv + a.eps;
+    float rstd;
+    if (ms >= kMinSquare && ms <= 3.4e38f) {
+        rstd = 1.f / sqrtf(ms);
+    } else {  // one for the whole row: the squares leave fp32's range, those of the row times 2^-72 or 2^100 do not
+        const float f = ms > 1.f ? 0x1p-72f : 0x1p100f;
+        s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < W; ++e) s2 += x[k][e] * f * (x[k][e] * f);
+        rstd = f / sqrtf(sum(s2) * inv + a.eps * f * f);
+    }
     if (live && lane == 0 && a.rstd) a.rstd[row] = rstd;
     // 8 bits: y = w s p2 f with p2 the power of two in rstd, so that only the product with w rounds; lo is what it loses
     const bool normal = rstd > kMinScale && rstd < 3e38f;
