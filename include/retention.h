@@ -544,9 +544,9 @@ ret_status_t ret_rms_norm_bwd(const void* dy, const void* x, const float* weight
  * past them are zero, and state_out is the state after lengths[b] tokens. x_ld: elements from a token's row of x to the next
  * token's (0: D), so that x can be a slice of a wider projection's rows; sequence b starts at row b N.
  * dtypes: x and the states in in_dt, y in out_dt; pairs as in ret_chunkwise_fwd; arithmetic in fp32. Supported: W in
- * {2, 3, 4}, B N <= 2^40, and no launch of 2^32 work-items. Pointers 16-byte aligned, x and lengths like one of their
- * elements (rows move as 16-byte vectors where D and x_ld are multiples of 8 and x is 16-byte aligned). Written buffers must
- * not overlap others. Kernel: "ret_short_conv".
+ * {2, 3, 4}, N <= 2^31 - 17, B N <= 2^40, D <= 2^28, x_ld <= 2^32, and no launch of 2^32 work-items. Pointers 16-byte
+ * aligned, x and lengths like one of their elements (rows move as 16-byte vectors where D and x_ld are multiples of 8 and x
+ * is 16-byte aligned). Written buffers must not overlap others. Kernel: "ret_short_conv".
  *
  * ret_short_conv_step computes one token of every sequence: x, y [B, D] (x_ld from sequence to sequence), state [B, W - 1, D]
  * moved on in place. Kernel: "ret_short_conv_step".

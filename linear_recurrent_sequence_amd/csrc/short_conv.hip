@@ -420,6 +420,11 @@ ConvKernels conv_kernels_get(int W, bool vec, bool xb, bool yb) {
 
 size_t esize(ret_dtype_t t) { return t == RET_BF16 ? 2 : 4; }
 
+// Tokens are int, and a strip's walk goes a few past the last.
+bool conv_sizes_fit(int B, int N, int D) {
+    return N <= INT32_MAX - 16 && (long long)B * N <= 1LL << 40 && D <= 1 << 28;
+}
+
 ret_status_t check_conv(const void* x, const void* w, const void* y, int B, int N, int D, int W, int64_t* ld,
                         ret_dtype_t in_dt, ret_dtype_t out_dt, int act) {
     if (!x || !w || !y) return fail(RET_ERR_INVALID_ARG, "null x/weight/output pointer");
@@ -432,7 +437,7 @@ ret_status_t check_conv(const void* x, const void* w, const void* y, int B, int 
     if (W < 2 || W > 4) return fail(RET_ERR_UNSUPPORTED, "short convolution: width %d is not 2, 3 or 4", W);
     if (*ld == 0) *ld = D;
     if (*ld < D) return fail(RET_ERR_INVALID_ARG, "rows of x (%lld apart) are shorter than D=%d", (long long)*ld, D);
-    if ((long long)B * N > 1LL << 40 || *ld > 1LL << 32 || D > 1 << 28)
+    if (!conv_sizes_fit(B, N, D) || *ld > 1LL << 32)
         return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d N=%d D=%d ld=%lld too large", B, N, D, (long long)*ld);
     return RET_OK;
 }
@@ -442,7 +447,7 @@ bool conv_vec(const void* x, int D, int64_t ld) { return D % 8 == 0 && ld % 8 ==
 int64_t conv_cblocks(int D, int v) { return (D + 64 * v - 1) / (64 * v); }  // v: channels a thread
 
 // Half of `most` and so on down to `least`, until there are two waves a SIMD.
-int conv_strip(int B, int N, int64_t cblocks, int most, int least) {
+int conv_strip(int B, int64_t N, int64_t cblocks, int most, int least) {
     while (most > least && cblocks * B * ((N + most - 1) / most) < 2048) most /= 2;
     return most;
 }
@@ -455,7 +460,7 @@ ConvBwdPlan conv_bwd_plan(int B, int N, int D, bool vec) {
     ConvBwdPlan p;
     p.cblocks = conv_cblocks(D, vec ? kConvV : 1);
     p.strip = conv_strip(B, N, p.cblocks, kConvBwdStrip, kConvBwdStripLeast);
-    p.strips = (N + p.strip - 1) / p.strip;
+    p.strips = ((int64_t)N + p.strip - 1) / p.strip;
     const int64_t most = (B * p.strips + kConvWaves - 1) / kConvWaves, want = (1024 + p.cblocks - 1) / p.cblocks;
     p.parts = most < want ? most : want;
     return p;
@@ -477,7 +482,7 @@ ret_status_t ret_short_conv_fwd(const void* x, int64_t x_ld, const float* weight
     const bool vec = conv_vec(x, D, x_ld);
     const int64_t cblocks = conv_cblocks(D, vec ? kConvV : 1);
     const int strip = conv_strip(B, N, cblocks, kConvStrip, kConvStripLeast);
-    const int64_t strips = (N + strip - 1) / strip;
+    const int64_t strips = ((int64_t)N + strip - 1) / strip;
     const unsigned long long wgs = (unsigned long long)cblocks * ((strips + kConvWaves - 1) / kConvWaves) * B;
     if (!grid_fits(wgs, 1, 1, 64 * kConvWaves))
         return fail(RET_ERR_UNSUPPORTED, "short convolution: B=%d N=%d D=%d exceed a launch", B, N, D);
@@ -498,7 +503,7 @@ ret_status_t ret_short_conv_fwd(const void* x, int64_t x_ld, const float* weight
 }
 
 size_t ret_short_conv_bwd_workspace_bytes(int B, int N, int D, int W) {
-    if (B <= 0 || N <= 0 || D <= 0 || W < 2 || W > 4) return 0;
+    if (B <= 0 || N <= 0 || D <= 0 || W < 2 || W > 4 || !conv_sizes_fit(B, N, D)) return 0;
     // either kernel's (x may be a slice that the vectors do not take)
     int64_t parts = conv_bwd_plan(B, N, D, false).parts;
     if (D % 8 == 0) parts = std::max(parts, conv_bwd_plan(B, N, D, true).parts);
