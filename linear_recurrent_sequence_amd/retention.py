@@ -948,7 +948,7 @@ def _arg(t, name, shape, dtypes, dev):
 
 def _rows_arg(t, name, shape, dtypes, dev, inner):
     """(address, elements from row to row, 0 where contiguous) of a tensor that may be a slice of wider rows (_token_rows)."""
-    if t is None or t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.is_contiguous():
         return _arg(t, name, shape, dtypes, dev), 0
     if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev:
         _arg(t.contiguous(), name, shape, dtypes, dev)  # says what is wrong
@@ -964,8 +964,8 @@ def _gpu_of(t, name):
 
 def _workspace(ws, dev):
     """(address, bytes) of a workspace."""
-    if ws is None:
-        return None, 0
+    if not isinstance(ws, torch.Tensor):
+        return _arg(ws, "workspace", None, None, dev), 0
     return _arg(ws, "workspace", ws.shape, (ws.dtype,), dev), ws.numel() * ws.element_size()
 
 
@@ -1017,7 +1017,7 @@ def ret_rms_norm_bwd(dy, x, rstd, dx, weight=None, dsum=None, dweight=None, work
     lib = load()
     rows, D = _norm_rows(x)
     for name, t in (("dy", dy), ("dx", dx), ("rstd", rstd)):
-        if t is None:
+        if not isinstance(t, torch.Tensor):
             raise ValueError("%s must be a tensor" % name)
     dev = _gpu_of(x, "x")
     args = (_arg(dy, "dy", x.shape, _IO, dev), _arg(x, "x", x.shape, (x.dtype,), dev),
@@ -1117,7 +1117,7 @@ def ret_short_conv_bwd(dy, x, weight, dx, dweight=None, bias=None, dbias=None, s
     W = _conv_width(x, weight, 3)
     B, N, D = x.shape
     for name, t in (("dy", dy), ("dx", dx)):
-        if t is None:
+        if not isinstance(t, torch.Tensor):
             raise ValueError("%s must be a tensor" % name)
     _delta_lengths(lengths, B)
     dev, xt, ot, state = _gpu_of(x, "x"), (x.dtype,), (dx.dtype,), (B, W - 1, D)
@@ -1164,7 +1164,7 @@ def _scan_sizes(u, dt, A, b, c, step=False):
     if not isinstance(b, torch.Tensor) or b.dim() != nd + 1 or b.shape[:-2] != u.shape[:-1]:
         raise ValueError("b must be a tensor [%s, G, S]" % ("B" if step else "B, N"))
     for name, t in (("dt", dt), ("A", A), ("c", c)):
-        if t is None:
+        if not isinstance(t, torch.Tensor):
             raise ValueError("%s must be a tensor" % name)
     G, S = b.shape[-2:]
     if G == 0 or u.shape[-1] % G:
@@ -1255,7 +1255,7 @@ def ret_selective_scan_bwd(u, dt, A, b, c, dy, du, ddt, dA, db, dc, d_skip=None,
     G, S = _scan_sizes(u, dt, A, b, c)
     B, N, D = u.shape
     for name, t in (("dy", dy), ("du", du), ("ddt", ddt), ("db", db), ("dc", dc)):
-        if t is None:
+        if not isinstance(t, torch.Tensor):
             raise ValueError("%s must be a tensor" % name)
     if dz is not None and z is None:
         raise ValueError("dz without z")
