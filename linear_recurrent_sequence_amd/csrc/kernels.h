@@ -57,10 +57,17 @@ struct FwdArgs {
     double theta[kMaxPairs];
 };
 
-// swish(g) = g sigmoid(g), the sigmoid as 1 / (1 + 2^(-g log2 e)) on the hardware 2^x and reciprocal (about
-// 1 ulp each).
-__device__ __forceinline__ float swish_hw(float g) {
-    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+// The sigmoid as 1 / (1 + 2^(-g log2 e)) on the hardware 2^x and reciprocal (about 1 ulp each), and swish(g) = g sigmoid(g).
+__device__ __forceinline__ float sigmoid_hw(float g) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+}
+__device__ __forceinline__ float swish_hw(float g) { return g * sigmoid_hw(g); }
+
+// Tokens of sequence b: its length, cut to 0 .. N, or N without lengths.
+__device__ __forceinline__ int length_of(const int32_t* lengths, int b, int N) {
+    if (!lengths) return N;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > N ? N : n;
 }
 
 // Sum over LPG consecutive lanes (a power of 2, aligned), left in every one of them. Within a row of 16 lanes

@@ -47,19 +47,6 @@ struct ScanArgs {
     int deal;                            // of workgroups to the XCDs: ScanDeal
 };
 
-// One value of either type as fp32.
-template <class E>
-__device__ __forceinline__ float at(const void* p, long long i) {
-    if constexpr (sizeof(typename E::st) == 2) return bf16_to_f32(((const uint16_t*)p)[i]);
-    else return ((const float*)p)[i];
-}
-
-__device__ __forceinline__ int scan_length(const int32_t* lengths, int b, int N) {
-    if (!lengths) return N;
-    const int n = lengths[b];
-    return n < 0 ? 0 : n > N ? N : n;
-}
-
 // Workgroup number -> position, so that the workgroups of neighbouring positions run on one XCD (they are dealt to the 8 in
 // turn): n is a multiple of 8.
 __device__ __forceinline__ long long xcd_order(long long id, long long n) { return (id & 7) * (n >> 3) + (id >> 3); }
@@ -77,10 +64,6 @@ __device__ __forceinline__ void softplus(float x, float* value, float* slope) {
     *value = fmaf(2.f * r, p, x > 0.f ? x : 0.f);
     const float s = __builtin_amdgcn_rcpf(1.f + e);
     *slope = x > 0.f ? s : e * s;
-}
-
-__device__ __forceinline__ float sigmoid_of(float x) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
 
 // A in units of log2(e), so that a_t = 2^(dt_t A). An infinite A (a state without memory) becomes the largest number: steps of

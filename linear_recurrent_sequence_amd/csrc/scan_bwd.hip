@@ -24,9 +24,6 @@ namespace ret {
 
 namespace {
 
-template <int S>
-struct GradShape : ScanShape<S> {};
-
 // A sum is added to here, not when it is wanted: until then its terms, one a token, would take registers.
 __device__ __forceinline__ void sum_now(float& s) { __asm__ volatile("" : "+v"(s)); }
 
@@ -52,7 +49,7 @@ __device__ __forceinline__ float halving_sums(const float (&v)[8], int lane) {
 // A wave's block of 16 channels, loaded ahead.
 template <class E, int S>
 struct GradBlock {
-    typedef GradShape<S> P;
+    typedef ScanShape<S> P;
     typedef Raw<E> R;
     typename R::one u[P::TL], dt[P::TL], z[P::TL], dy[P::TL];
     float A[P::SL], bias;
@@ -69,10 +66,10 @@ struct GradBlock {
 // The decays of a wave's block, and what it leaves of a state from zero (h) and of a gradient behind it from zero (G).
 template <int S>
 __device__ __forceinline__ void grad_local(const float* Bs, const float* Cs, int q, const float (&A2)[S / 4],
-                                           const float (&dt)[GradShape<S>::TL], const float (&du)[GradShape<S>::TL],
-                                           const float (&dp)[GradShape<S>::TL], float (&al)[GradShape<S>::T][S / 4],
+                                           const float (&dt)[ScanShape<S>::TL], const float (&du)[ScanShape<S>::TL],
+                                           const float (&dp)[ScanShape<S>::TL], float (&al)[ScanShape<S>::T][S / 4],
                                            float (&h)[S / 4], float (&G)[S / 4]) {
-    constexpr int SL = S / 4, T = GradShape<S>::T, GT = SL >= 16 ? 1 : 16 / SL;
+    constexpr int SL = S / 4, T = ScanShape<S>::T, GT = SL >= 16 ? 1 : 16 / SL;
     float v[2][GT][SL];
 #pragma unroll
     for (int j = 0; j < SL; ++j) h[j] = G[j] = 0.f;
@@ -128,8 +125,8 @@ __device__ __forceinline__ bool grad_pos(const ScanBwdArgs& a, GradPos* p) {
 // P the product of the decays so far, h = a h + du B and G += P C dp. A wave walks a chunk on its own; where that leaves the
 // card idle (SPLIT) a workgroup's waves walk a block of it each and join them.
 template <class E, int S, bool SPLIT>
-__global__ __launch_bounds__(GradShape<S>::THREADS) void scan_local_bwd_kernel(ScanBwdArgs a) {
-    typedef GradShape<S> P;
+__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_local_bwd_kernel(ScanBwdArgs a) {
+    typedef ScanShape<S> P;
     constexpr int SL = P::SL, T = P::T, TL = P::TL, NW = P::NW;
     __shared__ float bc[NW][2][T * S];
     __shared__ float ex[SPLIT ? NW : 1][3][SPLIT ? 64 * SL : 1];
@@ -143,7 +140,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_local_bwd_kernel(S
     }
     const int d = at.cb * kScanCh + (lane >> 2), dc = d < D ? d : D - 1;
     const int g = __builtin_amdgcn_readfirstlane(dc / (D / a.f.G));
-    const int n = scan_length(a.f.lengths, at.b, a.f.N), c0 = at.seg * P::CH, first = SPLIT ? c0 + w * T : c0;
+    const int n = length_of(a.f.lengths, at.b, a.f.N), c0 = at.seg * P::CH, first = SPLIT ? c0 + w * T : c0;
     const int c1 = n - first < (SPLIT ? T : P::CH) ? n : first + (SPLIT ? T : P::CH);
     const long long row0 = (long long)at.b * a.f.N, seg = ((long long)at.b * a.f.nseg + at.seg) * D + d;
     const float bias = a.f.bias ? a.f.bias[dc] : 0.f;
@@ -275,8 +272,8 @@ __global__ __launch_bounds__(256) void scan_join_bwd_kernel(ScanBwdArgs a) {
 }
 
 template <class E, class O, int S>
-__global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBwdArgs a) {
-    typedef GradShape<S> P;
+__global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_grad_kernel(ScanBwdArgs a) {
+    typedef ScanShape<S> P;
     typedef Raw<E> R;
     typedef typename O::st ost;
     constexpr int SL = P::SL, T = P::T, TL = P::TL, NW = P::NW;
@@ -290,7 +287,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
     GradPos pos;
     if (!grad_pos(a, &pos)) return;
     const int part = pos.part, chunk = pos.chunk, b = pos.b, g = pos.g, cb0 = pos.cb0, cb1 = pos.cb1;
-    const int n = scan_length(a.f.lengths, b, N), c0 = chunk * P::CH, t0 = c0 + w * T;
+    const int n = length_of(a.f.lengths, b, N), c0 = chunk * P::CH, t0 = c0 + w * T;
     const int live = n - t0;  // tokens of the wave's block before n
     const long long row0 = (long long)b * N;
     float* out_bc = a.part_bc + ((long long)part * a.f.B * N + row0) * 2 * S;
@@ -359,7 +356,7 @@ __global__ __launch_bounds__(GradShape<S>::THREADS) void scan_grad_kernel(ScanBw
         if (a.f.z)
 #pragma unroll
             for (int i = 0; i < TL; ++i) {
-                const float z = R::value(x.z[i]), s = sigmoid_of(z);
+                const float z = R::value(x.z[i]), s = sigmoid_hw(z);
                 dzf[i] = dp[i] * (s * (1.f + z * (1.f - s)));
                 dp[i] *= z * s;
             }
@@ -590,7 +587,7 @@ template <class E, class O, int S>
 bool pick(ScanBwdKernels* o) {
     *o = {scan_local_bwd_kernel<E, S, false>, scan_local_bwd_kernel<E, S, true>, scan_join_bwd_kernel<S>,
           scan_grad_kernel<E, O, S>, scan_sums_kernel<O, S>,
-          GradShape<S>::CH, GradShape<S>::NW};
+          ScanShape<S>::CH, ScanShape<S>::NW};
     return true;
 }
 template <class E, class O>

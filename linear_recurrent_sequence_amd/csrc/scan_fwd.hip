@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256) void scan_walk_kernel(ScanArgs a) {
     if (at.cb * kScanCh >= a.D) return;
     const int d = at.cb * kScanCh + (lane >> 2), dc = d < a.D ? d : a.D - 1;
     const int g = __builtin_amdgcn_readfirstlane(dc / (a.D / a.G));  // one for the whole wave
-    const int n = scan_length(a.lengths, at.b, a.N);
+    const int n = length_of(a.lengths, at.b, a.N);
     const int s0 = at.seg * a.seg_tokens, s1 = a.N - s0 < a.seg_tokens ? a.N : s0 + a.seg_tokens, e1 = s1 < n ? s1 : n;
     const long long row0 = (long long)at.b * a.N;
     const float bias = a.bias ? a.bias[dc] : 0.f, skip = !LOCAL && a.skip ? a.skip[dc] : 0.f;
@@ -148,7 +148,7 @@ __global__ __launch_bounds__(ScanShape<S>::THREADS) void scan_chunks_kernel(Scan
     if (!scan_pos(a, &at)) return;
     const int d = at.cb * kScanCh + (lane >> 2), dc = d < a.D ? d : a.D - 1;
     const int g = __builtin_amdgcn_readfirstlane(dc / (a.D / a.G));
-    const int n = scan_length(a.lengths, at.b, a.N);
+    const int n = length_of(a.lengths, at.b, a.N);
     const int s0 = at.seg * a.seg_tokens, s1 = a.N - s0 < a.seg_tokens ? a.N : s0 + a.seg_tokens;
     const long long row0 = (long long)at.b * a.N;
     const float bias = a.bias ? a.bias[dc] : 0.f, skip = a.skip ? a.skip[dc] : 0.f;

@@ -59,16 +59,6 @@ struct ConvStepArgs {
     int B, D, silu, cblocks, seqs;
 };
 
-__device__ __forceinline__ float sigmoid_hw(float x) {
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
-}
-
-__device__ __forceinline__ int length_of(const int32_t* lengths, int b, int N) {
-    if (!lengths) return N;
-    const int n = lengths[b];
-    return n < 0 ? 0 : n > N ? N : n;
-}
-
 // V channels' weights [V][W] as w[j][v], and biases.
 template <int V, int W>
 __device__ __forceinline__ void load_weights(const float* w, const float* bias, long long c, int D, float (&o)[W][V],
