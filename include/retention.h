@@ -545,8 +545,8 @@ ret_status_t ret_rms_norm_bwd(const void* dy, const void* x, const float* weight
  * token's (0: D), so that x can be a slice of a wider projection's rows; sequence b starts at row b N.
  * dtypes: x and the states in in_dt, y in out_dt; pairs as in ret_chunkwise_fwd; arithmetic in fp32. Supported: W in
  * {2, 3, 4}, N <= 2^31 - 17, B N <= 2^40, D <= 2^28, x_ld <= 2^32, and no launch of 2^32 work-items. Pointers 16-byte
- * aligned, x and lengths like one of their elements (rows move as 16-byte vectors where D and x_ld are multiples of 8 and x
- * is 16-byte aligned). Written buffers must not overlap others. Kernel: "ret_short_conv".
+ * aligned, x and lengths like one of their elements (rows move as vectors of 4 elements where D and x_ld are multiples of 8
+ * and x is 16-byte aligned, else one by one). Written buffers must not overlap others. Kernel: "ret_short_conv".
  *
  * ret_short_conv_step computes one token of every sequence: x, y [B, D] (x_ld from sequence to sequence), state [B, W - 1, D]
  * moved on in place. Kernel: "ret_short_conv_step".
@@ -617,7 +617,8 @@ ret_status_t ret_selective_scan_step(const void* u, const void* dt, const float*
  * Gradients of ret_selective_scan_fwd: with dy = dL/dy [B, N, D] in in_dt and, optionally, dstate_out = dL/dstate_out fp32,
  * writes du, ddt [B, N, D] (ddt: that of dt before dt_bias and softplus), db, dc [B, N, G, S] (summed over the channels of a
  * group) in out_dt, contiguous, and, unless NULL, dz (out_dt), dA float[D, S], dd_skip, ddt_bias float[D] and dstate_in. The
- * other arguments are the forward call's. Gradients of the padding past lengths[b] are zero. workspace:
+ * other arguments are the forward call's. Gradients of the padding past lengths[b] are zero, and it has no part in any other,
+ * whatever the states are; a step that softplus underflows to 0 has no gradient through its decay. workspace:
  * ret_selective_scan_bwd_workspace_bytes (the states entering and the gradients leaving chunks of 128 tokens (32 and 16 at 32
  * and 64 states), partial sums of db and dc over up to 512 channels and of dA over a chunk). Limits as the forward's in
  * segments. Sums have one order: the same call gives the same bits. opts: the timer. Kernels: "ret_scan_local_bwd",

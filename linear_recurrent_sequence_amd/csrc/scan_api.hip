@@ -71,7 +71,9 @@ constexpr Cost kCost[4] = {{99.f, 0.070f, 23.f, 310.f, 0.085f},   // 8 states
                            {122.f, 0.095f, 30.f, 230.f, 0.117f},  // 16
                            {200.f, 0.149f, 78.f, 400.f, 0.186f},  // 32
                            {370.f, 0.258f, 155.f, 378.f, 0.325f}};  // 64
-constexpr int kSegWaves = 8192, kSegLeast = 64;  // waves that the segments are for (8 a SIMD), tokens of a segment at least
+// Waves that the segments are for (8 a SIMD: as many as run at once of the local pass, of the walk 5), tokens of a segment at
+// least.
+constexpr int kSegWaves = 8192, kSegLeast = 64;
 
 struct Plan {
     bool walk;

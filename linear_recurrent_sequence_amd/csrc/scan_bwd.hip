@@ -10,14 +10,18 @@
 //
 // dB and dC are sums over all channels. A wave adds its 16 channels up by halving exchanges, 8 values at a time (16
 // instructions for 8 values where separate sums would take 32), keeps one register for each of its groups of 8 over the
-// `run` blocks of channels that its workgroup does one after another, and leaves them as partial sums for sum_bc. Every sum
+// blocks of channels that its workgroup does one after another, and leaves them as partial sums for the sums' kernel. Every sum
 // has one order. Through LDS instead (each wave's products laid down and read back transposed, one add a value) grad took
-// 656 us where this takes 635.
+// 656 us where this took 635.
 //
 // Bound by the vector units: grad has 28 instructions per token, channel and state of a wave's 16 x 4, which are 440 us of the
-// 635 that 2 x 2048 tokens of 8192 channels and 16 states take (two waves a SIMD, whose registers are full; waves of 8 tokens
-// with room for four joined twice as often and took as long); local has 11 and takes 172, join 14, the sums 13. The tensors'
-// bytes alone are 93.
+// 598 that 2 x 2048 tokens of 8192 channels and 16 states take (two waves a SIMD, whose registers are full; waves of 8 tokens
+// with room for four joined twice as often and took as long); local has 11 and takes 155, join 14, the sums 12: together 778.
+// The tensors' bytes alone are 92. At 8 states 436 + 124 + 7 + 7 us.
+//
+// At 32 and 64 states a chunk is 32 and 16 tokens instead of 128, so that the states, gradients and sums at its edges are 4 and
+// 8 times as many a token, and grad takes 264 and 346 registers, which leaves one wave a SIMD: grad 1558 and 3324 us, local 278
+// and 614, join 93 and 444, the sums 30 and 108.
 #include "scan_bwd.h"
 
 namespace ret {

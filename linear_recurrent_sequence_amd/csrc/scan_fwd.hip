@@ -3,8 +3,9 @@
 // them; the tensors' bytes take half of that time at 16 states.
 //
 // walk: a wave takes 16 channels along the tokens with their states in registers; one pass, for as many waves as there are
-// blocks of channels. 4 x 2741 tokens of 8192 channels (16 states, bf16, gated): 470 us, 2 waves a SIMD, each of them 185
-// cycles a token where 124 are left when 8 share the SIMD.
+// blocks of channels. 4 x 2741 tokens of 8192 channels (16 states, bf16, gated): 469 us, 2 waves a SIMD, 186 cycles a token
+// and wave where 148 are left when 5 share the SIMD (as many as its 87 registers let): B and C of a token come from LDS right
+// before they are used, and few waves leave that time open. fp32: 510 us.
 //
 // chunks: a workgroup walks the chunks of its sequence, NW waves a chunk, each its own T tokens. A wave computes its decays
 // once, keeps them in 64 registers a lane, and from them the state its tokens leave if they start from zero; the waves exchange
@@ -13,8 +14,8 @@
 // walking wave takes 122, but three times the instructions: for few blocks of channels. 64 tokens of 128 channels 7.6 us.
 //
 // Few, long sequences are cut into segments: local, a walk, leaves each segment's state from zero; join carries the states
-// over the segments by their decays, exp(A sum dt); then the walk starts from them. 65536 tokens of 1024 channels: 219 + 15 +
-// 244 us; the two passes are within 1.3 of the cycles above.
+// over the segments by their decays, exp(A sum dt); then the walk starts from them. 65536 tokens of 1024 channels: 189 + 15 +
+// 279 us, of which the cycles above, in two passes, are 320.
 #include "scan.h"
 
 namespace ret {

@@ -8,8 +8,9 @@
 // last W dpre) in registers, so that a strip reads its tokens once and W - 1 (2 W - 2) more of its neighbours'. Each kernel
 // reads and writes its tensors once and is bound by HBM. The gradients' sums over tokens stay in registers over a
 // workgroup's strips, meet in LDS and leave one partial row per workgroup, added up in a fixed order by a second kernel.
-// 4 x 2048 tokens of 8192 channels, bf16, width 4: gradients 88 to 93 us and 5 for the sums, 4.6 TB/s of the 5.1 that a large
-// copy reaches (the rows before and behind a strip come twice, mostly from L2). 3 x 2741 forward 56 to 62 us.
+// 4 x 2048 tokens of 8192 channels, width 4: gradients 94 to 96 us in bf16, 5 of them for the sums, 4.5 TB/s of the 5.1 that a
+// large copy reaches (the rows before and behind a strip come twice, mostly from L2); 214 in fp32, 132 in bf16 where 8190
+// channels go one by one. 3 x 2741 tokens forward 66 us, in fp32 115.
 #include <algorithm>
 
 #include "host.h"
@@ -188,6 +189,8 @@ __global__ __launch_bounds__(64 * kConvWaves) void conv_fwd_kernel(ConvArgs a) {
 // Strips of a workgroup's waves: part p takes strips p kConvWaves + wave, then every parts kConvWaves further, over all
 // sequences. A strip yields dx of tokens t0 - (W - 1) .. t1 - W: with dpre from t0 on that needs the W - 1 dpre before t0,
 // computed again; the last strip of a sequence goes on to the end of dx with dpre of zero, the first starts in the state.
+// Three waves a SIMD: of vectors at width 4 that spills 1 register in bf16, 6 with fp32 outputs and 77 in fp32 (120 bytes a
+// lane), and 2 at width 3 in fp32.
 template <int V, int W, bool XB, bool YB>
 __global__ __launch_bounds__(64 * kConvWaves, 3) void conv_bwd_kernel(ConvBwdArgs a) {
     __shared__ float meet[kConvWaves - 1][64][V];
@@ -401,7 +404,8 @@ ConvKernels conv_of_types(bool xb, bool yb) {
     return {conv_fwd_kernel<V, W, true, false>, conv_bwd_kernel<V, W, true, false>, conv_step_kernel<V, W, true, false>};
 }
 
-// vec: kConvV channels a thread as vectors, where every row starts on 16 bytes; else channel by channel.
+// vec: kConvV channels a thread as vectors (8 bytes in bf16, 16 in fp32), where every row starts on 16 bytes; else channel by
+// channel.
 ConvKernels conv_kernels_get(int W, bool vec, bool xb, bool yb) {
     if (W == 2) return vec ? conv_of_types<kConvV, 2>(xb, yb) : conv_of_types<1, 2>(xb, yb);
     if (W == 3) return vec ? conv_of_types<kConvV, 3>(xb, yb) : conv_of_types<1, 3>(xb, yb);
